@@ -12,6 +12,10 @@
  *                     bonus token;
  *   sv_kv_commit      copy of the committed rows into the cache and the length
  *                     update (cache length == committed-token count).
+ * and, around it: the paged cache filled with rotated prompt rows
+ * (sv_kv_append_paged), the same cache in 4 bits (sv_kv_append_q4,
+ * sv_kv_commit_q4, sv_verify_attn_q4, sv_kv_gather_q4), and the sampling
+ * controls on the block's logits (sv_logits_process).
  *
  * Sources, cited by page title and section:
  *   [SCS]  "SpecDec-Context-Scaling project guide", sec. 3, 3.1, 3.2, 7.1
@@ -86,6 +90,8 @@ typedef enum sv_status {
 #define SV_DEVERR_PATH        0x20u  /* commit: n_acc outside [0, R) or path entry outside [0, R) */
 #define SV_DEVERR_TIMEOUT     0x40u  /* an internal bounded wait gave up (should never happen) */
 #define SV_DEVERR_PAGE        0x80u  /* paged KV: a page-table entry outside [0, num_pages) */
+#define SV_DEVERR_ROWS   0x01000000u /* offsets of rows (append) or entries (biases) that fall or leave the array */
+#define SV_DEVERR_PARAM  0x02000000u /* a per-sequence sampling parameter that is not finite, or a factor <= 0 */
 /* (A library built with -DSV_DEBUG also reports failed internal self-checks,
  * as bit 31 plus a check code in bits 8..23.) */
 
@@ -237,6 +243,55 @@ SV_API sv_status sv_lm_head_ex(const uint16_t* hid, const uint16_t* W, float* lo
 SV_API size_t sv_lm_head_argmax_bytes(int32_t N, int32_t V);
 SV_API sv_status sv_lm_head_argmax(const uint16_t* hid, const uint16_t* W, float* logits, int32_t N, int32_t H,
                                    int32_t V, uint64_t* argmax, size_t argmax_bytes, uint32_t flags, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Sampling controls between the LM head and the acceptance.                 */
+/* ------------------------------------------------------------------------ */
+
+/* Penalties for repeated tokens, biases and grammar masks on the logits of a
+ * verify block.  For row j of sequence b and token v let n be the times v
+ * occurs among the sequence's generated tokens hist[b][prompt_len[b] ..
+ * hist_len[b] - 1] and on the row's path in the block (tok of j and of the rows
+ * before it, or of its ancestors in a tree): when the row's token is drawn, the
+ * drafts on its path have been said.  Then, each step rounded to fp32,
+ *     x = l > 0 ? l / repetition[b] : l * repetition[b]   if n > 0 or v is in
+ *                                      the prompt hist[b][0 .. prompt_len[b] - 1]
+ *     x = (x - frequency[b] * n) - presence[b]            if n > 0
+ *     x = x + bias                                        if v has one
+ *     x = mask_value                                      if the row's mask bit
+ *                                      of v is 0 (NaN and infinity included)
+ * Every control is optional (NULL).
+ *   logits     [B][R][V] fp32, 1 <= R <= 128
+ *   hist       [B][hist_cap] int32, hist_len [B]: the tokens before the block
+ *              (the pending token tok[b][0] is not among them); prompt_len [B]
+ *              or NULL (no prompt)
+ *   tok, parent  the block, as for sv_accept_greedy
+ *   repetition, frequency, presence  [B] fp32
+ *   bias_off   [B + 1] int32, bias_tok, bias_val [n_bias]: sequence b's entries
+ *              bias_off[b] .. bias_off[b+1] - 1; of a token named twice the
+ *              later entry holds
+ *   mask       [B][R][ceil(V / 32)] words, bit v % 32 of word v / 32 set where
+ *              the row allows v; bits past V are ignored
+ *   mask_value not NaN; a finite one (such as -1e30) keeps a masked row valid for
+ *              sv_accept_sample, which reports infinite logits
+ *   out        [B][R][V] fp32, logits itself, or NULL
+ *   argmax     NULL or [B * R][ceil(V / 128)] keys of the processed logits, as
+ *              sv_lm_head_argmax writes them (sv_lm_head_argmax_bytes(B * R, V)
+ *              bytes); out or argmax must be given
+ * Token ids outside [0, V) are ignored (SV_DEVERR_TOKEN); a history length
+ * outside [0, hist_cap] is clamped (SV_DEVERR_LENGTH); bias offsets that fall
+ * or leave [0, n_bias] drop the sequence's biases (SV_DEVERR_ROWS); a
+ * parameter that is not finite, or a repetition <= 0, counts as absent
+ * (SV_DEVERR_PARAM); a malformed tree path counts the row's own token alone
+ * (SV_DEVERR_TREE); NaN among logits that keys are formed from sets
+ * SV_DEVERR_NONFINITE. */
+SV_API sv_status sv_logits_process(const float* logits, int32_t B, int32_t R, int32_t V, const int32_t* hist,
+                                   int32_t hist_cap, const int32_t* hist_len, const int32_t* prompt_len,
+                                   const int32_t* tok, const int32_t* parent, const float* repetition,
+                                   const float* frequency, const float* presence, const int32_t* bias_off,
+                                   const int32_t* bias_tok, const float* bias_val, int32_t n_bias,
+                                   const uint32_t* mask, float mask_value, float* out, uint64_t* argmax,
+                                   size_t argmax_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Greedy acceptance ([SCS] sec. 3 and 3.1).                                 */
@@ -433,6 +488,110 @@ SV_API sv_status sv_kv_commit_paged(uint16_t* k_pool, uint16_t* v_pool, int32_t 
  *   bytes == 0: SV_OK, nothing launched.
  * Ownership: the caller's; the library keeps nothing. */
 SV_API sv_status sv_copy(void* dst, const void* src, size_t bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Filling the paged cache: prompts, prefill chunks and single tokens.       */
+/* ------------------------------------------------------------------------ */
+
+/* Appends N new rows of one layer to the paged caches of B sequences, K
+ * rotated by its position on the way (the caches hold rotated K, see
+ * sv_verify_attn).  Sequence b's rows are row_off[b] .. row_off[b+1] - 1 of k
+ * and v, and row row_off[b] + i goes to position p = len[b] + i, row p % 64 of
+ * page page_table[b][p / 64].  len is read, not advanced: every layer appends
+ * at the same positions, and the caller adds the counts after the last one.
+ *   k, v       [N] rows of [Hkv][D] bf16, rows k_stride and v_stride elements
+ *              apart (multiples of 8, at least Hkv * D: slices of a fused
+ *              projection are fine); rows outside every sequence (padding
+ *              before row_off[0] or from row_off[B] on) are not read
+ *   row_off    [B + 1] int32, non-decreasing, within [0, N]
+ *   rope       NULL (K copied as it is) or [rope_positions][rot] fp32: for each
+ *              position the rot / 2 cosines, then the rot / 2 sines of its
+ *              angles.  Dims d and d + rot/2 (or, with SV_ROPE_INTERLEAVED, 2d
+ *              and 2d + 1) turn together,
+ *                  y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin,
+ *              each product and sum rounded to fp32, the results to bf16; dims
+ *              from rot on are copied.  rot % 16 == 0, 16 <= rot <= D.
+ *   k_pool, v_pool, num_pages, page_table, max_pages  as for
+ *              sv_verify_attn_paged; D % 8 == 0, D <= 1024
+ * A row whose position is negative, at or past max_pages * 64 or past the rope
+ * table is dropped (SV_DEVERR_LENGTH), as is one whose page lies outside the
+ * pool (SV_DEVERR_PAGE) and every row of a sequence whose offsets fall or leave
+ * [0, N] (SV_DEVERR_ROWS).  Everything else in the pools stays as it is.
+ * Sequences of one call may not share a page that one of them appends to.
+ * N = 0 does nothing. */
+#define SV_ROPE_INTERLEAVED 1u
+SV_API sv_status sv_kv_append_paged(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                                    int32_t N, const int32_t* row_off, int32_t B, int32_t Hkv, int32_t D,
+                                    const float* rope, int32_t rope_positions, int32_t rot, uint16_t* k_pool,
+                                    uint16_t* v_pool, int32_t num_pages, const int32_t* page_table,
+                                    int32_t max_pages, const int32_t* len, uint32_t flags, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The 4-bit paged KV cache: 72 bytes a row in place of 256.                 */
+/* ------------------------------------------------------------------------ */
+
+/* A row (one position of one KV head, D = 128) is four groups of 32 dims; a
+ * group holds a bf16 scale s and a code c in 0..15 per dim, for the value
+ * (c - 8) s.  What this library writes has s = amax / 7 rounded up to 4
+ * significant bits and limited to [2^-100, 2^118] (0 for an all-zero group) and
+ * c = 8 + min(max(rint(x / s), -7), 7): values are off by at most s / 2, and
+ * (c - 8) s is exactly a bf16.  A group that holds NaN or infinity gets the
+ * scale NaN (it reads back as NaN) and sets SV_DEVERR_NONFINITE.
+ * The pools are [num_pages][Hkv][SV_KV_Q4_BYTES] bytes, 64 positions a page,
+ * position p of sequence b in page page_table[b][p / 64] as for the bf16 pools.
+ * A (page, head) of K:  codes  [4 groups][64 positions][16 bytes], the 32 dims
+ *                       of a group as four little-endian 32-bit words of 8;
+ *                       scales [64 positions][4 groups] from byte 4096 on.
+ * A (page, head) of V:  codes  [8 octets of positions][128 dims][4 bytes], a
+ *                       word holding 8 positions of one dim;
+ *                       scales [4 groups][64 positions] from byte 4096 on.
+ * Element e of a word's 8 sits at bit 4 (e >> 1) + 16 (e & 1). */
+#define SV_KV_Q4_BYTES 4608
+
+/* sv_kv_append_paged into a 4-bit cache (D = 128): the same rows, rotated and
+ * rounded to bf16 as there, then quantised.  Positions beside the new ones keep
+ * their values. */
+SV_API sv_status sv_kv_append_q4(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
+                                 const int32_t* row_off, int32_t B, int32_t Hkv, const float* rope,
+                                 int32_t rope_positions, int32_t rot, void* k_pool, void* v_pool, int32_t num_pages,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* len, uint32_t flags,
+                                 void* stream);
+
+/* sv_kv_commit_paged into 4-bit pools [L][num_pages][Hkv][SV_KV_Q4_BYTES]
+ * (D = 128): the accepted block rows quantised into positions len[b] ..
+ * len[b] + n_acc[b], then len[b] += n_acc[b] + 1.  A sequence that would pass
+ * max_pages * 64, whose path is bad or whose rows reach a page outside the pool
+ * is left untouched, length included (SV_DEVERR_LENGTH, _PATH, _PAGE). */
+SV_API sv_status sv_kv_commit_q4(void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table,
+                                 int32_t max_pages, const uint16_t* k_blk, const uint16_t* v_blk, int32_t L,
+                                 int32_t B, int32_t Hkv, int32_t R, const int32_t* path, const int32_t* n_acc,
+                                 int32_t* len, void* stream);
+
+/* Reads a window of a 4-bit cache back as bf16 rows (for a prefill chunk's
+ * attention over the context before it, or to move a cache to bf16):
+ *     out[l][b][h][i] = the row at position start[b] + i,  0 <= i < n,
+ * and zeros where that position is at or past len[b].
+ *   k_out, v_out [L][B][Hkv][n][128] bf16, not overlapping the pools
+ * start[b] < 0 or len[b] outside [0, max_pages * 64] sets SV_DEVERR_LENGTH (the
+ * length is clamped; a negative start gives zeros); a page outside the pool
+ * reads as zeros and sets SV_DEVERR_PAGE.  n = 0 does nothing. */
+SV_API sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t num_pages,
+                                 const int32_t* page_table, int32_t max_pages, int32_t L, int32_t B, int32_t Hkv,
+                                 const int32_t* start, const int32_t* len, int32_t n, uint16_t* k_out,
+                                 uint16_t* v_out, void* stream);
+
+/* sv_verify_attn_paged over a 4-bit cache (k_pool, v_pool as above; the block's
+ * K and V stay bf16).  The cache's values enter the products exactly; otherwise
+ * numerics, masks, flags and errors are those of sv_verify_attn_paged.  The
+ * workspace (sv_verify_attn_q4_workspace bytes, any contents, possibly 0) may
+ * be shared by calls in stream order; calls running concurrently, and captured
+ * graphs that may, need their own. */
+SV_API size_t sv_verify_attn_q4_workspace(const sv_attn_shape* shape);
+SV_API sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool,
+                                   const void* v_pool, int32_t num_pages, const int32_t* page_table,
+                                   int32_t max_pages, const int32_t* len, const uint16_t* k_blk,
+                                   const uint16_t* v_blk, const int32_t* parent, float scale, uint16_t* out, void* ws,
+                                   size_t ws_bytes, uint32_t flags, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Diagnostics: the device building blocks of sv_accept_sample, exposed so    */

@@ -12,6 +12,7 @@
 
 #include <mutex>
 
+#include "kv_append.cuh"
 #include "sv.h"
 #include "sv_internal.h"
 
@@ -374,6 +375,198 @@ sv_status sv_kv_commit_paged(uint16_t* k_pool, uint16_t* v_pool, int32_t num_pag
     return launch_status(sv::launch_kv_commit(k_pool, v_pool, k_blk, v_blk, L, B, Hkv, D, max_pages * SV_KV_PAGE, R,
                                               path, n_acc, len, page_table, max_pages, num_pages,
                                               as_stream(stream)));
+}
+
+// Checks and fills what the two append calls share.
+static sv_status append_args(sv::AppendArgs& a, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                             int64_t v_stride, int32_t N, const int32_t* row_off, int32_t B, int32_t Hkv, int32_t D,
+                             const float* rope, int32_t rope_positions, int32_t rot, const void* k_pool,
+                             const void* v_pool, int32_t num_pages, const int32_t* page_table, int32_t max_pages,
+                             const int32_t* len, uint32_t flags) {
+    if (flags & ~SV_ROPE_INTERLEAVED) return SV_ERR_ARG;
+    if (!k || !v || !row_off || !k_pool || !v_pool || !page_table || !len) return SV_ERR_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool) || (rope && !aligned16(rope)))
+        return SV_ERR_ARG;
+    if (B < 1 || Hkv < 1 || Hkv > 65535 || D < 8 || D % 8 || D > 1024 || num_pages < 1 || max_pages < 1)
+        return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(max_pages) * SV_KV_PAGE > 2147483647) return SV_ERR_SHAPE;
+    const int64_t row = static_cast<int64_t>(Hkv) * D;
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return SV_ERR_SHAPE;
+    if (rope && (rot < 16 || rot % 16 || rot > D || rope_positions < 1)) return SV_ERR_SHAPE;
+    const int32_t cap = max_pages * SV_KV_PAGE;
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.N = N;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.row_off = row_off;
+    a.len = len;
+    a.rope = rope;
+    a.rot = rope ? rot : 0;
+    a.cap = rope && rope_positions < cap ? rope_positions : cap;
+    a.interleaved = (flags & SV_ROPE_INTERLEAVED) != 0;
+    a.pages = page_table;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.err = sv::device_error_word();
+    return SV_OK;
+}
+
+sv_status sv_kv_append_paged(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
+                             const int32_t* row_off, int32_t B, int32_t Hkv, int32_t D, const float* rope,
+                             int32_t rope_positions, int32_t rot, uint16_t* k_pool, uint16_t* v_pool,
+                             int32_t num_pages, const int32_t* page_table, int32_t max_pages, const int32_t* len,
+                             uint32_t flags, void* stream) {
+    if (N < 0) return SV_ERR_SHAPE;
+    if (N == 0) return SV_OK;
+    sv::AppendArgs a;
+    const sv_status s = append_args(a, k, v, k_stride, v_stride, N, row_off, B, Hkv, D, rope, rope_positions, rot,
+                                    k_pool, v_pool, num_pages, page_table, max_pages, len, flags);
+    if (s != SV_OK) return s;
+    return launch_status(sv::launch_kv_append(a, k_pool, v_pool, as_stream(stream)));
+}
+
+sv_status sv_kv_append_q4(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
+                          const int32_t* row_off, int32_t B, int32_t Hkv, const float* rope, int32_t rope_positions,
+                          int32_t rot, void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table,
+                          int32_t max_pages, const int32_t* len, uint32_t flags, void* stream) {
+    if (N < 0) return SV_ERR_SHAPE;
+    if (N == 0) return SV_OK;
+    sv::AppendArgs a;
+    const sv_status s = append_args(a, k, v, k_stride, v_stride, N, row_off, B, Hkv, 128, rope, rope_positions, rot,
+                                    k_pool, v_pool, num_pages, page_table, max_pages, len, flags);
+    if (s != SV_OK) return s;
+    if (sv::append_q4_items(N, B, Hkv) / 8 >= 2147483647) return SV_ERR_SHAPE;
+    return launch_status(sv::launch_append_q4(a, static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool),
+                                              as_stream(stream)));
+}
+
+sv_status sv_kv_commit_q4(void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table, int32_t max_pages,
+                          const uint16_t* k_blk, const uint16_t* v_blk, int32_t L, int32_t B, int32_t Hkv, int32_t R,
+                          const int32_t* path, const int32_t* n_acc, int32_t* len, void* stream) {
+    if (!k_pool || !v_pool || !page_table || !k_blk || !v_blk || !path || !n_acc || !len) return SV_ERR_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_blk) || !aligned16(v_blk)) return SV_ERR_ARG;
+    if (L < 1 || B < 1 || Hkv < 1 || R < 1 || R > 128 || num_pages < 1 || max_pages < 1) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(max_pages) * SV_KV_PAGE > 2147483647 || static_cast<int64_t>(B) * 8 > 2147483647 ||
+        static_cast<int64_t>(L) * Hkv > (1 << 24))
+        return SV_ERR_SHAPE;
+    return launch_status(sv::launch_commit_q4(static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), k_blk, v_blk,
+                                              L, B, Hkv, R, path, n_acc, len, page_table, max_pages, num_pages,
+                                              as_stream(stream)));
+}
+
+sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t num_pages, const int32_t* page_table,
+                          int32_t max_pages, int32_t L, int32_t B, int32_t Hkv, const int32_t* start,
+                          const int32_t* len, int32_t n, uint16_t* k_out, uint16_t* v_out, void* stream) {
+    if (n < 0) return SV_ERR_SHAPE;
+    if (n == 0) return SV_OK;
+    if (!k_pool || !v_pool || !page_table || !start || !len || !k_out || !v_out) return SV_ERR_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) || !aligned16(v_out)) return SV_ERR_ARG;
+    if (L < 1 || B < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1 || n > (1 << 30)) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(max_pages) * SV_KV_PAGE > 2147483647) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(L) * B > (1 << 30) || static_cast<int64_t>(L) * B * Hkv > (int64_t(1) << 31) ||
+        sv::gather_q4_items(L, B, Hkv, n) / 8 >= 2147483647)
+        return SV_ERR_SHAPE;
+    return launch_status(sv::launch_gather_q4(static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), L,
+                                              B, Hkv, start, len, n, page_table, max_pages, num_pages, k_out, v_out,
+                                              as_stream(stream)));
+}
+
+size_t sv_verify_attn_q4_workspace(const sv_attn_shape* shape) {
+    if (check_attn_shape(shape) != SV_OK) return 0;
+    return sv::attn_q4_workspace(*shape);
+}
+
+sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool, const void* v_pool,
+                            int32_t num_pages, const int32_t* page_table, int32_t max_pages, const int32_t* len,
+                            const uint16_t* k_blk, const uint16_t* v_blk, const int32_t* parent, float scale,
+                            uint16_t* out, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
+    if (flags & ~SV_ATTN_CACHE_READY) return SV_ERR_ARG;
+    const sv_status st = check_attn_shape(shape);
+    if (st != SV_OK) return st;
+    if (!q || !k_pool || !v_pool || !page_table || !len || !k_blk || !v_blk || !out) return SV_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_blk) || !aligned16(v_blk) ||
+        !aligned16(out) || (ws && !aligned16(ws)))
+        return SV_ERR_ARG;
+    if (num_pages < 1 || max_pages < 1) return SV_ERR_SHAPE;
+    if (static_cast<int64_t>(max_pages) * SV_KV_PAGE != shape->T_cap) return SV_ERR_SHAPE;
+    const size_t need = sv::attn_q4_workspace(*shape);
+    if (!ws && need > 0) return SV_ERR_ARG;
+    if (!(scale > 0.0f)) return SV_ERR_ARG;
+    if (ws_bytes < need) return SV_ERR_WORKSPACE;
+    sv::AttnQ4Args a;
+    a.q = q;
+    a.k_pool = static_cast<const uint8_t*>(k_pool);
+    a.v_pool = static_cast<const uint8_t*>(v_pool);
+    a.pages = page_table;
+    a.len = len;
+    a.k_blk = k_blk;
+    a.v_blk = v_blk;
+    a.parent = parent;
+    a.out = out;
+    a.err = sv::device_error_word();
+    a.B = shape->B;
+    a.R = shape->R;
+    a.Hq = shape->Hq;
+    a.Hkv = shape->Hkv;
+    a.G = shape->Hq / shape->Hkv;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.cache_ready = (flags & SV_ATTN_CACHE_READY) != 0;
+    return launch_status(sv::launch_verify_attn_q4(a, ws, as_stream(stream)));
+}
+
+sv_status sv_logits_process(const float* logits, int32_t B, int32_t R, int32_t V, const int32_t* hist,
+                            int32_t hist_cap, const int32_t* hist_len, const int32_t* prompt_len, const int32_t* tok,
+                            const int32_t* parent, const float* repetition, const float* frequency,
+                            const float* presence, const int32_t* bias_off, const int32_t* bias_tok,
+                            const float* bias_val, int32_t n_bias, const uint32_t* mask, float mask_value, float* out,
+                            uint64_t* argmax, size_t argmax_bytes, void* stream) {
+    if (!logits || (!out && !argmax)) return SV_ERR_ARG;
+    if (B < 1 || B > 65535 || R < 1 || R > 128 || V < 1 || V > (1 << 30)) return SV_ERR_SHAPE;
+    if (!aligned16(logits) || (out && !aligned16(out)) || (argmax && !aligned16(argmax))) return SV_ERR_ARG;
+    if (hist && (!hist_len || !aligned16(hist))) return SV_ERR_ARG;
+    // counts share a word with three flags
+    if (hist && (hist_cap < 1 || hist_cap > (1 << 28))) return SV_ERR_SHAPE;
+    if (parent && !tok) return SV_ERR_ARG;
+    if (bias_off && n_bias < 0) return SV_ERR_SHAPE;
+    if (bias_off && n_bias > 0 && (!bias_tok || !bias_val)) return SV_ERR_ARG;
+    if (mask_value != mask_value) return SV_ERR_ARG;
+    if (argmax && argmax_bytes / sizeof(uint64_t) / B / R < (static_cast<size_t>(V) + SV_ARGMAX_SLAB - 1) / SV_ARGMAX_SLAB)
+        return SV_ERR_WORKSPACE;
+    if (out && out != logits) {   // in place, or apart
+        const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(logits);
+        const uintptr_t n = static_cast<uintptr_t>(B) * R * V * sizeof(float);
+        if (o < i + n && i < o + n) return SV_ERR_ARG;
+    }
+    sv::LogitsArgs a;
+    a.logits = logits;
+    a.B = B;
+    a.R = R;
+    a.V = V;
+    a.hist = hist;
+    a.hist_cap = hist_cap;
+    a.hist_len = hist_len;
+    a.prompt_len = prompt_len;
+    a.tok = tok;
+    a.parent = parent;
+    a.rep = repetition;
+    a.freq = frequency;
+    a.pres = presence;
+    a.bias_off = bias_off;
+    a.bias_tok = bias_tok;
+    a.bias_val = bias_val;
+    a.n_bias = n_bias;
+    a.mask = mask;
+    a.mask_value = mask_value;
+    a.out = out;
+    a.argmax = argmax;
+    a.err = sv::device_error_word();
+    return launch_status(sv::launch_logits_process(a, as_stream(stream)));
 }
 
 // Device or page-locked host memory (the kernel reaches both through unified

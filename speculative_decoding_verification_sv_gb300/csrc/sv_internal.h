@@ -148,6 +148,55 @@ cudaError_t launch_verify_attn(const sv_attn_shape& s, const uint16_t* q, const 
                                void* ws, bool cache_ready, const int32_t* pages, int max_pages, int num_pages,
                                cudaStream_t st);
 
+// kv_append.cu, kv_q4.cu
+struct AppendArgs;   // kv_append.cuh
+cudaError_t launch_kv_append(const AppendArgs& a, uint16_t* k_pool, uint16_t* v_pool, cudaStream_t st);
+int64_t append_q4_items(int N, int B, int Hkv);   // warps of the launch
+cudaError_t launch_append_q4(const AppendArgs& a, uint8_t* k_pool, uint8_t* v_pool, cudaStream_t st);
+cudaError_t launch_commit_q4(uint8_t* k_pool, uint8_t* v_pool, const uint16_t* k_blk, const uint16_t* v_blk, int L,
+                             int B, int Hkv, int R, const int32_t* path, const int32_t* n_acc, int32_t* len,
+                             const int32_t* pages, int max_pages, int num_pages, cudaStream_t st);
+int64_t gather_q4_items(int L, int B, int Hkv, int n);   // warps of the launch
+cudaError_t launch_gather_q4(const uint8_t* k_pool, const uint8_t* v_pool, int L, int B, int Hkv, const int32_t* start,
+                             const int32_t* len, int n, const int32_t* pages, int max_pages, int num_pages,
+                             uint16_t* k_out, uint16_t* v_out, cudaStream_t st);
+
+// verify_attn_q4.cu
+struct AttnQ4Args {
+    const uint16_t* q;
+    const uint8_t *k_pool, *v_pool;
+    const int32_t* pages;    // [B][max_pages]
+    const int32_t* len;
+    const uint16_t *k_blk, *v_blk;
+    const int32_t* parent;
+    uint16_t* out;
+    unsigned int* err;
+    int B, R, Hq, Hkv, G, max_pages, num_pages;
+    float scale_log2;
+    bool cache_ready;
+};
+size_t attn_q4_workspace(const sv_attn_shape& s);
+cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st);
+
+// logits_process.cu
+struct LogitsArgs {
+    const float* logits;
+    int B, R, V;
+    const int32_t* hist;
+    int hist_cap;
+    const int32_t *hist_len, *prompt_len, *tok, *parent;
+    const float *rep, *freq, *pres;
+    const int32_t *bias_off, *bias_tok;
+    const float* bias_val;
+    int n_bias;
+    const uint32_t* mask;
+    float mask_value;
+    float* out;
+    uint64_t* argmax;
+    unsigned int* err;
+};
+cudaError_t launch_logits_process(const LogitsArgs& a, cudaStream_t st);
+
 // TMA descriptor encoding (driver entry point fetched through the runtime).
 bool encode_tmap_2d_bf16(void* tmap, const void* base, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
                          uint32_t box_inner, uint32_t box_outer);
