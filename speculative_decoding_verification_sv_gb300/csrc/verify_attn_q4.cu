@@ -2,9 +2,37 @@
 // cache (format: kv_q4.cuh) and the block's own bf16 K/V.
 //
 // out = softmax(scale q K^T) V over the cached positions and the block rows
-// that the row may see, as verify_attn.cu; the cache's bytes are 0.28 of the
-// bf16 cache's.  One CTA per (sequence, head, row): 128 keys at a time, a
-// thread a key for the scores and a dim for the values.
+// that the row may see.  The cache is 0.28 of the bf16 cache's bytes, so what
+// bounds verify_attn.cu (HBM) bounds this kernel less than the work on the SM:
+// unpacking the codes, the exponentials, and shared memory.
+//
+// Both products run transposed, S^T = K Q^T and O^T = V^T P^T, with the cache
+// as the A operand in tensor memory (tcgen05.mma, M = 128 keys or dims, N = 64
+// rows).  A thread then unpacks one key's K, or one dim's V, straight from the
+// packed bytes into its own TMEM lane: the 16-bit forms of K and V never pass
+// through shared memory (written there and read back by the MMA they would cost
+// 1024 of its cycles a step, against 656 for everything that is left), and the
+// MMAs fill all 128 rows of the tensor core where a block of 63 query rows
+// would fill half.
+//   S^T: lane = key, column = query row.  B = Q, K-major in shared memory.
+//   P:   exp2(s - m), bf16, written by the key's thread as one line of
+//        [keys][64 rows] in shared memory, the MN-major B of the second product.
+//   O^T: lane = dim, column = row.
+// A row's maximum runs across lanes here, so it is not formed every step: P is
+// taken against a reference m that some earlier key of the row gave, as long as
+// no score passes it by more than 2^kSlack (bf16 and fp32 have the same range:
+// nothing is lost); a vote over the step's warps finds the rare pass, and then,
+// as in a range's first step, the true maximum is formed and O, l are rescaled.
+//
+// Work.  A unit is one (sequence, KV head, tile of 64 query rows); its pages,
+// and the block as one more, are laid end to end over all units, and each CTA
+// (one an SM) takes an equal run of them, whatever the sequences' lengths.  A
+// unit that lies in several CTAs' runs leaves partial rows (m, l, O) in the
+// workspace -- at most two a CTA -- and a second small kernel joins them.
+//
+// Warps: 8 softmax (TMEM quadrant w % 4, row half w / 4), 4 unpack K, 4 unpack
+// V, one issues the copies (two pages of K and V, 18 KB, a ring stage: each
+// (page, head) is one 4608-byte bulk copy), one the MMAs.
 #include <math.h>
 
 #include "kv_q4.cuh"
@@ -13,123 +41,834 @@
 namespace sv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kRows = 64;                 // query rows of a tile
+constexpr int kStepKeys = 128;            // two pages
+constexpr int kStages = 6;
+constexpr int kStageBytes = 4 * kQ4Bytes; // K of two pages, V of two pages
+constexpr int kMaxR = 128;
+constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 32 * 18;
+constexpr int kGrain = 4;                 // pages a CTA takes at least (where there are as many)
+constexpr float kSlack = 40.0f;           // log2 of the largest P
+constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
+constexpr int kCombineThreads = 128;
 
-__global__ void __launch_bounds__(kThreads) attn_q4_kernel(AttnQ4Args a) {
-    __shared__ float q_s[kQ4D], p_s[kThreads], red_s[4];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int j = blockIdx.x % a.R, h = blockIdx.x / a.R, b = blockIdx.y, g = h / a.G;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int t = a.len[b];
-    const int cap = a.max_pages * kQ4Page;
-    if (t < 0 || t > cap) {
-        if (tid == 0) raise_error(a.err, SV_DEVERR_LENGTH);
-        t = t < 0 ? 0 : cap;
+// TMEM columns: two K operands, two V operands (64 columns: 128 bf16 each), two
+// S^T, one O^T
+constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 384, kTmemCols = 512;
+
+constexpr int kOffQ = 0;                                  // [2 halves of 64 dims][64 rows][128 B], swizzled
+constexpr int kOffP = kOffQ + kRows * kQ4D * 2;           // 2 x [128 keys][128 B], swizzled
+constexpr int kPBytes = kStepKeys * kRows * 2;
+constexpr int kOffRing = kOffP + 2 * kPBytes;
+constexpr int kOffBar = kOffRing + kStages * kStageBytes;
+constexpr int kOffNm = kOffBar + 256;                     // [64] -m, m the rows' references
+constexpr int kOffMove = kOffNm + kRows * 4;              // [64] m_old - m_new
+constexpr int kOffRed = kOffMove + kRows * 4;             // [4 quadrants][64]
+constexpr int kOffBad = kOffRed + 4 * kRows * 4;          // [kStages] pages of the stage outside the pool
+constexpr int kOffPar = kOffBad + 32;                     // [128] parents
+constexpr int kOffAnc = kOffPar + kMaxR * 4;              // [128][2] 64-bit path masks
+constexpr int kSmemBytes = kOffAnc + kMaxR * 16 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+static_assert(kStages * 4 <= 32, "bad-page words");
+
+struct Work {
+    int U;         // units of a sequence: Hkv * row tiles
+    int row_tiles;
+    int tile_rows; // rows of a tile but the last
+};
+
+// Pages of sequence b (its length clamped into the table), the block not counted.
+__device__ __forceinline__ int ctx_len(const AttnQ4Args& a, int b) {
+    const int t = a.len[b];
+    return t < 0 ? 0 : min(t, a.max_pages * kQ4Page);
+}
+__device__ __forceinline__ int ctx_pages(int t) { return (t + kQ4Page - 1) / kQ4Page; }
+
+// Work of all sequences (sum of pages + 1), and of those before sequence
+// `before`; one warp, every lane gets both.
+__device__ __forceinline__ int2 work_sums(const AttnQ4Args& a, int before) {
+    int all = 0, head = 0;
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) {
+        const int w = ctx_pages(ctx_len(a, b)) + 1;
+        all += w;
+        if (b < before) head += w;
     }
-    const size_t qo = ((static_cast<size_t>(b) * a.R + j) * a.Hq + h) * kQ4D + tid;
-    q_s[tid] = bf16_bits_f32(a.q[qo]);
-    // the row's path: bit i of anc set iff block row i is visible
-    uint64_t anc[2] = {0ull, 0ull};
-    if (a.parent) {
-        const int32_t* par = a.parent + static_cast<size_t>(b) * a.R;
-        int i = j;
-        bool bad = false;
-        for (int steps = 0; steps <= a.R && i >= 0; ++steps) {
-            anc[i >> 6] |= 1ull << (i & 63);
-            const int p = par[i];
-            if ((i == 0 && p != -1) || (i > 0 && (p < 0 || p >= i))) {
-                bad = true;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, off);
+        head += __shfl_xor_sync(0xffffffffu, head, off);
+    }
+    return make_int2(all, head);
+}
+
+// CTAs that share W pages, and the first page of CTA i among them.
+__device__ __forceinline__ int active_ctas(int W, int grid) { return max(1, min(grid, W / kGrain)); }
+__device__ __forceinline__ int cta_first(int W, int i, int n) {
+    return static_cast<int>(static_cast<int64_t>(W) * i / n);
+}
+// the CTA whose run holds page x
+__device__ __forceinline__ int cta_of(int W, int x, int n) {
+    int i = static_cast<int>((static_cast<int64_t>(x) * n) / W);
+    while (cta_first(W, i + 1, n) <= x) ++i;
+    while (cta_first(W, i, n) > x) --i;
+    return i;
+}
+
+// The runs of this CTA, unit by unit; every warp walks them by itself.
+struct Walk {
+    int pos, end;          // what is left of the CTA's run
+    int b, unit, off;      // where pos lies: sequence, unit of it, page of the unit
+    int t, np;             // length and pages of sequence b
+    // the current run
+    int p0, p1;            // its pages
+    bool block, whole;     // the block is in it; it is all of the unit
+
+    __device__ __forceinline__ void start(const AttnQ4Args& a, const Work& w, int cta, int grid) {
+        const int W = work_sums(a, 0).x * w.U;
+        const int n = active_ctas(W, grid);
+        pos = end = 0;
+        b = -1;
+        if (cta >= n) return;
+        pos = cta_first(W, cta, n);
+        end = cta_first(W, cta + 1, n);
+        // the sequence that pos lies in
+        int base = 0;
+        const int lane = threadIdx.x & 31;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int wt = b0 + lane < a.B ? (ctx_pages(ctx_len(a, b0 + lane)) + 1) * w.U : 0;
+            int sum = wt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += x;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, base + sum > pos);
+            if (m != 0u) {
+                const int k = __ffs(m) - 1;
+                b = b0 + k;
+                base += __shfl_sync(0xffffffffu, sum - wt, k);
                 break;
             }
-            i = p;
+            base += __shfl_sync(0xffffffffu, sum, 31);
         }
-        if (bad) {
-            if (tid == 0) raise_error(a.err, SV_DEVERR_TREE);
-            anc[0] = j < 64 ? 1ull << j : 0ull;
-            anc[1] = j >= 64 ? 1ull << (j - 64) : 0ull;
-        }
+        t = ctx_len(a, b);
+        np = ctx_pages(t);
+        unit = (pos - base) / (np + 1);
+        off = (pos - base) % (np + 1);
     }
-    __syncthreads();
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    const size_t blk_row = (static_cast<size_t>(b) * a.Hkv + g) * a.R;
-    for (int k0 = 0; k0 < t + a.R; k0 += kThreads) {
-        const int key = k0 + tid;
-        const int bi = key - t;   // block row, if >= 0
-        float s = -INFINITY;
-        auto block_of = [&](int p) -> const uint8_t* {
-            const int pg = a.pages[static_cast<size_t>(b) * a.max_pages + p / kQ4Page];
-            if (pg < 0 || pg >= a.num_pages) {
-                raise_error(a.err, SV_DEVERR_PAGE);
-                return nullptr;
+    __device__ __forceinline__ bool next(const AttnQ4Args& a, const Work& w) {
+        if (pos >= end) return false;
+        const int n = min(end - pos, np + 1 - off);
+        p0 = off;
+        p1 = min(off + n, np);
+        block = off + n == np + 1;
+        whole = n == np + 1;
+        pos += n;
+        cur_b = b;
+        cur_unit = unit;
+        cur_t = t;
+        off = 0;
+        if (block && ++unit == w.U) {
+            unit = 0;
+            if (++b < a.B) {
+                t = ctx_len(a, b);
+                np = ctx_pages(t);
             }
-            return reinterpret_cast<const uint8_t*>((static_cast<size_t>(pg) * a.Hkv + g) * kQ4Bytes);
+        }
+        return true;
+    }
+    int cur_b, cur_unit, cur_t;
+    __device__ __forceinline__ int ctx_steps() const { return (p1 - p0 + 1) / 2; }
+};
+
+// --- packed arithmetic ---------------------------------------------------------
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// bf16 pair 128 + c of elements 2k, 2k + 1 of a word
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int k) { return (w >> (4 * k) & 0x000F000Fu) | 0x43004300u; }
+constexpr uint32_t kM136 = 0xC308C308u;   // bf16 pair of -136
+
+// OR of a predicate over the softmax warps, and their barrier
+__device__ __forceinline__ bool soft_any(bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(p))
+        : "memory");
+    return r != 0u;
+}
+__device__ __forceinline__ void soft_sync() { named_barrier(1, 32 * kSoftWarps); }
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// kRT: rows a softmax thread takes; 2 kRT rows of the tile are live (the
+// others' columns of Q and P are zero)
+template <int kRT>
+__global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work wk, float* __restrict__ ws) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    uint64_t* ring_full = bars;                   // [kStages]
+    uint64_t* ring_empty = ring_full + kStages;   // [kStages]
+    uint64_t* k_full = ring_empty + kStages;      // [2] K operand unpacked
+    uint64_t* v_full = k_full + 2;                // [2]
+    uint64_t* s_full = v_full + 2;                // [2] S^T formed (and the K operand read)
+    uint64_t* s_empty = s_full + 2;               // [2] scores read
+    uint64_t* p_full = s_empty + 2;               // [2] P written (and O rescaled)
+    uint64_t* pv_done = p_full + 2;               // [2] O^T has the step (P and the V operand read)
+    uint64_t* q_ready = pv_done + 2;
+    uint64_t* o_free = q_ready + 1;               // O^T read by the epilogue
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(o_free + 1);
+    static_assert((2 * kStages + 14) * 8 + 4 <= 256, "barrier area");
+    float* nm_s = reinterpret_cast<float*>(smem + kOffNm);
+    float* move_s = reinterpret_cast<float*>(smem + kOffMove);
+    float* red_s = reinterpret_cast<float*>(smem + kOffRed);
+    volatile uint32_t* bad_s = reinterpret_cast<volatile uint32_t*>(smem + kOffBad);
+    int32_t* par_s = reinterpret_cast<int32_t*>(smem + kOffPar);
+    uint64_t* anc_s = reinterpret_cast<uint64_t*>(smem + kOffAnc);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&ring_full[i], 1);
+            mbar_init(&ring_empty[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 4);
+            mbar_init(&v_full[i], 4);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], kSoftWarps);
+            mbar_init(&p_full[i], kSoftWarps);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(q_ready, kSoftWarps);
+        mbar_init(o_free, kSoftWarps);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_s, kTmemCols);
+    if (2 * kRT < kRows) {   // the columns of P past the live rows stay zero
+        for (int x = threadIdx.x; x < 2 * kPBytes / 16; x += kThreads)
+            reinterpret_cast<uint4*>(smem + kOffP)[x] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    const int q4 = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    auto tK = [tmem](int i) { return tmem + kColK + static_cast<uint32_t>(i) * 64u; };
+    auto tV = [tmem](int i) { return tmem + kColV + static_cast<uint32_t>(i) * 64u; };
+    auto tS = [tmem](int i) { return tmem + kColS + static_cast<uint32_t>(i) * 64u; };
+    const uint32_t tO = tmem + kColO;
+
+    // With cache_ready the lengths, the page table and the committed pages were
+    // final before the preceding kernel ran: the walk and the page copies start
+    // under it, and whoever touches anything else waits first.
+    const bool early = a.cache_ready;
+    if (!early) pdl_wait();
+    Walk walk;
+    walk.start(a, wk, blockIdx.x, gridDim.x);
+
+    if (warp == kTmaWarp) {
+        // ---------------- page copies ----------------
+        int c = 0;   // context steps so far
+        while (walk.next(a, wk)) {
+            const int g = walk.cur_unit / wk.row_tiles;
+            const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
+            const int np = walk.p1 - walk.p0;
+            for (int i0 = 0; i0 < np; i0 += 32) {
+                // 32 table entries at once: lane l holds page p0 + i0 + l
+                int pg = i0 + lane < np ? __ldg(tab + walk.p0 + i0 + lane) : 0;
+                const bool bad = pg < 0 || pg >= a.num_pages;
+                if (bad) {
+                    raise_error(a.err, SV_DEVERR_PAGE);
+                    pg = -1;
+                }
+                for (int i = 0; i < 32 && i0 + i < np; i += 2, ++c) {
+                    const int pa = __shfl_sync(0xffffffffu, pg, i), pb = __shfl_sync(0xffffffffu, pg, i + 1);
+                    const bool two = i0 + i + 1 < np;
+                    if (lane == 0) {
+                        const int s = c % kStages;
+                        mbar_wait(&ring_empty[s], ((c / kStages) & 1) ^ 1, a.err);
+                        uint8_t* st = smem + kOffRing + s * kStageBytes;
+                        const bool la = pa >= 0, lb = two && pb >= 0;
+                        bad_s[s] = (la ? 0u : 1u) | (two && pb < 0 ? 2u : 0u);
+                        mbar_arrive_expect_tx(&ring_full[s], (la ? 2 * kQ4Bytes : 0) + (lb ? 2 * kQ4Bytes : 0));
+                        const size_t oa = (static_cast<size_t>(pa) * a.Hkv + g) * kQ4Bytes;
+                        const size_t ob = (static_cast<size_t>(pb) * a.Hkv + g) * kQ4Bytes;
+                        if (la) bulk_g2s(st, a.k_pool + oa, kQ4Bytes, &ring_full[s]);
+                        if (lb) bulk_g2s(st + kQ4Bytes, a.k_pool + ob, kQ4Bytes, &ring_full[s]);
+                        if (la) bulk_g2s(st + 2 * kQ4Bytes, a.v_pool + oa, kQ4Bytes, &ring_full[s]);
+                        if (lb) bulk_g2s(st + 3 * kQ4Bytes, a.v_pool + ob, kQ4Bytes, &ring_full[s]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------- MMA issuer ----------------
+        constexpr uint32_t id_s = idesc_bf16_f32(128, 2 * kRT, false, false);
+        constexpr uint32_t id_o = idesc_bf16_f32(128, kRows, false, true);
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
+        int it = 0, seg = 0;
+        auto pv = [&](int i, bool first) {
+            const int x = i & 1;
+            if (first) mbar_wait(o_free, (seg & 1) ^ 1, a.err);
+            mbar_wait(&v_full[x], (i >> 1) & 1, a.err);
+            mbar_wait(&p_full[x], (i >> 1) & 1, a.err);
+            tc_fence_after();
+            const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + x * kPBytes), 16, 1024);
+#pragma unroll
+            for (int kc = 0; kc < kStepKeys / 16; ++kc)
+                tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || !first) ? 1u : 0u);
+            tc_commit(&pv_done[x]);
         };
-        if (bi < 0) {
-            const uint8_t* off = block_of(key);
-            s = 0.f;
-            const bool there = a.pages[static_cast<size_t>(b) * a.max_pages + key / kQ4Page] >= 0 &&
-                               a.pages[static_cast<size_t>(b) * a.max_pages + key / kQ4Page] < a.num_pages;
-            if (there) {
-                const uint8_t* blk = a.k_pool + reinterpret_cast<size_t>(off);
-                for (int gr = 0; gr < 4; ++gr) {
-                    const float sc = bf16_bits_f32(
-                        *reinterpret_cast<const uint16_t*>(blk + q4_k_scale_off(gr, key & 63)));
-                    const uint32_t* w = reinterpret_cast<const uint32_t*>(blk + q4_k_code_off(gr, key & 63));
-                    for (int d = 0; d < 32; ++d) {
-                        const int c = static_cast<int>(w[d >> 3] >> q4_shift(d & 7) & 15u) - 8;
-                        s = fmaf(q_s[gr * 32 + d], c * sc, s);
+        while (walk.next(a, wk)) {
+            const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
+            if (lane == 0) {
+                mbar_wait(q_ready, seg & 1, a.err);
+                for (int st = 0; st < n; ++st) {
+                    const int i = it + st, x = i & 1;
+                    mbar_wait(&k_full[x], (i >> 1) & 1, a.err);
+                    mbar_wait(&s_empty[x], ((i >> 1) & 1) ^ 1, a.err);
+                    tc_fence_after();
+#pragma unroll
+                    for (int kc = 0; kc < kQ4D / 16; ++kc)
+                        tc_mma_ts(tS(x), tK(x) + kc * 8, qd + (((kc >> 2) * kRows * 128 + (kc & 3) * 32) >> 4), id_s,
+                                  kc > 0 ? 1u : 0u);
+                    tc_commit(&s_full[x]);
+                    if (st > 0) pv(i - 1, st == 1);
+                }
+                pv(it + n - 1, n == 1);
+            }
+            __syncwarp();
+            it += n;
+            ++seg;
+        }
+    } else if (warp >= kKWarp) {
+        // ---------------- unpacking: a key's K (warps 8-11), a dim's V (12-15) ----------------
+        const bool is_v = warp >= kVWarp;
+        const int l = q4 * 32 + lane;   // TMEM lane: key of the step, or dim
+        uint64_t* full = is_v ? v_full : k_full;
+        uint64_t* freed = is_v ? pv_done : s_full;
+        int it = 0, c = 0;
+        bool waited = !early;
+        auto put = [&](int col, const uint32_t(&w)[16]) {
+            tmem_st16((is_v ? tV(it & 1) : tK(it & 1)) + lane_off + col, w);
+        };
+        auto done = [&]() {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[it & 1]);
+        };
+        while (walk.next(a, wk)) {
+            for (int st = 0; st < walk.ctx_steps(); ++st, ++it, ++c) {
+                const int s = c % kStages;
+                const uint8_t* stage = smem + kOffRing + s * kStageBytes;
+                mbar_wait(&ring_full[s], (c / kStages) & 1, a.err);
+                const uint32_t bad = bad_s[s];
+                mbar_wait(&freed[it & 1], ((it >> 1) & 1) ^ 1, a.err);
+                tc_fence_after();
+                if (!is_v) {
+                    const uint8_t* blk = stage + (l >> 6) * kQ4Bytes;
+                    const int pos = l & 63;
+                    const uint2 sc = *reinterpret_cast<const uint2*>(blk + q4_k_scale_off(0, pos));
+                    const bool zero = (bad >> (l >> 6) & 1u) != 0u;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint4 cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(g, pos));
+                        const uint32_t sw = g < 2 ? sc.x : sc.y;
+                        uint32_t s2 = __byte_perm(sw, 0u, (g & 1) ? 0x3232 : 0x1010);
+                        if (zero) s2 = 0u;
+                        const uint32_t o2 = bmul2(s2, kM136);
+                        const uint32_t ww[4] = {cw.x, cw.y, cw.z, cw.w};
+                        uint32_t r[16];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) r[4 * w + k] = bfma2(code_pair(ww[w], k), s2, o2);
+                        put(16 * g, r);
+                    }
+                } else {
+                    // keys of the step that exist: the others, and pages outside
+                    // the pool, are zeros (0 * a non-finite V would be NaN)
+                    const int live = min(kStepKeys, walk.cur_t - (walk.p0 + 2 * st) * kQ4Page);
+                    const int have = min(live, (walk.p1 - walk.p0 - 2 * st) * kQ4Page);
+                    const bool part = have < kStepKeys || bad != 0u;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {   // 32 keys
+                        const uint8_t* blk = stage + (2 + (h >> 1)) * kQ4Bytes;
+                        uint32_t r[16];
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            const int oct = (h & 1) * 4 + o;
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off(oct, l));
+                            const uint4 sc = *reinterpret_cast<const uint4*>(blk + q4_v_scale_off(q4, 8 * oct));
+                            const uint32_t ss[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                r[4 * o + k] = bfma2(code_pair(w, k), ss[k], bmul2(ss[k], kM136));
+                        }
+                        if (part) {
+                            const bool zero = (bad >> (h >> 1) & 1u) != 0u;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int key = 32 * h + 2 * k;
+                                if (zero || key >= have) r[k] = 0u;
+                                else if (key + 1 >= have) r[k] &= 0xFFFFu;
+                            }
+                        }
+                        put(16 * h, r);
+                    }
+                }
+                done();
+                if (lane == 0) mbar_arrive(&ring_empty[s]);
+            }
+            if (walk.block) {
+                if (!waited) pdl_wait();
+                waited = true;
+                mbar_wait(&freed[it & 1], ((it >> 1) & 1) ^ 1, a.err);
+                tc_fence_after();
+                const int g = walk.cur_unit / wk.row_tiles;
+                const size_t row0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R;
+                if (!is_v) {
+                    const uint4* src = reinterpret_cast<const uint4*>(a.k_blk + (row0 + l) * kQ4D);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t r[16];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (l < a.R) v = __ldg(src + 4 * x + y);
+                            r[4 * y] = v.x, r[4 * y + 1] = v.y, r[4 * y + 2] = v.z, r[4 * y + 3] = v.w;
+                        }
+                        put(16 * x, r);
+                    }
+                } else {
+                    const uint16_t* src = a.v_blk + row0 * kQ4D + l;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t r[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int key = 32 * h + 2 * k;
+                            const uint32_t lo = key < a.R ? __ldg(src + key * kQ4D) : 0u;
+                            const uint32_t hi = key + 1 < a.R ? __ldg(src + (key + 1) * kQ4D) : 0u;
+                            r[k] = lo | hi << 16;
+                        }
+                        put(16 * h, r);
+                    }
+                }
+                done();
+                ++it;
+            }
+        }
+        if (!waited) pdl_wait();
+    } else {
+        // ---------------- softmax, epilogue ----------------
+        if (early) pdl_wait();
+        const int hh = warp >> 2;              // rows hh * kRT .. of the tile
+        const int l = q4 * 32 + lane;          // key of the step; dim in the epilogue
+        const int tid = threadIdx.x;
+        const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2);
+        const int rows = a.R * a.G;
+        int it = 0, seg = 0, part = 0;
+        while (walk.next(a, wk)) {
+            const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
+            const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
+            if (tid == 0) {
+                const int t = a.len[b];
+                if (t < 0 || t > a.max_pages * kQ4Page) raise_error(a.err, SV_DEVERR_LENGTH);
+            }
+            // Q rows (zeros past the last), K-major, 128-byte swizzle; the S MMAs
+            // of the run before have read theirs (its last scores were waited for)
+            for (int x = tid; x < 2 * kRT * 16; x += 32 * kSoftWarps) {
+                const int r = x >> 4, ch = x & 15;
+                uint8_t* dst = smem + kOffQ + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                if (r < nrows) {
+                    const int gr = row0 + r;
+                    const uint16_t* src =
+                        a.q + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D;
+                    cp_async16(dst, reinterpret_cast<const uint4*>(src) + ch);
+                } else {
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            if (tid < kRows) nm_s[tid] = 0.f;
+            const bool tree = walk.block && a.parent != nullptr;
+            if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);
+            soft_sync();   // nm_s, par_s
+            if (tree) {
+                if (tid < a.R) {
+                    uint64_t m0 = 0, m1 = 0;
+                    int i = tid;
+                    bool bad = false;
+                    for (int n = 0; n <= a.R && i >= 0; ++n) {
+                        if (i < 64) m0 |= 1ull << i;
+                        else m1 |= 1ull << (i - 64);
+                        const int p = par_s[i];
+                        if ((i == 0 && p != -1) || (i > 0 && (p < 0 || p >= i))) {
+                            bad = true;
+                            break;
+                        }
+                        i = p;
+                    }
+                    if (bad) {
+                        raise_error(a.err, SV_DEVERR_TREE);
+                        m0 = tid < 64 ? 1ull << tid : 0ull;
+                        m1 = tid >= 64 ? 1ull << (tid - 64) : 0ull;
+                    }
+                    anc_s[2 * tid] = m0;
+                    anc_s[2 * tid + 1] = m1;
+                }
+                soft_sync();
+            }
+            uint64_t sum2[kRT / 2];
+#pragma unroll
+            for (int i = 0; i < kRT / 2; ++i) sum2[i] = 0ull;
+            const int nctx = walk.ctx_steps(), n = nctx + (walk.block ? 1 : 0);
+            for (int st = 0; st < n; ++st, ++it) {
+                const int x = it & 1;
+                mbar_wait(&s_full[x], (it >> 1) & 1, a.err);
+                tc_fence_after();
+                // visible keys: of the context, those before the length (the second
+                // page of a step may be missing); block row l is seen from query rows
+                // l G on, or where it lies on a tree row's path
+                const bool blk = st >= nctx;
+                const bool live =
+                    blk ? l < a.R : (walk.p0 + 2 * st) * kQ4Page + l < min(walk.cur_t, walk.p1 * kQ4Page);
+                const int lo = !live ? kRows : blk && !tree ? l * a.G - row0 - hh * kRT : 0;
+                // exponents against the rows' references, 16 rows at a time; the scores
+                // are not kept
+                uint64_t e2[kRT / 2];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c0 = 0; c0 < kRT; c0 += 16) {
+                    uint32_t s[16];
+                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
+                    if (lo > c0) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c0 + e < lo) s[e] = 0xff800000u;
+                    }
+                    if (blk && tree && live) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int gr = row0 + min(hh * kRT + c0 + e, nrows - 1);
+                            if ((anc_s[2 * (gr / a.G) + (l >> 6)] >> (l & 63) & 1ull) == 0ull) s[e] = 0xff800000u;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT + c0)[i];
+                        uint64_t* e = e2 + c0 / 2 + 2 * i;
+                        e[0] = fma2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), sc2, pack2(nm.x, nm.y));
+                        e[1] = fma2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2,
+                                    pack2(nm.z, nm.w));
+                        float p, q;
+                        unpack2(e[0], p, q);
+                        mx = fmax3(mx, p, q);
+                        unpack2(e[1], p, q);
+                        mx = fmax3(mx, p, q);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[x]);
+                // a run's first step has no reference yet (it is 0: the exponents are
+                // the scaled scores); later a score may pass the reference too far
+                if (soft_any(st == 0 || mx > kSlack)) {
+#pragma unroll
+                    for (int i = 0; i < kRT / 2; ++i) {
+                        float p, q;
+                        unpack2(e2[i], p, q);
+                        p = warp_max(p);
+                        q = warp_max(q);
+                        if (lane == 0)
+                            *reinterpret_cast<float2*>(red_s + q4 * kRows + hh * kRT + 2 * i) = make_float2(p, q);
+                    }
+                    soft_sync();
+                    if (tid < 2 * kRT) {
+                        // the reference moves to the step's maximum: up, or in the first
+                        // step to wherever it is (not to -inf: all scores of the row are)
+                        float d = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
+                                        fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
+                        if (d == -INFINITY || (st > 0 && d < 0.f)) d = 0.f;
+                        nm_s[tid] -= d;
+                        move_s[tid] = -d;
+                    }
+                    soft_sync();
+#pragma unroll
+                    for (int i = 0; i < kRT / 2; ++i) {
+                        const float2 d = *reinterpret_cast<const float2*>(move_s + hh * kRT + 2 * i);
+                        e2[i] = add2(e2[i], pack2(d.x, d.y));
+                    }
+                    if (st > 0) {
+#pragma unroll
+                        for (int i = 0; i < kRT / 2; ++i) {
+                            const float2 d = *reinterpret_cast<const float2*>(move_s + hh * kRT + 2 * i);
+                            float p, q;
+                            unpack2(sum2[i], p, q);
+                            sum2[i] = pack2(p * fast_exp2(d.x), q * fast_exp2(d.y));
+                        }
+                        // O^T (lane = dim) once the step before is in it
+                        mbar_wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1, a.err);
+                        tc_fence_after();
+#pragma unroll
+                        for (int c0 = 0; c0 < kRT; c0 += 16) {
+                            const uint32_t ta = tO + lane_off + hh * kRT + c0;
+                            uint32_t o[16];
+                            tmem_ld16_sync(ta, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * fast_exp2(move_s[hh * kRT + c0 + e]));
+                            tmem_st16(ta, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // P buffer x is free once the step before last is in O
+                if (it >= 2) mbar_wait(&pv_done[x], ((it - 2) >> 1) & 1, a.err);
+                uint8_t* prow = smem + kOffP + x * kPBytes + l * 128;
+#pragma unroll
+                for (int ch = 0; ch < kRT / 8; ++ch) {   // eight rows: 16 bytes of the key's line
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float p, q;
+                        unpack2(e2[4 * ch + i], p, q);
+                        p = fast_exp2(p);
+                        q = fast_exp2(q);
+                        sum2[4 * ch + i] = add2(sum2[4 * ch + i], pack2(p, q));
+                        w[i] = pack_bf16x2(p, q);
+                    }
+                    *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + ch) ^ (l & 7)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            // the rows' sums over the keys: lane e of a warp ends with its row e's
+            // (halving the rows and the lanes that differ, step by step)
+            float sums[kRT];
+#pragma unroll
+            for (int i = 0; i < kRT / 2; ++i) unpack2(sum2[i], sums[2 * i], sums[2 * i + 1]);
+#pragma unroll
+            for (int cnt = kRT; cnt > 1; cnt >>= 1) {
+                const bool upper = (lane & (cnt >> 1)) != 0;
+#pragma unroll
+                for (int i = 0; i < kRT / 2; ++i) {
+                    if (i >= cnt / 2) break;
+                    const float give = upper ? sums[i] : sums[i + cnt / 2];
+                    const float keep = upper ? sums[i + cnt / 2] : sums[i];
+                    sums[i] = keep + __shfl_xor_sync(0xffffffffu, give, cnt >> 1);
+                }
+            }
+            if (kRT == 16) sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
+            if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sums[0];
+            mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, a.err);
+            tc_fence_after();
+            soft_sync();
+            float* rec = nullptr;
+            if (!walk.whole) rec = ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
+#pragma unroll
+            for (int c0 = 0; c0 < kRT; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16_sync(tO + lane_off + hh * kRT + c0, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int r = hh * kRT + c0 + e;
+                    if (r >= nrows) continue;
+                    const float lsum = (red_s[r] + red_s[kRows + r]) + (red_s[2 * kRows + r] + red_s[3 * kRows + r]);
+                    const float ov = __uint_as_float(o[e]);
+                    if (rec) {
+                        rec[r * kQ4D + l] = ov;
+                        if (l == 0)
+                            *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * r) = make_float2(-nm_s[r], lsum);
+                    } else {
+                        const int gr = row0 + r;
+                        a.out[((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D + l] =
+                            f32_bf16_bits(lsum != 0.f ? ov / lsum : 0.f);
                     }
                 }
             }
-        } else if (bi < a.R && (a.parent ? (anc[bi >> 6] >> (bi & 63) & 1ull) != 0ull : bi <= j)) {
-            s = 0.f;
-            for (int d = 0; d < kQ4D; ++d) s = fmaf(q_s[d], bf16_bits_f32(a.k_blk[(blk_row + bi) * kQ4D + d]), s);
+            part = 1;   // a partial run that is not the CTA's first is its last
+            tc_fence_before();
+            soft_sync();   // red_s and nm_s read by everyone before the next run writes them
+            if (lane == 0) mbar_arrive(o_free);
+            ++seg;
         }
-        s *= a.scale_log2;
-        float mt = s;
-        for (int off = 16; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-        if (lane == 0) red_s[warp] = mt;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red_s[0], red_s[1]), fmaxf(red_s[2], red_s[3])));
-        const float p = s == -INFINITY ? 0.f : exp2f(s - mn);
-        p_s[tid] = p;
-        const float c = m == -INFINITY ? 0.f : exp2f(m - mn);
-        __syncthreads();
-        float ps = 0.f;
-        o *= c;
-        for (int i = 0; i < kThreads; ++i) {
-            const float pi = p_s[i];
-            ps += pi;
-            if (pi == 0.f) continue;
-            const int ki = k0 + i;
-            float v = 0.f;
-            if (ki < t) {
-                const int pg = a.pages[static_cast<size_t>(b) * a.max_pages + ki / kQ4Page];
-                if (pg >= 0 && pg < a.num_pages) {
-                    const uint8_t* blk = a.v_pool + (static_cast<size_t>(pg) * a.Hkv + g) * kQ4Bytes;
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off((ki & 63) >> 3, tid));
-                    v = (static_cast<int>(w >> q4_shift(ki & 7) & 15u) - 8) *
-                        bf16_bits_f32(*reinterpret_cast<const uint16_t*>(blk + q4_v_scale_off(tid >> 5, ki & 63)));
-                }
-            } else {
-                v = bf16_bits_f32(a.v_blk[(blk_row + ki - t) * kQ4D + tid]);
-            }
-            o = fmaf(pi, v, o);
-        }
-        l = l * c + ps;
-        m = mn;
-        __syncthreads();
     }
-    a.out[qo] = f32_bf16_bits(l > 0.f ? o / l : 0.f);
+    __syncwarp();
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the partial rows of the units that lie in several CTAs' runs: one CTA a
+// row, its warps taking every fourth partial, eight in flight.
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_q4_kernel(AttnQ4Args a, Work wk, const float* __restrict__ ws, int grid) {
+    __shared__ float4 o_s[4][32];
+    __shared__ float2 ml_s[4];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv, gr = blockIdx.x;
+    const int rt = gr / wk.tile_rows, r = gr % wk.tile_rows;
+    const int2 sums = work_sums(a, b);
+    const int W = sums.x * wk.U, n = active_ctas(W, grid);
+    const int np = ctx_pages(ctx_len(a, b));
+    const int w0 = sums.y * wk.U + (g * wk.row_tiles + rt) * (np + 1), w1 = w0 + np + 1;
+    const int i0 = cta_of(W, w0, n), i1 = cta_of(W, w1 - 1, n);
+    if (i0 == i1) return;   // one CTA had the whole unit and wrote its rows
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = i0 + warp; c0 <= i1; c0 += 32) {
+        float2 ml[8];
+        float4 o[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = c0 + 4 * u;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i > i1) continue;
+            // a unit that starts inside CTA i0's run is its second partial
+            const int slot = i == i0 && w0 > cta_first(W, i0, n) ? 1 : 0;
+            const float* rec = ws + (static_cast<size_t>(i) * 2 + slot) * kRecFloats;
+            ml[u] = __ldcg(reinterpret_cast<const float2*>(rec + kRows * kQ4D + 2 * r));
+            o[u] = __ldcg(reinterpret_cast<const float4*>(rec + r * kQ4D) + lane);
+        }
+        float mn = M;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
+        const float c = M == -INFINITY ? 0.f : exp2f(M - mn);
+        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c, L *= c;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (ml[u].y == 0.f) continue;   // no key of the run was visible
+            const float w = exp2f(ml[u].x - mn);
+            L += w * ml[u].y;
+            acc.x += w * o[u].x;
+            acc.y += w * o[u].y;
+            acc.z += w * o[u].z;
+            acc.w += w * o[u].w;
+        }
+        M = mn;
+    }
+    o_s[warp][lane] = acc;
+    if (lane == 0) ml_s[warp] = make_float2(M, L);
+    __syncthreads();
+    if (warp != 0) return;
+    float mn = fmaxf(fmaxf(ml_s[0].x, ml_s[1].x), fmaxf(ml_s[2].x, ml_s[3].x));
+    L = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        if (ml_s[u].y == 0.f) continue;
+        const float w = exp2f(ml_s[u].x - mn);
+        const float4 o = o_s[u][lane];
+        L += w * ml_s[u].y;
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+    }
+    const float inv = L != 0.f ? 1.0f / L : 0.f;
+    uint16_t* dst = a.out + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D + 4 * lane;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+Work work_of(int R, int G, int Hkv) {
+    Work w;
+    const int rows = R * G;
+    w.row_tiles = (rows + kRows - 1) / kRows;
+    w.tile_rows = (rows + w.row_tiles - 1) / w.row_tiles;
+    w.U = Hkv * w.row_tiles;
+    return w;
+}
+
+int grid_of(const Work& w, int B, int max_pages) {
+    const int64_t most = static_cast<int64_t>(B) * w.U * (static_cast<int64_t>(max_pages) + 1) / kGrain;
+    const int sms = device_sm_count();
+    return static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
+}
+
+template <int kRT>
+cudaError_t launch_rt(const AttnQ4Args& a, const Work& w, int grid, float* ws, cudaStream_t st) {
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run([]() {
+        return cudaFuncSetAttribute(attn_q4_kernel<kRT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_q4_kernel<kRT>, dim3(grid), dim3(kThreads), kSmemBytes, st, a, w, ws);
 }
 
 }  // namespace
 
-size_t attn_q4_workspace(const sv_attn_shape&) { return 0; }
+size_t attn_q4_workspace(const sv_attn_shape& s) {
+    const Work w = work_of(s.R, s.Hq / s.Hkv, s.Hkv);
+    const int grid = grid_of(w, s.B, (s.T_cap + kQ4Page - 1) / kQ4Page);
+    return grid > 1 ? static_cast<size_t>(grid) * 2 * kRecFloats * sizeof(float) : 0;
+}
 
-cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void*, cudaStream_t st) {
-    return launch_pdl(attn_q4_kernel, dim3(a.Hq * a.R, a.B), dim3(kThreads), 0, st, a);
+cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st) {
+    const Work w = work_of(a.R, a.G, a.Hkv);
+    const int grid = grid_of(w, a.B, a.max_pages);
+    float* part = static_cast<float*>(ws);
+    const cudaError_t e = w.tile_rows <= 32 ? launch_rt<16>(a, w, grid, part, st) : launch_rt<32>(a, w, grid, part, st);
+    if (e != cudaSuccess || grid == 1) return e;
+    return launch_pdl(combine_q4_kernel, dim3(a.R * a.G, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w, part, grid);
 }
 
 }  // namespace sv
