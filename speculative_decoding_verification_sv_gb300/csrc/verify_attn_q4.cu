@@ -19,10 +19,10 @@
 //        [keys][64 rows] in shared memory, the MN-major B of the second product.
 //   O^T: lane = dim, column = row.
 // A row's maximum runs across lanes here, so it is not formed every step: P is
-// taken against a reference m that some earlier key of the row gave, as long as
-// no score passes it by more than 2^kSlack (bf16 and fp32 have the same range:
-// nothing is lost); a vote over the step's warps finds the rare pass, and then,
-// as in a range's first step, the true maximum is formed and O, l are rescaled.
+// taken against a reference, the row's maximum over the run's first step.  bf16
+// and fp32 have the same range, so nothing is lost by a P far above 1 as long as
+// no sum reaches kMostSum; a run where one does (a score some 60 powers of two
+// above the first step's) is done again with the reference moved every step.
 //
 // Work.  A unit is one (sequence, KV head, tile of 64 query rows); its pages,
 // and the block as one more, are laid end to end over all units, and each CTA
@@ -30,10 +30,15 @@
 // unit that lies in several CTAs' runs leaves partial rows (m, l, O) in the
 // workspace -- at most two a CTA -- and a second small kernel joins them.
 //
-// Warps: 8 softmax (TMEM quadrant w % 4, row half w / 4), 4 unpack K, 4 unpack
-// V, one issues the copies (two pages of K and V, 18 KB, a ring stage: each
-// (page, head) is one 4608-byte bulk copy), one the MMAs.
+// Warps: 16 softmax (8 where a tile has at most 32 rows; TMEM quadrant w % 4, 16
+// rows each), 4 unpack K, 8 unpack V (a page each), one issues the copies (two
+// pages of K and V, 18 KB, a ring stage: each (page, head) is one 4608-byte bulk
+// copy), one the MMAs.  Many warps with little code each: a role's step is a few
+// hundred instructions that depend on one another, and with one warp of a role a
+// sub-partition (8 softmax warps of 32 rows, 4 for V) a step took 2850 cycles.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv_q4.cuh"
 #include "sv_internal.h"
@@ -46,10 +51,16 @@ constexpr int kStepKeys = 128;            // two pages
 constexpr int kStages = 6;
 constexpr int kStageBytes = 4 * kQ4Bytes; // K of two pages, V of two pages
 constexpr int kMaxR = 128;
-constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17;
-constexpr int kThreads = 32 * 18;
+constexpr int kRT = 16;                   // rows a softmax thread takes
 constexpr int kGrain = 4;                 // pages a CTA takes at least (where there are as many)
-constexpr float kSlack = 40.0f;           // log2 of the largest P
+// kSW softmax warps (kSW / 4 groups of kRT rows), then 4 for K, 8 for V, copies, MMA
+template <int kSW>
+struct Roles {
+    static constexpr int kSoftWarps = kSW, kKWarp = kSW, kVWarp = kSW + 4, kTmaWarp = kSW + 12, kMmaWarp = kSW + 13;
+    static constexpr int kThreads = 32 * (kSW + 14);
+    static constexpr int kLive = kSW / 4 * kRT;   // rows of the tile that are taken; columns past them stay zero
+};
+constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 128;
 
@@ -63,12 +74,15 @@ constexpr int kPBytes = kStepKeys * kRows * 2;
 constexpr int kOffRing = kOffP + 2 * kPBytes;
 constexpr int kOffBar = kOffRing + kStages * kStageBytes;
 constexpr int kOffNm = kOffBar + 256;                     // [64] -m, m the rows' references
-constexpr int kOffMove = kOffNm + kRows * 4;              // [64] m_old - m_new
+constexpr int kOffMove = kOffNm + kRows * 4;              // [64] what O and l of the row are multiplied by
 constexpr int kOffRed = kOffMove + kRows * 4;             // [4 quadrants][64]
 constexpr int kOffBad = kOffRed + 4 * kRows * 4;          // [kStages] pages of the stage outside the pool
-constexpr int kOffPar = kOffBad + 32;                     // [128] parents
+constexpr int kOffFail = kOffBad + 32;                    // a sum left its range; then where the runs start
+constexpr int kOffPar = kOffFail + 32;                     // [128] parents
 constexpr int kOffAnc = kOffPar + kMaxR * 4;              // [128][2] 64-bit path masks
-constexpr int kSmemBytes = kOffAnc + kMaxR * 16 + 1024;
+constexpr int kOffRow = kOffAnc + kMaxR * 16;             // [64] (sequence, block row, head) of a tile row, -1 past the last
+constexpr int kOffJ = kOffRow + kRows * 4;                // [64] its block row
+constexpr int kSmemBytes = kOffJ + kRows * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 static_assert(kStages * 4 <= 32, "bad-page words");
 
@@ -179,6 +193,14 @@ struct Walk {
         return true;
     }
     int cur_b, cur_unit, cur_t;
+    __device__ __forceinline__ void save(volatile int* to) const {
+        to[0] = pos, to[1] = end, to[2] = b, to[3] = unit, to[4] = off;
+    }
+    __device__ __forceinline__ void load(const AttnQ4Args& a, const volatile int* from) {
+        pos = from[0], end = from[1], b = from[2], unit = from[3], off = from[4];
+        t = ctx_len(a, b);
+        np = ctx_pages(t);
+    }
     __device__ __forceinline__ int ctx_steps() const { return (p1 - p0 + 1) / 2; }
 };
 
@@ -216,20 +238,20 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int k) { return (w >> (4 * k) & 0x000F000Fu) | 0x43004300u; }
 constexpr uint32_t kM136 = 0xC308C308u;   // bf16 pair of -136
 
-// OR of a predicate over the softmax warps, and their barrier
-__device__ __forceinline__ bool soft_any(bool p) {
+// One lane of the (converged) warp, always the same one.  A branch on it is
+// known to be taken by one thread, and the MMAs' operands then stay in uniform
+// registers: 25 cycles an MMA issued in place of 45 under lane == 0 (M = 128, N
+// = 64, whose own time is 35).
+__device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(p))
-        : "memory");
+        : "=r"(r));
     return r != 0u;
 }
-__device__ __forceinline__ void soft_sync() { named_barrier(1, 32 * kSoftWarps); }
+
 
 __device__ __forceinline__ float warp_max(float v) {
     float r;
@@ -237,12 +259,33 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// kRT: rows a softmax thread takes; 2 kRT rows of the tile are live (the
-// others' columns of Q and P are zero)
-template <int kRT>
-__global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work wk, float* __restrict__ ws) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+// Sums of kN values over the lanes: half of the values are handed to the lane
+// whose number differs in the bit kN / 2, and so on; v[0] of lane e ends as value
+// e's sum over the lanes that agree with e below kN.
+template <int kN, int kLen>
+__device__ __forceinline__ void fold_sums_step(float (&v)[kLen]) {
+    const bool upper = (threadIdx.x & (kN / 2)) != 0;
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+        const float give = upper ? v[i] : v[i + kN / 2];
+        const float keep = upper ? v[i + kN / 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, kN / 2);
+    }
+    if constexpr (kN > 2) fold_sums_step<kN / 2>(v);
+}
+template <int kN>
+__device__ __forceinline__ void fold_sums(float (&v)[kN]) {
+    fold_sums_step<kN>(v);
+}
+
+template <int kSW>
+__global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
+    attn_q4_kernel(AttnQ4Args a, Work wk, float* __restrict__ ws) {
+    using Ro = Roles<kSW>;
+    constexpr int kSoftWarps = Ro::kSoftWarps, kKWarp = Ro::kKWarp, kVWarp = Ro::kVWarp, kTmaWarp = Ro::kTmaWarp,
+                  kMmaWarp = Ro::kMmaWarp, kThreads = Ro::kThreads, kLive = Ro::kLive;
+    // (aligned by its declaration: addresses are then constants, not registers)
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint64_t* ring_full = bars;                   // [kStages]
     uint64_t* ring_empty = ring_full + kStages;   // [kStages]
@@ -262,16 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     volatile uint32_t* bad_s = reinterpret_cast<volatile uint32_t*>(smem + kOffBad);
     int32_t* par_s = reinterpret_cast<int32_t*>(smem + kOffPar);
     uint64_t* anc_s = reinterpret_cast<uint64_t*>(smem + kOffAnc);
+    int* row_s = reinterpret_cast<int*>(smem + kOffRow);
+    int* j_s = reinterpret_cast<int*>(smem + kOffJ);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        *reinterpret_cast<volatile int*>(smem + kOffFail) = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ring_full[i], 1);
-            mbar_init(&ring_empty[i], 8);
+            mbar_init(&ring_empty[i], 12);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], 4);
-            mbar_init(&v_full[i], 4);
+            mbar_init(&v_full[i], 8);
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], kSoftWarps);
             mbar_init(&p_full[i], kSoftWarps);
@@ -282,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         fence_mbar_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_s, kTmemCols);
-    if (2 * kRT < kRows) {   // the columns of P past the live rows stay zero
+    if (kLive < kRows) {   // the columns of P past the live rows stay zero
         for (int x = threadIdx.x; x < 2 * kPBytes / 16; x += kThreads)
             reinterpret_cast<uint4*>(smem + kOffP)[x] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
@@ -305,10 +351,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     if (!early) pdl_wait();
     Walk walk;
     walk.start(a, wk, blockIdx.x, gridDim.x);
+    volatile int* fail_s = reinterpret_cast<volatile int*>(smem + kOffFail);
+    if (threadIdx.x == 0) walk.save(fail_s + 1);
+    // Each role runs the CTA's runs once, and once more with `safe` where a sum
+    // left its range (the softmax warps' verdict, after all have finished).
+    bool safe = false;
+    auto again = [&]() {
+        if (safe) return false;
+        __syncwarp();
+        named_barrier(2, kThreads);
+        safe = true;
+        if (*fail_s == 0) return false;
+        walk.load(a, fail_s + 1);
+        return true;
+    };
 
     if (warp == kTmaWarp) {
         // ---------------- page copies ----------------
         int c = 0;   // context steps so far
+        do {
         while (walk.next(a, wk)) {
             const int g = walk.cur_unit / wk.row_tiles;
             const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
@@ -342,9 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 }
             }
         }
+        } while (again());
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issuer ----------------
-        constexpr uint32_t id_s = idesc_bf16_f32(128, 2 * kRT, false, false);
+        constexpr uint32_t id_s = idesc_bf16_f32(128, kLive, false, false);
         constexpr uint32_t id_o = idesc_bf16_f32(128, kRows, false, true);
         const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
         int it = 0, seg = 0;
@@ -360,9 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || !first) ? 1u : 0u);
             tc_commit(&pv_done[x]);
         };
+        do {
         while (walk.next(a, wk)) {
             const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
-            if (lane == 0) {
+            if (elect_one()) {
                 mbar_wait(q_ready, seg & 1, a.err);
                 for (int st = 0; st < n; ++st) {
                     const int i = it + st, x = i & 1;
@@ -382,10 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             it += n;
             ++seg;
         }
+        } while (again());
     } else if (warp >= kKWarp) {
-        // ---------------- unpacking: a key's K (warps 8-11), a dim's V (12-15) ----------------
+        // ---------------- unpacking: a key's K, a dim's V (one page of the step a warp) ----------------
         const bool is_v = warp >= kVWarp;
         const int l = q4 * 32 + lane;   // TMEM lane: key of the step, or dim
+        const int half = is_v ? (warp - kVWarp) >> 2 : 0;   // V: page of the step
         uint64_t* full = is_v ? v_full : k_full;
         uint64_t* freed = is_v ? pv_done : s_full;
         int it = 0, c = 0;
@@ -399,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[it & 1]);
         };
+        do {
         while (walk.next(a, wk)) {
             for (int st = 0; st < walk.ctx_steps(); ++st, ++it, ++c) {
                 const int s = c % kStages;
@@ -407,19 +473,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 const uint32_t bad = bad_s[s];
                 mbar_wait(&freed[it & 1], ((it >> 1) & 1) ^ 1, a.err);
                 tc_fence_after();
+                // (loops, not straight code: the roles' bodies share the instruction
+                // cache of a sub-partition)
                 if (!is_v) {
                     const uint8_t* blk = stage + (l >> 6) * kQ4Bytes;
                     const int pos = l & 63;
-                    const uint2 sc = *reinterpret_cast<const uint2*>(blk + q4_k_scale_off(0, pos));
-                    const bool zero = (bad >> (l >> 6) & 1u) != 0u;
-#pragma unroll
+                    uint2 sc = *reinterpret_cast<const uint2*>(blk + q4_k_scale_off(0, pos));
+                    if (bad >> (l >> 6) & 1u) sc = make_uint2(0u, 0u);
+                    uint4 cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(0, pos));
+#pragma unroll 1
                     for (int g = 0; g < 4; ++g) {
-                        const uint4 cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(g, pos));
-                        const uint32_t sw = g < 2 ? sc.x : sc.y;
-                        uint32_t s2 = __byte_perm(sw, 0u, (g & 1) ? 0x3232 : 0x1010);
-                        if (zero) s2 = 0u;
+                        const uint32_t s2 = __byte_perm(sc.x, 0u, 0x1010);
+                        sc.x = g == 1 ? sc.y : sc.x >> 16;
                         const uint32_t o2 = bmul2(s2, kM136);
                         const uint32_t ww[4] = {cw.x, cw.y, cw.z, cw.w};
+                        if (g < 3) cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(g + 1, pos));
                         uint32_t r[16];
 #pragma unroll
                         for (int w = 0; w < 4; ++w)
@@ -430,34 +498,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 } else {
                     // keys of the step that exist: the others, and pages outside
                     // the pool, are zeros (0 * a non-finite V would be NaN)
-                    const int live = min(kStepKeys, walk.cur_t - (walk.p0 + 2 * st) * kQ4Page);
-                    const int have = min(live, (walk.p1 - walk.p0 - 2 * st) * kQ4Page);
-                    const bool part = have < kStepKeys || bad != 0u;
+                    const int have = min(walk.cur_t - (walk.p0 + 2 * st) * kQ4Page, (walk.p1 - walk.p0 - 2 * st) * kQ4Page);
+                    const uint8_t* cp = stage + (2 + half) * kQ4Bytes + q4_v_code_off(0, l);
+                    const uint8_t* sp = stage + (2 + half) * kQ4Bytes + q4_v_scale_off(q4, 0);
+                    auto unpack_v = [&](auto part_c) {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {   // 32 keys
+                            uint32_t r[16];
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {   // 32 keys
-                        const uint8_t* blk = stage + (2 + (h >> 1)) * kQ4Bytes;
-                        uint32_t r[16];
+                            for (int o = 0; o < 4; ++o) {
+                                const uint32_t w = *reinterpret_cast<const uint32_t*>(cp + o * 512);
+                                const uint4 sc = *reinterpret_cast<const uint4*>(sp + o * 16);
+                                uint32_t ss[4] = {sc.x, sc.y, sc.z, sc.w};
+                                if constexpr (decltype(part_c)::value) {
+                                    const int n = (bad >> half & 1u) ? 0 : have - 64 * half - 32 * h - 8 * o;
 #pragma unroll
-                        for (int o = 0; o < 4; ++o) {
-                            const int oct = (h & 1) * 4 + o;
-                            const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off(oct, l));
-                            const uint4 sc = *reinterpret_cast<const uint4*>(blk + q4_v_scale_off(q4, 8 * oct));
-                            const uint32_t ss[4] = {sc.x, sc.y, sc.z, sc.w};
+                                    for (int k = 0; k < 4; ++k)
+                                        ss[k] &= n > 2 * k + 1 ? ~0u : n > 2 * k ? 0xFFFFu : 0u;
+                                }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                r[4 * o + k] = bfma2(code_pair(w, k), ss[k], bmul2(ss[k], kM136));
-                        }
-                        if (part) {
-                            const bool zero = (bad >> (h >> 1) & 1u) != 0u;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const int key = 32 * h + 2 * k;
-                                if (zero || key >= have) r[k] = 0u;
-                                else if (key + 1 >= have) r[k] &= 0xFFFFu;
+                                for (int k = 0; k < 4; ++k)
+                                    r[4 * o + k] = bfma2(code_pair(w, k), ss[k], bmul2(ss[k], kM136));
                             }
+                            cp += 2048;
+                            sp += 64;
+                            put(32 * half + 16 * h, r);
                         }
-                        put(16 * h, r);
-                    }
+                    };
+                    if (have >= kStepKeys && bad == 0u) unpack_v(std::false_type{});
+                    else unpack_v(std::true_type{});
                 }
                 done();
                 if (lane == 0) mbar_arrive(&ring_empty[s]);
@@ -471,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 const size_t row0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R;
                 if (!is_v) {
                     const uint4* src = reinterpret_cast<const uint4*>(a.k_blk + (row0 + l) * kQ4D);
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         uint32_t r[16];
 #pragma unroll
@@ -484,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                     }
                 } else {
                     const uint16_t* src = a.v_blk + row0 * kQ4D + l;
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
+#pragma unroll 1
+                    for (int h = 2 * half; h < 2 * half + 2; ++h) {
                         uint32_t r[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
@@ -501,16 +570,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 ++it;
             }
         }
+        } while (again());
         if (!waited) pdl_wait();
     } else {
         // ---------------- softmax, epilogue ----------------
+        auto soft_sync = []() { named_barrier(1, 32 * kSoftWarps); };
         if (early) pdl_wait();
         const int hh = warp >> 2;              // rows hh * kRT .. of the tile
         const int l = q4 * 32 + lane;          // key of the step; dim in the epilogue
         const int tid = threadIdx.x;
         const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2);
         const int rows = a.R * a.G;
-        int it = 0, seg = 0, part = 0;
+        int it = 0, seg = 0;
+        do {
+        int part = 0;
         while (walk.next(a, wk)) {
             const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
             const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
@@ -518,29 +591,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 const int t = a.len[b];
                 if (t < 0 || t > a.max_pages * kQ4Page) raise_error(a.err, SV_DEVERR_LENGTH);
             }
+            if (tid < kRows) {
+                // (rows past the last take the last one's place in the tree)
+                const int gr = row0 + min(tid, nrows - 1), j = gr / a.G;
+                j_s[tid] = j;
+                row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr % a.G : -1;
+                nm_s[tid] = 0.f;
+            }
+            soft_sync();
             // Q rows (zeros past the last), K-major, 128-byte swizzle; the S MMAs
             // of the run before have read theirs (its last scores were waited for)
-            for (int x = tid; x < 2 * kRT * 16; x += 32 * kSoftWarps) {
-                const int r = x >> 4, ch = x & 15;
+            for (int x = tid; x < kLive * 16; x += 32 * kSoftWarps) {
+                const int r = x >> 4, ch = x & 15, row = row_s[r];
                 uint8_t* dst = smem + kOffQ + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                if (r < nrows) {
-                    const int gr = row0 + r;
-                    const uint16_t* src =
-                        a.q + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D;
-                    cp_async16(dst, reinterpret_cast<const uint4*>(src) + ch);
-                } else {
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-                }
+                if (row >= 0) cp_async16(dst, reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(row) * kQ4D) + ch);
+                else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (tid < kRows) nm_s[tid] = 0.f;
             const bool tree = walk.block && a.parent != nullptr;
             if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
             cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready);
-            soft_sync();   // nm_s, par_s
             if (tree) {
+                soft_sync();   // par_s
                 if (tid < a.R) {
                     uint64_t m0 = 0, m1 = 0;
                     int i = tid;
@@ -580,46 +654,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 const bool live =
                     blk ? l < a.R : (walk.p0 + 2 * st) * kQ4Page + l < min(walk.cur_t, walk.p1 * kQ4Page);
                 const int lo = !live ? kRows : blk && !tree ? l * a.G - row0 - hh * kRT : 0;
-                // exponents against the rows' references, 16 rows at a time; the scores
-                // are not kept
+                // the rows' exponents against their references
                 uint64_t e2[kRT / 2];
-                float mx = -INFINITY;
+                auto exponents = [&]() {
+                    uint32_t s[kRT];
+                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT, s);
+                    if (lo > 0) {
 #pragma unroll
-                for (int c0 = 0; c0 < kRT; c0 += 16) {
-                    uint32_t s[16];
-                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
-                    if (lo > c0) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c0 + e < lo) s[e] = 0xff800000u;
+                        for (int e = 0; e < kRT; ++e)
+                            if (e < lo) s[e] = 0xff800000u;
                     }
                     if (blk && tree && live) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int gr = row0 + min(hh * kRT + c0 + e, nrows - 1);
-                            if ((anc_s[2 * (gr / a.G) + (l >> 6)] >> (l & 63) & 1ull) == 0ull) s[e] = 0xff800000u;
+                        for (int e = 0; e < kRT; ++e) {
+                            if ((anc_s[2 * j_s[hh * kRT + e] + (l >> 6)] >> (l & 63) & 1ull) == 0ull) s[e] = 0xff800000u;
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT + c0)[i];
-                        uint64_t* e = e2 + c0 / 2 + 2 * i;
-                        e[0] = fma2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), sc2, pack2(nm.x, nm.y));
-                        e[1] = fma2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2,
-                                    pack2(nm.z, nm.w));
-                        float p, q;
-                        unpack2(e[0], p, q);
-                        mx = fmax3(mx, p, q);
-                        unpack2(e[1], p, q);
-                        mx = fmax3(mx, p, q);
+                    for (int i = 0; i < kRT / 4; ++i) {
+                        const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT)[i];
+                        e2[2 * i] = fma2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), sc2,
+                                         pack2(nm.x, nm.y));
+                        e2[2 * i + 1] = fma2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2,
+                                             pack2(nm.z, nm.w));
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[x]);
-                // a run's first step has no reference yet (it is 0: the exponents are
-                // the scaled scores); later a score may pass the reference too far
-                if (soft_any(st == 0 || mx > kSlack)) {
+                };
+                exponents();
+                // the run's first step gives the references (until then 0); with
+                // `safe` they follow the maximum from step to step
+                if (st == 0 || safe) {
 #pragma unroll
                     for (int i = 0; i < kRT / 2; ++i) {
                         float p, q;
@@ -630,65 +693,60 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                             *reinterpret_cast<float2*>(red_s + q4 * kRows + hh * kRT + 2 * i) = make_float2(p, q);
                     }
                     soft_sync();
-                    if (tid < 2 * kRT) {
-                        // the reference moves to the step's maximum: up, or in the first
-                        // step to wherever it is (not to -inf: all scores of the row are)
+                    if (tid < kLive) {
+                        // up, or in the first step to wherever the maximum is (not to
+                        // -inf: all scores of the row are)
                         float d = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
                                         fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
                         if (d == -INFINITY || (st > 0 && d < 0.f)) d = 0.f;
                         nm_s[tid] -= d;
-                        move_s[tid] = -d;
+                        move_s[tid] = fast_exp2(-d);
                     }
                     soft_sync();
-#pragma unroll
-                    for (int i = 0; i < kRT / 2; ++i) {
-                        const float2 d = *reinterpret_cast<const float2*>(move_s + hh * kRT + 2 * i);
-                        e2[i] = add2(e2[i], pack2(d.x, d.y));
-                    }
                     if (st > 0) {
 #pragma unroll
                         for (int i = 0; i < kRT / 2; ++i) {
-                            const float2 d = *reinterpret_cast<const float2*>(move_s + hh * kRT + 2 * i);
+                            const float2 c = *reinterpret_cast<const float2*>(move_s + hh * kRT + 2 * i);
                             float p, q;
                             unpack2(sum2[i], p, q);
-                            sum2[i] = pack2(p * fast_exp2(d.x), q * fast_exp2(d.y));
+                            sum2[i] = pack2(p * c.x, q * c.y);
                         }
                         // O^T (lane = dim) once the step before is in it
                         mbar_wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1, a.err);
                         tc_fence_after();
+                        const uint32_t ta = tO + lane_off + hh * kRT;
+                        uint32_t o[16];
+                        tmem_ld16_sync(ta, o);
 #pragma unroll
-                        for (int c0 = 0; c0 < kRT; c0 += 16) {
-                            const uint32_t ta = tO + lane_off + hh * kRT + c0;
-                            uint32_t o[16];
-                            tmem_ld16_sync(ta, o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * fast_exp2(move_s[hh * kRT + c0 + e]));
-                            tmem_st16(ta, o);
-                        }
+                        for (int e = 0; e < kRT; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + e]);
+                        tmem_st16(ta, o);
                         tmem_st_wait();
                     }
+                    exponents();
                 }
-                // P buffer x is free once the step before last is in O
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[x]);
+                // P buffer x is free once the step before last is in O; a key's line
+                // takes eight rows in 16 bytes
                 if (it >= 2) mbar_wait(&pv_done[x], ((it - 2) >> 1) & 1, a.err);
                 uint8_t* prow = smem + kOffP + x * kPBytes + l * 128;
+                uint32_t pk[kRT / 2];
 #pragma unroll
-                for (int ch = 0; ch < kRT / 8; ++ch) {   // eight rows: 16 bytes of the key's line
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float p, q;
-                        unpack2(e2[4 * ch + i], p, q);
-                        p = fast_exp2(p);
-                        q = fast_exp2(q);
-                        sum2[4 * ch + i] = add2(sum2[4 * ch + i], pack2(p, q));
-                        w[i] = pack_bf16x2(p, q);
-                    }
-                    *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + ch) ^ (l & 7)) << 4)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < kRT / 2; ++i) {
+                    float p, q;
+                    unpack2(e2[i], p, q);
+                    p = fast_exp2(p);
+                    q = fast_exp2(q);
+                    sum2[i] = add2(sum2[i], pack2(p, q));
+                    pk[i] = pack_bf16x2(p, q);
                 }
+#pragma unroll
+                for (int ch = 0; ch < kRT / 8; ++ch)
+                    *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + ch) ^ (l & 7)) << 4)) =
+                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
                 fence_proxy_async_smem();
-                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
@@ -697,42 +755,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             float sums[kRT];
 #pragma unroll
             for (int i = 0; i < kRT / 2; ++i) unpack2(sum2[i], sums[2 * i], sums[2 * i + 1]);
-#pragma unroll
-            for (int cnt = kRT; cnt > 1; cnt >>= 1) {
-                const bool upper = (lane & (cnt >> 1)) != 0;
-#pragma unroll
-                for (int i = 0; i < kRT / 2; ++i) {
-                    if (i >= cnt / 2) break;
-                    const float give = upper ? sums[i] : sums[i + cnt / 2];
-                    const float keep = upper ? sums[i + cnt / 2] : sums[i];
-                    sums[i] = keep + __shfl_xor_sync(0xffffffffu, give, cnt >> 1);
-                }
-            }
-            if (kRT == 16) sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
+            fold_sums(sums);
+            sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
             if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sums[0];
             mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, a.err);
             tc_fence_after();
             soft_sync();
             float* rec = nullptr;
             if (!walk.whole) rec = ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
+            {
+                uint32_t o[kRT];
+                tmem_ld16_sync(tO + lane_off + hh * kRT, o);
 #pragma unroll
-            for (int c0 = 0; c0 < kRT; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld16_sync(tO + lane_off + hh * kRT + c0, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int r = hh * kRT + c0 + e;
-                    if (r >= nrows) continue;
+                for (int e = 0; e < kRT; ++e) {
+                    const int r = hh * kRT + e;
+                    const int row = row_s[r];
+                    if (row < 0) continue;
                     const float lsum = (red_s[r] + red_s[kRows + r]) + (red_s[2 * kRows + r] + red_s[3 * kRows + r]);
                     const float ov = __uint_as_float(o[e]);
+                    if (!(lsum < kMostSum) || !(fabsf(ov) < INFINITY)) *fail_s = 1;
                     if (rec) {
                         rec[r * kQ4D + l] = ov;
                         if (l == 0)
                             *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * r) = make_float2(-nm_s[r], lsum);
                     } else {
-                        const int gr = row0 + r;
-                        a.out[((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D + l] =
-                            f32_bf16_bits(lsum != 0.f ? ov / lsum : 0.f);
+                        a.out[static_cast<size_t>(row) * kQ4D + l] = f32_bf16_bits(lsum != 0.f ? ov / lsum : 0.f);
                     }
                 }
             }
@@ -742,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             if (lane == 0) mbar_arrive(o_free);
             ++seg;
         }
+        } while (again());
     }
     __syncwarp();
     pdl_launch_dependents();
@@ -844,14 +892,14 @@ int grid_of(const Work& w, int B, int max_pages) {
     return static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
 }
 
-template <int kRT>
-cudaError_t launch_rt(const AttnQ4Args& a, const Work& w, int grid, float* ws, cudaStream_t st) {
+template <int kSW>
+cudaError_t launch_sw(const AttnQ4Args& a, const Work& w, int grid, float* ws, cudaStream_t st) {
     static PerDeviceOnce once;
     const cudaError_t e = once.run([]() {
-        return cudaFuncSetAttribute(attn_q4_kernel<kRT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        return cudaFuncSetAttribute(attn_q4_kernel<kSW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_q4_kernel<kRT>, dim3(grid), dim3(kThreads), kSmemBytes, st, a, w, ws);
+    return launch_pdl(attn_q4_kernel<kSW>, dim3(grid), dim3(Roles<kSW>::kThreads), kSmemBytes, st, a, w, ws);
 }
 
 }  // namespace
@@ -866,7 +914,7 @@ cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st
     const Work w = work_of(a.R, a.G, a.Hkv);
     const int grid = grid_of(w, a.B, a.max_pages);
     float* part = static_cast<float*>(ws);
-    const cudaError_t e = w.tile_rows <= 32 ? launch_rt<16>(a, w, grid, part, st) : launch_rt<32>(a, w, grid, part, st);
+    const cudaError_t e = w.tile_rows <= 32 ? launch_sw<8>(a, w, grid, part, st) : launch_sw<16>(a, w, grid, part, st);
     if (e != cudaSuccess || grid == 1) return e;
     return launch_pdl(combine_q4_kernel, dim3(a.R * a.G, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w, part, grid);
 }
