@@ -30,12 +30,9 @@
 // unit that lies in several CTAs' runs leaves partial rows (m, l, O) in the
 // workspace -- at most two a CTA -- and a second small kernel joins them.
 //
-// Warps: 16 softmax (8 where a tile has at most 32 rows; TMEM quadrant w % 4, 16
-// rows each), 4 unpack K, 8 unpack V (a page each), one issues the copies (two
-// pages of K and V, 18 KB, a ring stage: each (page, head) is one 4608-byte bulk
-// copy), one the MMAs.  Many warps with little code each: a role's step is a few
-// hundred instructions that depend on one another, and with one warp of a role a
-// sub-partition (8 softmax warps of 32 rows, 4 for V) a step took 2850 cycles.
+// Warps: 8 softmax (TMEM quadrant w % 4, half of the tile's rows each), 4 unpack
+// K, 4 unpack V, one issues the copies (two pages of K and V, 18 KB, a ring
+// stage: each (page, head) is one 4608-byte bulk copy), one the MMAs.
 #include <math.h>
 
 #include <type_traits>
@@ -51,15 +48,8 @@ constexpr int kStepKeys = 128;            // two pages
 constexpr int kStages = 6;
 constexpr int kStageBytes = 4 * kQ4Bytes; // K of two pages, V of two pages
 constexpr int kMaxR = 128;
-constexpr int kRT = 16;                   // rows a softmax thread takes
+constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17, kThreads = 32 * 18;
 constexpr int kGrain = 4;                 // pages a CTA takes at least (where there are as many)
-// kSW softmax warps (kSW / 4 groups of kRT rows), then 4 for K, 8 for V, copies, MMA
-template <int kSW>
-struct Roles {
-    static constexpr int kSoftWarps = kSW, kKWarp = kSW, kVWarp = kSW + 4, kTmaWarp = kSW + 12, kMmaWarp = kSW + 13;
-    static constexpr int kThreads = 32 * (kSW + 14);
-    static constexpr int kLive = kSW / 4 * kRT;   // rows of the tile that are taken; columns past them stay zero
-};
 constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 128;
@@ -139,7 +129,13 @@ struct Walk {
     bool block, whole;     // the block is in it; it is all of the unit
 
     __device__ __forceinline__ void start(const AttnQ4Args& a, const Work& w, int cta, int grid) {
-        const int W = work_sums(a, 0).x * w.U;
+        const int lane = threadIdx.x & 31;
+        // (the first 32 lengths stay in registers: a round trip less for most batches)
+        const int t0 = lane < a.B ? ctx_len(a, lane) : 0;
+        const int w0 = lane < a.B ? (ctx_pages(t0) + 1) * w.U : 0;
+        int W = w0;
+        for (int i = 32 + lane; i < a.B; i += 32) W += (ctx_pages(ctx_len(a, i)) + 1) * w.U;
+        W = __reduce_add_sync(0xffffffffu, W);
         const int n = active_ctas(W, grid);
         pos = end = 0;
         b = -1;
@@ -148,9 +144,9 @@ struct Walk {
         end = cta_first(W, cta + 1, n);
         // the sequence that pos lies in
         int base = 0;
-        const int lane = threadIdx.x & 31;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int wt = b0 + lane < a.B ? (ctx_pages(ctx_len(a, b0 + lane)) + 1) * w.U : 0;
+            const int tb = b0 == 0 ? t0 : b0 + lane < a.B ? ctx_len(a, b0 + lane) : 0;
+            const int wt = b0 == 0 ? w0 : b0 + lane < a.B ? (ctx_pages(tb) + 1) * w.U : 0;
             int sum = wt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -162,11 +158,11 @@ struct Walk {
                 const int k = __ffs(m) - 1;
                 b = b0 + k;
                 base += __shfl_sync(0xffffffffu, sum - wt, k);
+                t = __shfl_sync(0xffffffffu, tb, k);
                 break;
             }
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
-        t = ctx_len(a, b);
         np = ctx_pages(t);
         unit = (pos - base) / (np + 1);
         off = (pos - base) % (np + 1);
@@ -206,24 +202,6 @@ struct Walk {
 
 // --- packed arithmetic ---------------------------------------------------------
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
@@ -234,8 +212,19 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// bf16 pair 128 + c of elements 2k, 2k + 1 of a word
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int k) { return (w >> (4 * k) & 0x000F000Fu) | 0x43004300u; }
+// bf16 pair 128 + c of elements 2k, 2k + 1 of a word: one shift, one three-input
+// logical operation on registers (as immediates the two constants would take two)
+struct CodeMask {
+    uint32_t nibbles, exps;
+    __device__ __forceinline__ CodeMask() {
+        asm volatile("mov.u32 %0, 0x000F000F;\n\tmov.u32 %1, 0x43004300;" : "=r"(nibbles), "=r"(exps));
+    }
+    __device__ __forceinline__ uint32_t pair(uint32_t w, int k) const {
+        uint32_t r;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * k)), "r"(nibbles), "r"(exps));
+        return r;
+    }
+};
 constexpr uint32_t kM136 = 0xC308C308u;   // bf16 pair of -136
 
 // One lane of the (converged) warp, always the same one.  A branch on it is
@@ -278,12 +267,11 @@ __device__ __forceinline__ void fold_sums(float (&v)[kN]) {
     fold_sums_step<kN>(v);
 }
 
-template <int kSW>
-__global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
-    attn_q4_kernel(AttnQ4Args a, Work wk, float* __restrict__ ws) {
-    using Ro = Roles<kSW>;
-    constexpr int kSoftWarps = Ro::kSoftWarps, kKWarp = Ro::kKWarp, kVWarp = Ro::kVWarp, kTmaWarp = Ro::kTmaWarp,
-                  kMmaWarp = Ro::kMmaWarp, kThreads = Ro::kThreads, kLive = Ro::kLive;
+// kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (their
+// columns of P stay zero)
+template <int kRT>
+__global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work wk, float* __restrict__ ws) {
+    constexpr int kLive = 2 * kRT;
     // (aligned by its declaration: addresses are then constants, not registers)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -313,11 +301,11 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
         *reinterpret_cast<volatile int*>(smem + kOffFail) = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ring_full[i], 1);
-            mbar_init(&ring_empty[i], 12);
+            mbar_init(&ring_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], 4);
-            mbar_init(&v_full[i], 8);
+            mbar_init(&v_full[i], 4);
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], kSoftWarps);
             mbar_init(&p_full[i], kSoftWarps);
@@ -447,14 +435,14 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
         }
         } while (again());
     } else if (warp >= kKWarp) {
-        // ---------------- unpacking: a key's K, a dim's V (one page of the step a warp) ----------------
+        // ---------------- unpacking: a key's K, a dim's V ----------------
         const bool is_v = warp >= kVWarp;
         const int l = q4 * 32 + lane;   // TMEM lane: key of the step, or dim
-        const int half = is_v ? (warp - kVWarp) >> 2 : 0;   // V: page of the step
         uint64_t* full = is_v ? v_full : k_full;
         uint64_t* freed = is_v ? pv_done : s_full;
         int it = 0, c = 0;
         bool waited = !early;
+        const CodeMask cm;
         auto put = [&](int col, const uint32_t(&w)[16]) {
             tmem_st16((is_v ? tV(it & 1) : tK(it & 1)) + lane_off + col, w);
         };
@@ -473,15 +461,13 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
                 const uint32_t bad = bad_s[s];
                 mbar_wait(&freed[it & 1], ((it >> 1) & 1) ^ 1, a.err);
                 tc_fence_after();
-                // (loops, not straight code: the roles' bodies share the instruction
-                // cache of a sub-partition)
                 if (!is_v) {
                     const uint8_t* blk = stage + (l >> 6) * kQ4Bytes;
                     const int pos = l & 63;
                     uint2 sc = *reinterpret_cast<const uint2*>(blk + q4_k_scale_off(0, pos));
                     if (bad >> (l >> 6) & 1u) sc = make_uint2(0u, 0u);
                     uint4 cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(0, pos));
-#pragma unroll 1
+#pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t s2 = __byte_perm(sc.x, 0u, 0x1010);
                         sc.x = g == 1 ? sc.y : sc.x >> 16;
@@ -492,37 +478,35 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
 #pragma unroll
                         for (int w = 0; w < 4; ++w)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) r[4 * w + k] = bfma2(code_pair(ww[w], k), s2, o2);
+                            for (int k = 0; k < 4; ++k) r[4 * w + k] = bfma2(cm.pair(ww[w], k), s2, o2);
                         put(16 * g, r);
                     }
                 } else {
                     // keys of the step that exist: the others, and pages outside
                     // the pool, are zeros (0 * a non-finite V would be NaN)
                     const int have = min(walk.cur_t - (walk.p0 + 2 * st) * kQ4Page, (walk.p1 - walk.p0 - 2 * st) * kQ4Page);
-                    const uint8_t* cp = stage + (2 + half) * kQ4Bytes + q4_v_code_off(0, l);
-                    const uint8_t* sp = stage + (2 + half) * kQ4Bytes + q4_v_scale_off(q4, 0);
                     auto unpack_v = [&](auto part_c) {
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {   // 32 keys
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {   // 32 keys: half a page
+                            const uint8_t* blk = stage + (2 + (h >> 1)) * kQ4Bytes;
                             uint32_t r[16];
 #pragma unroll
                             for (int o = 0; o < 4; ++o) {
-                                const uint32_t w = *reinterpret_cast<const uint32_t*>(cp + o * 512);
-                                const uint4 sc = *reinterpret_cast<const uint4*>(sp + o * 16);
+                                const int oct = (h & 1) * 4 + o;
+                                const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off(oct, l));
+                                const uint4 sc = *reinterpret_cast<const uint4*>(blk + q4_v_scale_off(q4, 8 * oct));
                                 uint32_t ss[4] = {sc.x, sc.y, sc.z, sc.w};
                                 if constexpr (decltype(part_c)::value) {
-                                    const int n = (bad >> half & 1u) ? 0 : have - 64 * half - 32 * h - 8 * o;
+                                    const int n = (bad >> (h >> 1) & 1u) ? 0 : have - 32 * h - 8 * o;
 #pragma unroll
                                     for (int k = 0; k < 4; ++k)
                                         ss[k] &= n > 2 * k + 1 ? ~0u : n > 2 * k ? 0xFFFFu : 0u;
                                 }
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    r[4 * o + k] = bfma2(code_pair(w, k), ss[k], bmul2(ss[k], kM136));
+                                    r[4 * o + k] = bfma2(cm.pair(w, k), ss[k], bmul2(ss[k], kM136));
                             }
-                            cp += 2048;
-                            sp += 64;
-                            put(32 * half + 16 * h, r);
+                            put(16 * h, r);
                         }
                     };
                     if (have >= kStepKeys && bad == 0u) unpack_v(std::false_type{});
@@ -554,7 +538,7 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
                 } else {
                     const uint16_t* src = a.v_blk + row0 * kQ4D + l;
 #pragma unroll 1
-                    for (int h = 2 * half; h < 2 * half + 2; ++h) {
+                    for (int h = 0; h < 4; ++h) {
                         uint32_t r[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
@@ -579,7 +563,7 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
         const int hh = warp >> 2;              // rows hh * kRT .. of the tile
         const int l = q4 * 32 + lane;          // key of the step; dim in the epilogue
         const int tid = threadIdx.x;
-        const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2);
+        const float sc = a.scale_log2;
         const int rows = a.R * a.G;
         int it = 0, seg = 0;
         do {
@@ -639,58 +623,63 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
                 }
                 soft_sync();
             }
-            uint64_t sum2[kRT / 2];
+            float sums[kRT];
 #pragma unroll
-            for (int i = 0; i < kRT / 2; ++i) sum2[i] = 0ull;
+            for (int i = 0; i < kRT; ++i) sums[i] = 0.f;
             const int nctx = walk.ctx_steps(), n = nctx + (walk.block ? 1 : 0);
-            for (int st = 0; st < n; ++st, ++it) {
+            auto step = [&](int st, auto masked_c) {
+                constexpr bool kMasked = decltype(masked_c)::value;
                 const int x = it & 1;
                 mbar_wait(&s_full[x], (it >> 1) & 1, a.err);
                 tc_fence_after();
-                // visible keys: of the context, those before the length (the second
-                // page of a step may be missing); block row l is seen from query rows
-                // l G on, or where it lies on a tree row's path
-                const bool blk = st >= nctx;
-                const bool live =
-                    blk ? l < a.R : (walk.p0 + 2 * st) * kQ4Page + l < min(walk.cur_t, walk.p1 * kQ4Page);
-                const int lo = !live ? kRows : blk && !tree ? l * a.G - row0 - hh * kRT : 0;
-                // the rows' exponents against their references
-                uint64_t e2[kRT / 2];
-                auto exponents = [&]() {
-                    uint32_t s[kRT];
-                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT, s);
-                    if (lo > 0) {
-#pragma unroll
-                        for (int e = 0; e < kRT; ++e)
-                            if (e < lo) s[e] = 0xff800000u;
-                    }
-                    if (blk && tree && live) {
-#pragma unroll
-                        for (int e = 0; e < kRT; ++e) {
-                            if ((anc_s[2 * j_s[hh * kRT + e] + (l >> 6)] >> (l & 63) & 1ull) == 0ull) s[e] = 0xff800000u;
+                // the rows that see this thread's key (bit e: row hh * kRT + e), in the
+                // steps where some do not: of the context, keys before the length (the
+                // second page of a step may be missing); block row l is seen from query
+                // rows l G on, or by the tree rows on whose path it lies
+                uint32_t seen = ~0u;
+                if constexpr (kMasked) {
+                    if (st < nctx) {
+                        if ((walk.p0 + 2 * st) * kQ4Page + l >= min(walk.cur_t, walk.p1 * kQ4Page)) seen = 0u;
+                    } else {
+                        seen = 0u;
+#pragma unroll 1
+                        for (int e = 0; e < kRT && l < a.R; ++e) {
+                            const int j = j_s[hh * kRT + e];
+                            const bool see = tree ? (anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) != 0ull : l <= j;
+                            seen |= see ? 1u << e : 0u;
                         }
                     }
+                }
+                // exponents of rows c0 .. of the thread's against their references
+                auto exponents = [&](int c0, float(&e)[16]) {
+                    uint32_t s[16];
+                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
 #pragma unroll
-                    for (int i = 0; i < kRT / 4; ++i) {
-                        const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT)[i];
-                        e2[2 * i] = fma2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), sc2,
-                                         pack2(nm.x, nm.y));
-                        e2[2 * i + 1] = fma2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2,
-                                             pack2(nm.z, nm.w));
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT + c0)[i];
+                        e[4 * i] = fmaf(__uint_as_float(s[4 * i]), sc, nm.x);
+                        e[4 * i + 1] = fmaf(__uint_as_float(s[4 * i + 1]), sc, nm.y);
+                        e[4 * i + 2] = fmaf(__uint_as_float(s[4 * i + 2]), sc, nm.z);
+                        e[4 * i + 3] = fmaf(__uint_as_float(s[4 * i + 3]), sc, nm.w);
+                    }
+                    if constexpr (kMasked) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (!(seen >> (c0 + i) & 1u)) e[i] = -INFINITY;
                     }
                 };
-                exponents();
                 // the run's first step gives the references (until then 0); with
                 // `safe` they follow the maximum from step to step
                 if (st == 0 || safe) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kRT; c0 += 16) {
+                        float e[16];
+                        exponents(c0, e);
 #pragma unroll
-                    for (int i = 0; i < kRT / 2; ++i) {
-                        float p, q;
-                        unpack2(e2[i], p, q);
-                        p = warp_max(p);
-                        q = warp_max(q);
-                        if (lane == 0)
-                            *reinterpret_cast<float2*>(red_s + q4 * kRows + hh * kRT + 2 * i) = make_float2(p, q);
+                        for (int i = 0; i < 16; ++i) {
+                            e[i] = warp_max(e[i]);
+                            if (lane == 0) red_s[q4 * kRows + hh * kRT + c0 + i] = e[i];
+                        }
                     }
                     soft_sync();
                     if (tid < kLive) {
@@ -705,84 +694,101 @@ __global__ void __launch_bounds__(Roles<kSW>::kThreads, 1)
                     soft_sync();
                     if (st > 0) {
 #pragma unroll
-                        for (int i = 0; i < kRT / 2; ++i) {
-                            const float2 c = *reinterpret_cast<const float2*>(move_s + hh * kRT + 2 * i);
-                            float p, q;
-                            unpack2(sum2[i], p, q);
-                            sum2[i] = pack2(p * c.x, q * c.y);
-                        }
+                        for (int i = 0; i < kRT; ++i) sums[i] *= move_s[hh * kRT + i];
                         // O^T (lane = dim) once the step before is in it
                         mbar_wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1, a.err);
                         tc_fence_after();
-                        const uint32_t ta = tO + lane_off + hh * kRT;
-                        uint32_t o[16];
-                        tmem_ld16_sync(ta, o);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kRT; c0 += 16) {
+                            const uint32_t ta = tO + lane_off + hh * kRT + c0;
+                            uint32_t o[16];
+                            tmem_ld16_sync(ta, o);
 #pragma unroll
-                        for (int e = 0; e < kRT; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + e]);
-                        tmem_st16(ta, o);
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
+                            tmem_st16(ta, o);
+                        }
                         tmem_st_wait();
                     }
-                    exponents();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[x]);
                 // P buffer x is free once the step before last is in O; a key's line
                 // takes eight rows in 16 bytes
                 if (it >= 2) mbar_wait(&pv_done[x], ((it - 2) >> 1) & 1, a.err);
                 uint8_t* prow = smem + kOffP + x * kPBytes + l * 128;
-                uint32_t pk[kRT / 2];
 #pragma unroll
-                for (int i = 0; i < kRT / 2; ++i) {
-                    float p, q;
-                    unpack2(e2[i], p, q);
-                    p = fast_exp2(p);
-                    q = fast_exp2(q);
-                    sum2[i] = add2(sum2[i], pack2(p, q));
-                    pk[i] = pack_bf16x2(p, q);
+                for (int c0 = 0; c0 < kRT; c0 += 16) {
+                    float e[16];
+                    exponents(c0, e);
+                    if (c0 + 16 == kRT) {   // the scores are read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_empty[x]);
+                    }
+#pragma unroll
+                    for (int ch = 0; ch < 2; ++ch) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float p = fast_exp2(e[8 * ch + 2 * i]), q = fast_exp2(e[8 * ch + 2 * i + 1]);
+                            sums[c0 + 8 * ch + 2 * i] += p;
+                            sums[c0 + 8 * ch + 2 * i + 1] += q;
+                            w[i] = pack_bf16x2(p, q);
+                        }
+                        *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + c0 / 8 + ch) ^ (l & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
-#pragma unroll
-                for (int ch = 0; ch < kRT / 8; ++ch)
-                    *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + ch) ^ (l & 7)) << 4)) =
-                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
-            }
+                ++it;
+            };
+            // context steps that are whole, the last one where it is not, the block
+            // (apart, so that the whole ones carry no mask code)
+            const bool ragged = nctx > 0 && ((walk.p1 - walk.p0) & 1 || walk.p1 * kQ4Page > walk.cur_t);
+            const int nwhole = nctx - (ragged ? 1 : 0);
+#pragma unroll 1
+            for (int st = 0; st < nwhole; ++st) step(st, std::false_type{});
+#pragma unroll 1
+            for (int st = nwhole; st < n; ++st) step(st, std::true_type{});
             // the rows' sums over the keys: lane e of a warp ends with its row e's
             // (halving the rows and the lanes that differ, step by step)
-            float sums[kRT];
-#pragma unroll
-            for (int i = 0; i < kRT / 2; ++i) unpack2(sum2[i], sums[2 * i], sums[2 * i + 1]);
             fold_sums(sums);
-            sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
+            if (kRT == 16) sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
             if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sums[0];
+            float* rec = walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
+            soft_sync();
+            bool bad = false;
+            if (tid < kLive) {
+                const float lsum =
+                    (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
+                bad = !(lsum < kMostSum);
+                if (rec) *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * tid) = make_float2(-nm_s[tid], lsum);
+                move_s[tid] = lsum != 0.f ? 1.0f / lsum : 0.f;
+            }
             mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, a.err);
             tc_fence_after();
             soft_sync();
-            float* rec = nullptr;
-            if (!walk.whole) rec = ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
-            {
-                uint32_t o[kRT];
-                tmem_ld16_sync(tO + lane_off + hh * kRT, o);
 #pragma unroll
-                for (int e = 0; e < kRT; ++e) {
-                    const int r = hh * kRT + e;
-                    const int row = row_s[r];
-                    if (row < 0) continue;
-                    const float lsum = (red_s[r] + red_s[kRows + r]) + (red_s[2 * kRows + r] + red_s[3 * kRows + r]);
-                    const float ov = __uint_as_float(o[e]);
-                    if (!(lsum < kMostSum) || !(fabsf(ov) < INFINITY)) *fail_s = 1;
-                    if (rec) {
-                        rec[r * kQ4D + l] = ov;
-                        if (l == 0)
-                            *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * r) = make_float2(-nm_s[r], lsum);
-                    } else {
-                        a.out[static_cast<size_t>(row) * kQ4D + l] = f32_bf16_bits(lsum != 0.f ? ov / lsum : 0.f);
+            for (int c0 = 0; c0 < kRT; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16_sync(tO + lane_off + hh * kRT + c0, o);
+                if (rec) {   // (rows past the tile's last are written too, and never read)
+                    float* dst = rec + (hh * kRT + c0) * kQ4D + l;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) __stcg(dst + e * kQ4D, __uint_as_float(o[e]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int row = row_s[hh * kRT + c0 + e];
+                        const uint16_t v = f32_bf16_bits(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
+                        if (row >= 0) a.out[static_cast<size_t>(row) * kQ4D + l] = v;
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) bad |= !(fabsf(__uint_as_float(o[e])) < INFINITY);
             }
+            if (bad) *fail_s = 1;
             part = 1;   // a partial run that is not the CTA's first is its last
             tc_fence_before();
             soft_sync();   // red_s and nm_s read by everyone before the next run writes them
@@ -892,14 +898,14 @@ int grid_of(const Work& w, int B, int max_pages) {
     return static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
 }
 
-template <int kSW>
-cudaError_t launch_sw(const AttnQ4Args& a, const Work& w, int grid, float* ws, cudaStream_t st) {
+template <int kRT>
+cudaError_t launch_rt(const AttnQ4Args& a, const Work& w, int grid, float* ws, cudaStream_t st) {
     static PerDeviceOnce once;
     const cudaError_t e = once.run([]() {
-        return cudaFuncSetAttribute(attn_q4_kernel<kSW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        return cudaFuncSetAttribute(attn_q4_kernel<kRT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_q4_kernel<kSW>, dim3(grid), dim3(Roles<kSW>::kThreads), kSmemBytes, st, a, w, ws);
+    return launch_pdl(attn_q4_kernel<kRT>, dim3(grid), dim3(kThreads), kSmemBytes, st, a, w, ws);
 }
 
 }  // namespace
@@ -914,7 +920,7 @@ cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st
     const Work w = work_of(a.R, a.G, a.Hkv);
     const int grid = grid_of(w, a.B, a.max_pages);
     float* part = static_cast<float*>(ws);
-    const cudaError_t e = w.tile_rows <= 32 ? launch_sw<8>(a, w, grid, part, st) : launch_sw<16>(a, w, grid, part, st);
+    const cudaError_t e = w.tile_rows <= 32 ? launch_rt<16>(a, w, grid, part, st) : launch_rt<32>(a, w, grid, part, st);
     if (e != cudaSuccess || grid == 1) return e;
     return launch_pdl(combine_q4_kernel, dim3(a.R * a.G, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w, part, grid);
 }
