@@ -52,7 +52,7 @@ constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp =
 constexpr int kGrain = 4;                 // pages a CTA takes at least (where there are as many)
 constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 256;
 
 // TMEM columns: two K operands, two V operands (64 columns: 128 bf16 each), two
 // S^T, one O^T
@@ -398,25 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         constexpr uint32_t id_o = idesc_bf16_f32(128, kRows, false, true);
         const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
         int it = 0, seg = 0;
-        auto pv = [&](int i, bool first) {
-            const int x = i & 1;
-            if (first) mbar_wait(o_free, (seg & 1) ^ 1, a.err);
-            mbar_wait(&v_full[x], (i >> 1) & 1, a.err);
-            mbar_wait(&p_full[x], (i >> 1) & 1, a.err);
-            tc_fence_after();
-            const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + x * kPBytes), 16, 1024);
-#pragma unroll
-            for (int kc = 0; kc < kStepKeys / 16; ++kc)
-                tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || !first) ? 1u : 0u);
-            tc_commit(&pv_done[x]);
-        };
         do {
         while (walk.next(a, wk)) {
             const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
             if (elect_one()) {
-                mbar_wait(q_ready, seg & 1, a.err);
-                for (int st = 0; st < n; ++st) {
-                    const int i = it + st, x = i & 1;
+                // S of step i + 2 goes ahead of P V of step i: it only waits for the
+                // scores of step i to be read, not for their P
+                auto scores = [&](int i) {
+                    const int x = i & 1;
                     mbar_wait(&k_full[x], (i >> 1) & 1, a.err);
                     mbar_wait(&s_empty[x], ((i >> 1) & 1) ^ 1, a.err);
                     tc_fence_after();
@@ -425,9 +414,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                         tc_mma_ts(tS(x), tK(x) + kc * 8, qd + (((kc >> 2) * kRows * 128 + (kc & 3) * 32) >> 4), id_s,
                                   kc > 0 ? 1u : 0u);
                     tc_commit(&s_full[x]);
-                    if (st > 0) pv(i - 1, st == 1);
+                };
+                mbar_wait(q_ready, seg & 1, a.err);
+#pragma unroll 1
+                for (int st = -2; st < n; ++st) {
+                    if (st + 2 < n) scores(it + st + 2);
+                    if (st < 0) continue;
+                    const int i = it + st, x = i & 1;
+                    if (st == 0) mbar_wait(o_free, (seg & 1) ^ 1, a.err);
+                    mbar_wait(&v_full[x], (i >> 1) & 1, a.err);
+                    mbar_wait(&p_full[x], (i >> 1) & 1, a.err);
+                    tc_fence_after();
+                    const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + x * kPBytes), 16, 1024);
+#pragma unroll
+                    for (int kc = 0; kc < kStepKeys / 16; ++kc)
+                        tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || st > 0) ? 1u : 0u);
+                    tc_commit(&pv_done[x]);
                 }
-                pv(it + n - 1, n == 1);
             }
             __syncwarp();
             it += n;
@@ -807,16 +810,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     }
 }
 
-// Joins the partial rows of the units that lie in several CTAs' runs: one CTA a
-// row, its warps taking every fourth partial, eight in flight.
+// Joins the partial rows of the units that lie in several CTAs' runs: a warp a
+// row, a lane four dims, eight partials in flight.
 __global__ void __launch_bounds__(kCombineThreads)
     combine_q4_kernel(AttnQ4Args a, Work wk, const float* __restrict__ ws, int grid) {
-    __shared__ float4 o_s[4][32];
-    __shared__ float2 ml_s[4];
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv, gr = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int gr = blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5);
+    if (gr >= a.R * a.G) return;
+    const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
     const int rt = gr / wk.tile_rows, r = gr % wk.tile_rows;
     const int2 sums = work_sums(a, b);
     const int W = sums.x * wk.U, n = active_ctas(W, grid);
@@ -826,12 +829,12 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (i0 == i1) return;   // one CTA had the whole unit and wrote its rows
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = i0 + warp; c0 <= i1; c0 += 32) {
+    for (int c0 = i0; c0 <= i1; c0 += 8) {
         float2 ml[8];
         float4 o[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int i = c0 + 4 * u;
+            const int i = c0 + u;
             ml[u] = make_float2(-INFINITY, 0.f);
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i > i1) continue;
@@ -849,7 +852,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c, L *= c;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (ml[u].y == 0.f) continue;   // no key of the run was visible
+            if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
             const float w = exp2f(ml[u].x - mn);
             L += w * ml[u].y;
             acc.x += w * o[u].x;
@@ -858,24 +861,6 @@ __global__ void __launch_bounds__(kCombineThreads)
             acc.w += w * o[u].w;
         }
         M = mn;
-    }
-    o_s[warp][lane] = acc;
-    if (lane == 0) ml_s[warp] = make_float2(M, L);
-    __syncthreads();
-    if (warp != 0) return;
-    float mn = fmaxf(fmaxf(ml_s[0].x, ml_s[1].x), fmaxf(ml_s[2].x, ml_s[3].x));
-    L = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        if (ml_s[u].y == 0.f) continue;
-        const float w = exp2f(ml_s[u].x - mn);
-        const float4 o = o_s[u][lane];
-        L += w * ml_s[u].y;
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
     }
     const float inv = L != 0.f ? 1.0f / L : 0.f;
     uint16_t* dst = a.out + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D + 4 * lane;
@@ -922,7 +907,7 @@ cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st
     float* part = static_cast<float*>(ws);
     const cudaError_t e = w.tile_rows <= 32 ? launch_rt<16>(a, w, grid, part, st) : launch_rt<32>(a, w, grid, part, st);
     if (e != cudaSuccess || grid == 1) return e;
-    return launch_pdl(combine_q4_kernel, dim3(a.R * a.G, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w, part, grid);
+    return launch_pdl(combine_q4_kernel, dim3((a.R * a.G + 7) / 8, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w, part, grid);
 }
 
 }  // namespace sv
