@@ -422,77 +422,93 @@ KV_Q4_BYTES = 4608   # bytes of one (page, head) of a 4-bit cache (SV_KV_Q4_BYTE
 ROPE_INTERLEAVED = 1
 
 
-def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, device):
-    """The pointer of an argument, once its type, device, layout and shape (-1:
-    any) are as the call wants them."""
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
+    """The pointer of an argument (None: NULL), once its type, device, shape and
+    layout are what the call wants."""
     if t is None:
         return None
-    if t.device != device or t.dtype != dtype:
-        raise (TypeError if t.device == device else ValueError)(
-            f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    if t.dim() != len(shape) or any(w != -1 and w != g for w, g in zip(shape, t.shape)):
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _cuda_device(t: torch.Tensor, name: str) -> torch.device:
+def _cuda_device(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _launch(fn: str, device: torch.device, stream, *args):
-    """Calls fn(*args, stream) with `device` current, on `stream` or on the
+def _dims(t: torch.Tensor, name: str, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {list(t.shape)}")
+    return t.shape
+
+
+# the current stream's handle, without an object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _launch(fn: str, dev: int, stream, *args):
+    """Calls fn(*args, stream) with cuda:`dev` current, on `stream` or on the
     device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        _check(fn, getattr(lib, fn)(*args, stream.cuda_stream))
+        handle = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
-        with torch.cuda.device(device):
-            _check(fn, getattr(lib, fn)(*args, stream.cuda_stream))
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = getattr(lib, fn)(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib, fn)(*args, handle)
+    if status:
+        _check(fn, status)
 
 
-def _rows(t: torch.Tensor, name: str, shape, device):
+def _rows(t: torch.Tensor, name: str, shape, dev: int):
     """The pointer and row stride of [N, Hkv, D] bf16 rows that may lie apart."""
-    if t.device != device or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16 on {device}, got {t.dtype} on {t.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    N, H, D = shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must have shape {list(shape)} on cuda:{dev}, got {list(t.shape)} on {t.device}")
+    n, h, d = shape
+    apart, between, within = t.stride()
+    if (d > 1 and within != 1) or (h > 1 and between != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if N > 1 else H * D
+    return t.data_ptr(), apart if n > 1 else h * d
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, dev: int, stream):
     """An output or workspace, taken from the memory of the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _append(fn, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved, stream, page, dtype, dims):
-    if k.dim() != 3:
-        raise ValueError(f"k must be [N, Hkv, D], got {list(k.shape)}")
+def _append(fn, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved, stream, block, dtype, head_dim):
     dev = _cuda_device(k, "k")
-    N, H, D = k.shape
-    kp, ks = _rows(k, "k", (N, H, D), dev)
-    vp, vs = _rows(v, "v", (N, H, D), dev)
-    B = length.shape[0] if length.dim() == 1 else -1
-    args = [kp, vp, ks, vs, N, _arg(row_off, "row_off", torch.int32, (B + 1,), dev), B, H, *dims]
-    pool = (-1, H) + page
-    kpl, vpl = _arg(k_pool, "k_pool", dtype, pool, dev), _arg(v_pool, "v_pool", dtype, (k_pool.shape[0],) + pool[1:], dev)
-    tab = _arg(page_table, "page_table", torch.int32, (B, -1), dev)
-    ln = _arg(length, "length", torch.int32, (B,), dev)
-    rp = _arg(rope, "rope", torch.float32, (-1, -1), dev)
-    _launch(fn, dev, stream, *args, rp, 0 if rope is None else rope.shape[0], 0 if rope is None else rope.shape[1], kpl,
-            vpl, k_pool.shape[0], tab, page_table.shape[1], ln, ROPE_INTERLEAVED if interleaved else 0)
+    shape = _dims(k, "k", 3)
+    N, H, _ = shape
+    (kp, ks), (vp, vs) = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
+    B, max_pages = _dims(page_table, "page_table", 2)
+    P = k_pool.shape[0]
+    pool = (P, H) + block
+    i32 = torch.int32
+    positions, rot = (0, 0) if rope is None else _dims(rope, "rope", 2)
+    _launch(fn, dev, stream, kp, vp, ks, vs, N, _arg(row_off, "row_off", i32, (B + 1,), dev), B, H, *head_dim,
+            _arg(rope, "rope", torch.float32, (positions, rot), dev), positions, rot,
+            _arg(k_pool, "k_pool", dtype, pool, dev), _arg(v_pool, "v_pool", dtype, pool, dev), P,
+            _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, _arg(length, "length", i32, (B,), dev),
+            ROPE_INTERLEAVED if interleaved else 0)
 
 
 def kv_append_paged(k, v, row_off, k_pool, v_pool, page_table, length, rope=None, interleaved=False, stream=None):
@@ -516,38 +532,34 @@ def kv_append_q4(k, v, row_off, k_pool, v_pool, page_table, length, rope=None, i
 def kv_commit_q4(k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length, stream=None):
     """pools [L,num_pages,Hkv,4608] uint8; page_table [B,max_pages]; blocks [L,B,Hkv,R,128] bf16;
     path [B,R], n_acc [B], length [B] int32 (length updated in place)."""
-    if k_blk.dim() != 5:
-        raise ValueError(f"k_blk must be [L, B, Hkv, R, 128], got {list(k_blk.shape)}")
     dev = _cuda_device(k_blk, "k_blk")
-    L, B, H, R, _ = k_blk.shape
-    i32, u8, bf = torch.int32, torch.uint8, torch.bfloat16
-    kp = _arg(k_pool, "k_pool", u8, (L, -1, H, KV_Q4_BYTES), dev)
-    P = k_pool.shape[1]
-    _launch("sv_kv_commit_q4", dev, stream, kp, _arg(v_pool, "v_pool", u8, (L, P, H, KV_Q4_BYTES), dev), P,
-            _arg(page_table, "page_table", i32, (B, -1), dev), page_table.shape[1],
-            _arg(k_blk, "k_blk", bf, (L, B, H, R, 128), dev), _arg(v_blk, "v_blk", bf, (L, B, H, R, 128), dev), L, B, H, R,
-            _arg(path, "path", i32, (B, R), dev), _arg(n_acc, "n_acc", i32, (B,), dev),
-            _arg(length, "length", i32, (B,), dev))
+    L, B, H, R, _ = _dims(k_blk, "k_blk", 5)
+    max_pages = _dims(page_table, "page_table", 2)[1]
+    P = _dims(k_pool, "k_pool", 4)[1]
+    i32, u8, bf, pool, blk = torch.int32, torch.uint8, torch.bfloat16, (L, P, H, KV_Q4_BYTES), (L, B, H, R, 128)
+    _launch("sv_kv_commit_q4", dev, stream, _arg(k_pool, "k_pool", u8, pool, dev), _arg(v_pool, "v_pool", u8, pool, dev), P,
+            _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, _arg(k_blk, "k_blk", bf, blk, dev),
+            _arg(v_blk, "v_blk", bf, blk, dev), L, B, H, R, _arg(path, "path", i32, (B, R), dev),
+            _arg(n_acc, "n_acc", i32, (B,), dev), _arg(length, "length", i32, (B,), dev))
 
 
 def kv_gather_q4(k_pool, v_pool, page_table, start, length, n, k_out=None, v_out=None, stream=None):
     """Positions start[b] .. start[b]+n-1 of every sequence of 4-bit pools
     [L,num_pages,Hkv,4608] uint8 as bf16 rows, zeros at and past length[b].
     Returns (k_out, v_out) [L,B,Hkv,n,128] bf16."""
-    if k_pool.dim() != 4:
-        raise ValueError(f"k_pool must be [L, num_pages, Hkv, {KV_Q4_BYTES}], got {list(k_pool.shape)}")
     dev = _cuda_device(k_pool, "k_pool")
-    L, P, H, _ = k_pool.shape
-    B = page_table.shape[0]
-    i32, u8, bf = torch.int32, torch.uint8, torch.bfloat16
-    shape = (L, B, H, n, 128)
-    if k_out is None:
-        k_out = _empty(shape, bf, dev, stream)
-    if v_out is None:
-        v_out = _empty(shape, bf, dev, stream)
-    _launch("sv_kv_gather_q4", dev, stream, _arg(k_pool, "k_pool", u8, (L, P, H, KV_Q4_BYTES), dev),
-            _arg(v_pool, "v_pool", u8, (L, P, H, KV_Q4_BYTES), dev), P, _arg(page_table, "page_table", i32, (B, -1), dev),
-            page_table.shape[1], L, B, H, _arg(start, "start", i32, (B,), dev), _arg(length, "length", i32, (B,), dev), n,
+    pool = _dims(k_pool, "k_pool", 4)
+    L, P, H, _ = pool
+    B, max_pages = _dims(page_table, "page_table", 2)
+    i32, u8, bf, shape = torch.int32, torch.uint8, torch.bfloat16, (L, B, H, n, 128)
+    if k_out is None and v_out is None:
+        k_out, v_out = _empty((2, *shape), bf, dev, stream).unbind(0)
+    elif k_out is None or v_out is None:
+        raise ValueError("k_out and v_out are given together")
+    pool = (L, P, H, KV_Q4_BYTES)
+    _launch("sv_kv_gather_q4", dev, stream, _arg(k_pool, "k_pool", u8, pool, dev), _arg(v_pool, "v_pool", u8, pool, dev), P,
+            _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, L, B, H,
+            _arg(start, "start", i32, (B,), dev), _arg(length, "length", i32, (B,), dev), n,
             _arg(k_out, "k_out", bf, shape, dev), _arg(v_out, "v_out", bf, shape, dev))
     return k_out, v_out
 
@@ -562,29 +574,25 @@ def verify_attn_q4(q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent=N
     """verify_attn_paged over a 4-bit cache: pools [num_pages,Hkv,4608] uint8;
     q [B,R,Hq,128] and blocks [B,Hkv,R,128] bf16; page_table [B,max_pages],
     length [B] int32.  Returns out [B,R,Hq,128] bf16."""
-    if q.dim() != 4 or k_pool.dim() != 3:
-        raise ValueError(f"q must be [B, R, Hq, 128] and k_pool [num_pages, Hkv, {KV_Q4_BYTES}], "
-                         f"got {list(q.shape)} and {list(k_pool.shape)}")
     dev = _cuda_device(q, "q")
-    B, R, Hq, D = q.shape
-    P, H, _ = k_pool.shape
-    max_pages = page_table.shape[1] if page_table.dim() == 2 else -1
-    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    rows = _dims(q, "q", 4)
+    B, R, Hq, D = rows
+    P, H, _ = _dims(k_pool, "k_pool", 3)
+    max_pages = _dims(page_table, "page_table", 2)[1]
+    bf, i32, u8, pool, blk = torch.bfloat16, torch.int32, torch.uint8, (P, H, KV_Q4_BYTES), (B, H, R, D)
     if out is None:
-        out = _empty(q.shape, bf, dev, stream)
-    args = [_arg(q, "q", bf, (B, R, Hq, D), dev), _arg(k_pool, "k_pool", u8, (P, H, KV_Q4_BYTES), dev),
-            _arg(v_pool, "v_pool", u8, (P, H, KV_Q4_BYTES), dev), P,
-            _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, _arg(length, "length", i32, (B,), dev),
-            _arg(k_blk, "k_blk", bf, (B, H, R, D), dev), _arg(v_blk, "v_blk", bf, (B, H, R, D), dev),
-            _arg(parent, "parent", i32, (B, R), dev), D ** -0.5 if scale is None else float(scale),
-            _arg(out, "out", bf, (B, R, Hq, D), dev)]
+        out = _empty(rows, bf, dev, stream)
     s = ctypes.byref(_AttnShape(B, R, Hq, H, D, max_pages * KV_PAGE))
-    nbytes = int(lib.sv_verify_attn_q4_workspace(s))
+    nbytes = lib.sv_verify_attn_q4_workspace(s)
     if ws is None:
-        ws = _empty(nbytes, u8, dev, stream) if nbytes else None
-    elif ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
-        raise ValueError(f"ws must be contiguous, on {dev} and hold {nbytes} bytes")
-    _launch("sv_verify_attn_q4", dev, stream, s, *args, None if ws is None else ws.data_ptr(), nbytes,
+        ws = _empty((nbytes,), u8, dev, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
+        raise ValueError(f"ws must be contiguous, on cuda:{dev} and hold {nbytes} bytes")
+    _launch("sv_verify_attn_q4", dev, stream, s, _arg(q, "q", bf, rows, dev), _arg(k_pool, "k_pool", u8, pool, dev),
+            _arg(v_pool, "v_pool", u8, pool, dev), P, _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages,
+            _arg(length, "length", i32, (B,), dev), _arg(k_blk, "k_blk", bf, blk, dev), _arg(v_blk, "v_blk", bf, blk, dev),
+            _arg(parent, "parent", i32, (B, R), dev), D ** -0.5 if scale is None else float(scale),
+            _arg(out, "out", bf, rows, dev), ws.data_ptr() if nbytes else None, nbytes,
             ATTN_CACHE_READY if cache_ready else 0)
     return out
 
@@ -598,34 +606,37 @@ def logits_process(logits, tok=None, parent=None, hist=None, hist_len=None, prom
     frequency, presence [B] and bias_val [n] fp32; bias_off [B+1] int32.  out may
     be logits itself.  Returns (out [B,R,V] or None, argmax keys
     [B*R, ceil(V/128)] int64 or None); an argmax buffer implies write_argmax."""
-    if logits.dim() != 3:
-        raise ValueError(f"logits must be [B, R, V], got {list(logits.shape)}")
     dev = _cuda_device(logits, "logits")
-    B, R, V = logits.shape
-    f32, i32 = torch.float32, torch.int32
+    shape = _dims(logits, "logits", 3)
+    B, R, V = shape
+    f32, i32, S = torch.float32, torch.int32, (V + ARGMAX_SLAB - 1) // ARGMAX_SLAB
     if not write_logits:
         out = None
     elif out is None:
-        out = _empty(logits.shape, f32, dev, stream)
-    S = (V + ARGMAX_SLAB - 1) // ARGMAX_SLAB
+        out = _empty(shape, f32, dev, stream)
     if argmax is None and write_argmax:
         argmax = _empty((B * R, S), torch.int64, dev, stream)
-    if hist is not None and hist_len is None:
-        raise ValueError("hist needs hist_len")
-    if bias_off is not None and (bias_tok is None or bias_val is None):
-        raise ValueError("bias_off needs bias_tok and bias_val")
-    cap = hist.shape[1] if hist is not None and hist.dim() == 2 else 0
-    nb = bias_tok.shape[0] if bias_off is not None and bias_tok.dim() == 1 else 0
-    hp = _arg(hist, "hist", i32, (B, cap), dev)
-    _launch("sv_logits_process", dev, stream, _arg(logits, "logits", f32, (B, R, V), dev), B, R, V,
-            hp if cap else None, cap, _arg(hist_len, "hist_len", i32, (B,), dev),
+    cap = nb = 0
+    if hist is not None:
+        if hist_len is None:
+            raise ValueError("hist needs hist_len")
+        cap = _dims(hist, "hist", 2)[1]
+        _arg(hist, "hist", i32, (B, cap), dev)
+        if cap == 0:
+            hist = None
+    if bias_off is not None:
+        if bias_tok is None or bias_val is None:
+            raise ValueError("bias_off needs bias_tok and bias_val")
+        nb = _dims(bias_tok, "bias_tok", 1)[0]
+    _launch("sv_logits_process", dev, stream, _arg(logits, "logits", f32, shape, dev), B, R, V,
+            _arg(hist, "hist", i32, (B, cap), dev), cap, _arg(hist_len, "hist_len", i32, (B,), dev),
             _arg(prompt_len, "prompt_len", i32, (B,), dev), _arg(tok, "tok", i32, (B, R), dev),
             _arg(parent, "parent", i32, (B, R), dev), _arg(repetition, "repetition", f32, (B,), dev),
             _arg(frequency, "frequency", f32, (B,), dev), _arg(presence, "presence", f32, (B,), dev),
             _arg(bias_off, "bias_off", i32, (B + 1,), dev), _arg(bias_tok, "bias_tok", i32, (nb,), dev),
             _arg(bias_val, "bias_val", f32, (nb,), dev), nb, _arg(mask, "mask", i32, (B, R, (V + 31) // 32), dev),
-            float(mask_value), _arg(out, "out", f32, (B, R, V), dev),
-            _arg(argmax, "argmax", torch.int64, (B * R, S), dev), 0 if argmax is None else argmax.numel() * 8)
+            float(mask_value), _arg(out, "out", f32, shape, dev), _arg(argmax, "argmax", torch.int64, (B * R, S), dev),
+            B * R * S * 8 if argmax is not None else 0)
     return out, argmax
 
 
