@@ -261,7 +261,7 @@ SV_API sv_status sv_lm_head_argmax(const uint16_t* hid, const uint16_t* W, float
  *     x = mask_value                                      if the row's mask bit
  *                                      of v is 0 (NaN and infinity included)
  * Every control is optional (NULL).
- *   logits     [B][R][V] fp32, 1 <= R <= 128
+ *   logits     [B][R][V] fp32, 1 <= B <= 65535, 1 <= R <= 128, 1 <= V <= 2^24
  *   hist       [B][hist_cap] int32, hist_len [B]: the tokens before the block
  *              (the pending token tok[b][0] is not among them); prompt_len [B]
  *              or NULL (no prompt)

@@ -527,7 +527,7 @@ sv_status sv_logits_process(const float* logits, int32_t B, int32_t R, int32_t V
                             const float* bias_val, int32_t n_bias, const uint32_t* mask, float mask_value, float* out,
                             uint64_t* argmax, size_t argmax_bytes, void* stream) {
     if (!logits || (!out && !argmax)) return SV_ERR_ARG;
-    if (B < 1 || B > 65535 || R < 1 || R > 128 || V < 1 || V > (1 << 30)) return SV_ERR_SHAPE;
+    if (B < 1 || B > 65535 || R < 1 || R > 128 || V < 1 || V > (1 << 24)) return SV_ERR_SHAPE;
     if (!aligned16(logits) || (out && !aligned16(out)) || (argmax && !aligned16(argmax))) return SV_ERR_ARG;
     if (hist && (!hist_len || !aligned16(hist))) return SV_ERR_ARG;
     // counts share a word with three flags
