@@ -18,11 +18,11 @@
 //   P:   exp2(s - m), bf16, written by the key's thread as one line of
 //        [keys][64 rows] in shared memory, the MN-major B of the second product.
 //   O^T: lane = dim, column = row.
-// A row's maximum runs across lanes here, so it is not formed every step: P is
-// taken against a reference, the row's maximum over the run's first step.  bf16
-// and fp32 have the same range, so nothing is lost by a P far above 1 as long as
-// no sum reaches kMostSum; a run where one does (a score some 60 powers of two
-// above the first step's) is done again with the reference moved every step.
+// A row's maximum runs across lanes here, so it is not formed: P is taken against
+// a reference, the row's score with the run's first key.  bf16 and fp32 have the
+// same range, so nothing is lost by a P far above 1 as long as no sum reaches
+// kMostSum; a run where one does (some score 60 powers of two above the first
+// key's) is done again with the reference moved to the maximum every step.
 //
 // Work.  A unit is one (sequence, KV head, tile of 64 query rows); its pages,
 // and the block as one more, are laid end to end over all units, and each CTA
@@ -32,7 +32,8 @@
 //
 // Warps: 8 softmax (TMEM quadrant w % 4, half of the tile's rows each), 4 unpack
 // K, 4 unpack V, one issues the copies (two pages of K and V, 18 KB, a ring
-// stage: each (page, head) is one 4608-byte bulk copy), one the MMAs.
+// stage: each (page, head) is one 4608-byte bulk copy), one the MMAs, one brings
+// the query rows of the next run while the present one is worked on.
 #include <math.h>
 
 #include <type_traits>
@@ -48,7 +49,7 @@ constexpr int kStepKeys = 128;            // two pages
 constexpr int kStages = 6;
 constexpr int kStageBytes = 4 * kQ4Bytes; // K of two pages, V of two pages
 constexpr int kMaxR = 128;
-constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17, kThreads = 32 * 18;
+constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17, kQWarp = 18, kThreads = 32 * 19;
 constexpr int kGrain = 4;                 // pages a CTA takes at least (where there are as many)
 constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
@@ -58,8 +59,9 @@ constexpr int kCombineThreads = 256;
 // S^T, one O^T
 constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 384, kTmemCols = 512;
 
-constexpr int kOffQ = 0;                                  // [2 halves of 64 dims][64 rows][128 B], swizzled
-constexpr int kOffP = kOffQ + kRows * kQ4D * 2;           // 2 x [128 keys][128 B], swizzled
+constexpr int kOffQ = 0;                                  // 2 x [2 halves of 64 dims][64 rows][128 B], swizzled
+constexpr int kQBytes = kRows * kQ4D * 2;
+constexpr int kOffP = kOffQ + 2 * kQBytes;                // 2 x [128 keys][128 B], swizzled
 constexpr int kPBytes = kStepKeys * kRows * 2;
 constexpr int kOffRing = kOffP + 2 * kPBytes;
 constexpr int kOffBar = kOffRing + kStages * kStageBytes;
@@ -71,8 +73,7 @@ constexpr int kOffFail = kOffBad + 32;                    // a sum left its rang
 constexpr int kOffPar = kOffFail + 32;                     // [128] parents
 constexpr int kOffAnc = kOffPar + kMaxR * 4;              // [128][2] 64-bit path masks
 constexpr int kOffRow = kOffAnc + kMaxR * 16;             // [64] (sequence, block row, head) of a tile row, -1 past the last
-constexpr int kOffJ = kOffRow + kRows * 4;                // [64] its block row
-constexpr int kSmemBytes = kOffJ + kRows * 4;
+constexpr int kSmemBytes = kOffRow + kRows * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 static_assert(kStages * 4 <= 32, "bad-page words");
 
@@ -80,6 +81,7 @@ struct Work {
     int U;         // units of a sequence: Hkv * row tiles
     int row_tiles;
     int tile_rows; // rows of a tile but the last
+    int inv_g;     // ceil(2^16 / G): r * inv_g >> 16 is r / G for every row r < 2048 of G <= 16
 };
 
 // Pages of sequence b (its length clamped into the table), the block not counted.
@@ -283,10 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     uint64_t* s_empty = s_full + 2;               // [2] scores read
     uint64_t* p_full = s_empty + 2;               // [2] P written (and O rescaled)
     uint64_t* pv_done = p_full + 2;               // [2] O^T has the step (P and the V operand read)
-    uint64_t* q_ready = pv_done + 2;
-    uint64_t* o_free = q_ready + 1;               // O^T read by the epilogue
+    uint64_t* q_ready = pv_done + 2;              // [2] query rows there
+    uint64_t* q_free = q_ready + 2;               // [2] the run's S^T are formed
+    uint64_t* o_free = q_free + 2;               // O^T read by the epilogue
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(o_free + 1);
-    static_assert((2 * kStages + 14) * 8 + 4 <= 256, "barrier area");
+    static_assert((2 * kStages + 17) * 8 + 4 <= 256, "barrier area");
     float* nm_s = reinterpret_cast<float*>(smem + kOffNm);
     float* move_s = reinterpret_cast<float*>(smem + kOffMove);
     float* red_s = reinterpret_cast<float*>(smem + kOffRed);
@@ -294,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     int32_t* par_s = reinterpret_cast<int32_t*>(smem + kOffPar);
     uint64_t* anc_s = reinterpret_cast<uint64_t*>(smem + kOffAnc);
     int* row_s = reinterpret_cast<int*>(smem + kOffRow);
-    int* j_s = reinterpret_cast<int*>(smem + kOffJ);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -310,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             mbar_init(&s_empty[i], kSoftWarps);
             mbar_init(&p_full[i], kSoftWarps);
             mbar_init(&pv_done[i], 1);
+            mbar_init(&q_ready[i], 1);
+            mbar_init(&q_free[i], 1);
         }
-        mbar_init(q_ready, kSoftWarps);
         mbar_init(o_free, kSoftWarps);
         fence_mbar_init();
     }
@@ -344,6 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     // Each role runs the CTA's runs once, and once more with `safe` where a sum
     // left its range (the softmax warps' verdict, after all have finished).
     bool safe = false;
+    // a warp's wait; its lanes go on together (what follows is warp-collective)
+    auto wait = [&](uint64_t* bar, int parity) {
+        mbar_wait(bar, static_cast<uint32_t>(parity), a.err);
+        __syncwarp();
+    };
     auto again = [&]() {
         if (safe) return false;
         __syncwarp();
@@ -396,12 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         // ---------------- MMA issuer ----------------
         constexpr uint32_t id_s = idesc_bf16_f32(128, kLive, false, false);
         constexpr uint32_t id_o = idesc_bf16_f32(128, kRows, false, true);
-        const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
         int it = 0, seg = 0;
         do {
         while (walk.next(a, wk)) {
             const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
             if (elect_one()) {
+                const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ + (seg & 1) * kQBytes), 16, 1024);
                 // S of step i + 2 goes ahead of P V of step i: it only waits for the
                 // scores of step i to be read, not for their P
                 auto scores = [&](int i) {
@@ -414,8 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                         tc_mma_ts(tS(x), tK(x) + kc * 8, qd + (((kc >> 2) * kRows * 128 + (kc & 3) * 32) >> 4), id_s,
                                   kc > 0 ? 1u : 0u);
                     tc_commit(&s_full[x]);
+                    if (i == it + n - 1) tc_commit(&q_free[seg & 1]);
                 };
-                mbar_wait(q_ready, seg & 1, a.err);
+                mbar_wait(&q_ready[seg & 1], (seg >> 1) & 1, a.err);
 #pragma unroll 1
                 for (int st = -2; st < n; ++st) {
                     if (st + 2 < n) scores(it + st + 2);
@@ -434,6 +443,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             }
             __syncwarp();
             it += n;
+            ++seg;
+        }
+        } while (again());
+    } else if (warp == kQWarp) {
+        // ---------------- query rows ----------------
+        if (early) pdl_wait();
+        int seg = 0;
+        do {
+        while (walk.next(a, wk)) {
+            const int g = walk.cur_unit / wk.row_tiles, row0 = walk.cur_unit % wk.row_tiles * wk.tile_rows;
+            const int nrows = min(wk.tile_rows, a.R * a.G - row0);
+            // where each row lies (two a lane), -1 past the last
+            int at[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 32 * h + lane, gr = row0 + r, j = gr * wk.inv_g >> 16;
+                at[h] = r < nrows ? (walk.cur_b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
+            }
+            wait(&q_free[seg & 1], ((seg >> 1) & 1) ^ 1);
+            uint8_t* q_s = smem + kOffQ + (seg & 1) * kQBytes;
+            // K-major, 128-byte swizzle, zeros past the last row: half a warp a row
+            const int ch = lane & 15;
+#pragma unroll
+            for (int h = 0; h < kLive / 32; ++h) {
+#pragma unroll 8
+                for (int i = 0; i < 32; i += 2) {
+                    const int r = 32 * h + i + (lane >> 4), row = __shfl_sync(0xffffffffu, at[h], r & 31);
+                    uint8_t* dst = q_s + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                    if (row >= 0) cp_async16(dst, reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(row) * kQ4D) + ch);
+                    else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
             ++seg;
         }
         } while (again());
@@ -460,9 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             for (int st = 0; st < walk.ctx_steps(); ++st, ++it, ++c) {
                 const int s = c % kStages;
                 const uint8_t* stage = smem + kOffRing + s * kStageBytes;
-                mbar_wait(&ring_full[s], (c / kStages) & 1, a.err);
+                wait(&ring_full[s], (c / kStages) & 1);
                 const uint32_t bad = bad_s[s];
-                mbar_wait(&freed[it & 1], ((it >> 1) & 1) ^ 1, a.err);
+                wait(&freed[it & 1], ((it >> 1) & 1) ^ 1);
                 tc_fence_after();
                 if (!is_v) {
                     const uint8_t* blk = stage + (l >> 6) * kQ4Bytes;
@@ -521,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             if (walk.block) {
                 if (!waited) pdl_wait();
                 waited = true;
-                mbar_wait(&freed[it & 1], ((it >> 1) & 1) ^ 1, a.err);
+                wait(&freed[it & 1], ((it >> 1) & 1) ^ 1);
                 tc_fence_after();
                 const int g = walk.cur_unit / wk.row_tiles;
                 const size_t row0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R;
@@ -561,7 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         if (!waited) pdl_wait();
     } else {
         // ---------------- softmax, epilogue ----------------
-        auto soft_sync = []() { named_barrier(1, 32 * kSoftWarps); };
+        // (the barrier counts whole warps: they arrive converged)
+        auto soft_sync = []() {
+            __syncwarp();
+            named_barrier(1, 32 * kSoftWarps);
+        };
         if (early) pdl_wait();
         const int hh = warp >> 2;              // rows hh * kRT .. of the tile
         const int l = q4 * 32 + lane;          // key of the step; dim in the epilogue
@@ -579,29 +628,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 if (t < 0 || t > a.max_pages * kQ4Page) raise_error(a.err, SV_DEVERR_LENGTH);
             }
             if (tid < kRows) {
-                // (rows past the last take the last one's place in the tree)
-                const int gr = row0 + min(tid, nrows - 1), j = gr / a.G;
-                j_s[tid] = j;
-                row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr % a.G : -1;
+                const int gr = row0 + tid, j = gr * wk.inv_g >> 16;
+                row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
                 nm_s[tid] = 0.f;
-            }
-            soft_sync();
-            // Q rows (zeros past the last), K-major, 128-byte swizzle; the S MMAs
-            // of the run before have read theirs (its last scores were waited for)
-            for (int x = tid; x < kLive * 16; x += 32 * kSoftWarps) {
-                const int r = x >> 4, ch = x & 15, row = row_s[r];
-                uint8_t* dst = smem + kOffQ + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                if (row >= 0) cp_async16(dst, reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(row) * kQ4D) + ch);
-                else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
             }
             const bool tree = walk.block && a.parent != nullptr;
             if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
-            cp_async_wait_all();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready);
+            soft_sync();   // row_s, nm_s, par_s
             if (tree) {
-                soft_sync();   // par_s
                 if (tid < a.R) {
                     uint64_t m0 = 0, m1 = 0;
                     int i = tid;
@@ -630,26 +664,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
 #pragma unroll
             for (int i = 0; i < kRT; ++i) sums[i] = 0.f;
             const int nctx = walk.ctx_steps(), n = nctx + (walk.block ? 1 : 0);
-            auto step = [&](int st, auto masked_c) {
-                constexpr bool kMasked = decltype(masked_c)::value;
+            auto step = [&](int st, auto general_c) {
+                constexpr bool kGeneral = decltype(general_c)::value;
                 const int x = it & 1;
-                mbar_wait(&s_full[x], (it >> 1) & 1, a.err);
+                wait(&s_full[x], (it >> 1) & 1);
                 tc_fence_after();
                 // the rows that see this thread's key (bit e: row hh * kRT + e), in the
                 // steps where some do not: of the context, keys before the length (the
                 // second page of a step may be missing); block row l is seen from query
                 // rows l G on, or by the tree rows on whose path it lies
                 uint32_t seen = ~0u;
-                if constexpr (kMasked) {
+                if constexpr (kGeneral) {
                     if (st < nctx) {
                         if ((walk.p0 + 2 * st) * kQ4Page + l >= min(walk.cur_t, walk.p1 * kQ4Page)) seen = 0u;
+                    } else if (!tree) {
+                        const int lo = l < a.R ? l * a.G - row0 - hh * kRT : kRT;
+                        seen = lo >= kRT ? 0u : lo > 0 ? ~0u << lo : ~0u;
                     } else {
+                        // block row by block row: its G query rows see the same keys
                         seen = 0u;
-#pragma unroll 1
-                        for (int e = 0; e < kRT && l < a.R; ++e) {
-                            const int j = j_s[hh * kRT + e];
-                            const bool see = tree ? (anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) != 0ull : l <= j;
-                            seen |= see ? 1u << e : 0u;
+                        const int r0 = row0 + hh * kRT, r1 = min(r0 + kRT, rows);
+                        int j = r0 * wk.inv_g >> 16;
+                        for (int r = j * a.G - r0; l < a.R && r + r0 < r1; ++j, r += a.G) {
+                            if ((anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) == 0ull) continue;
+                            const uint32_t run = (1u << a.G) - 1u;   // (G <= 16)
+                            seen |= r >= 0 ? run << r : run >> -r;
                         }
                     }
                 }
@@ -665,15 +704,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                         e[4 * i + 2] = fmaf(__uint_as_float(s[4 * i + 2]), sc, nm.z);
                         e[4 * i + 3] = fmaf(__uint_as_float(s[4 * i + 3]), sc, nm.w);
                     }
-                    if constexpr (kMasked) {
+                    if constexpr (kGeneral) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (!(seen >> (c0 + i) & 1u)) e[i] = -INFINITY;
                     }
                 };
-                // the run's first step gives the references (until then 0); with
-                // `safe` they follow the maximum from step to step
-                if (st == 0 || safe) {
+                // the references (until now 0): the first key's scores (any finite number
+                // will do: it need not be visible), or, with `safe`, the running maxima
+                if constexpr (kGeneral) {
+                if (st == 0 && !safe) {
+                    if (q4 == 0) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kRT; c0 += 16) {
+                            uint32_t s[16];
+                            tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float e = __uint_as_float(s[i]) * -sc;
+                                s[i] = fabsf(e) < INFINITY ? __float_as_uint(e) : 0u;
+                            }
+                            if (lane == 0) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4)
+                                    *reinterpret_cast<uint4*>(nm_s + hh * kRT + c0 + i) =
+                                        make_uint4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    soft_sync();
+                }
+                if (safe) {
 #pragma unroll 1
                     for (int c0 = 0; c0 < kRT; c0 += 16) {
                         float e[16];
@@ -699,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
 #pragma unroll
                         for (int i = 0; i < kRT; ++i) sums[i] *= move_s[hh * kRT + i];
                         // O^T (lane = dim) once the step before is in it
-                        mbar_wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1, a.err);
+                        wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1);
                         tc_fence_after();
 #pragma unroll 1
                         for (int c0 = 0; c0 < kRT; c0 += 16) {
@@ -714,9 +776,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                         tmem_st_wait();
                     }
                 }
+                }
                 // P buffer x is free once the step before last is in O; a key's line
                 // takes eight rows in 16 bytes
-                if (it >= 2) mbar_wait(&pv_done[x], ((it - 2) >> 1) & 1, a.err);
+                if (it >= 2) wait(&pv_done[x], ((it - 2) >> 1) & 1);
                 uint8_t* prow = smem + kOffP + x * kPBytes + l * 128;
 #pragma unroll
                 for (int c0 = 0; c0 < kRT; c0 += 16) {
@@ -746,14 +809,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 if (lane == 0) mbar_arrive(&p_full[x]);
                 ++it;
             };
-            // context steps that are whole, the last one where it is not, the block
-            // (apart, so that the whole ones carry no mask code)
+            // the plain steps -- whole context steps but the run's first -- apart, so
+            // that they carry neither masks nor references
             const bool ragged = nctx > 0 && ((walk.p1 - walk.p0) & 1 || walk.p1 * kQ4Page > walk.cur_t);
-            const int nwhole = nctx - (ragged ? 1 : 0);
+            const int nwhole = safe ? 0 : nctx - (ragged ? 1 : 0);
 #pragma unroll 1
-            for (int st = 0; st < nwhole; ++st) step(st, std::false_type{});
-#pragma unroll 1
-            for (int st = nwhole; st < n; ++st) step(st, std::true_type{});
+            for (int st = 0; st < n; ++st) {
+                if (st > 0 && st < nwhole) step(st, std::false_type{});
+                else step(st, std::true_type{});
+            }
             // the rows' sums over the keys: lane e of a warp ends with its row e's
             // (halving the rows and the lanes that differ, step by step)
             fold_sums(sums);
@@ -769,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 if (rec) *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * tid) = make_float2(-nm_s[tid], lsum);
                 move_s[tid] = lsum != 0.f ? 1.0f / lsum : 0.f;
             }
-            mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, a.err);
+            wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
             tc_fence_after();
             soft_sync();
 #pragma unroll
@@ -874,6 +938,7 @@ Work work_of(int R, int G, int Hkv) {
     w.row_tiles = (rows + kRows - 1) / kRows;
     w.tile_rows = (rows + w.row_tiles - 1) / w.row_tiles;
     w.U = Hkv * w.row_tiles;
+    w.inv_g = (65536 + G - 1) / G;
     return w;
 }
 
