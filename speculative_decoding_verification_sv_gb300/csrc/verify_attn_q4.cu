@@ -61,9 +61,10 @@ constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 384, kTmemCols =
 
 constexpr int kOffQ = 0;                                  // 2 x [2 halves of 64 dims][64 rows][128 B], swizzled
 constexpr int kQBytes = kRows * kQ4D * 2;
-constexpr int kOffP = kOffQ + 2 * kQBytes;                // 2 x [128 keys][128 B], swizzled
+constexpr int kOffP = kOffQ + 2 * kQBytes;                // kPBufs x [128 keys][128 B], swizzled
+constexpr int kPBufs = 4;
 constexpr int kPBytes = kStepKeys * kRows * 2;
-constexpr int kOffRing = kOffP + 2 * kPBytes;
+constexpr int kOffRing = kOffP + kPBufs * kPBytes;
 constexpr int kOffBar = kOffRing + kStages * kStageBytes;
 constexpr int kOffNm = kOffBar + 256;                     // [64] -m, m the rows' references
 constexpr int kOffMove = kOffNm + kRows * 4;              // [64] what O and l of the row are multiplied by
@@ -73,7 +74,8 @@ constexpr int kOffFail = kOffBad + 32;                    // a sum left its rang
 constexpr int kOffPar = kOffFail + 32;                     // [128] parents
 constexpr int kOffAnc = kOffPar + kMaxR * 4;              // [128][2] 64-bit path masks
 constexpr int kOffRow = kOffAnc + kMaxR * 16;             // [64] (sequence, block row, head) of a tile row, -1 past the last
-constexpr int kSmemBytes = kOffRow + kRows * 4;
+constexpr int kOffScale = kOffRow + kRows * 4;            // [4 V warps][s of 64 key pairs, then -136 s]
+constexpr int kSmemBytes = kOffScale + 4 * 512;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 static_assert(kStages * 4 <= 32, "bad-page words");
 
@@ -283,13 +285,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     uint64_t* v_full = k_full + 2;                // [2]
     uint64_t* s_full = v_full + 2;                // [2] S^T formed (and the K operand read)
     uint64_t* s_empty = s_full + 2;               // [2] scores read
-    uint64_t* p_full = s_empty + 2;               // [2] P written (and O rescaled)
-    uint64_t* pv_done = p_full + 2;               // [2] O^T has the step (P and the V operand read)
+    uint64_t* p_full = s_empty + 2;               // [kPBufs] P written (and O rescaled): one each, as a warp may
+                                                  // be two steps ahead of another
+    uint64_t* pv_done = p_full + kPBufs;               // [2] O^T has the step (P and the V operand read)
     uint64_t* q_ready = pv_done + 2;              // [2] query rows there
     uint64_t* q_free = q_ready + 2;               // [2] the run's S^T are formed
     uint64_t* o_free = q_free + 2;               // O^T read by the epilogue
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(o_free + 1);
-    static_assert((2 * kStages + 17) * 8 + 4 <= 256, "barrier area");
+    static_assert((2 * kStages + 15 + kPBufs) * 8 + 4 <= 256, "barrier area");
     float* nm_s = reinterpret_cast<float*>(smem + kOffNm);
     float* move_s = reinterpret_cast<float*>(smem + kOffMove);
     float* red_s = reinterpret_cast<float*>(smem + kOffRed);
@@ -310,17 +313,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             mbar_init(&v_full[i], 4);
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], kSoftWarps);
-            mbar_init(&p_full[i], kSoftWarps);
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_ready[i], 1);
             mbar_init(&q_free[i], 1);
         }
+        for (int i = 0; i < kPBufs; ++i) mbar_init(&p_full[i], kSoftWarps);
         mbar_init(o_free, kSoftWarps);
         fence_mbar_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_s, kTmemCols);
     if (kLive < kRows) {   // the columns of P past the live rows stay zero
-        for (int x = threadIdx.x; x < 2 * kPBytes / 16; x += kThreads)
+        for (int x = threadIdx.x; x < kPBufs * kPBytes / 16; x += kThreads)
             reinterpret_cast<uint4*>(smem + kOffP)[x] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -432,9 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                     const int i = it + st, x = i & 1;
                     if (st == 0) mbar_wait(o_free, (seg & 1) ^ 1, a.err);
                     mbar_wait(&v_full[x], (i >> 1) & 1, a.err);
-                    mbar_wait(&p_full[x], (i >> 1) & 1, a.err);
+                    mbar_wait(&p_full[i % kPBufs], (i / kPBufs) & 1, a.err);
                     tc_fence_after();
-                    const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + x * kPBytes), 16, 1024);
+                    const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + i % kPBufs * kPBytes), 16, 1024);
 #pragma unroll
                     for (int kc = 0; kc < kStepKeys / 16; ++kc)
                         tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || st > 0) ? 1u : 0u);
@@ -533,32 +536,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                     // keys of the step that exist: the others, and pages outside
                     // the pool, are zeros (0 * a non-finite V would be NaN)
                     const int have = min(walk.cur_t - (walk.p0 + 2 * st) * kQ4Page, (walk.p1 - walk.p0 - 2 * st) * kQ4Page);
-                    auto unpack_v = [&](auto part_c) {
+                    // the warp's 32 dims are one group: the step's 64 pairs of scales and
+                    // -136 times them, formed once by its lanes
+                    uint32_t* sc_s = reinterpret_cast<uint32_t*>(smem + kOffScale + q4 * 512);
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {   // 32 keys: half a page
-                            const uint8_t* blk = stage + (2 + (h >> 1)) * kQ4Bytes;
-                            uint32_t r[16];
-#pragma unroll
-                            for (int o = 0; o < 4; ++o) {
-                                const int oct = (h & 1) * 4 + o;
-                                const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off(oct, l));
-                                const uint4 sc = *reinterpret_cast<const uint4*>(blk + q4_v_scale_off(q4, 8 * oct));
-                                uint32_t ss[4] = {sc.x, sc.y, sc.z, sc.w};
-                                if constexpr (decltype(part_c)::value) {
-                                    const int n = (bad >> (h >> 1) & 1u) ? 0 : have - 32 * h - 8 * o;
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        ss[k] &= n > 2 * k + 1 ? ~0u : n > 2 * k ? 0xFFFFu : 0u;
-                                }
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    r[4 * o + k] = bfma2(cm.pair(w, k), ss[k], bmul2(ss[k], kM136));
-                            }
-                            put(16 * h, r);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t s2 = *reinterpret_cast<const uint32_t*>(stage + (2 + h) * kQ4Bytes +
+                                                                         q4_v_scale_off(q4, 2 * lane));
+                        if (have < kStepKeys || bad != 0u) {
+                            const int n = (bad >> h & 1u) ? 0 : have - kQ4Page * h - 2 * lane;
+                            s2 &= n > 1 ? ~0u : n > 0 ? 0xFFFFu : 0u;
                         }
-                    };
-                    if (have >= kStepKeys && bad == 0u) unpack_v(std::false_type{});
-                    else unpack_v(std::true_type{});
+                        sc_s[32 * h + lane] = s2;
+                        sc_s[64 + 32 * h + lane] = bmul2(s2, kM136);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {   // 32 keys: half a page
+                        const uint8_t* blk = stage + (2 + (h >> 1)) * kQ4Bytes;
+                        uint32_t r[16];
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off((h & 1) * 4 + o, l));
+                            const uint4 sv = reinterpret_cast<const uint4*>(sc_s)[4 * h + o];
+                            const uint4 ov = reinterpret_cast<const uint4*>(sc_s)[16 + 4 * h + o];
+                            r[4 * o] = bfma2(cm.pair(w, 0), sv.x, ov.x);
+                            r[4 * o + 1] = bfma2(cm.pair(w, 1), sv.y, ov.y);
+                            r[4 * o + 2] = bfma2(cm.pair(w, 2), sv.z, ov.z);
+                            r[4 * o + 3] = bfma2(cm.pair(w, 3), sv.w, ov.w);
+                        }
+                        put(16 * h, r);
+                    }
                 }
                 done();
                 if (lane == 0) mbar_arrive(&ring_empty[s]);
@@ -777,10 +785,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                     }
                 }
                 }
-                // P buffer x is free once the step before last is in O; a key's line
-                // takes eight rows in 16 bytes
-                if (it >= 2) wait(&pv_done[x], ((it - 2) >> 1) & 1);
-                uint8_t* prow = smem + kOffP + x * kPBytes + l * 128;
+                // a key's line of P takes eight rows in 16 bytes.  (The buffer is free: S of
+                // this step was issued behind P V of three steps before.)
+                uint8_t* prow = smem + kOffP + it % kPBufs * kPBytes + l * 128;
 #pragma unroll
                 for (int c0 = 0; c0 < kRT; c0 += 16) {
                     float e[16];
@@ -806,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
+                if (lane == 0) mbar_arrive(&p_full[it % kPBufs]);
                 ++it;
             };
             // the plain steps -- whole context steps but the run's first -- apart, so
