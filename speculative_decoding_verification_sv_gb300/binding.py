@@ -494,6 +494,24 @@ def _empty(shape, dtype, dev: int, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+_workspaces = {}   # (device, stream handle) -> the largest workspace asked for there
+
+
+def _workspace(nbytes: int, dev: int, stream) -> torch.Tensor:
+    """Scratch for a call that was given none.  Eager calls on the current stream
+    keep one per stream, grown as needed: they use it in stream order, as the
+    memory of a tensor freed and allocated again there would be.  A call on
+    another stream, or one that is being captured (a graph may be replayed
+    beside others), gets memory of its own."""
+    if stream is not None or torch.cuda.is_current_stream_capturing():
+        return _empty((nbytes,), torch.uint8, dev, stream)
+    key = (dev, _raw_stream(dev))
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws
+
+
 def _append(fn, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved, stream, block, dtype, head_dim):
     dev = _cuda_device(k, "k")
     shape = _dims(k, "k", 3)
@@ -552,10 +570,10 @@ def kv_gather_q4(k_pool, v_pool, page_table, start, length, n, k_out=None, v_out
     L, P, H, _ = pool
     B, max_pages = _dims(page_table, "page_table", 2)
     i32, u8, bf, shape = torch.int32, torch.uint8, torch.bfloat16, (L, B, H, n, 128)
-    if k_out is None and v_out is None:
-        k_out, v_out = _empty((2, *shape), bf, dev, stream).unbind(0)
-    elif k_out is None or v_out is None:
-        raise ValueError("k_out and v_out are given together")
+    if k_out is None:
+        k_out = _empty(shape, bf, dev, stream)
+    if v_out is None:
+        v_out = _empty(shape, bf, dev, stream)
     pool = (L, P, H, KV_Q4_BYTES)
     _launch("sv_kv_gather_q4", dev, stream, _arg(k_pool, "k_pool", u8, pool, dev), _arg(v_pool, "v_pool", u8, pool, dev), P,
             _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, L, B, H,
@@ -583,16 +601,22 @@ def verify_attn_q4(q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent=N
     if out is None:
         out = _empty(rows, bf, dev, stream)
     s = ctypes.byref(_AttnShape(B, R, Hq, H, D, max_pages * KV_PAGE))
-    nbytes = lib.sv_verify_attn_q4_workspace(s)
-    if ws is None:
-        ws = _empty((nbytes,), u8, dev, stream)
+    if torch.cuda.current_device() == dev:
+        nbytes = lib.sv_verify_attn_q4_workspace(s)
+    else:
+        with torch.cuda.device(dev):
+            nbytes = lib.sv_verify_attn_q4_workspace(s)
+    if nbytes == 0:
+        ws = None
+    elif ws is None:
+        ws = _workspace(nbytes, dev, stream)
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
         raise ValueError(f"ws must be contiguous, on cuda:{dev} and hold {nbytes} bytes")
     _launch("sv_verify_attn_q4", dev, stream, s, _arg(q, "q", bf, rows, dev), _arg(k_pool, "k_pool", u8, pool, dev),
             _arg(v_pool, "v_pool", u8, pool, dev), P, _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages,
             _arg(length, "length", i32, (B,), dev), _arg(k_blk, "k_blk", bf, blk, dev), _arg(v_blk, "v_blk", bf, blk, dev),
             _arg(parent, "parent", i32, (B, R), dev), D ** -0.5 if scale is None else float(scale),
-            _arg(out, "out", bf, rows, dev), ws.data_ptr() if nbytes else None, nbytes,
+            _arg(out, "out", bf, rows, dev), None if ws is None else ws.data_ptr(), nbytes,
             ATTN_CACHE_READY if cache_ready else 0)
     return out
 
