@@ -1,20 +1,22 @@
-"""Thin ctypes binding over libsv.so (the C ABI in include/sv.h).
+"""Thin binding over libsv.so (the C ABI in include/sv.h): ctypes, and for the
+cache and logits calls a CPython extension (csrc/py_calls.cpp).
 
 Argument marshalling only: every step of the verify round runs in the
 library's CUDA kernels.  Tensors must be CUDA tensors of the stated dtype,
 contiguous; workspaces are allocated with torch when the caller passes none.
-There is no fallback: if the library is missing or fails to load, importing
-this module raises.
+There is no fallback: if the library or the extension is missing or fails to
+load, importing this module raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
 import torch
 
-from .build import LIB
+from .build import CALLS, LIB
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -105,6 +107,19 @@ lib = _load()
 def _check(fn: str, status: int):
     if status != 0:
         raise SVError(fn, status, lib.sv_status_string(status).decode())
+
+
+def _load_calls():
+    if not os.path.exists(CALLS):
+        raise ImportError(f"sv_calls.so not built ({CALLS}); run __graft_entry__.build() first")
+    spec = importlib.util.spec_from_file_location("sv_calls", CALLS)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.set_check(_check)
+    return m
+
+
+calls = _load_calls()
 
 
 def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
@@ -416,117 +431,19 @@ def copy(dst: torch.Tensor, src: torch.Tensor, stream=None) -> torch.Tensor:
 # the paged cache filled, the 4-bit cache, sampling controls
 #
 # These calls know every argument's shape, so they check them all (the C ABI
-# cannot), and launch on the tensors' own device.
+# cannot): TypeError or ValueError before anything is enqueued.  They launch with
+# the tensors' own device current, on `stream` or that device's current stream,
+# and take outputs and workspaces that they are not given from its memory.
 
 KV_Q4_BYTES = 4608   # bytes of one (page, head) of a 4-bit cache (SV_KV_Q4_BYTES)
-ROPE_INTERLEAVED = 1
 
 
-def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
-    """The pointer of an argument (None: NULL), once its type, device, shape and
-    layout are what the call wants."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _cuda_device(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
-
-
-def _dims(t: torch.Tensor, name: str, n: int):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got shape {list(t.shape)}")
-    return t.shape
-
-
-# the current stream's handle, without an object around it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _launch(fn: str, dev: int, stream, *args):
-    """Calls fn(*args, stream) with cuda:`dev` current, on `stream` or on the
-    device's current stream."""
-    if stream is None:
-        handle = _raw_stream(dev)
-    elif stream.device.index != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
-    else:
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
-        status = getattr(lib, fn)(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = getattr(lib, fn)(*args, handle)
-    if status:
-        _check(fn, status)
-
-
-def _rows(t: torch.Tensor, name: str, shape, dev: int):
-    """The pointer and row stride of [N, Hkv, D] bf16 rows that may lie apart."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name} must have shape {list(shape)} on cuda:{dev}, got {list(t.shape)} on {t.device}")
-    n, h, d = shape
-    apart, between, within = t.stride()
-    if (d > 1 and within != 1) or (h > 1 and between != d):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), apart if n > 1 else h * d
-
-
-def _empty(shape, dtype, dev: int, stream):
-    """An output or workspace, taken from the memory of the stream that writes it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _on(stream, like, f, *args):
+    """f(*args) with `stream`, which must be on `like`'s device, current."""
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-_workspaces = {}   # (device, stream handle) -> the largest workspace asked for there
-
-
-def _workspace(nbytes: int, dev: int, stream) -> torch.Tensor:
-    """Scratch for a call that was given none.  Eager calls on the current stream
-    keep one per stream, grown as needed: they use it in stream order, as the
-    memory of a tensor freed and allocated again there would be.  A call on
-    another stream, or one that is being captured (a graph may be replayed
-    beside others), gets memory of its own."""
-    if stream is not None or torch.cuda.is_current_stream_capturing():
-        return _empty((nbytes,), torch.uint8, dev, stream)
-    key = (dev, _raw_stream(dev))
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return ws
-
-
-def _append(fn, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved, stream, block, dtype, head_dim):
-    dev = _cuda_device(k, "k")
-    shape = _dims(k, "k", 3)
-    N, H, _ = shape
-    (kp, ks), (vp, vs) = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
-    B, max_pages = _dims(page_table, "page_table", 2)
-    P = k_pool.shape[0]
-    pool = (P, H) + block
-    i32 = torch.int32
-    positions, rot = (0, 0) if rope is None else _dims(rope, "rope", 2)
-    _launch(fn, dev, stream, kp, vp, ks, vs, N, _arg(row_off, "row_off", i32, (B + 1,), dev), B, H, *head_dim,
-            _arg(rope, "rope", torch.float32, (positions, rot), dev), positions, rot,
-            _arg(k_pool, "k_pool", dtype, pool, dev), _arg(v_pool, "v_pool", dtype, pool, dev), P,
-            _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, _arg(length, "length", i32, (B,), dev),
-            ROPE_INTERLEAVED if interleaved else 0)
+        return f(*args)
 
 
 def kv_append_paged(k, v, row_off, k_pool, v_pool, page_table, length, rope=None, interleaved=False, stream=None):
@@ -535,51 +452,29 @@ def kv_append_paged(k, v, row_off, k_pool, v_pool, page_table, length, rope=None
     pools [num_pages,Hkv,64,D] bf16, page_table [B,max_pages], row_off [B+1],
     length [B] int32 (not advanced).  rope None or [positions,rot] fp32, each
     position's rot/2 cosines, then its sines: K is rotated on the way."""
-    _append("sv_kv_append_paged", k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved, stream,
-            (KV_PAGE, k.shape[-1]), torch.bfloat16, [k.shape[-1]])
+    args = (False, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
+    calls.kv_append(*args) if stream is None else _on(stream, k, calls.kv_append, *args)
 
 
 def kv_append_q4(k, v, row_off, k_pool, v_pool, page_table, length, rope=None, interleaved=False, stream=None):
     """kv_append_paged into 4-bit pools [num_pages,Hkv,4608] uint8 (D = 128)."""
-    if k.shape[-1] != 128:
-        raise ValueError(f"a 4-bit cache holds rows of 128 dims, got {k.shape[-1]}")
-    _append("sv_kv_append_q4", k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved, stream,
-            (KV_Q4_BYTES,), torch.uint8, [])
+    args = (True, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
+    calls.kv_append(*args) if stream is None else _on(stream, k, calls.kv_append, *args)
 
 
 def kv_commit_q4(k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length, stream=None):
     """pools [L,num_pages,Hkv,4608] uint8; page_table [B,max_pages]; blocks [L,B,Hkv,R,128] bf16;
     path [B,R], n_acc [B], length [B] int32 (length updated in place)."""
-    dev = _cuda_device(k_blk, "k_blk")
-    L, B, H, R, _ = _dims(k_blk, "k_blk", 5)
-    max_pages = _dims(page_table, "page_table", 2)[1]
-    P = _dims(k_pool, "k_pool", 4)[1]
-    i32, u8, bf, pool, blk = torch.int32, torch.uint8, torch.bfloat16, (L, P, H, KV_Q4_BYTES), (L, B, H, R, 128)
-    _launch("sv_kv_commit_q4", dev, stream, _arg(k_pool, "k_pool", u8, pool, dev), _arg(v_pool, "v_pool", u8, pool, dev), P,
-            _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, _arg(k_blk, "k_blk", bf, blk, dev),
-            _arg(v_blk, "v_blk", bf, blk, dev), L, B, H, R, _arg(path, "path", i32, (B, R), dev),
-            _arg(n_acc, "n_acc", i32, (B,), dev), _arg(length, "length", i32, (B,), dev))
+    args = (k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length)
+    calls.kv_commit_q4(*args) if stream is None else _on(stream, k_blk, calls.kv_commit_q4, *args)
 
 
 def kv_gather_q4(k_pool, v_pool, page_table, start, length, n, k_out=None, v_out=None, stream=None):
     """Positions start[b] .. start[b]+n-1 of every sequence of 4-bit pools
     [L,num_pages,Hkv,4608] uint8 as bf16 rows, zeros at and past length[b].
     Returns (k_out, v_out) [L,B,Hkv,n,128] bf16."""
-    dev = _cuda_device(k_pool, "k_pool")
-    pool = _dims(k_pool, "k_pool", 4)
-    L, P, H, _ = pool
-    B, max_pages = _dims(page_table, "page_table", 2)
-    i32, u8, bf, shape = torch.int32, torch.uint8, torch.bfloat16, (L, B, H, n, 128)
-    if k_out is None:
-        k_out = _empty(shape, bf, dev, stream)
-    if v_out is None:
-        v_out = _empty(shape, bf, dev, stream)
-    pool = (L, P, H, KV_Q4_BYTES)
-    _launch("sv_kv_gather_q4", dev, stream, _arg(k_pool, "k_pool", u8, pool, dev), _arg(v_pool, "v_pool", u8, pool, dev), P,
-            _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages, L, B, H,
-            _arg(start, "start", i32, (B,), dev), _arg(length, "length", i32, (B,), dev), n,
-            _arg(k_out, "k_out", bf, shape, dev), _arg(v_out, "v_out", bf, shape, dev))
-    return k_out, v_out
+    args = (k_pool, v_pool, page_table, start, length, n, k_out, v_out)
+    return calls.kv_gather_q4(*args) if stream is None else _on(stream, k_pool, calls.kv_gather_q4, *args)
 
 
 def verify_attn_q4_workspace(B, R, Hq, Hkv, D, T_cap) -> int:
@@ -592,33 +487,8 @@ def verify_attn_q4(q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent=N
     """verify_attn_paged over a 4-bit cache: pools [num_pages,Hkv,4608] uint8;
     q [B,R,Hq,128] and blocks [B,Hkv,R,128] bf16; page_table [B,max_pages],
     length [B] int32.  Returns out [B,R,Hq,128] bf16."""
-    dev = _cuda_device(q, "q")
-    rows = _dims(q, "q", 4)
-    B, R, Hq, D = rows
-    P, H, _ = _dims(k_pool, "k_pool", 3)
-    max_pages = _dims(page_table, "page_table", 2)[1]
-    bf, i32, u8, pool, blk = torch.bfloat16, torch.int32, torch.uint8, (P, H, KV_Q4_BYTES), (B, H, R, D)
-    if out is None:
-        out = _empty(rows, bf, dev, stream)
-    s = ctypes.byref(_AttnShape(B, R, Hq, H, D, max_pages * KV_PAGE))
-    if torch.cuda.current_device() == dev:
-        nbytes = lib.sv_verify_attn_q4_workspace(s)
-    else:
-        with torch.cuda.device(dev):
-            nbytes = lib.sv_verify_attn_q4_workspace(s)
-    if nbytes == 0:
-        ws = None
-    elif ws is None:
-        ws = _workspace(nbytes, dev, stream)
-    elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
-        raise ValueError(f"ws must be contiguous, on cuda:{dev} and hold {nbytes} bytes")
-    _launch("sv_verify_attn_q4", dev, stream, s, _arg(q, "q", bf, rows, dev), _arg(k_pool, "k_pool", u8, pool, dev),
-            _arg(v_pool, "v_pool", u8, pool, dev), P, _arg(page_table, "page_table", i32, (B, max_pages), dev), max_pages,
-            _arg(length, "length", i32, (B,), dev), _arg(k_blk, "k_blk", bf, blk, dev), _arg(v_blk, "v_blk", bf, blk, dev),
-            _arg(parent, "parent", i32, (B, R), dev), D ** -0.5 if scale is None else float(scale),
-            _arg(out, "out", bf, rows, dev), None if ws is None else ws.data_ptr(), nbytes,
-            ATTN_CACHE_READY if cache_ready else 0)
-    return out
+    args = (q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent, scale, out, ws, cache_ready)
+    return calls.verify_attn_q4(*args) if stream is None else _on(stream, q, calls.verify_attn_q4, *args)
 
 
 def logits_process(logits, tok=None, parent=None, hist=None, hist_len=None, prompt_len=None, repetition=None,
@@ -630,38 +500,9 @@ def logits_process(logits, tok=None, parent=None, hist=None, hist_len=None, prom
     frequency, presence [B] and bias_val [n] fp32; bias_off [B+1] int32.  out may
     be logits itself.  Returns (out [B,R,V] or None, argmax keys
     [B*R, ceil(V/128)] int64 or None); an argmax buffer implies write_argmax."""
-    dev = _cuda_device(logits, "logits")
-    shape = _dims(logits, "logits", 3)
-    B, R, V = shape
-    f32, i32, S = torch.float32, torch.int32, (V + ARGMAX_SLAB - 1) // ARGMAX_SLAB
-    if not write_logits:
-        out = None
-    elif out is None:
-        out = _empty(shape, f32, dev, stream)
-    if argmax is None and write_argmax:
-        argmax = _empty((B * R, S), torch.int64, dev, stream)
-    cap = nb = 0
-    if hist is not None:
-        if hist_len is None:
-            raise ValueError("hist needs hist_len")
-        cap = _dims(hist, "hist", 2)[1]
-        _arg(hist, "hist", i32, (B, cap), dev)
-        if cap == 0:
-            hist = None
-    if bias_off is not None:
-        if bias_tok is None or bias_val is None:
-            raise ValueError("bias_off needs bias_tok and bias_val")
-        nb = _dims(bias_tok, "bias_tok", 1)[0]
-    _launch("sv_logits_process", dev, stream, _arg(logits, "logits", f32, shape, dev), B, R, V,
-            _arg(hist, "hist", i32, (B, cap), dev), cap, _arg(hist_len, "hist_len", i32, (B,), dev),
-            _arg(prompt_len, "prompt_len", i32, (B,), dev), _arg(tok, "tok", i32, (B, R), dev),
-            _arg(parent, "parent", i32, (B, R), dev), _arg(repetition, "repetition", f32, (B,), dev),
-            _arg(frequency, "frequency", f32, (B,), dev), _arg(presence, "presence", f32, (B,), dev),
-            _arg(bias_off, "bias_off", i32, (B + 1,), dev), _arg(bias_tok, "bias_tok", i32, (nb,), dev),
-            _arg(bias_val, "bias_val", f32, (nb,), dev), nb, _arg(mask, "mask", i32, (B, R, (V + 31) // 32), dev),
-            float(mask_value), _arg(out, "out", f32, shape, dev), _arg(argmax, "argmax", torch.int64, (B * R, S), dev),
-            B * R * S * 8 if argmax is not None else 0)
-    return out, argmax
+    args = (logits, tok, parent, hist, hist_len, prompt_len, repetition, frequency, presence, bias_off, bias_tok, bias_val,
+            mask, mask_value, out, argmax, write_logits, write_argmax)
+    return calls.logits_process(*args) if stream is None else _on(stream, logits, calls.logits_process, *args)
 
 
 def get_device_error(stream=None) -> int:

@@ -1,8 +1,11 @@
-"""Builds libsv.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libsv.so in-tree with nvcc for sm_103a (GB300), and the Python
+extension over it.
 
 Each .cu file under csrc/ is compiled in parallel to an object, then linked
 into one shared library with the CUDA runtime linked statically, so the
-library only needs the driver at run time.  Output: csrc/_build/libsv.so.
+library only needs the driver at run time.  csrc/py_calls.cpp is compiled
+beside them against the installed torch.  Output: csrc/_build/libsv.so and
+csrc/_build/sv_calls.so.
 """
 from __future__ import annotations
 
@@ -11,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,6 +23,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 DEBUG = os.environ.get("SV_DEBUG", "") == "1"
 OUT_DIR = os.path.join(CSRC, "_build_debug" if DEBUG else "_build")
 LIB = os.path.join(OUT_DIR, "libsv.so")
+CALLS = os.path.join(OUT_DIR, "sv_calls.so")
+CALLS_SRC = os.path.join(CSRC, "py_calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -48,6 +54,23 @@ def _stale(target, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _calls_compile(obj):
+    import torch   # the headers and the ABI that the extension has to match
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    inc = [root, os.path.join(root, "torch", "csrc", "api", "include"), cuda, sysconfig.get_paths()["include"], INCLUDE]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + \
+        [x for d in inc for x in ("-isystem" if d != INCLUDE else "-I", d)] + ["-c", CALLS_SRC, "-o", obj]
+
+
+def _calls_link(obj, out):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-shared", "-o", out, obj, "-L", OUT_DIR, "-lsv", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN:" + lib]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -61,20 +84,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if force or _stale(obj, [src] + headers):
             jobs.append([nvcc] + ARCH + flags + ["-c", src, "-o", obj])
 
+    calls_obj = os.path.join(OUT_DIR, "py_calls.o")
+    calls = force or _stale(calls_obj, [CALLS_SRC, os.path.join(INCLUDE, "sv.h")])
+    if calls:
+        jobs.insert(0, _calls_compile(calls_obj))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed: " + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("compilation failed: " + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
 
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
+    if force or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs + ["-ldl", "-lpthread", "-lrt"])
         os.replace(tmp, LIB)
+    if force or _stale(CALLS, [calls_obj]):
+        run(_calls_link(calls_obj, CALLS + ".tmp"))
+        os.replace(CALLS + ".tmp", CALLS)
     return LIB
 
 
