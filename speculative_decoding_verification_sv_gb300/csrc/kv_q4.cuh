@@ -59,32 +59,43 @@ __device__ __forceinline__ float q4_scale(float amax) {
 }
 
 // code of x given the group's scale s and rs = 1 / s rounded to nearest
-// (0 when s is 0 or NaN: the code is then 8, the value 0 or NaN).  x / s is
-// Markstein's correction of x rs, which rounds as the division does wherever
-// the quotient is not negligible; the clamped quotient plus 1.5 * 2^23 + 8
-// leaves 8 + rint in the low bits (8 is even: ties still go to even).
+// (0 when s is 0 or NaN: the code is then 8, the value 0 or NaN), on top of
+// kQ4CodeBase.  x / s is Markstein's correction of x rs, which rounds as the
+// division does wherever the quotient is not negligible; the clamped quotient
+// plus 1.5 * 2^23 + 8 leaves 8 + rint above the bits of 1.5 * 2^23 (8 is even:
+// ties still go to even). 
+constexpr uint32_t kQ4CodeBase = 0x4B400000u;
 __device__ __forceinline__ uint32_t q4_code(float x, float s, float rs) {
     const float q = __fmul_rn(x, rs);
     const float d = __fmaf_rn(__fmaf_rn(-q, s, x), rs, q);
     const float c = __fadd_rn(fminf(fmaxf(d, -7.0f), 7.0f), 12582920.0f);
-    return rs == 0.0f ? 8u : (__float_as_uint(c) & 15u);
+    return rs == 0.0f ? kQ4CodeBase + 8u : __float_as_uint(c);
 }
-
 __device__ __forceinline__ float bf16_bits_f32(uint32_t b) { return __uint_as_float(b << 16); }
 __device__ __forceinline__ uint16_t f32_bf16_bits(float x) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// Four consecutive dims of a row in a lane (dims 4 lane ..), eight lanes a
-// group: the lane's codes and the group's scale.
-__device__ __forceinline__ void q4_quantise4(const float (&x)[4], uint32_t (&c)[4], float& s) {
-    float a = q4_amax(q4_amax(x[0], x[1]), q4_amax(x[2], x[3]));
+// Eight rows, four consecutive dims of each in a lane (dims 4 lane ..), eight
+// lanes a group.  Every lane ends up with the scale of row lane & 7 of its
+// group, so that the division and the reciprocal are done once a lane: a
+// reduction that halves the rows a lane holds with every step.
+__device__ __forceinline__ void q4_scales8(const float (&x)[8][4], float& s, float& rs) {
+    const int lane = threadIdx.x & 31;
+    float a[8];
 #pragma unroll
-    for (int off = 1; off < 8; off <<= 1) a = q4_amax(a, __shfl_xor_sync(0xffffffffu, a, off));
-    s = q4_scale(a);
-    const float rs = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    for (int i = 0; i < 8; ++i) a[i] = q4_amax(q4_amax(x[i][0], x[i][1]), q4_amax(x[i][2], x[i][3]));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = q4_code(x[e], s, rs);
+    for (int half = 4; half > 0; half >>= 1) {
+        const bool up = (lane & half) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + half], half);
+            a[i] = q4_amax(up ? a[i + half] : a[i], other);
+        }
+    }
+    s = q4_scale(a[0]);
+    rs = s > 0.0f ? __frcp_rn(s) : 0.0f;
 }
 
 }  // namespace sv

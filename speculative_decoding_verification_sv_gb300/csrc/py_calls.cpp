@@ -18,6 +18,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <array>
 #include <cmath>
 #include <map>
 #include <mutex>
@@ -258,6 +259,17 @@ Output output(const Args& a, PyObject* o, const char* name, at::ScalarType type,
     return {p, std::move(r)};
 }
 
+// A tensor of its own over part of another's memory.
+Output half_of(const at::Tensor& both, at::IntArrayRef shape, int64_t offset) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(both.storage()), both.key_set(), both.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(offset);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    void* p = t.data_ptr();
+    THPObjectPtr r(THPVariable_Wrap(std::move(t)));
+    if (!r) throw python_error();
+    return {p, std::move(r)};
+}
+
 // (k_pool, v_pool, page_table, start, length, n, k_out, v_out) -> (k_out, v_out)
 PyObject* kv_gather_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -274,8 +286,16 @@ PyObject* kv_gather_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const int32_t* tab = a.ints(o[2], "page_table", {B, max_pages});
     const int32_t* start = a.ints(o[3], "start", {B});
     const int32_t* len = a.ints(o[4], "length", {B});
-    Output k = output(a, o[6], "k_out", at::kBFloat16, {L, B, H, count, 128});
-    Output v = output(a, o[7], "v_out", at::kBFloat16, {L, B, H, count, 128});
+    const std::array<int64_t, 5> shape{L, B, H, count, 128};
+    Output k, v;
+    if (o[6] == Py_None && o[7] == Py_None) {   // both from one allocation
+        const at::Tensor both = a.empty({2, L, B, H, count, 128}, at::kBFloat16);
+        k = half_of(both, shape, 0);
+        v = half_of(both, shape, both.numel() / 2);
+    } else {
+        k = output(a, o[6], "k_out", at::kBFloat16, shape);
+        v = output(a, o[7], "v_out", at::kBFloat16, shape);
+    }
     enqueue("sv_kv_gather_q4", [&] {
         return sv_kv_gather_q4(kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), size32(L, "L"),
                                size32(B, "B"), size32(H, "Hkv"), start, len, n32, static_cast<uint16_t*>(k.ptr),

@@ -439,7 +439,7 @@ sv_status sv_kv_append_q4(const uint16_t* k, const uint16_t* v, int64_t k_stride
     const sv_status s = append_args(a, k, v, k_stride, v_stride, N, row_off, B, Hkv, 128, rope, rope_positions, rot,
                                     k_pool, v_pool, num_pages, page_table, max_pages, len, flags);
     if (s != SV_OK) return s;
-    if (sv::append_q4_items(N, B, Hkv) / 8 >= 2147483647) return SV_ERR_SHAPE;
+    if (sv::append_q4_items(N, B, Hkv) >= 2147483647) return SV_ERR_SHAPE;
     return launch_status(sv::launch_append_q4(a, static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool),
                                               as_stream(stream)));
 }
@@ -468,7 +468,7 @@ sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t num_pa
     if (L < 1 || B < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1 || n > (1 << 30)) return SV_ERR_SHAPE;
     if (static_cast<int64_t>(max_pages) * SV_KV_PAGE > 2147483647) return SV_ERR_SHAPE;
     if (static_cast<int64_t>(L) * B > (1 << 30) || static_cast<int64_t>(L) * B * Hkv > (int64_t(1) << 31) ||
-        sv::gather_q4_items(L, B, Hkv, n) / 8 >= 2147483647)
+        sv::gather_q4_items(L, B, Hkv, n) >= 2147483647)
         return SV_ERR_SHAPE;
     return launch_status(sv::launch_gather_q4(static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), L,
                                               B, Hkv, start, len, n, page_table, max_pages, num_pages, k_out, v_out,
