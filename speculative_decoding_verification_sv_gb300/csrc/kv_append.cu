@@ -4,7 +4,11 @@
 // A prompt, a prefill chunk or single decoded tokens: N rows of B sequences,
 // sequence b's being rows row_off[b] .. row_off[b + 1], at the positions from
 // len[b] on.  Pure movement: 1 KB read and 1 KB written per row and pair of KV
-// heads, bound by HBM for prompts and by latency for single tokens.
+// heads.  Bound by the chain of loads that finds a row's place (offsets, length,
+// page), three rounds of warps an SM deep for a long prompt: 8 x 2048 rows of 4
+// heads take 13.9 us (4.6 TB/s), 64 single tokens 2.7 us.  With the row sent for
+// only after its place was known it was 16.1 us; with more warps an SM (48, for
+// spills) 15.1 us; a thread a 16-byte piece in place of a warp a row 26 us.
 #include "kv_append.cuh"
 #include "sv_internal.h"
 
@@ -29,9 +33,9 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                       pack_bf16x2(x[6], x[7]));
 }
 
-// One warp a row.  V moves in 16-byte pieces, and while those loads are on their
-// way the lanes turn K: 16 bytes of the first half of a pair and 16 of the
-// second (half split), or 16 bytes of pairs, then the dims that stay.
+// One warp a row, in 16-byte pieces.  K is turned by 16 bytes of the first half of
+// a pair and 16 of the second (half split), or 16 bytes of pairs; then the dims that
+// stay.
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, uint16_t* __restrict__ k_pool,
                                                              uint16_t* __restrict__ v_pool) {
     pdl_wait();
@@ -39,6 +43,28 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, uint1
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (row >= a.N) return;
+    // the row itself is sent for before its place is known
+    const uint16_t* vrow = a.v + static_cast<int64_t>(row) * a.v_stride;
+    const uint16_t* krow = a.k + static_cast<int64_t>(row) * a.k_stride;
+    const int per = a.D / 8, pieces = a.Hkv * per;
+    const int rot = a.rope ? a.rot : 0, half = rot / 2;
+    const int turned = a.interleaved ? rot / 8 : half / 8, kper = turned + (a.D - rot) / 8;
+    const bool split = !a.interleaved;   // a piece's pairs: 16 bytes here, 16 bytes half a rotation on
+    uint4 v[kAhead], k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0;
+    auto load_v = [&](int x0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (x0 + 32 * u < pieces) v[u] = __ldg(reinterpret_cast<const uint4*>(vrow) + x0 + 32 * u);
+    };
+    auto load_k = [&](int x) {
+        if (x >= a.Hkv * kper) return;
+        const int h = x / kper, c = x - h * kper;
+        const uint16_t* src = krow + h * a.D + (c < turned ? c * 8 : rot + (c - turned) * 8);
+        k0 = __ldg(reinterpret_cast<const uint4*>(src));
+        if (split && c < turned) k1 = __ldg(reinterpret_cast<const uint4*>(src + half));
+    };
+    load_k(lane);
+    load_v(lane);
     // the row's place: its sequence, position and page
     const int b = warp_last_at_most(a.B, row, [&](int i) { return static_cast<int64_t>(__ldg(a.row_off + i)); });
     if (b < 0) return;
@@ -62,59 +88,46 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, uint1
     }
     const int64_t head_stride = static_cast<int64_t>(kPage) * a.D;   // of a page
     const int64_t dst = (static_cast<int64_t>(pg) * a.Hkv * kPage + pos % kPage) * a.D;
-    const uint16_t* vrow = a.v + static_cast<int64_t>(row) * a.v_stride;
-    const uint16_t* krow = a.k + static_cast<int64_t>(row) * a.k_stride;
-    const int per = a.D / 8, pieces = a.Hkv * per;
-
-    for (int x0 = lane; x0 < pieces; x0 += 32 * kAhead) {
-        uint4 v[kAhead];
+    const float* cs = a.rope + static_cast<size_t>(pos) * rot;
+    for (int x = lane; x < a.Hkv * kper; x += 32) {
+        if (x != lane) load_k(x);
+        const int h = x / kper, c = x - h * kper;
+        const int d = c < turned ? c * 8 : rot + (c - turned) * 8;
+        uint4* to = reinterpret_cast<uint4*>(k_pool + dst + h * head_stride + d);
+        float y[8], z[8];
+        if (c >= turned) {
+            *to = k0;
+        } else if (!split) {
+            const float4 co = __ldg(reinterpret_cast<const float4*>(cs + d / 2));
+            const float4 si = __ldg(reinterpret_cast<const float4*>(cs + half + d / 2));
+            unpack8(k0, y);
+            rope_turn(y[0], y[1], co.x, si.x);
+            rope_turn(y[2], y[3], co.y, si.y);
+            rope_turn(y[4], y[5], co.z, si.z);
+            rope_turn(y[6], y[7], co.w, si.w);
+            *to = pack8(y);
+        } else {
+            float4 co[2], si[2];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (x0 + 32 * u < pieces) v[u] = __ldg(reinterpret_cast<const uint4*>(vrow) + x0 + 32 * u);
-        if (x0 == lane) {   // K, under the first loads of V
-            const int rot = a.rope ? a.rot : 0, half = rot / 2;
-            const float* cs = a.rope + static_cast<size_t>(pos) * rot;
-            const int turned = a.interleaved ? rot / 8 : half / 8, kper = turned + (a.D - rot) / 8;
-            for (int x = lane; x < a.Hkv * kper; x += 32) {
-                const int h = x / kper, c = x - h * kper;
-                const int d = c < turned ? c * 8 : rot + (c - turned) * 8;
-                const uint16_t* src = krow + h * a.D + d;
-                uint4* to = reinterpret_cast<uint4*>(k_pool + dst + h * head_stride + d);
-                float y[8], z[8];
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
-                if (c >= turned) {
-                    *to = w;
-                } else if (a.interleaved) {
-                    const float4 co = __ldg(reinterpret_cast<const float4*>(cs + d / 2));
-                    const float4 si = __ldg(reinterpret_cast<const float4*>(cs + half + d / 2));
-                    unpack8(w, y);
-                    rope_turn(y[0], y[1], co.x, si.x);
-                    rope_turn(y[2], y[3], co.y, si.y);
-                    rope_turn(y[4], y[5], co.z, si.z);
-                    rope_turn(y[6], y[7], co.w, si.w);
-                    *to = pack8(y);
-                } else {
-                    const uint4 w2 = __ldg(reinterpret_cast<const uint4*>(src + half));
-                    float4 co[2], si[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        co[e] = __ldg(reinterpret_cast<const float4*>(cs + d) + e);
-                        si[e] = __ldg(reinterpret_cast<const float4*>(cs + half + d) + e);
-                    }
-                    unpack8(w, y);
-                    unpack8(w2, z);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        rope_turn(y[4 * e], z[4 * e], co[e].x, si[e].x);
-                        rope_turn(y[4 * e + 1], z[4 * e + 1], co[e].y, si[e].y);
-                        rope_turn(y[4 * e + 2], z[4 * e + 2], co[e].z, si[e].z);
-                        rope_turn(y[4 * e + 3], z[4 * e + 3], co[e].w, si[e].w);
-                    }
-                    *to = pack8(y);
-                    *reinterpret_cast<uint4*>(k_pool + dst + h * head_stride + d + half) = pack8(z);
-                }
+            for (int e = 0; e < 2; ++e) {
+                co[e] = __ldg(reinterpret_cast<const float4*>(cs + d) + e);
+                si[e] = __ldg(reinterpret_cast<const float4*>(cs + half + d) + e);
             }
+            unpack8(k0, y);
+            unpack8(k1, z);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                rope_turn(y[4 * e], z[4 * e], co[e].x, si[e].x);
+                rope_turn(y[4 * e + 1], z[4 * e + 1], co[e].y, si[e].y);
+                rope_turn(y[4 * e + 2], z[4 * e + 2], co[e].z, si[e].z);
+                rope_turn(y[4 * e + 3], z[4 * e + 3], co[e].w, si[e].w);
+            }
+            *to = pack8(y);
+            *reinterpret_cast<uint4*>(k_pool + dst + h * head_stride + d + half) = pack8(z);
         }
+    }
+    for (int x0 = lane; x0 < pieces; x0 += 32 * kAhead) {
+        if (x0 != lane) load_v(x0);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int x = x0 + 32 * u;
