@@ -115,12 +115,12 @@ __device__ __forceinline__ int active_ctas(int W, int grid) { return max(1, min(
 __device__ __forceinline__ int cta_first(int W, int i, int n) {
     return static_cast<int>(static_cast<int64_t>(W) * i / n);
 }
-// the CTA whose run holds page x
+// The CTA whose run holds page x: the largest i with floor(W i / n) <= x, that is
+// W i < (x + 1) n.
 __device__ __forceinline__ int cta_of(int W, int x, int n) {
-    int i = static_cast<int>((static_cast<int64_t>(x) * n) / W);
-    while (cta_first(W, i + 1, n) <= x) ++i;
-    while (cta_first(W, i, n) > x) --i;
-    return i;
+    const int64_t most = (static_cast<int64_t>(x) + 1) * n - 1;
+    return most < (int64_t(1) << 32) ? static_cast<int>(static_cast<uint32_t>(most) / static_cast<uint32_t>(W))
+                                     : static_cast<int>(most / W);
 }
 
 // The runs of this CTA, unit by unit; every warp walks them by itself.
@@ -897,6 +897,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int np = ctx_pages(ctx_len(a, b));
     const int w0 = sums.y * wk.U + (g * wk.row_tiles + rt) * (np + 1), w1 = w0 + np + 1;
     const int i0 = cta_of(W, w0, n), i1 = cta_of(W, w1 - 1, n);
+    const bool later = static_cast<int64_t>(w0) * n > static_cast<int64_t>(W) * i0;   // w0 is past CTA i0's first page
     if (i0 == i1) return;   // one CTA had the whole unit and wrote its rows
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(kCombineThreads)
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i > i1) continue;
             // a unit that starts inside CTA i0's run is its second partial
-            const int slot = i == i0 && w0 > cta_first(W, i0, n) ? 1 : 0;
+            const int slot = i == i0 && later ? 1 : 0;
             const float* rec = ws + (static_cast<size_t>(i) * 2 + slot) * kRecFloats;
             ml[u] = __ldcg(reinterpret_cast<const float2*>(rec + kRows * kQ4D + 2 * r));
             o[u] = __ldcg(reinterpret_cast<const float4*>(rec + r * kQ4D) + lane);
