@@ -34,12 +34,16 @@
 // K, 4 unpack V, one issues the copies (two pages of K and V, 18 KB, a ring
 // stage: each (page, head) is one 4608-byte bulk copy), one the MMAs, one brings
 // the query rows of the next run while the present one is worked on.
+#include <cooperative_groups.h>
 #include <math.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "kv_q4.cuh"
 #include "sv_internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace sv {
 namespace {
@@ -54,6 +58,8 @@ constexpr int kGrain = 4;                 // pages a CTA takes at least (where t
 constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 256;
+constexpr int kMaxCluster = 8;
+constexpr int kJoinPages = 9, kClusterPages = 2;   // (see plan)
 
 // TMEM columns: two K operands, two V operands (64 columns: 128 bf16 each), two
 // S^T, one O^T
@@ -83,6 +89,7 @@ struct Work {
     int U;         // units of a sequence: Hkv * row tiles
     int row_tiles;
     int tile_rows; // rows of a tile but the last
+    int cluster;   // CTAs of a unit where each unit has a cluster, 0 where the pages are split evenly
     int inv_g;     // ceil(2^16 / G): r * inv_g >> 16 is r / G for every row r < 2048 of G <= 16
 };
 
@@ -170,6 +177,15 @@ struct Walk {
         np = ctx_pages(t);
         unit = (pos - base) / (np + 1);
         off = (pos - base) % (np + 1);
+    }
+    // Unit u's pages for CTA `rank` of the cluster that has the unit.
+    __device__ __forceinline__ void start_unit(const AttnQ4Args& a, const Work& w, int u, int rank) {
+        b = u / w.U;
+        unit = u - b * w.U;
+        t = ctx_len(a, b);
+        np = ctx_pages(t);
+        pos = off = static_cast<int>(static_cast<int64_t>(np + 1) * rank / w.cluster);
+        end = static_cast<int>(static_cast<int64_t>(np + 1) * (rank + 1) / w.cluster);
     }
     __device__ __forceinline__ bool next(const AttnQ4Args& a, const Work& w) {
         if (pos >= end) return false;
@@ -271,9 +287,48 @@ __device__ __forceinline__ void fold_sums(float (&v)[kN]) {
     fold_sums_step<kN>(v);
 }
 
+// Joins n partials of a row, eight in flight; get(i, ml, o) loads the i-th's
+// (m, l) and the lane's four dims of its O.
+template <typename Get>
+__device__ __forceinline__ void join_row(int n, Get&& get, uint16_t* dst) {
+    const int lane = threadIdx.x & 31;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < n; c0 += 8) {
+        float2 ml[8];
+        float4 o[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c0 + u < n) get(c0 + u, ml[u], o[u]);
+        }
+        float mn = M;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
+        const float c = M == -INFINITY ? 0.f : exp2f(M - mn);
+        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c, L *= c;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
+            const float w = exp2f(ml[u].x - mn);
+            L += w * ml[u].y;
+            acc.x += w * o[u].x;
+            acc.y += w * o[u].y;
+            acc.z += w * o[u].z;
+            acc.w += w * o[u].w;
+        }
+        M = mn;
+    }
+    const float inv = L != 0.f ? 1.0f / L : 0.f;
+    *reinterpret_cast<uint2*>(dst + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
 // kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (their
 // columns of P stay zero)
-template <int kRT>
+template <int kRT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work wk, float* __restrict__ ws) {
     constexpr int kLive = 2 * kRT;
     // (aligned by its declaration: addresses are then constants, not registers)
@@ -344,7 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     const bool early = a.cache_ready;
     if (!early) pdl_wait();
     Walk walk;
-    walk.start(a, wk, blockIdx.x, gridDim.x);
+    const int rank = kCluster ? blockIdx.x % wk.cluster : 0;
+    if constexpr (kCluster) walk.start_unit(a, wk, blockIdx.x / wk.cluster, rank);
+    else walk.start(a, wk, blockIdx.x, gridDim.x);
     volatile int* fail_s = reinterpret_cast<volatile int*>(smem + kOffFail);
     if (threadIdx.x == 0) walk.save(fail_s + 1);
     // Each role runs the CTA's runs once, and once more with `safe` where a sum
@@ -830,7 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             fold_sums(sums);
             if (kRT == 16) sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
             if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sums[0];
-            float* rec = walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
+            // (a cluster's partials stay on chip: the copies into the ring have all been read)
+            float* rec = kCluster ? reinterpret_cast<float*>(smem + kOffRing)
+                         : walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
             soft_sync();
             bool bad = false;
             if (tid < kLive) {
@@ -850,7 +909,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 if (rec) {   // (rows past the tile's last are written too, and never read)
                     float* dst = rec + (hh * kRT + c0) * kQ4D + l;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) __stcg(dst + e * kQ4D, __uint_as_float(o[e]));
+                    for (int e = 0; e < 16; ++e) {
+                        if constexpr (kCluster) dst[e * kQ4D] = __uint_as_float(o[e]);
+                        else __stcg(dst + e * kQ4D, __uint_as_float(o[e]));
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -862,6 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
 #pragma unroll
                 for (int e = 0; e < 16; ++e) bad |= !(fabsf(__uint_as_float(o[e])) < INFINITY);
             }
+            if constexpr (kCluster) fence_proxy_async_smem();   // (copies may be made there again)
             if (bad) *fail_s = 1;
             part = 1;   // a partial run that is not the CTA's first is its last
             tc_fence_before();
@@ -870,8 +933,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             ++seg;
         }
         } while (again());
+        if constexpr (kCluster) {   // no page of the unit fell to this CTA
+            if (seg == 0 && tid < kRows)
+                *reinterpret_cast<float2*>(smem + kOffRing + (kRows * kQ4D + 2 * tid) * 4) = make_float2(-INFINITY, 0.f);
+        }
     }
     __syncwarp();
+    if constexpr (kCluster) {
+        cluster_sync_warp();   // every CTA's partial is there
+        cg::cluster_group cluster = cg::this_cluster();
+        const int u = blockIdx.x / wk.cluster, b = u / wk.U, ub = u - b * wk.U, g = ub / wk.row_tiles;
+        const int row0 = (ub - g * wk.row_tiles) * wk.tile_rows, nrows = min(wk.tile_rows, a.R * a.G - row0);
+        for (int r = rank + wk.cluster * warp; r < nrows; r += wk.cluster * (kThreads / 32)) {
+            const int gr = row0 + r, j = gr * wk.inv_g >> 16;
+            auto get = [&](int i, float2& ml, float4& o) {
+                const float* rec = reinterpret_cast<const float*>(cluster.map_shared_rank(smem + kOffRing, i));
+                ml = *reinterpret_cast<const float2*>(rec + kRows * kQ4D + 2 * r);
+                o = *(reinterpret_cast<const float4*>(rec + r * kQ4D) + lane);
+            };
+            join_row(wk.cluster, get, a.out + (static_cast<size_t>(b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ4D);
+        }
+        __syncwarp();
+        cluster_sync_warp();   // this CTA's partial has been read
+    }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -881,8 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     }
 }
 
-// Joins the partial rows of the units that lie in several CTAs' runs: a warp a
-// row, a lane four dims, eight partials in flight.
+// Joins the partial rows of the units that lie in several CTAs' runs, a warp a row.
 __global__ void __launch_bounds__(kCombineThreads)
     combine_q4_kernel(AttnQ4Args a, Work wk, const float* __restrict__ ws, int grid) {
     pdl_wait();
@@ -899,49 +982,18 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int i0 = cta_of(W, w0, n), i1 = cta_of(W, w1 - 1, n);
     const bool later = static_cast<int64_t>(w0) * n > static_cast<int64_t>(W) * i0;   // w0 is past CTA i0's first page
     if (i0 == i1) return;   // one CTA had the whole unit and wrote its rows
-    float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = i0; c0 <= i1; c0 += 8) {
-        float2 ml[8];
-        float4 o[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = c0 + u;
-            ml[u] = make_float2(-INFINITY, 0.f);
-            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i > i1) continue;
-            // a unit that starts inside CTA i0's run is its second partial
-            const int slot = i == i0 && later ? 1 : 0;
-            const float* rec = ws + (static_cast<size_t>(i) * 2 + slot) * kRecFloats;
-            ml[u] = __ldcg(reinterpret_cast<const float2*>(rec + kRows * kQ4D + 2 * r));
-            o[u] = __ldcg(reinterpret_cast<const float4*>(rec + r * kQ4D) + lane);
-        }
-        float mn = M;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
-        const float c = M == -INFINITY ? 0.f : exp2f(M - mn);
-        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c, L *= c;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
-            const float w = exp2f(ml[u].x - mn);
-            L += w * ml[u].y;
-            acc.x += w * o[u].x;
-            acc.y += w * o[u].y;
-            acc.z += w * o[u].z;
-            acc.w += w * o[u].w;
-        }
-        M = mn;
-    }
-    const float inv = L != 0.f ? 1.0f / L : 0.f;
-    uint16_t* dst = a.out + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D + 4 * lane;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    auto get = [&](int i, float2& ml, float4& o) {
+        // a unit that starts inside CTA i0's run is its second partial
+        const float* rec = ws + (static_cast<size_t>(i0 + i) * 2 + (i == 0 && later ? 1 : 0)) * kRecFloats;
+        ml = __ldcg(reinterpret_cast<const float2*>(rec + kRows * kQ4D + 2 * r));
+        o = __ldcg(reinterpret_cast<const float4*>(rec + r * kQ4D) + lane);
+    };
+    join_row(i1 - i0 + 1, get,
+             a.out + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D);
 }
 
 Work work_of(int R, int G, int Hkv) {
-    Work w;
+    Work w{};
     const int rows = R * G;
     w.row_tiles = (rows + kRows - 1) / kRows;
     w.tile_rows = (rows + w.row_tiles - 1) / w.row_tiles;
@@ -950,36 +1002,103 @@ Work work_of(int R, int G, int Hkv) {
     return w;
 }
 
-int grid_of(const Work& w, int B, int max_pages) {
-    const int64_t most = static_cast<int64_t>(B) * w.U * (static_cast<int64_t>(max_pages) + 1) / kGrain;
+template <int kRT, bool kCluster>
+cudaError_t prepare() {
+    static PerDeviceOnce once;
+    return once.run([]() {
+        return cudaFuncSetAttribute(attn_q4_kernel<kRT, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    });
+}
+
+// Clusters of c CTAs (one an SM) that can be resident at once; 0 where that cannot be asked.
+int resident_clusters(int c) {
+    static std::mutex mu;
+    static int cache[64][kMaxCluster + 1] = {};   // + 1
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return 0;
+    }
+    std::lock_guard<std::mutex> lk(mu);
+    if (cache[dev][c]) return cache[dev][c] - 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (prepare<32, true>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, attn_q4_kernel<32, true>, &cfg) != cudaSuccess)
+        n = 0;
+    cudaGetLastError();
+    cache[dev][c] = n + 1;
+    return n;
+}
+
+// How the work is split, in pages that the busiest CTA takes: evenly over the SMs
+// and joined by a second kernel, or a cluster of 2, 4 or 8 CTAs for each unit, joined
+// on chip.  The second kernel and the partials' way through L2 cost about kJoinPages, the
+// cluster's barriers and remote reads kClusterPages.
+void plan(Work& w, int B, int max_pages, int& grid) {
+    const int64_t units = static_cast<int64_t>(B) * w.U, pages = units * (static_cast<int64_t>(max_pages) + 1);
     const int sms = device_sm_count();
-    return static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
+    const int64_t most = pages / kGrain;
+    grid = static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
+    w.cluster = 0;
+    int64_t best = (pages + grid - 1) / grid + (grid > 1 ? kJoinPages : 0);
+    for (int c = kMaxCluster; c >= 2; c /= 2) {
+        const int64_t cost = (max_pages + c) / c + kClusterPages;
+        if (cost >= best || units > resident_clusters(c)) continue;
+        best = cost;
+        w.cluster = c;
+    }
+    if (w.cluster) grid = static_cast<int>(units) * w.cluster;
 }
 
 template <int kRT>
 cudaError_t launch_rt(const AttnQ4Args& a, const Work& w, int grid, float* ws, cudaStream_t st) {
-    static PerDeviceOnce once;
-    const cudaError_t e = once.run([]() {
-        return cudaFuncSetAttribute(attn_q4_kernel<kRT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    });
+    if (w.cluster == 0) {
+        const cudaError_t e = prepare<kRT, false>();
+        if (e != cudaSuccess) return e;
+        return launch_pdl(attn_q4_kernel<kRT, false>, dim3(grid), dim3(kThreads), kSmemBytes, st, a, w, ws);
+    }
+    const cudaError_t e = prepare<kRT, true>();
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_q4_kernel<kRT>, dim3(grid), dim3(kThreads), kSmemBytes, st, a, w, ws);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = w.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, attn_q4_kernel<kRT, true>, a, w, ws);
 }
 
 }  // namespace
 
 size_t attn_q4_workspace(const sv_attn_shape& s) {
-    const Work w = work_of(s.R, s.Hq / s.Hkv, s.Hkv);
-    const int grid = grid_of(w, s.B, (s.T_cap + kQ4Page - 1) / kQ4Page);
-    return grid > 1 ? static_cast<size_t>(grid) * 2 * kRecFloats * sizeof(float) : 0;
+    Work w = work_of(s.R, s.Hq / s.Hkv, s.Hkv);
+    int grid;
+    plan(w, s.B, (s.T_cap + kQ4Page - 1) / kQ4Page, grid);
+    return grid > 1 && w.cluster == 0 ? static_cast<size_t>(grid) * 2 * kRecFloats * sizeof(float) : 0;
 }
 
 cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st) {
-    const Work w = work_of(a.R, a.G, a.Hkv);
-    const int grid = grid_of(w, a.B, a.max_pages);
+    Work w = work_of(a.R, a.G, a.Hkv);
+    int grid;
+    plan(w, a.B, a.max_pages, grid);
     float* part = static_cast<float*>(ws);
     const cudaError_t e = w.tile_rows <= 32 ? launch_rt<16>(a, w, grid, part, st) : launch_rt<32>(a, w, grid, part, st);
-    if (e != cudaSuccess || grid == 1) return e;
+    if (e != cudaSuccess || grid == 1 || w.cluster != 0) return e;
     return launch_pdl(combine_q4_kernel, dim3((a.R * a.G + 7) / 8, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w, part, grid);
 }
 

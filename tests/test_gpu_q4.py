@@ -187,6 +187,47 @@ def test_attn_scale_and_capacity(sv):
     run(sv, 1, 5, 12, 2, [90], seed=5, cache_ready=True)
 
 
+@pytest.mark.parametrize("B,R,Hq,H,lens,is_tree", [
+    (1, 5, 12, 2, [1000], False), (3, 9, 28, 4, [63, 0, 700], False), (2, 65, 28, 4, [130, 5], True), (1, 1, 1, 1, [1], False),
+    (2, 20, 16, 2, [640, 129], True)])
+def test_attn_split_over_all_sms(sv, B, R, Hq, H, lens, is_tree):
+    """A long table (its capacity sets how the work is split): the pages are laid
+    end to end over the SMs, and units in several of them joined by the second
+    kernel.  Shorter tables give each unit a cluster of CTAs."""
+    mp = 250
+    assert sv.verify_attn_q4_workspace(B, R, Hq, H, 128, mp * 64) > 0
+    assert sv.verify_attn_q4_workspace(1, 5, 12, 2, 128, 4096) == 0
+    r = np.random.default_rng(R)
+    par = np.full((B, R), -1, np.int32)
+    for j in range(1, R):
+        par[:, j] = r.integers(max(0, j - 6), j, B)
+    run(sv, B, R, Hq, H, lens, parent=par if is_tree else None, seed=R, mp=mp)
+    run(sv, B, R, Hq, H, lens, parent=par if is_tree else None, seed=R, mp=mp, scale=9.0)
+
+
+def test_attn_references_far_below(sv):
+    """The first key's score far below the others': the sums leave their range
+    and the run is done again with the running maxima, in a cluster and over all
+    SMs."""
+    r = np.random.default_rng(8)
+    for mp in (9, 250):
+        P, t, R, Hq = mp + 1, 520, 3, 4
+        table = r.permutation(P)[:mp].reshape(1, mp).astype(np.int32)
+        kp, vp = random_pool(r, P, 1, is_v=False), random_pool(r, P, 1, is_v=True)
+        q = np.abs(ref.bf16_round(r.standard_normal((1, R, Hq, 128)))) + 0.5
+        kb, vb = ref.bf16_round(r.standard_normal((2, 1, 1, R, 128)))
+        ref.put_row(kp[table[0, 0], 0], 0, np.full(128, -6.0), False)
+        for p in (70, 300, 519):
+            ref.put_row(kp[table[0, p // 64], 0], p % 64, np.full(128, 1.0 + p / 200), False)
+        q = ref.bf16_round(q)
+        out = sv.verify_attn_q4(bf(q).cuda(), torch.from_numpy(kp).cuda(), torch.from_numpy(vp).cuda(), i32(table), i32([t]),
+                                bf(kb).cuda(), bf(vb).cuda(), scale=0.5)
+        rows = lambda pool, is_v: ref.get_rows(pool[table[0, :9]], is_v).transpose(1, 0, 2, 3).reshape(1, 576, 128)[:, :t]  # noqa: E731
+        want, wgt, big = ref.attention(q[0], rows(kp, False), rows(vp, True), kb[0], vb[0], None, 0.5)
+        assert np.all(np.abs(out[0].double().cpu().numpy() - want) <= tol(want, wgt, big, t + R))
+        assert sv.get_device_error() == 0
+
+
 def test_attn_sharp_softmax(sv):
     """Scores far apart (scale 20): the running maximum is rescaled again and
     again, and a single key takes the row."""

@@ -195,11 +195,12 @@ def test_two_graphs_at_once(sv):
     """Two captured attentions share no scratch: replayed together on two streams
     beside an eager one, each gives its own result."""
     r = np.random.default_rng(5)
-    P, t, n = 40, 2500, 3
+    P, t, n = 260, 16600, 3      # (long enough that the pages are split over all SMs)
     kp, vp = (torch.from_numpy(random_pool(r, P, H, is_v=x)).cuda() for x in (False, True))
     table, length = i32([list(range(P))]), i32([t])
     mk = lambda *s: bf(r.standard_normal(s)).cuda()  # noqa: E731
     qs, kb, vb = [mk(1, R, HQ, 128) for _ in range(n)], mk(1, H, R, 128), mk(1, H, R, 128)
+    assert sv.verify_attn_q4_workspace(1, R, HQ, H, 128, P * 64) > 0
     want = [sv.verify_attn_q4(q, kp, vp, table, length, kb, vb) for q in qs]
     torch.cuda.synchronize()
     graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(n)]
@@ -333,14 +334,17 @@ def test_other_refusals_of_the_binding(sv):
         f(**{**a, "hist_len": None})
     with pytest.raises(ValueError):
         f(**{**a, "bias_val": None})
-    f, a = c["verify_attn_q4"]
-    need = sv.verify_attn_q4_workspace(B, R, HQ, H, 128, MP * 64)
+    b = 100      # more units than clusters: the partials need scratch
+    need = sv.verify_attn_q4_workspace(b, R, HQ, H, 128, 64)
     assert need > 0
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    pool = torch.zeros(9, H, 4608, dtype=torch.uint8, device="cuda")
+    a = (z(b, R, HQ, 128), pool, pool.clone(), i32([[0]] * b), i32([0] * b), z(b, H, R, 128), z(b, H, R, 128))
     with pytest.raises(ValueError):
-        f(**a, ws=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+        sv.verify_attn_q4(*a, ws=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
-        f(**a, ws=torch.empty(need, dtype=torch.uint8))
-    f(**a, ws=torch.empty(need, dtype=torch.uint8, device="cuda"))
+        sv.verify_attn_q4(*a, ws=torch.empty(need, dtype=torch.uint8))
+    sv.verify_attn_q4(*a, ws=torch.empty(need, dtype=torch.uint8, device="cuda"))
     f, a = c["kv_gather_q4"]
     with pytest.raises(ValueError):
         f(**{**a, "n": -1})
