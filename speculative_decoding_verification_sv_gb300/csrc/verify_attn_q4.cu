@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if constexpr (kCluster) pdl_launch_dependents();
     const uint32_t tmem = *tmem_s;
     const int q4 = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
@@ -562,6 +563,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         };
         do {
         while (walk.next(a, wk)) {
+            // the block's rows, read at the end of the run by loads that wait for one
+            // another, are brought near meanwhile (256 bytes a row; a thread a line or two)
+            const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + walk.cur_unit / wk.row_tiles) * a.R * kQ4D;
+            if (walk.block && waited) {
+                const uint16_t* near = (is_v ? a.v_blk : a.k_blk) + blk0;
+                for (int x = l; x < 2 * a.R; x += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(near + 64 * x));
+            }
             for (int st = 0; st < walk.ctx_steps(); ++st, ++it, ++c) {
                 const int s = c % kStages;
                 const uint8_t* stage = smem + kOffRing + s * kStageBytes;
@@ -633,10 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 waited = true;
                 wait(&freed[it & 1], ((it >> 1) & 1) ^ 1);
                 tc_fence_after();
-                const int g = walk.cur_unit / wk.row_tiles;
-                const size_t row0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R;
                 if (!is_v) {
-                    const uint4* src = reinterpret_cast<const uint4*>(a.k_blk + (row0 + l) * kQ4D);
+                    const uint4* src = reinterpret_cast<const uint4*>(a.k_blk + blk0 + l * kQ4D);
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         uint32_t r[16];
@@ -649,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                         put(16 * x, r);
                     }
                 } else {
-                    const uint16_t* src = a.v_blk + row0 * kQ4D + l;
+                    const uint16_t* src = a.v_blk + blk0 + l;
 #pragma unroll 1
                     for (int h = 0; h < 4; ++h) {
                         uint32_t r[16];
@@ -956,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         __syncwarp();
         cluster_sync_warp();   // this CTA's partial has been read
     }
-    pdl_launch_dependents();
+    if constexpr (!kCluster) pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
