@@ -24,16 +24,25 @@
 // kMostSum; a run where one does (some score 60 powers of two above the first
 // key's) is done again with the reference moved to the maximum every step.
 //
-// Work.  A unit is one (sequence, KV head, tile of 64 query rows); its pages,
-// and the block as one more, are laid end to end over all units, and each CTA
-// (one an SM) takes an equal run of them, whatever the sequences' lengths.  A
-// unit that lies in several CTAs' runs leaves partial rows (m, l, O) in the
-// workspace -- at most two a CTA -- and a second small kernel joins them.
+// Work.  A unit is one (sequence, KV head, tile of 64 query rows).  Where there are
+// few of them over a short table each has a cluster of CTAs that leave their partial
+// rows (m, l, O) in shared memory and join them over it.  Otherwise the units' pages,
+// and the block as one more, are laid end to end over all units, and each CTA (one an
+// SM) takes an equal run of them, whatever the sequences' lengths; a unit that lies in
+// several CTAs' runs leaves partials in the workspace -- at most two a CTA -- and a
+// second small kernel joins them.
 //
 // Warps: 8 softmax (TMEM quadrant w % 4, half of the tile's rows each), 4 unpack
 // K, 4 unpack V, one issues the copies (two pages of K and V, 18 KB, a ring
 // stage: each (page, head) is one 4608-byte bulk copy), one the MMAs, one brings
 // the query rows of the next run while the present one is worked on.
+//
+// Measured.  16 x 9 rows of 28 heads over 4, 8192 positions: 36.0 us, 470 TFLOP/s and
+// 2.2 TB/s of the cache's 76 MB: bound by issue slots, about 4300 warp instructions a
+// step of 128 keys (8192 codes of K and of V unpacked, 8192 exponentials) on four
+// schedulers, at 0.65 us a step.  One sequence of 5 rows, 12 heads over 2, 4096
+// positions: 10.4 us, a chain of latencies: 2 us until the first page is there, 3 us for
+// five steps, 1.5 us for the last sums and O, 3 us for the cluster's join and end.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -59,7 +68,6 @@ constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to sta
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 256;
 constexpr int kMaxCluster = 8;
-constexpr int kJoinPages = 9, kClusterPages = 2;   // (see plan)
 
 // TMEM columns: two K operands, two V operands (64 columns: 128 bf16 each), two
 // S^T, one O^T
@@ -427,39 +435,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         // ---------------- page copies ----------------
         int c = 0;   // context steps so far
         do {
-        while (walk.next(a, wk)) {
-            const int g = walk.cur_unit / wk.row_tiles;
-            const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
-            const int np = walk.p1 - walk.p0;
-            for (int i0 = 0; i0 < np; i0 += 32) {
-                // 32 table entries at once: lane l holds page p0 + i0 + l
-                int pg = i0 + lane < np ? __ldg(tab + walk.p0 + i0 + lane) : 0;
-                const bool bad = pg < 0 || pg >= a.num_pages;
-                if (bad) {
-                    raise_error(a.err, SV_DEVERR_PAGE);
-                    pg = -1;
-                }
-                for (int i = 0; i < 32 && i0 + i < np; i += 2, ++c) {
-                    const int pa = __shfl_sync(0xffffffffu, pg, i), pb = __shfl_sync(0xffffffffu, pg, i + 1);
-                    const bool two = i0 + i + 1 < np;
-                    if (lane == 0) {
-                        const int s = c % kStages;
-                        mbar_wait(&ring_empty[s], ((c / kStages) & 1) ^ 1, a.err);
-                        uint8_t* st = smem + kOffRing + s * kStageBytes;
-                        const bool la = pa >= 0, lb = two && pb >= 0;
-                        bad_s[s] = (la ? 0u : 1u) | (two && pb < 0 ? 2u : 0u);
-                        mbar_arrive_expect_tx(&ring_full[s], (la ? 2 * kQ4Bytes : 0) + (lb ? 2 * kQ4Bytes : 0));
-                        const size_t oa = (static_cast<size_t>(pa) * a.Hkv + g) * kQ4Bytes;
-                        const size_t ob = (static_cast<size_t>(pb) * a.Hkv + g) * kQ4Bytes;
-                        if (la) bulk_g2s(st, a.k_pool + oa, kQ4Bytes, &ring_full[s]);
-                        if (lb) bulk_g2s(st + kQ4Bytes, a.k_pool + ob, kQ4Bytes, &ring_full[s]);
-                        if (la) bulk_g2s(st + 2 * kQ4Bytes, a.v_pool + oa, kQ4Bytes, &ring_full[s]);
-                        if (lb) bulk_g2s(st + 3 * kQ4Bytes, a.v_pool + ob, kQ4Bytes, &ring_full[s]);
+            while (walk.next(a, wk)) {
+                const int g = walk.cur_unit / wk.row_tiles;
+                const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
+                const int np = walk.p1 - walk.p0;
+                for (int i0 = 0; i0 < np; i0 += 32) {
+                    // 32 table entries at once: lane l holds page p0 + i0 + l
+                    int pg = i0 + lane < np ? __ldg(tab + walk.p0 + i0 + lane) : 0;
+                    const bool bad = pg < 0 || pg >= a.num_pages;
+                    if (bad) {
+                        raise_error(a.err, SV_DEVERR_PAGE);
+                        pg = -1;
                     }
-                    __syncwarp();
+                    for (int i = 0; i < 32 && i0 + i < np; i += 2, ++c) {
+                        const int pa = __shfl_sync(0xffffffffu, pg, i), pb = __shfl_sync(0xffffffffu, pg, i + 1);
+                        const bool two = i0 + i + 1 < np;
+                        if (lane == 0) {
+                            const int s = c % kStages;
+                            mbar_wait(&ring_empty[s], ((c / kStages) & 1) ^ 1, a.err);
+                            uint8_t* st = smem + kOffRing + s * kStageBytes;
+                            const bool la = pa >= 0, lb = two && pb >= 0;
+                            bad_s[s] = (la ? 0u : 1u) | (two && pb < 0 ? 2u : 0u);
+                            mbar_arrive_expect_tx(&ring_full[s], (la ? 2 * kQ4Bytes : 0) + (lb ? 2 * kQ4Bytes : 0));
+                            const size_t oa = (static_cast<size_t>(pa) * a.Hkv + g) * kQ4Bytes;
+                            const size_t ob = (static_cast<size_t>(pb) * a.Hkv + g) * kQ4Bytes;
+                            if (la) bulk_g2s(st, a.k_pool + oa, kQ4Bytes, &ring_full[s]);
+                            if (lb) bulk_g2s(st + kQ4Bytes, a.k_pool + ob, kQ4Bytes, &ring_full[s]);
+                            if (la) bulk_g2s(st + 2 * kQ4Bytes, a.v_pool + oa, kQ4Bytes, &ring_full[s]);
+                            if (lb) bulk_g2s(st + 3 * kQ4Bytes, a.v_pool + ob, kQ4Bytes, &ring_full[s]);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
-        }
         } while (again());
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issuer ----------------
@@ -467,81 +475,81 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         constexpr uint32_t id_o = idesc_bf16_f32(128, kRows, false, true);
         int it = 0, seg = 0;
         do {
-        while (walk.next(a, wk)) {
-            const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
-            if (elect_one()) {
-                const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ + (seg & 1) * kQBytes), 16, 1024);
-                // S of step i + 2 goes ahead of P V of step i: it only waits for the
-                // scores of step i to be read, not for their P
-                auto scores = [&](int i) {
-                    const int x = i & 1;
-                    mbar_wait(&k_full[x], (i >> 1) & 1, a.err);
-                    mbar_wait(&s_empty[x], ((i >> 1) & 1) ^ 1, a.err);
-                    tc_fence_after();
+            while (walk.next(a, wk)) {
+                const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
+                if (elect_one()) {
+                    const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ + (seg & 1) * kQBytes), 16, 1024);
+                    // S of step i + 2 goes ahead of P V of step i: it only waits for the
+                    // scores of step i to be read, not for their P
+                    auto scores = [&](int i) {
+                        const int x = i & 1;
+                        mbar_wait(&k_full[x], (i >> 1) & 1, a.err);
+                        mbar_wait(&s_empty[x], ((i >> 1) & 1) ^ 1, a.err);
+                        tc_fence_after();
 #pragma unroll
-                    for (int kc = 0; kc < kQ4D / 16; ++kc)
-                        tc_mma_ts(tS(x), tK(x) + kc * 8, qd + (((kc >> 2) * kRows * 128 + (kc & 3) * 32) >> 4), id_s,
-                                  kc > 0 ? 1u : 0u);
-                    tc_commit(&s_full[x]);
-                    if (i == it + n - 1) tc_commit(&q_free[seg & 1]);
-                };
-                mbar_wait(&q_ready[seg & 1], (seg >> 1) & 1, a.err);
+                        for (int kc = 0; kc < kQ4D / 16; ++kc)
+                            tc_mma_ts(tS(x), tK(x) + kc * 8, qd + (((kc >> 2) * kRows * 128 + (kc & 3) * 32) >> 4), id_s,
+                                      kc > 0 ? 1u : 0u);
+                        tc_commit(&s_full[x]);
+                        if (i == it + n - 1) tc_commit(&q_free[seg & 1]);
+                    };
+                    mbar_wait(&q_ready[seg & 1], (seg >> 1) & 1, a.err);
 #pragma unroll 1
-                for (int st = -2; st < n; ++st) {
-                    if (st + 2 < n) scores(it + st + 2);
-                    if (st < 0) continue;
-                    const int i = it + st, x = i & 1;
-                    if (st == 0) mbar_wait(o_free, (seg & 1) ^ 1, a.err);
-                    mbar_wait(&v_full[x], (i >> 1) & 1, a.err);
-                    mbar_wait(&p_full[i % kPBufs], (i / kPBufs) & 1, a.err);
-                    tc_fence_after();
-                    const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + i % kPBufs * kPBytes), 16, 1024);
+                    for (int st = -2; st < n; ++st) {
+                        if (st + 2 < n) scores(it + st + 2);
+                        if (st < 0) continue;
+                        const int i = it + st, x = i & 1;
+                        if (st == 0) mbar_wait(o_free, (seg & 1) ^ 1, a.err);
+                        mbar_wait(&v_full[x], (i >> 1) & 1, a.err);
+                        mbar_wait(&p_full[i % kPBufs], (i / kPBufs) & 1, a.err);
+                        tc_fence_after();
+                        const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + i % kPBufs * kPBytes), 16, 1024);
 #pragma unroll
-                    for (int kc = 0; kc < kStepKeys / 16; ++kc)
-                        tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || st > 0) ? 1u : 0u);
-                    tc_commit(&pv_done[x]);
+                        for (int kc = 0; kc < kStepKeys / 16; ++kc)
+                            tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || st > 0) ? 1u : 0u);
+                        tc_commit(&pv_done[x]);
+                    }
                 }
+                __syncwarp();
+                it += n;
+                ++seg;
             }
-            __syncwarp();
-            it += n;
-            ++seg;
-        }
         } while (again());
     } else if (warp == kQWarp) {
         // ---------------- query rows ----------------
         if (early) pdl_wait();
         int seg = 0;
         do {
-        while (walk.next(a, wk)) {
-            const int g = walk.cur_unit / wk.row_tiles, row0 = walk.cur_unit % wk.row_tiles * wk.tile_rows;
-            const int nrows = min(wk.tile_rows, a.R * a.G - row0);
-            // where each row lies (two a lane), -1 past the last
-            int at[2];
+            while (walk.next(a, wk)) {
+                const int g = walk.cur_unit / wk.row_tiles, row0 = walk.cur_unit % wk.row_tiles * wk.tile_rows;
+                const int nrows = min(wk.tile_rows, a.R * a.G - row0);
+                // where each row lies (two a lane), -1 past the last
+                int at[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 32 * h + lane, gr = row0 + r, j = gr * wk.inv_g >> 16;
-                at[h] = r < nrows ? (walk.cur_b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
-            }
-            wait(&q_free[seg & 1], ((seg >> 1) & 1) ^ 1);
-            uint8_t* q_s = smem + kOffQ + (seg & 1) * kQBytes;
-            // K-major, 128-byte swizzle, zeros past the last row: half a warp a row
-            const int ch = lane & 15;
-#pragma unroll
-            for (int h = 0; h < kLive / 32; ++h) {
-#pragma unroll 8
-                for (int i = 0; i < 32; i += 2) {
-                    const int r = 32 * h + i + (lane >> 4), row = __shfl_sync(0xffffffffu, at[h], r & 31);
-                    uint8_t* dst = q_s + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                    if (row >= 0) cp_async16(dst, reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(row) * kQ4D) + ch);
-                    else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                for (int h = 0; h < 2; ++h) {
+                    const int r = 32 * h + lane, gr = row0 + r, j = gr * wk.inv_g >> 16;
+                    at[h] = r < nrows ? (walk.cur_b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
                 }
+                wait(&q_free[seg & 1], ((seg >> 1) & 1) ^ 1);
+                uint8_t* q_s = smem + kOffQ + (seg & 1) * kQBytes;
+                // K-major, 128-byte swizzle, zeros past the last row: half a warp a row
+                const int ch = lane & 15;
+#pragma unroll
+                for (int h = 0; h < kLive / 32; ++h) {
+#pragma unroll 8
+                    for (int i = 0; i < 32; i += 2) {
+                        const int r = 32 * h + i + (lane >> 4), row = __shfl_sync(0xffffffffu, at[h], r & 31);
+                        uint8_t* dst = q_s + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                        if (row >= 0) cp_async16(dst, reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(row) * kQ4D) + ch);
+                        else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
+                ++seg;
             }
-            cp_async_wait_all();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
-            ++seg;
-        }
         } while (again());
     } else if (warp >= kKWarp) {
         // ---------------- unpacking: a key's K, a dim's V ----------------
@@ -562,117 +570,117 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             if (lane == 0) mbar_arrive(&full[it & 1]);
         };
         do {
-        while (walk.next(a, wk)) {
-            // the block's rows, read at the end of the run by loads that wait for one
-            // another, are brought near meanwhile (256 bytes a row; a thread a line or two)
-            const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + walk.cur_unit / wk.row_tiles) * a.R * kQ4D;
-            if (walk.block && waited) {
-                const uint16_t* near = (is_v ? a.v_blk : a.k_blk) + blk0;
-                for (int x = l; x < 2 * a.R; x += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(near + 64 * x));
-            }
-            for (int st = 0; st < walk.ctx_steps(); ++st, ++it, ++c) {
-                const int s = c % kStages;
-                const uint8_t* stage = smem + kOffRing + s * kStageBytes;
-                wait(&ring_full[s], (c / kStages) & 1);
-                const uint32_t bad = bad_s[s];
-                wait(&freed[it & 1], ((it >> 1) & 1) ^ 1);
-                tc_fence_after();
-                if (!is_v) {
-                    const uint8_t* blk = stage + (l >> 6) * kQ4Bytes;
-                    const int pos = l & 63;
-                    uint2 sc = *reinterpret_cast<const uint2*>(blk + q4_k_scale_off(0, pos));
-                    if (bad >> (l >> 6) & 1u) sc = make_uint2(0u, 0u);
-                    uint4 cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(0, pos));
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint32_t s2 = __byte_perm(sc.x, 0u, 0x1010);
-                        sc.x = g == 1 ? sc.y : sc.x >> 16;
-                        const uint32_t o2 = bmul2(s2, kM136);
-                        const uint32_t ww[4] = {cw.x, cw.y, cw.z, cw.w};
-                        if (g < 3) cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(g + 1, pos));
-                        uint32_t r[16];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) r[4 * w + k] = bfma2(cm.pair(ww[w], k), s2, o2);
-                        put(16 * g, r);
-                    }
-                } else {
-                    // keys of the step that exist: the others, and pages outside
-                    // the pool, are zeros (0 * a non-finite V would be NaN)
-                    const int have = min(walk.cur_t - (walk.p0 + 2 * st) * kQ4Page, (walk.p1 - walk.p0 - 2 * st) * kQ4Page);
-                    // the warp's 32 dims are one group: the step's 64 pairs of scales and
-                    // -136 times them, formed once by its lanes
-                    uint32_t* sc_s = reinterpret_cast<uint32_t*>(smem + kOffScale + q4 * 512);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t s2 = *reinterpret_cast<const uint32_t*>(stage + (2 + h) * kQ4Bytes +
-                                                                         q4_v_scale_off(q4, 2 * lane));
-                        if (have < kStepKeys || bad != 0u) {
-                            const int n = (bad >> h & 1u) ? 0 : have - kQ4Page * h - 2 * lane;
-                            s2 &= n > 1 ? ~0u : n > 0 ? 0xFFFFu : 0u;
-                        }
-                        sc_s[32 * h + lane] = s2;
-                        sc_s[64 + 32 * h + lane] = bmul2(s2, kM136);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {   // 32 keys: half a page
-                        const uint8_t* blk = stage + (2 + (h >> 1)) * kQ4Bytes;
-                        uint32_t r[16];
-#pragma unroll
-                        for (int o = 0; o < 4; ++o) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off((h & 1) * 4 + o, l));
-                            const uint4 sv = reinterpret_cast<const uint4*>(sc_s)[4 * h + o];
-                            const uint4 ov = reinterpret_cast<const uint4*>(sc_s)[16 + 4 * h + o];
-                            r[4 * o] = bfma2(cm.pair(w, 0), sv.x, ov.x);
-                            r[4 * o + 1] = bfma2(cm.pair(w, 1), sv.y, ov.y);
-                            r[4 * o + 2] = bfma2(cm.pair(w, 2), sv.z, ov.z);
-                            r[4 * o + 3] = bfma2(cm.pair(w, 3), sv.w, ov.w);
-                        }
-                        put(16 * h, r);
-                    }
+            while (walk.next(a, wk)) {
+                // the block's rows, read at the end of the run by loads that wait for one
+                // another, are brought near meanwhile (256 bytes a row; a thread a line or two)
+                const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + walk.cur_unit / wk.row_tiles) * a.R * kQ4D;
+                if (walk.block && waited) {
+                    const uint16_t* near = (is_v ? a.v_blk : a.k_blk) + blk0;
+                    for (int x = l; x < 2 * a.R; x += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(near + 64 * x));
                 }
-                done();
-                if (lane == 0) mbar_arrive(&ring_empty[s]);
-            }
-            if (walk.block) {
-                if (!waited) pdl_wait();
-                waited = true;
-                wait(&freed[it & 1], ((it >> 1) & 1) ^ 1);
-                tc_fence_after();
-                if (!is_v) {
-                    const uint4* src = reinterpret_cast<const uint4*>(a.k_blk + blk0 + l * kQ4D);
-#pragma unroll 1
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t r[16];
+                for (int st = 0; st < walk.ctx_steps(); ++st, ++it, ++c) {
+                    const int s = c % kStages;
+                    const uint8_t* stage = smem + kOffRing + s * kStageBytes;
+                    wait(&ring_full[s], (c / kStages) & 1);
+                    const uint32_t bad = bad_s[s];
+                    wait(&freed[it & 1], ((it >> 1) & 1) ^ 1);
+                    tc_fence_after();
+                    if (!is_v) {
+                        const uint8_t* blk = stage + (l >> 6) * kQ4Bytes;
+                        const int pos = l & 63;
+                        uint2 sc = *reinterpret_cast<const uint2*>(blk + q4_k_scale_off(0, pos));
+                        if (bad >> (l >> 6) & 1u) sc = make_uint2(0u, 0u);
+                        uint4 cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(0, pos));
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (l < a.R) v = __ldg(src + 4 * x + y);
-                            r[4 * y] = v.x, r[4 * y + 1] = v.y, r[4 * y + 2] = v.z, r[4 * y + 3] = v.w;
-                        }
-                        put(16 * x, r);
-                    }
-                } else {
-                    const uint16_t* src = a.v_blk + blk0 + l;
-#pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t r[16];
+                        for (int g = 0; g < 4; ++g) {
+                            const uint32_t s2 = __byte_perm(sc.x, 0u, 0x1010);
+                            sc.x = g == 1 ? sc.y : sc.x >> 16;
+                            const uint32_t o2 = bmul2(s2, kM136);
+                            const uint32_t ww[4] = {cw.x, cw.y, cw.z, cw.w};
+                            if (g < 3) cw = *reinterpret_cast<const uint4*>(blk + q4_k_code_off(g + 1, pos));
+                            uint32_t r[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int key = 32 * h + 2 * k;
-                            const uint32_t lo = key < a.R ? __ldg(src + key * kQ4D) : 0u;
-                            const uint32_t hi = key + 1 < a.R ? __ldg(src + (key + 1) * kQ4D) : 0u;
-                            r[k] = lo | hi << 16;
+                            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) r[4 * w + k] = bfma2(cm.pair(ww[w], k), s2, o2);
+                            put(16 * g, r);
                         }
-                        put(16 * h, r);
+                    } else {
+                        // keys of the step that exist: the others, and pages outside
+                        // the pool, are zeros (0 * a non-finite V would be NaN)
+                        const int have = min(walk.cur_t - (walk.p0 + 2 * st) * kQ4Page, (walk.p1 - walk.p0 - 2 * st) * kQ4Page);
+                        // the warp's 32 dims are one group: the step's 64 pairs of scales and
+                        // -136 times them, formed once by its lanes
+                        uint32_t* sc_s = reinterpret_cast<uint32_t*>(smem + kOffScale + q4 * 512);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t s2 = *reinterpret_cast<const uint32_t*>(stage + (2 + h) * kQ4Bytes +
+                                                                             q4_v_scale_off(q4, 2 * lane));
+                            if (have < kStepKeys || bad != 0u) {
+                                const int n = (bad >> h & 1u) ? 0 : have - kQ4Page * h - 2 * lane;
+                                s2 &= n > 1 ? ~0u : n > 0 ? 0xFFFFu : 0u;
+                            }
+                            sc_s[32 * h + lane] = s2;
+                            sc_s[64 + 32 * h + lane] = bmul2(s2, kM136);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {   // 32 keys: half a page
+                            const uint8_t* blk = stage + (2 + (h >> 1)) * kQ4Bytes;
+                            uint32_t r[16];
+#pragma unroll
+                            for (int o = 0; o < 4; ++o) {
+                                const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + q4_v_code_off((h & 1) * 4 + o, l));
+                                const uint4 sv = reinterpret_cast<const uint4*>(sc_s)[4 * h + o];
+                                const uint4 ov = reinterpret_cast<const uint4*>(sc_s)[16 + 4 * h + o];
+                                r[4 * o] = bfma2(cm.pair(w, 0), sv.x, ov.x);
+                                r[4 * o + 1] = bfma2(cm.pair(w, 1), sv.y, ov.y);
+                                r[4 * o + 2] = bfma2(cm.pair(w, 2), sv.z, ov.z);
+                                r[4 * o + 3] = bfma2(cm.pair(w, 3), sv.w, ov.w);
+                            }
+                            put(16 * h, r);
+                        }
                     }
+                    done();
+                    if (lane == 0) mbar_arrive(&ring_empty[s]);
                 }
-                done();
-                ++it;
+                if (walk.block) {
+                    if (!waited) pdl_wait();
+                    waited = true;
+                    wait(&freed[it & 1], ((it >> 1) & 1) ^ 1);
+                    tc_fence_after();
+                    if (!is_v) {
+                        const uint4* src = reinterpret_cast<const uint4*>(a.k_blk + blk0 + l * kQ4D);
+#pragma unroll 1
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t r[16];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                if (l < a.R) v = __ldg(src + 4 * x + y);
+                                r[4 * y] = v.x, r[4 * y + 1] = v.y, r[4 * y + 2] = v.z, r[4 * y + 3] = v.w;
+                            }
+                            put(16 * x, r);
+                        }
+                    } else {
+                        const uint16_t* src = a.v_blk + blk0 + l;
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t r[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int key = 32 * h + 2 * k;
+                                const uint32_t lo = key < a.R ? __ldg(src + key * kQ4D) : 0u;
+                                const uint32_t hi = key + 1 < a.R ? __ldg(src + (key + 1) * kQ4D) : 0u;
+                                r[k] = lo | hi << 16;
+                            }
+                            put(16 * h, r);
+                        }
+                    }
+                    done();
+                    ++it;
+                }
             }
-        }
         } while (again());
         if (!waited) pdl_wait();
     } else {
@@ -690,254 +698,254 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         const int rows = a.R * a.G;
         int it = 0, seg = 0;
         do {
-        int part = 0;
-        while (walk.next(a, wk)) {
-            const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
-            const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
-            if (tid == 0) {
-                const int t = a.len[b];
-                if (t < 0 || t > a.max_pages * kQ4Page) raise_error(a.err, SV_DEVERR_LENGTH);
-            }
-            if (tid < kRows) {
-                const int gr = row0 + tid, j = gr * wk.inv_g >> 16;
-                row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
-                nm_s[tid] = 0.f;
-            }
-            const bool tree = walk.block && a.parent != nullptr;
-            if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
-            soft_sync();   // row_s, nm_s, par_s
-            if (tree) {
-                if (tid < a.R) {
-                    uint64_t m0 = 0, m1 = 0;
-                    int i = tid;
-                    bool bad = false;
-                    for (int n = 0; n <= a.R && i >= 0; ++n) {
-                        if (i < 64) m0 |= 1ull << i;
-                        else m1 |= 1ull << (i - 64);
-                        const int p = par_s[i];
-                        if ((i == 0 && p != -1) || (i > 0 && (p < 0 || p >= i))) {
-                            bad = true;
-                            break;
-                        }
-                        i = p;
-                    }
-                    if (bad) {
-                        raise_error(a.err, SV_DEVERR_TREE);
-                        m0 = tid < 64 ? 1ull << tid : 0ull;
-                        m1 = tid >= 64 ? 1ull << (tid - 64) : 0ull;
-                    }
-                    anc_s[2 * tid] = m0;
-                    anc_s[2 * tid + 1] = m1;
+            int part = 0;
+            while (walk.next(a, wk)) {
+                const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
+                const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
+                if (tid == 0) {
+                    const int t = a.len[b];
+                    if (t < 0 || t > a.max_pages * kQ4Page) raise_error(a.err, SV_DEVERR_LENGTH);
                 }
-                soft_sync();
-            }
-            float sums[kRT];
-#pragma unroll
-            for (int i = 0; i < kRT; ++i) sums[i] = 0.f;
-            const int nctx = walk.ctx_steps(), n = nctx + (walk.block ? 1 : 0);
-            auto step = [&](int st, auto general_c) {
-                constexpr bool kGeneral = decltype(general_c)::value;
-                const int x = it & 1;
-                wait(&s_full[x], (it >> 1) & 1);
-                tc_fence_after();
-                // the rows that see this thread's key (bit e: row hh * kRT + e), in the
-                // steps where some do not: of the context, keys before the length (the
-                // second page of a step may be missing); block row l is seen from query
-                // rows l G on, or by the tree rows on whose path it lies
-                uint32_t seen = ~0u;
-                if constexpr (kGeneral) {
-                    if (st < nctx) {
-                        if ((walk.p0 + 2 * st) * kQ4Page + l >= min(walk.cur_t, walk.p1 * kQ4Page)) seen = 0u;
-                    } else if (!tree) {
-                        const int lo = l < a.R ? l * a.G - row0 - hh * kRT : kRT;
-                        seen = lo >= kRT ? 0u : lo > 0 ? ~0u << lo : ~0u;
-                    } else {
-                        // block row by block row: its G query rows see the same keys
-                        seen = 0u;
-                        const int r0 = row0 + hh * kRT, r1 = min(r0 + kRT, rows);
-                        int j = r0 * wk.inv_g >> 16;
-                        for (int r = j * a.G - r0; l < a.R && r + r0 < r1; ++j, r += a.G) {
-                            if ((anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) == 0ull) continue;
-                            const uint32_t run = (1u << a.G) - 1u;   // (G <= 16)
-                            seen |= r >= 0 ? run << r : run >> -r;
-                        }
-                    }
+                if (tid < kRows) {
+                    const int gr = row0 + tid, j = gr * wk.inv_g >> 16;
+                    row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
+                    nm_s[tid] = 0.f;
                 }
-                // exponents of rows c0 .. of the thread's against their references
-                auto exponents = [&](int c0, float(&e)[16]) {
-                    uint32_t s[16];
-                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT + c0)[i];
-                        e[4 * i] = fmaf(__uint_as_float(s[4 * i]), sc, nm.x);
-                        e[4 * i + 1] = fmaf(__uint_as_float(s[4 * i + 1]), sc, nm.y);
-                        e[4 * i + 2] = fmaf(__uint_as_float(s[4 * i + 2]), sc, nm.z);
-                        e[4 * i + 3] = fmaf(__uint_as_float(s[4 * i + 3]), sc, nm.w);
-                    }
-                    if constexpr (kGeneral) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!(seen >> (c0 + i) & 1u)) e[i] = -INFINITY;
-                    }
-                };
-                // the references (until now 0): the first key's scores (any finite number
-                // will do: it need not be visible), or, with `safe`, the running maxima
-                if constexpr (kGeneral) {
-                if (st == 0 && !safe) {
-                    if (q4 == 0) {
-#pragma unroll 1
-                        for (int c0 = 0; c0 < kRT; c0 += 16) {
-                            uint32_t s[16];
-                            tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float e = __uint_as_float(s[i]) * -sc;
-                                s[i] = fabsf(e) < INFINITY ? __float_as_uint(e) : 0u;
+                const bool tree = walk.block && a.parent != nullptr;
+                if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
+                soft_sync();   // row_s, nm_s, par_s
+                if (tree) {
+                    if (tid < a.R) {
+                        uint64_t m0 = 0, m1 = 0;
+                        int i = tid;
+                        bool bad = false;
+                        for (int n = 0; n <= a.R && i >= 0; ++n) {
+                            if (i < 64) m0 |= 1ull << i;
+                            else m1 |= 1ull << (i - 64);
+                            const int p = par_s[i];
+                            if ((i == 0 && p != -1) || (i > 0 && (p < 0 || p >= i))) {
+                                bad = true;
+                                break;
                             }
-                            if (lane == 0) {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4)
-                                    *reinterpret_cast<uint4*>(nm_s + hh * kRT + c0 + i) =
-                                        make_uint4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-                            }
-                            __syncwarp();
+                            i = p;
                         }
+                        if (bad) {
+                            raise_error(a.err, SV_DEVERR_TREE);
+                            m0 = tid < 64 ? 1ull << tid : 0ull;
+                            m1 = tid >= 64 ? 1ull << (tid - 64) : 0ull;
+                        }
+                        anc_s[2 * tid] = m0;
+                        anc_s[2 * tid + 1] = m1;
                     }
                     soft_sync();
                 }
-                if (safe) {
+                float sums[kRT];
+#pragma unroll
+                for (int i = 0; i < kRT; ++i) sums[i] = 0.f;
+                const int nctx = walk.ctx_steps(), n = nctx + (walk.block ? 1 : 0);
+                auto step = [&](int st, auto general_c) {
+                    constexpr bool kGeneral = decltype(general_c)::value;
+                    const int x = it & 1;
+                    wait(&s_full[x], (it >> 1) & 1);
+                    tc_fence_after();
+                    // the rows that see this thread's key (bit e: row hh * kRT + e), in the
+                    // steps where some do not: of the context, keys before the length (the
+                    // second page of a step may be missing); block row l is seen from query
+                    // rows l G on, or by the tree rows on whose path it lies
+                    uint32_t seen = ~0u;
+                    if constexpr (kGeneral) {
+                        if (st < nctx) {
+                            if ((walk.p0 + 2 * st) * kQ4Page + l >= min(walk.cur_t, walk.p1 * kQ4Page)) seen = 0u;
+                        } else if (!tree) {
+                            const int lo = l < a.R ? l * a.G - row0 - hh * kRT : kRT;
+                            seen = lo >= kRT ? 0u : lo > 0 ? ~0u << lo : ~0u;
+                        } else {
+                            // block row by block row: its G query rows see the same keys
+                            seen = 0u;
+                            const int r0 = row0 + hh * kRT, r1 = min(r0 + kRT, rows);
+                            int j = r0 * wk.inv_g >> 16;
+                            for (int r = j * a.G - r0; l < a.R && r + r0 < r1; ++j, r += a.G) {
+                                if ((anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) == 0ull) continue;
+                                const uint32_t run = (1u << a.G) - 1u;   // (G <= 16)
+                                seen |= r >= 0 ? run << r : run >> -r;
+                            }
+                        }
+                    }
+                    // exponents of rows c0 .. of the thread's against their references
+                    auto exponents = [&](int c0, float(&e)[16]) {
+                        uint32_t s[16];
+                        tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT + c0)[i];
+                            e[4 * i] = fmaf(__uint_as_float(s[4 * i]), sc, nm.x);
+                            e[4 * i + 1] = fmaf(__uint_as_float(s[4 * i + 1]), sc, nm.y);
+                            e[4 * i + 2] = fmaf(__uint_as_float(s[4 * i + 2]), sc, nm.z);
+                            e[4 * i + 3] = fmaf(__uint_as_float(s[4 * i + 3]), sc, nm.w);
+                        }
+                        if constexpr (kGeneral) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (!(seen >> (c0 + i) & 1u)) e[i] = -INFINITY;
+                        }
+                    };
+                    // the references (until now 0): the first key's scores (any finite number
+                    // will do: it need not be visible), or, with `safe`, the running maxima
+                    if constexpr (kGeneral) {
+                        if (st == 0 && !safe) {
+                            if (q4 == 0) {
 #pragma unroll 1
+                                for (int c0 = 0; c0 < kRT; c0 += 16) {
+                                    uint32_t s[16];
+                                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) {
+                                        const float e = __uint_as_float(s[i]) * -sc;
+                                        s[i] = fabsf(e) < INFINITY ? __float_as_uint(e) : 0u;
+                                    }
+                                    if (lane == 0) {
+#pragma unroll
+                                        for (int i = 0; i < 16; i += 4)
+                                            *reinterpret_cast<uint4*>(nm_s + hh * kRT + c0 + i) =
+                                                make_uint4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                                    }
+                                    __syncwarp();
+                                }
+                            }
+                            soft_sync();
+                        }
+                        if (safe) {
+#pragma unroll 1
+                            for (int c0 = 0; c0 < kRT; c0 += 16) {
+                                float e[16];
+                                exponents(c0, e);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    e[i] = warp_max(e[i]);
+                                    if (lane == 0) red_s[q4 * kRows + hh * kRT + c0 + i] = e[i];
+                                }
+                            }
+                            soft_sync();
+                            if (tid < kLive) {
+                                // up, or in the first step to wherever the maximum is (not to
+                                // -inf: all scores of the row are)
+                                float d = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
+                                                fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
+                                if (d == -INFINITY || (st > 0 && d < 0.f)) d = 0.f;
+                                nm_s[tid] -= d;
+                                move_s[tid] = fast_exp2(-d);
+                            }
+                            soft_sync();
+                            if (st > 0) {
+#pragma unroll
+                                for (int i = 0; i < kRT; ++i) sums[i] *= move_s[hh * kRT + i];
+                                // O^T (lane = dim) once the step before is in it
+                                wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1);
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c0 = 0; c0 < kRT; c0 += 16) {
+                                    const uint32_t ta = tO + lane_off + hh * kRT + c0;
+                                    uint32_t o[16];
+                                    tmem_ld16_sync(ta, o);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
+                                    tmem_st16(ta, o);
+                                }
+                                tmem_st_wait();
+                            }
+                        }
+                    }
+                    // a key's line of P takes eight rows in 16 bytes.  (The buffer is free: S of
+                    // this step was issued behind P V of three steps before.)
+                    uint8_t* prow = smem + kOffP + it % kPBufs * kPBytes + l * 128;
+#pragma unroll
                     for (int c0 = 0; c0 < kRT; c0 += 16) {
                         float e[16];
                         exponents(c0, e);
+                        if (c0 + 16 == kRT) {   // the scores are read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s_empty[x]);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            e[i] = warp_max(e[i]);
-                            if (lane == 0) red_s[q4 * kRows + hh * kRT + c0 + i] = e[i];
+                        for (int ch = 0; ch < 2; ++ch) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float p = fast_exp2(e[8 * ch + 2 * i]), q = fast_exp2(e[8 * ch + 2 * i + 1]);
+                                sums[c0 + 8 * ch + 2 * i] += p;
+                                sums[c0 + 8 * ch + 2 * i + 1] += q;
+                                w[i] = pack_bf16x2(p, q);
+                            }
+                            *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + c0 / 8 + ch) ^ (l & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    soft_sync();
-                    if (tid < kLive) {
-                        // up, or in the first step to wherever the maximum is (not to
-                        // -inf: all scores of the row are)
-                        float d = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
-                                        fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
-                        if (d == -INFINITY || (st > 0 && d < 0.f)) d = 0.f;
-                        nm_s[tid] -= d;
-                        move_s[tid] = fast_exp2(-d);
-                    }
-                    soft_sync();
-                    if (st > 0) {
-#pragma unroll
-                        for (int i = 0; i < kRT; ++i) sums[i] *= move_s[hh * kRT + i];
-                        // O^T (lane = dim) once the step before is in it
-                        wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1);
-                        tc_fence_after();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[it % kPBufs]);
+                    ++it;
+                };
+                // the plain steps -- whole context steps but the run's first -- apart, so
+                // that they carry neither masks nor references
+                const bool ragged = nctx > 0 && ((walk.p1 - walk.p0) & 1 || walk.p1 * kQ4Page > walk.cur_t);
+                const int nwhole = safe ? 0 : nctx - (ragged ? 1 : 0);
 #pragma unroll 1
-                        for (int c0 = 0; c0 < kRT; c0 += 16) {
-                            const uint32_t ta = tO + lane_off + hh * kRT + c0;
-                            uint32_t o[16];
-                            tmem_ld16_sync(ta, o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
-                            tmem_st16(ta, o);
-                        }
-                        tmem_st_wait();
-                    }
+                for (int st = 0; st < n; ++st) {
+                    if (st > 0 && st < nwhole) step(st, std::false_type{});
+                    else step(st, std::true_type{});
                 }
+                // the rows' sums over the keys: lane e of a warp ends with its row e's
+                // (halving the rows and the lanes that differ, step by step)
+                fold_sums(sums);
+                if (kRT == 16) sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
+                if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sums[0];
+                // (a cluster's partials stay on chip: the copies into the ring have all been read)
+                float* rec = kCluster ? reinterpret_cast<float*>(smem + kOffRing)
+                             : walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
+                soft_sync();
+                bool bad = false;
+                if (tid < kLive) {
+                    const float lsum =
+                        (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
+                    bad = !(lsum < kMostSum);
+                    if (rec) *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * tid) = make_float2(-nm_s[tid], lsum);
+                    move_s[tid] = lsum != 0.f ? 1.0f / lsum : 0.f;
                 }
-                // a key's line of P takes eight rows in 16 bytes.  (The buffer is free: S of
-                // this step was issued behind P V of three steps before.)
-                uint8_t* prow = smem + kOffP + it % kPBufs * kPBytes + l * 128;
+                wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+                tc_fence_after();
+                soft_sync();
 #pragma unroll
                 for (int c0 = 0; c0 < kRT; c0 += 16) {
-                    float e[16];
-                    exponents(c0, e);
-                    if (c0 + 16 == kRT) {   // the scores are read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s_empty[x]);
-                    }
+                    uint32_t o[16];
+                    tmem_ld16_sync(tO + lane_off + hh * kRT + c0, o);
+                    if (rec) {   // (rows past the tile's last are written too, and never read)
+                        float* dst = rec + (hh * kRT + c0) * kQ4D + l;
 #pragma unroll
-                    for (int ch = 0; ch < 2; ++ch) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float p = fast_exp2(e[8 * ch + 2 * i]), q = fast_exp2(e[8 * ch + 2 * i + 1]);
-                            sums[c0 + 8 * ch + 2 * i] += p;
-                            sums[c0 + 8 * ch + 2 * i + 1] += q;
-                            w[i] = pack_bf16x2(p, q);
+                        for (int e = 0; e < 16; ++e) {
+                            if constexpr (kCluster) dst[e * kQ4D] = __uint_as_float(o[e]);
+                            else __stcg(dst + e * kQ4D, __uint_as_float(o[e]));
                         }
-                        *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + c0 / 8 + ch) ^ (l & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int row = row_s[hh * kRT + c0 + e];
+                            const uint16_t v = f32_bf16_bits(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
+                            if (row >= 0) a.out[static_cast<size_t>(row) * kQ4D + l] = v;
+                        }
                     }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) bad |= !(fabsf(__uint_as_float(o[e])) < INFINITY);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[it % kPBufs]);
-                ++it;
-            };
-            // the plain steps -- whole context steps but the run's first -- apart, so
-            // that they carry neither masks nor references
-            const bool ragged = nctx > 0 && ((walk.p1 - walk.p0) & 1 || walk.p1 * kQ4Page > walk.cur_t);
-            const int nwhole = safe ? 0 : nctx - (ragged ? 1 : 0);
-#pragma unroll 1
-            for (int st = 0; st < n; ++st) {
-                if (st > 0 && st < nwhole) step(st, std::false_type{});
-                else step(st, std::true_type{});
+                if constexpr (kCluster) fence_proxy_async_smem();   // (copies may be made there again)
+                if (bad) *fail_s = 1;
+                part = 1;   // a partial run that is not the CTA's first is its last
+                tc_fence_before();
+                soft_sync();   // red_s and nm_s read by everyone before the next run writes them
+                if (lane == 0) mbar_arrive(o_free);
+                ++seg;
             }
-            // the rows' sums over the keys: lane e of a warp ends with its row e's
-            // (halving the rows and the lanes that differ, step by step)
-            fold_sums(sums);
-            if (kRT == 16) sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
-            if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sums[0];
-            // (a cluster's partials stay on chip: the copies into the ring have all been read)
-            float* rec = kCluster ? reinterpret_cast<float*>(smem + kOffRing)
-                         : walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
-            soft_sync();
-            bool bad = false;
-            if (tid < kLive) {
-                const float lsum =
-                    (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
-                bad = !(lsum < kMostSum);
-                if (rec) *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * tid) = make_float2(-nm_s[tid], lsum);
-                move_s[tid] = lsum != 0.f ? 1.0f / lsum : 0.f;
-            }
-            wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
-            tc_fence_after();
-            soft_sync();
-#pragma unroll
-            for (int c0 = 0; c0 < kRT; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld16_sync(tO + lane_off + hh * kRT + c0, o);
-                if (rec) {   // (rows past the tile's last are written too, and never read)
-                    float* dst = rec + (hh * kRT + c0) * kQ4D + l;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if constexpr (kCluster) dst[e * kQ4D] = __uint_as_float(o[e]);
-                        else __stcg(dst + e * kQ4D, __uint_as_float(o[e]));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int row = row_s[hh * kRT + c0 + e];
-                        const uint16_t v = f32_bf16_bits(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
-                        if (row >= 0) a.out[static_cast<size_t>(row) * kQ4D + l] = v;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) bad |= !(fabsf(__uint_as_float(o[e])) < INFINITY);
-            }
-            if constexpr (kCluster) fence_proxy_async_smem();   // (copies may be made there again)
-            if (bad) *fail_s = 1;
-            part = 1;   // a partial run that is not the CTA's first is its last
-            tc_fence_before();
-            soft_sync();   // red_s and nm_s read by everyone before the next run writes them
-            if (lane == 0) mbar_arrive(o_free);
-            ++seg;
-        }
         } while (again());
         if constexpr (kCluster) {   // no page of the unit fell to this CTA
             if (seg == 0 && tid < kRows)
@@ -1046,17 +1054,20 @@ int resident_clusters(int c) {
 
 // How the work is split, in pages that the busiest CTA takes: evenly over the SMs
 // and joined by a second kernel, or a cluster of 2, 4 or 8 CTAs for each unit, joined
-// on chip.  The second kernel and the partials' way through L2 cost about kJoinPages, the
-// cluster's barriers and remote reads kClusterPages.
+// on chip, whose barriers and remote reads cost about two pages.  The second kernel and
+// the partials' way through L2 cost about ten, and three for each ten partials of a unit.
+// Measured, cluster against even split: 5 x 12 heads over 2 of 4096 positions 10.0 and
+// 11.5 us, of 16384 17.9 and 18.8; 9 x 28 over 4, 4096: 11.2 and 13.8, 12288: 16.8 and
+// 16.7, 16384: 19.7 and 16.7; 65 x 28 over 4, 4096: 16.4 and 18.8, 8192: 22.1 and 23.5.
 void plan(Work& w, int B, int max_pages, int& grid) {
     const int64_t units = static_cast<int64_t>(B) * w.U, pages = units * (static_cast<int64_t>(max_pages) + 1);
     const int sms = device_sm_count();
     const int64_t most = pages / kGrain;
     grid = static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
     w.cluster = 0;
-    int64_t best = (pages + grid - 1) / grid + (grid > 1 ? kJoinPages : 0);
+    int64_t best = (pages + grid - 1) / grid + (grid > 1 ? 10 + 3 * (grid / units) / 10 : 0);
     for (int c = kMaxCluster; c >= 2; c /= 2) {
-        const int64_t cost = (max_pages + c) / c + kClusterPages;
+        const int64_t cost = (max_pages + c) / c + 2;
         if (cost >= best || units > resident_clusters(c)) continue;
         best = cost;
         w.cluster = c;
