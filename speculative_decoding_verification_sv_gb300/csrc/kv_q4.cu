@@ -10,6 +10,17 @@
 // back the words of an octet that was partly filled before, and writes each
 // word once.  No two warps of a launch share a word, and none waits for
 // another.
+//
+// Measured.  append, 4 x 1024 new rows of 4 heads at position 7168: 8 us of a pass,
+// bound by the chain that finds an octet's place, loads its rows and angles, quantises
+// and (at the ends of a sequence) merges; the rows are all sent for before the first
+// is looked at, and the scales are formed once a lane for eight rows (quantising row
+// by row took 15 us under the profiler, this 11.6).  gather, 32768 rows of 4 heads back
+// to bf16: 15 us, 4.6 TB/s read and written, bound by the stores.  commit, 16 sequences
+// of 28 layers: 15 us under the profiler, for one sequence 6 us: bound by the sequence
+// with the most octets, whose cluster of eight CTAs takes seven rounds of them.  A
+// warp an octet over the whole grid, with the lengths advanced by a second launch, took
+// 4 us less for 16 sequences, 1 us more for one, and a launch more on the host.
 #include <cooperative_groups.h>
 
 #include "kv_append.cuh"
