@@ -394,7 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if constexpr (kCluster) pdl_launch_dependents();
     const uint32_t tmem = *tmem_s;
     const int q4 = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
@@ -692,6 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
             named_barrier(1, 32 * kSoftWarps);
         };
         if (early) pdl_wait();
+        // A cluster's successor may start now.  (Not before the wait: the successor may
+        // read a cache that only this kernel's predecessor must not be writing.)
+        if constexpr (kCluster) pdl_launch_dependents();
         const int hh = warp >> 2;              // rows hh * kRT .. of the tile
         const int l = q4 * 32 + lane;          // key of the step; dim in the epilogue
         const int tid = threadIdx.x;

@@ -269,6 +269,71 @@ def test_a_stream_given(sv):
     assert all(torch.equal(x, y) for x, y in zip(*got))
 
 
+def test_cache_ready_sees_what_came_before_the_last_kernel(sv):
+    """cache_ready allows reading the cache under the preceding kernel, not under
+    the one before that: a commit, an unrelated attention, then one over the
+    committed cache."""
+    r = np.random.default_rng(9)
+    layers, b, n, mp = 28, 8, 9, 8
+    P = b * mp
+    table = i32(np.arange(P).reshape(b, mp))
+    pools = [torch.from_numpy(random_pool(r, layers, P, H, is_v=x)).cuda() for x in (False, True)]
+    keep = [p.clone() for p in pools]
+    blk = [torch.randn(layers, b, H, n, 128, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    mk = lambda *s: bf(r.standard_normal(s)).cuda()  # noqa: E731
+    q, kb, vb = mk(b, R, HQ, 128), mk(b, H, R, 128), mk(b, H, R, 128)
+    other = [torch.from_numpy(random_pool(r, 2, H, is_v=x)).cuda() for x in (False, True)]
+    small = (mk(1, R, HQ, 128), *other, i32([[0, 1]]), i32([100]), mk(1, H, R, 128), mk(1, H, R, 128))
+    length, start = i32([100 + 30 * i for i in range(b)]), i32([100 + 30 * i for i in range(b)])
+    path, n_acc = i32([list(range(n))] * b), i32([n - 1] * b)
+
+    def chain(ready, sync):
+        sv.kv_commit_q4(*pools, table, *blk, path, n_acc, length)
+        sync()
+        sv.verify_attn_q4(*small)
+        sync()
+        return sv.verify_attn_q4(q, pools[0][-1], pools[1][-1], table, length, kb, vb, cache_ready=ready)
+
+    def reset():
+        length.copy_(start)
+        for p, k in zip(pools, keep):
+            p.copy_(k)
+    want = chain(False, torch.cuda.synchronize)
+    reset()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        got = chain(True, lambda: None)
+    for _ in range(30):
+        reset()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert sv.get_device_error() == 0
+
+
+def test_outputs_are_ordinary_tensors(sv):
+    """Under inference mode and outside, the outputs can be written, viewed and
+    dropped one by one."""
+    r = np.random.default_rng(11)
+    kp, vp = (torch.from_numpy(random_pool(r, 1, 2, H, is_v=x)).cuda() for x in (False, True))
+    want = sv.kv_gather_q4(kp, vp, i32([[0, 1]]), i32([0]), i32([100]), 70)
+    for mode in (torch.inference_mode, torch.no_grad, torch.enable_grad):
+        with mode():
+            k, v = sv.kv_gather_q4(kp, vp, i32([[0, 1]]), i32([0]), i32([100]), 70)
+            assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and k.is_contiguous() and v.is_contiguous()
+            k.view(-1)[0] = 5.0
+            v.mul_(2)
+            assert torch.equal(v, want[1] * 2) and k[0, 0, 0, 0, 0] == 5
+            assert not k.requires_grad and k.dtype == torch.bfloat16
+            del k
+            assert torch.equal(v, want[1] * 2)
+            out = sv.verify_attn_q4(bf(r.standard_normal((1, R, HQ, 128))).cuda(), kp[0], vp[0], i32([[0, 1]]), i32([100]),
+                                    bf(r.standard_normal((1, H, R, 128))).cuda(), bf(r.standard_normal((1, H, R, 128))).cuda())
+            out.add_(1)
+
+
 # ---------------------------------------------------------------------------
 # refusals of the binding
 # ---------------------------------------------------------------------------
