@@ -150,9 +150,16 @@ at::Tensor workspace(const Args& a, size_t bytes) {
     if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return a.empty({n}, at::kByte);
     static auto* mu = new std::mutex;
     static auto* kept = new std::map<std::pair<int, void*>, at::Tensor>;
+    const std::pair<int, void*> key{a.device.index(), a.stream()};
+    at::Tensor t;
+    {
+        const std::lock_guard<std::mutex> lock(*mu);
+        t = (*kept)[key];
+    }
+    if (t.defined() && t.numel() >= n) return t;
+    t = a.empty({n}, at::kByte);
     const std::lock_guard<std::mutex> lock(*mu);
-    at::Tensor& t = (*kept)[{a.device.index(), a.stream()}];
-    if (!t.defined() || t.numel() < n) t = a.empty({n}, at::kByte);
+    (*kept)[key] = t;
     return t;
 }
 
