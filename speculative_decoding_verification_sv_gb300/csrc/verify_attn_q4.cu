@@ -81,7 +81,7 @@ constexpr int kPBufs = 4;
 constexpr int kPBytes = kStepKeys * kRows * 2;
 constexpr int kOffRing = kOffP + kPBufs * kPBytes;
 constexpr int kOffBar = kOffRing + kStages * kStageBytes;
-constexpr int kOffNm = kOffBar + 256;                     // [64] -m, m the rows' references
+constexpr int kOffNm = kOffBar + 272;                     // [64] -m, m the rows' references
 constexpr int kOffMove = kOffNm + kRows * 4;              // [64] what O and l of the row are multiplied by
 constexpr int kOffRed = kOffMove + kRows * 4;             // [4 quadrants][64]
 constexpr int kOffBad = kOffRed + 4 * kRows * 4;          // [kStages] pages of the stage outside the pool
@@ -354,9 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
     uint64_t* pv_done = p_full + kPBufs;               // [2] O^T has the step (P and the V operand read)
     uint64_t* q_ready = pv_done + 2;              // [2] query rows there
     uint64_t* q_free = q_ready + 2;               // [2] the run's S^T are formed
-    uint64_t* o_free = q_free + 2;               // O^T read by the epilogue
-    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(o_free + 1);
-    static_assert((2 * kStages + 15 + kPBufs) * 8 + 4 <= 256, "barrier area");
+    uint64_t* o_free = q_free + 2;                // O^T read by the epilogue
+    uint64_t* o_done = o_free + 1;                // O^T has the run's last step (pv_done is no help there: two
+                                                  // of its phases may be missing, and a wait passes at once)
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(o_done + 1);
+    static_assert((2 * kStages + 16 + kPBufs) * 8 + 4 <= 272, "barrier area");
     float* nm_s = reinterpret_cast<float*>(smem + kOffNm);
     float* move_s = reinterpret_cast<float*>(smem + kOffMove);
     float* red_s = reinterpret_cast<float*>(smem + kOffRed);
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
         }
         for (int i = 0; i < kPBufs; ++i) mbar_init(&p_full[i], kSoftWarps);
         mbar_init(o_free, kSoftWarps);
+        mbar_init(o_done, 1);
         fence_mbar_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_s, kTmemCols);
@@ -508,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                         for (int kc = 0; kc < kStepKeys / 16; ++kc)
                             tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || st > 0) ? 1u : 0u);
                         tc_commit(&pv_done[x]);
+                        if (st == n - 1) tc_commit(o_done);
                     }
                 }
                 __syncwarp();
@@ -909,14 +913,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                              : walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
                 soft_sync();
                 bool bad = false;
+                float lsum = 0.f;
                 if (tid < kLive) {
-                    const float lsum =
-                        (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
+                    lsum = (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
                     bad = !(lsum < kMostSum);
-                    if (rec) *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * tid) = make_float2(-nm_s[tid], lsum);
                     move_s[tid] = lsum != 0.f ? 1.0f / lsum : 0.f;
                 }
-                wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+                wait(o_done, seg & 1);
+                // (a cluster's partial overwrites the ring: only now have all pages been read)
+                if (rec && tid < kLive)
+                    *reinterpret_cast<float2*>(rec + kRows * kQ4D + 2 * tid) = make_float2(-nm_s[tid], lsum);
                 tc_fence_after();
                 soft_sync();
 #pragma unroll

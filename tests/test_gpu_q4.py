@@ -268,6 +268,50 @@ def test_attn_bad_inputs_are_reported(sv):
     assert sv.get_device_error() == 0x10
 
 
+@pytest.mark.parametrize("B,R,Hq,H,t", [
+    (1, 1, 28, 4, 7744), (1, 1, 28, 4, 8192), (9, 1, 8, 8, 2160), (6, 23, 12, 2, 4000), (4, 1, 4, 1, 9400), (1, 38, 32, 8, 4111),
+    (16, 3, 28, 4, 2286), (2, 1, 28, 4, 9927)])
+def test_attn_many_steps(sv, B, R, Hq, H, t):
+    """Runs long enough that every ring stage is used again: each group of 32 dims
+    within twice what rounding P and the output leave at random (halves of 2^-8 of
+    their magnitudes, uniform: / sqrt(3)), its root mean square over the rows."""
+    q, (kp, vp), table, kb, vb = _device_inputs(B, R, Hq, H, t, seed=t)
+    lens = i32([t - 29 * b for b in range(B)])
+    k, v = sv.kv_gather_q4(kp[None], vp[None], table, i32([0] * B), lens, t)
+    out = sv.verify_attn_q4(q, kp, vp, table, lens, kb, vb)
+    see = torch.cat([torch.arange(t, device="cuda")[None, :] < lens[:, None],
+                     torch.ones(B, R, dtype=torch.bool, device="cuda")], 1)[:, None, :].repeat(1, R, 1)
+    see[:, :, t:] = torch.tril(torch.ones(R, R, dtype=torch.bool, device="cuda"))
+    for h in range(H):
+        kk, vv = (torch.cat([c[0, :, h].double(), n[:, h].double()], 1) for c, n in ((k, kb), (v, vb)))
+        z = torch.einsum("brgd,bkd->brgk", q.view(B, R, H, Hq // H, 128)[:, :, h].double(), kk) * 128 ** -0.5
+        p = torch.softmax(z.masked_fill(~see[:, :, None, :], float("-inf")), -1)
+        want = torch.einsum("brgk,bkd->brgd", p, vv)
+        err = out.view(B, R, H, Hq // H, 128)[:, :, h].double() - want
+        rms = lambda x: x.pow(2).reshape(B, R, Hq // H, 4, 32).mean((1, 2, 4)).sqrt()  # noqa: E731
+        rounded = 2.0 ** -8 / 3 ** 0.5 * torch.sqrt(rms(want) ** 2 + torch.einsum("brgk,bkd->brgd", p ** 2, vv ** 2).reshape(
+            B, R, Hq // H, 4, 32).mean((1, 2, 4)))
+        assert bool((rms(err) <= 2 * rounded + 1e-6).all()), float((rms(err) / rounded).max())
+    assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("B,R,Hq,H,t", [(9, 1, 8, 8, 2160), (6, 23, 12, 2, 16353), (1, 1, 28, 4, 7840), (14, 3, 12, 2, 4617)])
+def test_attn_repeats_itself(sv, B, R, Hq, H, t):
+    """The same call gives the same bits, with its inputs in L2 or not (the last
+    product's end has to be waited for however late it is)."""
+    q, (kp, vp), table, kb, vb = _device_inputs(B, R, Hq, H, t, seed=t)
+    lens = i32([t - 31 * b for b in range(B)])
+    flush = torch.empty(2 ** 28, dtype=torch.uint8, device="cuda")
+    want = sv.verify_attn_q4(q, kp, vp, table, lens, kb, vb)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        if i % 2:
+            flush.fill_(i % 251)
+        differ += (sv.verify_attn_q4(q, kp, vp, table, lens, kb, vb) != want).any()
+    assert int(differ) == 0
+    assert sv.get_device_error() == 0
+
+
 def _device_inputs(B, R, Hq, H, t, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
     mp = (t + 63) // 64
