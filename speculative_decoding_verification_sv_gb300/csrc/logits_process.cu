@@ -438,10 +438,12 @@ template <bool kVec, bool kKeys>
 cudaError_t launch_logits(const LogitsArgs& a, int slice, size_t smem, cudaStream_t st) {
     static PerDeviceOnce once;
     const cudaError_t e = once.run([]() {
-        return cudaFuncSetAttribute(logits_kernel<kVec, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 10 + kWarps * kChunk * 4);
+        return cudaFuncSetAttribute(logits_kernel<kVec, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMaxSlice * 10 + kWarps * kChunk * 4);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(logits_kernel<kVec, kKeys>, dim3(static_cast<unsigned int>((a.V + slice - 1) / slice) * a.B), dim3(kThreads), smem, st, a, slice);
+    const unsigned int ctas = static_cast<unsigned int>((a.V + slice - 1) / slice) * a.B;
+    return launch_pdl(logits_kernel<kVec, kKeys>, dim3(ctas), dim3(kThreads), smem, st, a, slice);
 }
 
 }  // namespace

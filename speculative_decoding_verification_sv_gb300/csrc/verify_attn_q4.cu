@@ -40,10 +40,10 @@
 // Measured.  16 x 9 rows of 28 heads over 4, 8192 positions: 36.7 us, 461 TFLOP/s and
 // 2.1 TB/s of the cache's 76 MB: bound by the schedulers, about 4660 warp instructions
 // a step of 128 keys (16384 codes of K and 16384 of V unpacked, 8192 exponentials), most
-// of them on pipes that take one every other cycle (54% of all issue slots), at 0.65 us
-// a step.  One sequence of 5 rows, 12 heads over 2, 4096
-// positions: 10.5 us, a chain of latencies: 2 us until the first page is there, 3 us for
-// five steps, 1.5 us for the last sums and O, 3 us for the cluster's join and end.
+// of them on pipes that take one every other cycle (54% of all issue slots), at 0.7 to 1
+// us a step.  One sequence of 5 rows, 12 heads over 2, 4096 positions: 10.5 us, a chain of
+// latencies: 2 us until the first page is there, 3 us for five steps, 1.5 us for the last
+// sums and O, 3 us for the cluster's join and end.
 #include <cooperative_groups.h>
 #include <math.h>
 
