@@ -584,8 +584,9 @@ SV_API sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t
  * K and V stay bf16).  The cache's values enter the products exactly; otherwise
  * numerics, masks, flags and errors are those of sv_verify_attn_paged.  The
  * workspace (sv_verify_attn_q4_workspace bytes, any contents, possibly 0) may
- * be shared by calls in stream order; calls running concurrently, and captured
- * graphs that may, need their own. */
+ * be shared by calls in stream order.  A call that has one makes two launches:
+ * threads that call on one stream at the same time, calls running concurrently,
+ * and captured graphs that may, need their own. */
 SV_API size_t sv_verify_attn_q4_workspace(const sv_attn_shape* shape);
 SV_API sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool,
                                    const void* v_pool, int32_t num_pages, const int32_t* page_table,

@@ -11,7 +11,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -20,9 +19,6 @@
 
 #include <array>
 #include <cmath>
-#include <map>
-#include <mutex>
-#include <optional>
 #include <utility>
 
 #include "sv.h"
@@ -138,29 +134,6 @@ void enqueue(const char* fn, F&& f) {
     Py_XDECREF(r);
     if (r) PyErr_Format(PyExc_RuntimeError, "%s: status %d", fn, static_cast<int>(s));
     throw python_error();
-}
-
-// Scratch for a call that was given none.  Eager calls keep one per stream,
-// grown as needed: they use it in stream order, as the memory of a tensor freed
-// and allocated again there would be.  A call that is being captured gets memory
-// of its own: its graph may be replayed beside others.  (Never destroyed: the
-// process may end after CUDA has.)
-at::Tensor workspace(const Args& a, size_t bytes) {
-    const auto n = static_cast<int64_t>(bytes);
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return a.empty({n}, at::kByte);
-    static auto* mu = new std::mutex;
-    static auto* kept = new std::map<std::pair<int, void*>, at::Tensor>;
-    const std::pair<int, void*> key{a.device.index(), a.stream()};
-    at::Tensor t;
-    {
-        const std::lock_guard<std::mutex> lock(*mu);
-        t = (*kept)[key];
-    }
-    if (t.defined() && t.numel() >= n) return t;
-    t = a.empty({n}, at::kByte);
-    const std::lock_guard<std::mutex> lock(*mu);
-    (*kept)[key] = t;
-    return t;
 }
 
 void want(Py_ssize_t got, Py_ssize_t n) { TORCH_CHECK_TYPE(got == n, "expected ", n, " arguments, got ", got); }
@@ -342,7 +315,9 @@ PyObject* verify_attn_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
         TORCH_CHECK_VALUE(ws.device() == a.device && ws.is_contiguous() && ws.nbytes() >= bytes,
                           "ws must be contiguous, on ", a.device, " and hold ", bytes, " bytes");
     } else if (bytes > 0) {
-        ws = workspace(a, bytes);
+        // This call's own until both of its launches are enqueued: a thread that makes a
+        // call on the same stream can come between them.
+        ws = a.empty({static_cast<int64_t>(bytes)}, at::kByte);
     }
     Output out = output(a, o[9], "out", at::kBFloat16, {B, R, Hq, D});
     enqueue("sv_verify_attn_q4", [&] {

@@ -1,6 +1,7 @@
 """The cache and logits calls together, as a server makes them: prompts filled in,
 verify rounds over the 4-bit cache with the sampling controls and the acceptance,
 eager, captured and on other streams; and where offsets pass 32 bits."""
+import sys
 import threading
 
 import numpy as np
@@ -242,6 +243,60 @@ def test_two_threads_at_once(sv):
         for x, y in zip(alone[i], together[i]):
             assert all(torch.equal(p, q) for p, q in zip(x, y))
     assert sv.get_device_error() == 0
+
+
+def _split_attention(sv, seed, n):
+    """n calls (their q's and results) whose pages are split over all SMs, so that
+    each makes two launches with scratch between them."""
+    r = np.random.default_rng(seed)
+    P, t = 260, 16600
+    kp, vp = (torch.from_numpy(random_pool(r, P, H, is_v=x)).cuda() for x in (False, True))
+    mk = lambda *s: bf(r.standard_normal(s)).cuda()  # noqa: E731
+    rest = (kp, vp, i32([list(range(P))]), i32([t]), mk(1, H, R, 128), mk(1, H, R, 128))
+    assert sv.verify_attn_q4_workspace(1, R, HQ, H, 128, P * 64) > 0
+    qs = [mk(1, R, HQ, 128) for _ in range(n)]
+    want = [sv.verify_attn_q4(q, *rest) for q in qs]
+    torch.cuda.synchronize()
+    return qs, rest, want
+
+
+def test_two_threads_on_one_stream(sv):
+    """Threads that share a stream (torch's default one) come between each other's
+    launches: each call's scratch is its own."""
+    qs, rest, want = _split_attention(sv, 12, 4)
+    start, differ = threading.Barrier(len(qs)), [None] * len(qs)
+    outs = [[torch.empty_like(want[0]) for _ in range(1500)] for _ in qs]
+
+    def work(i):
+        start.wait()
+        for o in outs[i]:
+            sv.verify_attn_q4(qs[i], *rest, out=o)
+        differ[i] = (torch.stack(outs[i]) != want[i]).flatten(1).any(1).sum()
+    th = [threading.Thread(target=work, args=(i,)) for i in range(len(qs))]
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)      # (threads that wait for the interpreter get it soon)
+    for t in th:
+        t.start()
+    for t in th:
+        t.join()
+    sys.setswitchinterval(interval)
+    torch.cuda.synchronize()
+    assert [int(d) for d in differ] == [0] * len(qs)
+    assert sv.get_device_error() == 0
+
+
+def test_scratch_is_given_back(sv):
+    """What a call took for its scratch is free again afterwards, on every stream."""
+    qs, rest, want = _split_attention(sv, 13, 1)
+    before = torch.cuda.memory_allocated()
+    for _ in range(3):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out = sv.verify_attn_q4(qs[0], *rest)
+            torch.cuda.current_stream().synchronize()
+            assert torch.equal(out, want[0])
+            del out
+            torch.cuda.current_stream().synchronize()
+    assert torch.cuda.memory_allocated() == before
 
 
 def test_a_stream_given(sv):
