@@ -6,9 +6,11 @@
 // len[b] on.  Pure movement: 1 KB read and 1 KB written per row and pair of KV
 // heads.  Bound by the chain of loads that finds a row's place (offsets, length,
 // page), three rounds of warps an SM deep for a long prompt: 8 x 2048 rows of 4
-// heads take 13.9 us (4.6 TB/s), 64 single tokens 2.7 us.  With the row sent for
-// only after its place was known it was 16.1 us; with more warps an SM (48, for
-// spills) 15.1 us; a thread a 16-byte piece in place of a warp a row 26 us.
+// heads take 14.1 us (4.5 TB/s), 64 single tokens 3.0 us.  A row is sent for once
+// it is known to be no padding (the first offset and the last one, a round trip that
+// costs single tokens 0.3 us) and before its place is: sent for after that, the
+// prompts took 16.1 us; with more warps an SM (48, for spills) 15.1 us; a thread a
+// 16-byte piece in place of a warp a row 26 us.
 #include "kv_append.cuh"
 #include "sv_internal.h"
 
@@ -43,6 +45,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, uint1
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (row >= a.N) return;
+    // padding is not read
+    if (row < __ldg(a.row_off) || row >= __ldg(a.row_off + a.B)) return;
     // the row itself is sent for before its place is known
     const uint16_t* vrow = a.v + static_cast<int64_t>(row) * a.v_stride;
     const uint16_t* krow = a.k + static_cast<int64_t>(row) * a.k_stride;

@@ -191,3 +191,29 @@ def test_empty_append_does_nothing(sv):
     pool = torch.ones(3, 2, 64, 128, dtype=torch.bfloat16, device="cuda")
     sv.kv_append_paged(e, e, i32([0, 0]), pool, pool.clone(), i32([[0, 1]]), i32([3]))
     assert bool((pool == 1).all())
+
+
+def test_padding_rows_are_not_read(sv):
+    """Rows before the first sequence and behind the last are left alone.  The rows
+    lie in host memory here, which takes many times a launch's time to read."""
+    N, D = 1 << 17, 1024
+    rows = torch.zeros(N, 1, D, dtype=torch.bfloat16).pin_memory()
+    pages = N // 64
+    kp, vp = (torch.zeros(pages, 1, 64, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table, length = i32(np.arange(pages)[None]), i32([0])
+
+    def us(off):
+        off, best = i32(off), float("inf")
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            assert sv.lib.sv_kv_append_paged(rows.data_ptr(), rows.data_ptr(), D, D, N, off.data_ptr(), 1, 1, D, None, 0, 0, kp.data_ptr(),
+                                             vp.data_ptr(), pages, table.data_ptr(), pages, length.data_ptr(), 0,
+                                             torch.cuda.current_stream().cuda_stream) == 0
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) * 1e3)
+        return best
+    real, before, behind = us([0, N]), us([N - 3, N]), us([0, 3])
+    assert max(before, behind) < real / 4, (real, before, behind)
+    assert sv.get_device_error() == 0
