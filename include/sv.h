@@ -516,7 +516,9 @@ SV_API sv_status sv_copy(void* dst, const void* src, size_t bytes, void* stream)
  * A row whose position is negative, at or past max_pages * 64 or past the rope
  * table is dropped (SV_DEVERR_LENGTH), as is one whose page lies outside the
  * pool (SV_DEVERR_PAGE) and every row of a sequence whose offsets fall or leave
- * [0, N] (SV_DEVERR_ROWS).  Everything else in the pools stays as it is.
+ * [0, N] (SV_DEVERR_ROWS).  Where offsets fall, other sequences can name the same
+ * rows: some of those may be dropped too, but none lands at a place not its own.
+ * Everything else in the pools stays as it is.
  * Sequences of one call may not share a page that one of them appends to.
  * N = 0 does nothing. */
 #define SV_ROPE_INTERLEAVED 1u

@@ -43,6 +43,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, uint1
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
+    const uint32_t row_blocks = (a.N - 1) / (kThreads / 32) + 1;
+    if (blockIdx.x >= row_blocks) {
+        check_rows(a, (blockIdx.x - row_blocks) * kThreads + threadIdx.x);
+        return;
+    }
     const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (row >= a.N) return;
     // padding is not read
@@ -73,11 +78,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, uint1
     const int b = warp_last_at_most(a.B, row, [&](int i) { return static_cast<int64_t>(__ldg(a.row_off + i)); });
     if (b < 0) return;
     int r0, r1;
-    if (!append_rows(a, b, r0, r1)) {
-        if (lane == 0) raise_error(a.err, SV_DEVERR_ROWS);
-        return;
-    }
-    if (row < r0 || row >= r1) return;
+    if (!append_rows(a, b, r0, r1) || row < r0 || row >= r1) return;
     const int t = __ldg(a.len + b);
     const int64_t p = static_cast<int64_t>(t) + (row - r0);
     if (t < 0 || p >= a.cap) {
@@ -145,8 +146,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, uint1
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs& a, uint16_t* k_pool, uint16_t* v_pool, cudaStream_t st) {
-    return launch_pdl(kv_append_kernel, dim3((a.N + kThreads / 32 - 1) / (kThreads / 32)), dim3(kThreads), 0, st, a, k_pool,
-                      v_pool);
+    const uint32_t row_blocks = (a.N - 1) / (kThreads / 32) + 1, checks = (a.B - 1) / kThreads + 1;
+    return launch_pdl(kv_append_kernel, dim3(row_blocks + checks), dim3(kThreads), 0, st, a, k_pool, v_pool);
 }
 
 }  // namespace sv

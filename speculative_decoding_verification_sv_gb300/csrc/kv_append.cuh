@@ -29,6 +29,14 @@ __device__ __forceinline__ bool append_rows(const AppendArgs& a, int b, int& r0,
     return r0 >= 0 && r0 <= r1 && r1 <= a.N;
 }
 
+// Reports a sequence whose offsets do not name rows, thread i sequence i.  The
+// search for a row's sequence need not meet it: blocks of their own look at all of
+// them.
+__device__ __forceinline__ void check_rows(const AppendArgs& a, uint32_t i) {
+    int r0, r1;
+    if (i < static_cast<uint32_t>(a.B) && !append_rows(a, static_cast<int>(i), r0, r1)) raise_error(a.err, SV_DEVERR_ROWS);
+}
+
 // The largest b in [0, B) with key(b) <= x, -1 where there is none; one warp,
 // 32 probes a round.  With keys out of order some b is still returned.
 template <typename F>

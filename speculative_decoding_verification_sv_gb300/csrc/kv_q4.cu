@@ -178,6 +178,11 @@ __global__ void __launch_bounds__(kThreads, 4) append_q4_kernel(AppendArgs a, ui
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
+    const uint32_t item_blocks = (items - 1) / (kThreads / 32) + 1;
+    if (blockIdx.x >= item_blocks) {
+        check_rows(a, (blockIdx.x - item_blocks) * kThreads + threadIdx.x);
+        return;
+    }
     const uint32_t it = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (it >= items) return;
     const uint32_t slot = it / (2u * a.Hkv), sub = it - slot * (2u * a.Hkv), h = sub >> 1;
@@ -185,10 +190,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_q4_kernel(AppendArgs a, ui
     const int b = warp_last_at_most(a.B, slot, first_slot);
     if (b < 0) return;
     int r0, r1;
-    if (!append_rows(a, b, r0, r1)) {
-        if (lane == 0) raise_error(a.err, SV_DEVERR_ROWS);
-        return;
-    }
+    if (!append_rows(a, b, r0, r1)) return;
     const int t = __ldg(a.len + b);
     const int64_t octet = static_cast<int64_t>(t >> 3) + (slot - first_slot(b));
     const int64_t end = static_cast<int64_t>(t) + (r1 - r0);
@@ -387,7 +389,8 @@ int64_t append_q4_items(int N, int B, int Hkv) { return (static_cast<int64_t>(N)
 
 cudaError_t launch_append_q4(const AppendArgs& a, uint8_t* k_pool, uint8_t* v_pool, cudaStream_t st) {
     const int64_t items = append_q4_items(a.N, a.B, a.Hkv);
-    return launch_pdl(append_q4_kernel, dim3(warp_grid(items)), dim3(kThreads), 0, st, a, k_pool, v_pool,
+    const uint32_t checks = (a.B - 1) / kThreads + 1;
+    return launch_pdl(append_q4_kernel, dim3(warp_grid(items) + checks), dim3(kThreads), 0, st, a, k_pool, v_pool,
                       static_cast<uint32_t>(items));
 }
 

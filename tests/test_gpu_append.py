@@ -217,3 +217,35 @@ def test_padding_rows_are_not_read(sv):
     real, before, behind = us([0, N]), us([N - 3, N]), us([0, 3])
     assert max(before, behind) < real / 4, (real, before, behind)
     assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("off,N", [
+    ([0, 20, 10, 30], 30), ([0, 4, 2], 4), ([5, 0, 0], 5), ([0, 100, 3, 130], 130), ([0, 3, 3, 1, 3], 9), ([0, 40, 40, 90, 20], 90),
+    (list(range(70)) + [68], 69), ([0] * 150 + [9, 2] + [9] * 150, 9), ([0, 5, -7, 5], 5), ([0, 2, 1000, 9], 9)])
+def test_offsets_that_fall_are_reported(sv, q4, off, N):
+    """Wherever they fall.  Rows of the sequences whose offsets name rows land at
+    their places or, where the offsets fall, nowhere."""
+    H, D, B, mp = 1, 128, len(off) - 1, 3
+    r = np.random.default_rng(N)
+    k, v = ref.bf16_round(r.standard_normal((2, N, H, D)))
+    P = B * mp
+    table, length = r.permutation(P).reshape(B, mp).astype(np.int32), r.integers(0, 50, B).astype(np.int32)
+    pools = [torch.zeros(*((P, H, ref.Q4) if q4 else (P, H, 64, D)), dtype=torch.uint8 if q4 else torch.bfloat16, device="cuda")
+             for _ in range(2)]
+    (sv.kv_append_q4 if q4 else sv.kv_append_paged)(bf(k).cuda(), bf(v).cuda(), i32(off), *pools, i32(table), i32(length))
+    assert sv.get_device_error() == 0x01000000
+    good = [b for b in range(B) if 0 <= off[b] <= off[b + 1] <= N]
+    for pool, x, is_v in ((pools[0], k, False), (pools[1], v, True)):
+        rows = ref.get_rows(pool.cpu().numpy(), is_v)[:, 0] if q4 else pool[:, 0].double().cpu().numpy()
+        free = np.ones((P, 64), bool)
+        if q4:
+            c, s = ref.quantise(x[:, 0])
+            x = ((c - 8) * s[..., None]).reshape(N, 1, D)
+        for b in good:
+            for i in range(off[b], off[b + 1]):
+                p = int(length[b]) + i - off[b]
+                got = rows[table[b, p // 64], p % 64]
+                free[table[b, p // 64], p % 64] = False
+                assert np.array_equal(got, x[i, 0]) or not got.any(), (b, i)
+        assert not rows[free].any()
