@@ -503,7 +503,7 @@ SV_API sv_status sv_copy(void* dst, const void* src, size_t bytes, void* stream)
  *              apart (multiples of 8, at least Hkv * D: slices of a fused
  *              projection are fine); rows outside every sequence (padding
  *              before row_off[0] or from row_off[B] on) are not read
- *   row_off    [B + 1] int32, non-decreasing, within [0, N]
+ *   row_off    [B + 1] int32, non-decreasing, within [0, N]; 1 <= B <= 2^30
  *   rope       NULL (K copied as it is) or [rope_positions][rot] fp32: for each
  *              position the rot / 2 cosines, then the rot / 2 sines of its
  *              angles.  Dims d and d + rot/2 (or, with SV_ROPE_INTERLEAVED, 2d

@@ -387,7 +387,8 @@ static sv_status append_args(sv::AppendArgs& a, const uint16_t* k, const uint16_
     if (!k || !v || !row_off || !k_pool || !v_pool || !page_table || !len) return SV_ERR_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool) || (rope && !aligned16(rope)))
         return SV_ERR_ARG;
-    if (B < 1 || Hkv < 1 || Hkv > 65535 || D < 8 || D % 8 || D > 1024 || num_pages < 1 || max_pages < 1)
+    // (B: the search over the offsets rounds it up to a multiple of 32)
+    if (B < 1 || B > (1 << 30) || Hkv < 1 || Hkv > 65535 || D < 8 || D % 8 || D > 1024 || num_pages < 1 || max_pages < 1)
         return SV_ERR_SHAPE;
     if (static_cast<int64_t>(max_pages) * SV_KV_PAGE > 2147483647) return SV_ERR_SHAPE;
     const int64_t row = static_cast<int64_t>(Hkv) * D;

@@ -97,6 +97,12 @@ def test_append_head_dim_refusals():
     assert _append(D=12) == SHAPE and _append(D=2048, ks=4096, vs=4096) == SHAPE
 
 
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("B", [2 ** 30 + 1, 2 ** 31 - 1])
+def test_append_refuses_sequences_past_its_search(q4, B):
+    assert _append(q4, B=B) == SHAPE
+
+
 @pytest.mark.parametrize("at,val,want", [
     (0, None, ARG), (1, ODD, ARG), (2, 0, SHAPE), (3, None, ARG), (4, 0, SHAPE), (5, ODD, ARG), (7, 0, SHAPE), (8, 0, SHAPE),
     (9, 0, SHAPE), (10, 129, SHAPE), (10, 0, SHAPE), (11, None, ARG), (13, None, ARG), (4, 2 ** 26, SHAPE)])
