@@ -262,14 +262,14 @@ SV_API sv_status sv_lm_head_argmax(const uint16_t* hid, const uint16_t* W, float
  *                                      of v is 0 (NaN and infinity included)
  * Every control is optional (NULL).
  *   logits     [B][R][V] fp32, 1 <= B <= 65535, 1 <= R <= 128, 1 <= V <= 2^24
- *   hist       [B][hist_cap] int32, hist_len [B]: the tokens before the block
- *              (the pending token tok[b][0] is not among them); prompt_len [B]
- *              or NULL (no prompt)
+ *   hist       [B][hist_cap] int32, hist_len [B], hist_cap <= 2^28: the tokens
+ *              before the block (the pending token tok[b][0] is not among
+ *              them); prompt_len [B] or NULL (no prompt)
  *   tok, parent  the block, as for sv_accept_greedy
  *   repetition, frequency, presence  [B] fp32
  *   bias_off   [B + 1] int32, bias_tok, bias_val [n_bias]: sequence b's entries
  *              bias_off[b] .. bias_off[b+1] - 1; of a token named twice the
- *              later entry holds
+ *              later entry holds; n_bias <= 2^30
  *   mask       [B][R][ceil(V / 32)] words, bit v % 32 of word v / 32 set where
  *              the row allows v; bits past V are ignored
  *   mask_value not NaN; a finite one (such as -1e30) keeps a masked row valid for

@@ -534,7 +534,7 @@ sv_status sv_logits_process(const float* logits, int32_t B, int32_t R, int32_t V
     // counts share a word with three flags
     if (hist && (hist_cap < 1 || hist_cap > (1 << 28))) return SV_ERR_SHAPE;
     if (parent && !tok) return SV_ERR_ARG;
-    if (bias_off && n_bias < 0) return SV_ERR_SHAPE;
+    if (bias_off && (n_bias < 0 || n_bias > (1 << 30))) return SV_ERR_SHAPE;   // (entries are walked in strides)
     if (bias_off && n_bias > 0 && (!bias_tok || !bias_val)) return SV_ERR_ARG;
     if (mask_value != mask_value) return SV_ERR_ARG;
     if (argmax && argmax_bytes / sizeof(uint64_t) / B / R < (static_cast<size_t>(V) + SV_ARGMAX_SLAB - 1) / SV_ARGMAX_SLAB)

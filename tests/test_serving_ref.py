@@ -152,6 +152,11 @@ def test_logits_refusals(kw, want):
     assert _logits(**kw) == want
 
 
+@pytest.mark.parametrize("kw", [{"off": F, "bt": F, "bv": F, "nb": n} for n in (2 ** 30 + 1, 2 ** 31 - 1)] + [{"cap": 2 ** 28 + 1}])
+def test_logits_refuses_more_entries_than_it_can_walk(kw):
+    assert _logits(**kw) == SHAPE
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     bf, i32 = torch.bfloat16, torch.int32
     z = lambda *s, d=bf: torch.zeros(*s, dtype=d)  # noqa: E731
