@@ -22,7 +22,9 @@
 // a reference, the row's score with the run's first key.  bf16 and fp32 have the
 // same range, so nothing is lost by a P far above 1 as long as no sum reaches
 // kMostSum; a run where one does (some score 60 powers of two above the first
-// key's) is done again with the reference moved to the maximum every step.
+// key's) is done again with the reference moved to the maximum every step.  So is
+// one where a row's sum stays below kLeastSum: its reference is a key that it does
+// not see, or 0 for a score that is not finite, and its P may all be 0.
 //
 // Work.  A unit is one (sequence, KV head, tile of 64 query rows).  Where there are
 // few of them over a short table each has a cluster of CTAs that leave their partial
@@ -65,7 +67,8 @@ constexpr int kStageBytes = 4 * kQ4Bytes; // K of two pages, V of two pages
 constexpr int kMaxR = 128;
 constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17, kQWarp = 18, kThreads = 32 * 19;
 constexpr int kGrain = 4;                 // pages a CTA takes at least (where there are as many)
-constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand
+constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand,
+constexpr float kLeastSum = 0.5f;         // and at least (a reference that the row sees gives 1)
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 256;
 constexpr int kMaxCluster = 8;
@@ -796,8 +799,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                                 if (!(seen >> (c0 + i) & 1u)) e[i] = -INFINITY;
                         }
                     };
-                    // the references (until now 0): the first key's scores (any finite number
-                    // will do: it need not be visible), or, with `safe`, the running maxima
+                    // the references (until now 0): the first key's scores where they are finite,
+                    // or, with `safe`, the running maxima.  (A row that does not see that key, or
+                    // whose score with it is not finite, may find its sum below kLeastSum.)
                     if constexpr (kGeneral) {
                         if (st == 0 && !safe) {
                             if (q4 == 0) {
@@ -916,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 float lsum = 0.f;
                 if (tid < kLive) {
                     lsum = (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
-                    bad = !(lsum < kMostSum);
+                    bad = !(lsum < kMostSum) || (lsum < kLeastSum && tid < nrows);
                     move_s[tid] = lsum != 0.f ? 1.0f / lsum : 0.f;
                 }
                 wait(o_done, seg & 1);

@@ -228,6 +228,60 @@ def test_attn_references_far_below(sv):
         assert sv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("t,H,mp", [(0, 1, 1), (0, 2, 9), (0, 2, 250), (448, 1, 7), (512, 4, 250), (70, 2, 40)])
+def test_attn_malformed_row_sees_the_cache_and_itself(sv, t, H, mp):
+    """Block row 0, which a malformed row does not see, has a score 739 powers of two
+    above that row's own, and that one 739 above the cache's; also where a CTA's run
+    holds the block alone (7 pages in a cluster of 8; 8 pages and the block laid end to
+    end in fours)."""
+    r = np.random.default_rng(t)
+    P, R = mp + 1, 2
+    table = r.permutation(P)[:mp].reshape(1, mp).astype(np.int32)
+    kp, vp = random_pool(r, P, H, is_v=False), random_pool(r, P, H, is_v=True)
+    row = np.zeros(ref.Q4, np.uint8)
+    for p in range(64):
+        ref.put_row(row, p, np.full(128, -6.0), False)
+    kp[:] = row
+    q = np.full((1, R, H, 128), 2.0)
+    kb, vb = ref.bf16_round(r.standard_normal((2, 1, H, R, 128)))
+    kb[0, :, 0], kb[0, :, 1] = 2.0, -2.0
+    out = sv.verify_attn_q4(bf(q).cuda(), torch.from_numpy(kp).cuda(), torch.from_numpy(vp).cuda(), i32(table), i32([t]), bf(kb).cuda(),
+                            bf(vb).cuda(), i32([[-1, 7]]), scale=0.5)
+    assert sv.get_device_error() == 0x10
+    n = (t + 63) // 64
+    rows = lambda pool, is_v: ref.get_rows(pool[table[0, :n]], is_v).transpose(1, 0, 2, 3).reshape(H, n * 64, 128)[:, :t]  # noqa: E731
+    want, wgt, big = ref.attention(q[0], rows(kp, False), rows(vp, True), kb[0], vb[0], np.array([[-1, -1]]), 0.5)
+    assert np.all(np.abs(out[0].double().cpu().numpy() - want) <= tol(want, wgt, big, t + R))
+
+
+def _far_below(sv, t, mp, lost):
+    """The scores of the first `lost` positions are -infinity (products past fp32),
+    all others hundreds of powers of two below 0."""
+    r = np.random.default_rng(t + mp)
+    P, R, Hq = mp + 1, 3, 4
+    table = r.permutation(P)[:mp].reshape(1, mp).astype(np.int32)
+    kp, vp = random_pool(r, P, 1, is_v=False), random_pool(r, P, 1, is_v=True)
+    for p in range(t):
+        row = np.full(128, -(2.0 ** 118)) if p < lost else ref.bf16_round(-(2.0 ** -10) * r.uniform(1, 1.01, 128))
+        ref.put_row(kp[table[0, p // 64], 0], p % 64, row, False)
+    q = np.full((1, R, Hq, 128), 2.0 ** 15)
+    kb, vb = ref.bf16_round(r.standard_normal((2, 1, 1, R, 128)))
+    kb = ref.bf16_round(-(2.0 ** -10) * r.uniform(1, 1.01, kb.shape))
+    out = sv.verify_attn_q4(bf(q).cuda(), torch.from_numpy(kp).cuda(), torch.from_numpy(vp).cuda(), i32(table), i32([t]), bf(kb).cuda(),
+                            bf(vb).cuda())
+    n = (t + 63) // 64
+    rows = lambda pool, is_v: ref.get_rows(pool[table[0, :n]], is_v).transpose(1, 0, 2, 3).reshape(1, n * 64, 128)[:, lost:t]  # noqa: E731
+    want, wgt, big = ref.attention(q[0], rows(kp, False), rows(vp, True), kb[0], vb[0], None, 128 ** -0.5)
+    assert np.all(np.abs(out[0].double().cpu().numpy() - want) <= tol(want, wgt, big, t + R))
+    assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("mp", [4, 250])
+@pytest.mark.parametrize("t", [64, 130, 200])
+def test_attn_first_score_not_finite(sv, t, mp):
+    _far_below(sv, t, mp, 1)
+
+
 def test_attn_sharp_softmax(sv):
     """Scores far apart (scale 20): the running maximum is rescaled again and
     again, and a single key takes the row."""
