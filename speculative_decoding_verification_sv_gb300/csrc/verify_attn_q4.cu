@@ -752,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                 float sums[kRT];
 #pragma unroll
                 for (int i = 0; i < kRT; ++i) sums[i] = 0.f;
+                bool found = false;   // (safe) row tid has a reference
                 const int nctx = walk.ctx_steps(), n = nctx + (walk.block ? 1 : 0);
                 auto step = [&](int st, auto general_c) {
                     constexpr bool kGeneral = decltype(general_c)::value;
@@ -838,13 +839,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
                             }
                             soft_sync();
                             if (tid < kLive) {
-                                // up, or in the first step to wherever the maximum is (not to
-                                // -inf: all scores of the row are)
+                                // up, or where no score was finite so far (P, the sum and O are
+                                // 0 then) to wherever the maximum is
                                 float d = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
                                                 fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
-                                if (d == -INFINITY || (st > 0 && d < 0.f)) d = 0.f;
+                                const bool none = d == -INFINITY;
+                                if (none || (found && d < 0.f)) d = 0.f;
                                 nm_s[tid] -= d;
-                                move_s[tid] = fast_exp2(-d);
+                                move_s[tid] = found ? fast_exp2(-d) : 1.0f;
+                                found = found || !none;
                             }
                             soft_sync();
                             if (st > 0) {

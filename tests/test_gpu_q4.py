@@ -282,6 +282,13 @@ def test_attn_first_score_not_finite(sv, t, mp):
     _far_below(sv, t, mp, 1)
 
 
+@pytest.mark.parametrize("mp", [6, 250])
+@pytest.mark.parametrize("t,lost", [(1, 1), (128, 128), (200, 128), (300, 256), (300, 300), (384, 0)])
+def test_attn_first_steps_not_finite(sv, t, lost, mp):
+    """Whole steps of 128 keys whose scores are all -infinity come before the others."""
+    _far_below(sv, t, mp, lost)
+
+
 def test_attn_sharp_softmax(sv):
     """Scores far apart (scale 20): the running maximum is rescaled again and
     again, and a single key takes the row."""
