@@ -180,10 +180,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(LogitsArgs a, i
         if (a.hist && a.prompt_len) pl = __ldg(a.prompt_len + b);
         if (a.bias_off) o0 = __ldg(a.bias_off + b), o1 = __ldg(a.bias_off + b + 1);
         if (a.tok && tid < a.R) my_tok = __ldg(a.tok + static_cast<size_t>(b) * a.R + tid);
-        if (a.rep) rep = __ldg(a.rep + b);
-        if (a.freq) freq = __ldg(a.freq + b);
-        if (a.pres) pres = __ldg(a.pres + b);
     }
+    if (a.rep) rep = __ldg(a.rep + b);
+    if (a.freq) freq = __ldg(a.freq + b);
+    if (a.pres) pres = __ldg(a.pres + b);
 
     // Warp items of the pass over the slice: a chunk of columns of a row, a chunk's
     // rows one after the other, so that the warps share the rows of a chunk with many
@@ -323,11 +323,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(LogitsArgs a, i
             if (place_of(t) < static_cast<uint32_t>(sl.width)) atomicMax(&sl.bias[place_of(t)], static_cast<uint32_t>(i) + 1u);
         }
         if (bad_tok && report) raise_error(a.err, SV_DEVERR_TOKEN);
-        bool bad_param = false;
-        if (!(rep > 0.0f) || !isfinite(rep)) rep = 1.0f, bad_param = true;
-        if (!isfinite(freq)) freq = 0.0f, bad_param = true;
-        if (!isfinite(pres)) pres = 0.0f, bad_param = true;
-        if (bad_param && report && tid == 0) raise_error(a.err, SV_DEVERR_PARAM);
         __syncthreads();
         for (int chunk = warp; chunk < chunks; chunk += kWarps) {
             uint32_t hit = 0u;
@@ -351,6 +346,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(LogitsArgs a, i
         }
         __syncthreads();
     }
+
+    bool bad_param = false;
+    if (!(rep > 0.0f) || !isfinite(rep)) rep = 1.0f, bad_param = true;
+    if (!isfinite(freq)) freq = 0.0f, bad_param = true;
+    if (!isfinite(pres)) pres = 0.0f, bad_param = true;
+    if (bad_param && report && tid == 0) raise_error(a.err, SV_DEVERR_PARAM);
 
     // column r of the slice in row j
     auto control = [&](float y, int j, int r) {

@@ -167,3 +167,15 @@ def test_bad_inputs_are_reported(sv):
     q[0, 2] = -1
     want = ref.logits(x, **{**c, "parent": q})
     assert np.array_equal(out.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("bad", [dict(repetition=[1.0, 0.0]), dict(repetition=[-1.0, 1.0]), dict(frequency=[0.0, np.nan]),
+                                 dict(presence=[np.inf, 0.0])])
+@pytest.mark.parametrize("masked", [False, True])
+def test_bad_parameters_are_reported_without_tokens(sv, bad, masked):
+    """Also where there are no tokens that they would apply to."""
+    x = np.random.default_rng(0).standard_normal((2, 3, 1000)).astype(np.float32)
+    mask = dev(np.full((2, 3, 32), -1, np.int32)) if masked else None
+    out, _ = sv.logits_process(dev(x), mask=mask, **{k: dev(np.array(v, np.float32)) for k, v in bad.items()})
+    assert sv.get_device_error() == 0x02000000
+    assert np.array_equal(out.cpu().numpy(), x)
