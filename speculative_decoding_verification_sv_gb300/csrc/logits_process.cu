@@ -457,9 +457,10 @@ cudaError_t launch_logits_process(const LogitsArgs& a, cudaStream_t st) {
     const int chunks = (a.V + kChunk - 1) / kChunk;
     int slice = kChunk;
     int64_t best = INT64_MAX;
+    const int wave = kCtas * device_sm_count();
     for (int k = 1; k <= kMaxSlice / kChunk; ++k) {
         const int64_t ctas = static_cast<int64_t>((chunks + k - 1) / k) * a.B;
-        const int64_t cost = (ctas + kCtas * kSmCount - 1) / (kCtas * kSmCount) * (2 * k + 3);
+        const int64_t cost = (ctas + wave - 1) / wave * (2 * k + 3);
         if (cost < best) best = cost, slice = k * kChunk;
     }
     const bool counted = a.hist || a.tok || a.bias_off;
