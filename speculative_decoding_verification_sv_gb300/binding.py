@@ -4,8 +4,9 @@ cache and logits calls a CPython extension (csrc/py_calls.cpp).
 Argument marshalling only: every step of the verify round runs in the
 library's CUDA kernels.  Tensors must be CUDA tensors of the stated dtype,
 contiguous; workspaces are allocated with torch when the caller passes none.
-There is no fallback: if the library or the extension is missing or fails to
-load, importing this module raises.
+There is no fallback: if the library is missing or fails to load, importing this
+module raises, and so does the first call that needs the extension where that one
+is missing or fails to load.
 """
 from __future__ import annotations
 
@@ -110,6 +111,7 @@ def _check(fn: str, status: int):
 
 
 def _load_calls():
+    """The extension of the cache and logits calls; the other calls do without it."""
     if not os.path.exists(CALLS):
         raise ImportError(f"sv_calls.so not built ({CALLS}); run __graft_entry__.build() first")
     spec = importlib.util.spec_from_file_location("sv_calls", CALLS)
@@ -119,7 +121,14 @@ def _load_calls():
     return m
 
 
-calls = _load_calls()
+class _CallsAtFirstUse:
+    def __getattr__(self, name):
+        global calls
+        calls = _load_calls()
+        return getattr(calls, name)
+
+
+calls = _CallsAtFirstUse()
 
 
 def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):

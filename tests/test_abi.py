@@ -4,6 +4,8 @@ work is enqueued (no GPU needed)."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -164,3 +166,20 @@ def test_sample_shapes_checked(lib):
         b.accept_sample(lg, torch.zeros(1, 4, 16), tok, par)     # a tree wants 5
     with pytest.raises(ValueError):
         b.accept_sample_noalloc(lg, torch.zeros(1, 4, 16), tok, par)
+
+
+_WITHOUT_EXTENSION = """
+import pytest, torch
+from speculative_decoding_verification_sv_gb300 import build
+build.CALLS += ".missing"
+from speculative_decoding_verification_sv_gb300 import binding as sv
+assert sv.lib.sv_version() == 100
+for _ in range(2):
+    with pytest.raises(ImportError, match="not built"):
+        sv.logits_process(torch.zeros(1, 1, 8))
+"""
+
+
+def test_the_extension_is_loaded_by_the_calls_that_need_it():
+    r = subprocess.run([sys.executable, "-c", _WITHOUT_EXTENSION], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
