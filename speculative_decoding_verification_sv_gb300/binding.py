@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from .build import CALLS, LIB
+from .build import CALLS, LIB, calls_built_for, calls_target
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -114,6 +114,9 @@ def _load_calls():
     """The extension of the cache and logits calls; the other calls do without it."""
     if not os.path.exists(CALLS):
         raise ImportError(f"sv_calls.so not built ({CALLS}); run __graft_entry__.build() first")
+    if calls_built_for() != calls_target():   # (another torch's structures lie elsewhere)
+        raise ImportError(f"sv_calls.so was built for {calls_built_for()}, this is {calls_target()}; run "
+                          "__graft_entry__.build() again")
     spec = importlib.util.spec_from_file_location("sv_calls", CALLS)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)

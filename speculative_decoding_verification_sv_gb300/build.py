@@ -24,6 +24,7 @@ DEBUG = os.environ.get("SV_DEBUG", "") == "1"
 OUT_DIR = os.path.join(CSRC, "_build_debug" if DEBUG else "_build")
 LIB = os.path.join(OUT_DIR, "libsv.so")
 CALLS = os.path.join(OUT_DIR, "sv_calls.so")
+CALLS_FOR = os.path.join(OUT_DIR, "sv_calls.for")   # what it was built against
 CALLS_SRC = os.path.join(CSRC, "py_calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -52,6 +53,20 @@ def _stale(target, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def calls_target() -> str:
+    """The interpreter and the torch that the extension has to match."""
+    import torch
+    return f"Python {sys.version.split()[0]}, torch {torch.__version__}"
+
+
+def calls_built_for() -> str:
+    try:
+        with open(CALLS_FOR) as f:
+            return f.read()
+    except OSError:
+        return "an unknown Python and torch"
 
 
 def _calls_compile(obj):
@@ -85,7 +100,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             jobs.append([nvcc] + ARCH + flags + ["-c", src, "-o", obj])
 
     calls_obj = os.path.join(OUT_DIR, "py_calls.o")
-    calls = force or _stale(calls_obj, [CALLS_SRC, os.path.join(INCLUDE, "sv.h")])
+    calls = force or calls_built_for() != calls_target() or _stale(calls_obj, [CALLS_SRC, os.path.join(INCLUDE, "sv.h")])
     if calls:
         jobs.insert(0, _calls_compile(calls_obj))
 
@@ -103,9 +118,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         tmp = LIB + ".tmp"
         run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs + ["-ldl", "-lpthread", "-lrt"])
         os.replace(tmp, LIB)
-    if force or _stale(CALLS, [calls_obj]):
+    if calls or _stale(CALLS, [calls_obj]):
         run(_calls_link(calls_obj, CALLS + ".tmp"))
         os.replace(CALLS + ".tmp", CALLS)
+        with open(CALLS_FOR, "w") as f:
+            f.write(calls_target())
     return LIB
 
 

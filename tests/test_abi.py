@@ -183,3 +183,27 @@ for _ in range(2):
 def test_the_extension_is_loaded_by_the_calls_that_need_it():
     r = subprocess.run([sys.executable, "-c", _WITHOUT_EXTENSION], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+_OTHER_TORCH = """
+import pytest, torch
+from speculative_decoding_verification_sv_gb300 import binding as sv
+torch.__version__ = "2.0.0"
+with pytest.raises(ImportError, match="torch 2.0.0"):
+    sv.logits_process(torch.zeros(1, 1, 8))
+"""
+
+
+def test_an_extension_of_another_torch_is_refused_and_built_again(lib, monkeypatch):
+    from speculative_decoding_verification_sv_gb300 import build
+    r = subprocess.run([sys.executable, "-c", _OTHER_TORCH], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    made = os.stat(build.CALLS).st_mtime_ns
+    build.build()
+    assert os.stat(build.CALLS).st_mtime_ns == made      # as it is for this one
+    monkeypatch.setattr(build, "calls_target", lambda: "Python 3.12.3, torch 2.0.0")
+    ran = []
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kw: ran.append(cmd) or subprocess.CompletedProcess(cmd, 1, "", ""))
+    with pytest.raises(RuntimeError):
+        build.build()
+    assert [c[0] for c in ran] == ["g++"] and build.CALLS_SRC in ran[0]
