@@ -73,6 +73,26 @@ def test_append_matches_plain(sv, counts, length, H, rot, inter, q4):
     assert sv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("q4", [False, True])
+def test_append_many_sequences(sv, q4):
+    """Thousands of sequences, most of them without new rows: the search over the
+    offsets takes three rounds."""
+    B, H, D = 3000, 1, 128
+    r = np.random.default_rng(1)
+    counts = np.where(r.random(B) < 0.1, r.integers(1, 4, B), 0)
+    counts[[0, -1]] = 2
+    length = r.integers(0, 60, B).astype(np.int32)
+    _, off, N, table, k, v, P = make(2, counts, length, H, D, 1, extra_rows=2, first=1)
+    pools = [torch.zeros(*((P, H, ref.Q4) if q4 else (P, H, 64, D)), dtype=torch.uint8 if q4 else torch.bfloat16, device="cuda")
+             for _ in range(2)]
+    (sv.kv_append_q4 if q4 else sv.kv_append_paged)(bf(k).cuda(), bf(v).cuda(), i32(off), *pools, i32(table), i32(length))
+    zero = np.zeros((P, H, ref.Q4) if q4 else (P, H, 64, D), np.uint8 if q4 else np.uint16)
+    want = (ref.append_q4 if q4 else ref.append_bf16)(k, v, off, zero, zero, table, length, None, False, 64)
+    down = (lambda t: t.cpu().numpy()) if q4 else (lambda t: t.view(torch.int16).cpu().numpy().view(np.uint16))
+    assert all(np.array_equal(down(g), w) for g, w in zip(pools, want))
+    assert sv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("D,H,rot,inter", [(8, 3, 0, False), (16, 1, 16, True), (64, 2, 48, False), (256, 1, 256, False), (40, 2, 32, True)])
 def test_append_head_dims(sv, D, H, rot, inter):
     r, off, N, table, k, v, P = make(D, [37, 1], [60, 0], H, D, 2)

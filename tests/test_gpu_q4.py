@@ -181,6 +181,14 @@ def test_attn_tree(sv, B, R, Hq, H, lens):
     run(sv, B, R, Hq, H, lens, parent=par, seed=R)
 
 
+@pytest.mark.parametrize("B,R,Hq,H,mp", [(33, 1, 4, 2, 4), (70, 3, 4, 1, 6), (200, 1, 2, 2, 5)])
+def test_attn_many_sequences(sv, B, R, Hq, H, mp):
+    """More sequences than a warp has lanes, some of them empty."""
+    lens = np.random.default_rng(B).integers(0, mp * 64 + 1, B)
+    lens[[0, 31, 32, B - 1]] = [mp * 64, 0, 1, 0]
+    run(sv, B, R, Hq, H, lens.tolist(), seed=B, mp=mp)
+
+
 def test_attn_scale_and_capacity(sv):
     run(sv, 1, 4, 8, 2, [192], scale=0.7, seed=3)                 # a full table
     run(sv, 2, 4, 8, 2, [100, 3], scale=0.01, seed=4, mp=40)       # a table much longer than the contexts
