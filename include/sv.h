@@ -569,8 +569,9 @@ SV_API sv_status sv_kv_commit_q4(void* k_pool, void* v_pool, int32_t num_pages, 
                                  int32_t B, int32_t Hkv, int32_t R, const int32_t* path, const int32_t* n_acc,
                                  int32_t* len, void* stream);
 
-/* Reads a window of a 4-bit cache back as bf16 rows (for a prefill chunk's
- * attention over the context before it, or to move a cache to bf16):
+/* Reads a window of a 4-bit cache back as bf16 rows (to move a cache to bf16, or
+ * for an attention of the caller's over more rows than sv_verify_attn_q4 takes, as
+ * a prefill chunk's over the context before it):
  *     out[l][b][h][i] = the row at position start[b] + i,  0 <= i < n,
  * and zeros where that position is at or past len[b].
  *   k_out, v_out [L][B][Hkv][n][128] bf16, not overlapping the pools

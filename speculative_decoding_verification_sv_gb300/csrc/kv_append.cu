@@ -4,10 +4,10 @@
 // A prompt, a prefill chunk or single decoded tokens: N rows of B sequences,
 // sequence b's being rows row_off[b] .. row_off[b + 1], at the positions from
 // len[b] on.  Pure movement: 1 KB read and 1 KB written per row and pair of KV
-// heads.  Bound by the chain of loads that finds a row's place (offsets, length,
-// page), three rounds of warps an SM deep for a long prompt: 8 x 2048 rows of 4
-// heads take 14.1 us (4.5 TB/s), 64 single tokens 3.0 us.  A row is sent for once
-// it is known to be no padding (the first offset and the last one, a round trip that
+// heads.  Held up by the chain of loads that finds a row's place (offsets, length,
+// page), done for each row by itself, three rounds of warps an SM deep for a long
+// prompt: 8 x 2048 rows of 4 heads take 14.1 us (4.5 TB/s), 64 single tokens 3.0 us.
+// A row is sent for once it is known to be no padding (the first offset and the last one, a round trip that
 // costs single tokens 0.3 us) and before its place is: sent for after that, the
 // prompts took 16.1 us; with more warps an SM (48, for spills) 15.1 us; a thread a
 // 16-byte piece in place of a warp a row 26 us.

@@ -11,16 +11,18 @@
 // word once.  No two warps of a launch share a word, and none waits for
 // another.
 //
-// Measured.  append, 4 x 1024 new rows of 4 heads at position 7168: 8 us of a pass,
-// bound by the chain that finds an octet's place, loads its rows and angles, quantises
-// and (at the ends of a sequence) merges; the rows are all sent for before the first
-// is looked at, and the scales are formed once a lane for eight rows (quantising row
-// by row took 15 us under the profiler, this 11.6).  gather, 32768 rows of 4 heads back
-// to bf16: 15 us, 4.6 TB/s read and written, bound by the stores.  commit, 16 sequences
-// of 28 layers: 15 us under the profiler, for one sequence 6 us: bound by the sequence
-// with the most octets, whose cluster of eight CTAs takes seven rounds of them.  A
-// warp an octet over the whole grid, with the lengths advanced by a second launch, took
-// 4 us less for 16 sequences, 1 us more for one, and a launch more on the host.
+// Measured.  append, 4 x 1024 new rows of 4 heads at position 7168: 7.3 us, held up by
+// the chain that finds an octet's place, loads its rows and angles, quantises and (at
+// the ends of a sequence) merges; the rows are all sent for before the first is looked
+// at, and the scales are formed once a lane for eight rows (quantising row by row took
+// 15 us under the profiler, this 11.6).  gather, 32768 rows of 4 heads back to bf16: 15
+// us, 4.5 TB/s of stores, bound by them.  commit, 16 sequences of 28 layers: 12.4 us,
+// for one sequence 3.6 us: the 448 octets of a sequence whose rows lie in two (28
+// layers, 4 heads, K and V) are four rounds of the 128 warps of its cluster, each a
+// chain of the path, the row, the quantising and V's merge, and the SMs beside the 128
+// CTAs are idle.  A warp an octet over the whole grid, with the lengths advanced by a
+// second launch, took 4 us less for 16 sequences, 1 us more for one, and a launch more
+// on the host; one launch could do the same with a counter of each sequence's CTAs.
 #include <cooperative_groups.h>
 
 #include "kv_append.cuh"

@@ -17,6 +17,10 @@
 //   S^T: lane = key, column = query row.  B = Q, K-major in shared memory.
 //   P:   exp2(s - m), bf16, written by the key's thread as one line of
 //        [keys][64 rows] in shared memory, the MN-major B of the second product.
+//        (The MMA takes V and P of one type, and only bf16 holds V's scales exactly and
+//        a P above 65504.  Rounding moves a weight by at most 2^-8 of it, up or down; the
+//        row's sum is taken of P before it.  With the output's own rounding that is 0.0024 of the
+//        result, 0.0017 where P is fp32.)
 //   O^T: lane = dim, column = row.
 // A row's maximum runs across lanes here, so it is not formed: P is taken against
 // a reference, the row's score with the run's first key.  bf16 and fp32 have the
@@ -40,12 +44,16 @@
 // the query rows of the next run while the present one is worked on.
 //
 // Measured.  16 x 9 rows of 28 heads over 4, 8192 positions: 36.7 us, 461 TFLOP/s and
-// 2.1 TB/s of the cache's 76 MB: bound by the schedulers, about 4660 warp instructions
-// a step of 128 keys (16384 codes of K and 16384 of V unpacked, 8192 exponentials), most
-// of them on pipes that take one every other cycle (54% of all issue slots), at 0.7 to 1
-// us a step.  One sequence of 5 rows, 12 heads over 2, 4096 positions: 10.5 us, a chain of
-// latencies: 2 us until the first page is there, 3 us for five steps, 1.5 us for the last
-// sums and O, 3 us for the cluster's join and end.
+// 2.1 TB/s of the cache's 76 MB.  A step of 128 keys is about 4660 warp instructions
+// (16384 codes of K and 16384 of V unpacked, 8192 exponentials) and takes 0.7 to 1 us.  No
+// unit is full: 54% of the issue slots, the ALU 36%, the tensor pipe 24%, FMA 23%, LSU 21%,
+// special functions 13%; what holds a step up is that the roles wait for one another
+// and for tensor memory (of the cycles between two of a warp's instructions a third is
+// spent on such waits and barriers, an eighth each waiting for its turn to issue and for
+// the next instruction to be fetched).  With one row a sequence the same cache takes 31.4 us.
+// One sequence of 5 rows, 12 heads over 2, 4096 positions: 10.3 us, a chain of latencies:
+// 2 us until the first page is there, 3 us for five steps, 1.5 us for the last sums and O,
+// 3 us for the cluster's join and end.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -1072,9 +1080,11 @@ int resident_clusters(int c) {
 // and joined by a second kernel, or a cluster of 2, 4 or 8 CTAs for each unit, joined
 // on chip, whose barriers and remote reads cost about two pages.  The second kernel and
 // the partials' way through L2 cost about ten, and three for each ten partials of a unit.
-// Measured, cluster against even split: 5 x 12 heads over 2 of 4096 positions 10.0 and
-// 11.5 us, of 16384 17.9 and 18.8; 9 x 28 over 4, 4096: 11.2 and 13.8, 12288: 16.8 and
-// 16.7, 16384: 19.7 and 16.7; 65 x 28 over 4, 4096: 16.4 and 18.8, 8192: 22.1 and 23.5.
+// Measured, cluster against even split: 5 x 12 heads over 2 of 4096 positions 10.4 and
+// 11.8 us, of 16384 (the rule splits there) 18.1 and 19.2; 9 x 28 over 4, 4096: 11.5 and
+// 14.6, 12288: 17.4 and 17.4, 16384: 20.3 and 17.4; 65 x 28 over 4, 4096: 17.0 and 19.7,
+// 8192: 22.9 and 24.6.  The table's capacity decides, as the lengths are on the device: 5
+// x 12 heads over 4096 positions take 12.3 us with a table for 131072.
 void plan(Work& w, int B, int max_pages, int& grid) {
     const int64_t units = static_cast<int64_t>(B) * w.U, pages = units * (static_cast<int64_t>(max_pages) + 1);
     const int sms = device_sm_count();
