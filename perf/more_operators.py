@@ -10,7 +10,8 @@ The 8-bit cache: 16 positions of one head share a scale, a power of two; a value
 A (page, head) block is 8320 bytes: 8192 codes, then four fp32 scales (16 positions each), then 112 bytes of nothing.  K's
 codes are [64 positions][8 places][16 dims], dims 16 c .. of position p at place c ^ (p % 8); V's are [8 octets of
 positions][128 dims][8 positions].  The scale is the smallest 2^e, -120 <= e <= 119, with |x| <= 448 * 2^e for all that was
-written to the 16 positions since the first of them was: where later rows need a larger one, the earlier are held anew.
+written to the 16 positions since the first of them was: where later rows need a larger one, the earlier are held anew.  A
+row with NaN or infinity in it is held as NaN throughout and has no part in the scale.
 """
 import random
 
@@ -239,10 +240,8 @@ def _scale(amax):
 
 
 def _code(x, s):
-    """fp32 values -> codes (uint8); past 448 scales they are held as 448, NaN and infinity as NaN."""
-    y = (x / s).clamp(-448.0, 448.0)
-    y = torch.where(x.abs() < float("inf"), y, float("nan"))
-    return y.to(torch.float8_e4m3fn).view(torch.uint8)
+    """fp32 values -> codes (uint8); past 448 scales they are held as 448."""
+    return (x / s).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
 
 
 def _value(codes, s):
@@ -281,11 +280,13 @@ def _store8(pool, page, run, first, new, rows, is_v):
     [P, H, 8320], in place; first[N]: the run's first position is among them, so that what was there before is gone."""
     H = pool.shape[1]
     x = torch.where(new[:, :, None, None], rows.float(), 0.0).transpose(1, 2)                  # [N, H, 16, 128]
+    bad = ~(x.abs() < float("inf")).all(-1, keepdim=True)
     at = (page.long()[:, None], torch.arange(H, device=pool.device)[None, :])
     sc = pool.view(torch.float32)
     k = PAGE * D // 4 + run.long()[:, None]
     old = sc[at[0], at[1], k]
-    amax = torch.where(x.abs() < float("inf"), x.abs(), 0.0).amax((-1, -2))
+    amax = torch.where(bad, 0.0, x.abs()).amax((-1, -2))
+    x = torch.where(bad, float("nan"), x)
     s = torch.maximum(_scale(amax), torch.where(first[:, None], 0.0, old))
     place = (_places_v if is_v else _places_k)(pool.device).view(4, RUN, D)[run.long()][:, None]  # [N, 1, 16, 128]
     at = (at[0][:, :, None, None], at[1][:, :, None, None], place)
