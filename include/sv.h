@@ -14,8 +14,8 @@
  *                     update (cache length == committed-token count).
  * and, around it: the paged cache filled with rotated prompt rows
  * (sv_kv_append_paged), the same cache in 4 bits (sv_kv_append_q4,
- * sv_kv_commit_q4, sv_verify_attn_q4, sv_kv_gather_q4), and the sampling
- * controls on the block's logits (sv_logits_process).
+ * sv_kv_commit_q4, sv_verify_attn_q4, sv_kv_gather_q4) and in 8 bits (the _q8
+ * calls), and the sampling controls on the block's logits (sv_logits_process).
  *
  * Sources, cited by page title and section:
  *   [SCS]  "SpecDec-Context-Scaling project guide", sec. 3, 3.1, 3.2, 7.1
@@ -592,6 +592,68 @@ SV_API sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t
  * and captured graphs that may, need their own. */
 SV_API size_t sv_verify_attn_q4_workspace(const sv_attn_shape* shape);
 SV_API sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool,
+                                   const void* v_pool, int32_t num_pages, const int32_t* page_table,
+                                   int32_t max_pages, const int32_t* len, const uint16_t* k_blk,
+                                   const uint16_t* v_blk, const int32_t* parent, float scale, uint16_t* out, void* ws,
+                                   size_t ws_bytes, uint32_t flags, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The 8-bit paged KV cache: 128.25 bytes a row in place of 256.             */
+/* ------------------------------------------------------------------------ */
+
+/* Sixteen consecutive positions (a run: p / 16) of one KV head share an fp32 scale s
+ * = 2^e (D = 128); an element is an e4m3 code c for the value c s, which is exactly a
+ * bf16.  What this library writes has the smallest e in [-120, 119] with |x| <= 448 *
+ * 2^e for every row written to the run since its first position last was, and c = x /
+ * s rounded to nearest even (448 where x / s is more): values are off by at most 2^-4
+ * of themselves, or 2^-10 s.  A row written later that needs a larger scale has the
+ * earlier rows' codes rounded anew, from the values they held.  A row that holds NaN
+ * or infinity is held as NaN throughout (codes 0x7f), has no part in the scale and sets
+ * SV_DEVERR_NONFINITE.
+ * The pools are [num_pages][Hkv][SV_KV_Q8_BYTES] bytes, 64 positions a page, position
+ * p of sequence b in page page_table[b][p / 64] as for the bf16 pools.  A (page, head)
+ * holds 8192 bytes of codes, four fp32 scales, and 112 bytes that are not used.
+ *   codes of K  [64 positions][8 places][16 dims], dims 16 c .. of position p at
+ *               place c ^ (p % 8);
+ *   codes of V  [8 octets of positions][128 dims][8 positions]. */
+#define SV_KV_Q8_BYTES 8320
+#define SV_KV_Q8_RUN 16
+
+/* sv_kv_append_paged into an 8-bit cache (D = 128): the same rows, rotated and rounded
+ * to bf16 as there, then to e4m3.  Positions before the new ones keep their values but
+ * for the rounding above, where they share the first new row's run; positions behind
+ * the new ones in the last row's run hold nothing defined. */
+SV_API sv_status sv_kv_append_q8(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
+                                 const int32_t* row_off, int32_t B, int32_t Hkv, const float* rope,
+                                 int32_t rope_positions, int32_t rot, void* k_pool, void* v_pool, int32_t num_pages,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* len, uint32_t flags,
+                                 void* stream);
+
+/* sv_kv_commit_paged into 8-bit pools [L][num_pages][Hkv][SV_KV_Q8_BYTES] (D = 128):
+ * the accepted block rows into positions len[b] .. len[b] + n_acc[b], as
+ * sv_kv_append_q8 writes rows, then len[b] += n_acc[b] + 1.  A sequence that would pass
+ * max_pages * 64, whose path is bad or whose rows reach a page outside the pool is left
+ * untouched, length included (SV_DEVERR_LENGTH, _PATH, _PAGE). */
+SV_API sv_status sv_kv_commit_q8(void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table,
+                                 int32_t max_pages, const uint16_t* k_blk, const uint16_t* v_blk, int32_t L,
+                                 int32_t B, int32_t Hkv, int32_t R, const int32_t* path, const int32_t* n_acc,
+                                 int32_t* len, void* stream);
+
+/* sv_kv_gather_q4 from an 8-bit cache: a window of it read back as bf16 rows, with the
+ * same arguments, zeros and errors. */
+SV_API sv_status sv_kv_gather_q8(const void* k_pool, const void* v_pool, int32_t num_pages,
+                                 const int32_t* page_table, int32_t max_pages, int32_t L, int32_t B, int32_t Hkv,
+                                 const int32_t* start, const int32_t* len, int32_t n, uint16_t* k_out,
+                                 uint16_t* v_out, void* stream);
+
+/* sv_verify_attn_paged over an 8-bit cache (k_pool, v_pool as above; the block's K and
+ * V stay bf16).  The cache's values enter the products exactly; a query row, and a
+ * block row of K, enter to within 2^-17 of their largest element, and one that holds
+ * NaN or infinity as NaN; otherwise numerics, masks, flags and errors are those of
+ * sv_verify_attn_paged, and the workspace (sv_verify_attn_q8_workspace bytes, any
+ * contents, possibly 0) is as for sv_verify_attn_q4. */
+SV_API size_t sv_verify_attn_q8_workspace(const sv_attn_shape* shape);
+SV_API sv_status sv_verify_attn_q8(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool,
                                    const void* v_pool, int32_t num_pages, const int32_t* page_table,
                                    int32_t max_pages, const int32_t* len, const uint16_t* k_blk,
                                    const uint16_t* v_blk, const int32_t* parent, float scale, uint16_t* out, void* ws,

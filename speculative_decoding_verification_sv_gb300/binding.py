@@ -86,6 +86,11 @@ def _load():
     L.sv_verify_attn_q4_workspace.restype = _SZ
     L.sv_verify_attn_q4.argtypes = [_P, _P, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _F32, _P, _P, _SZ, ctypes.c_uint32,
                                     _P]
+    for q in ("append", "commit", "gather"):
+        getattr(L, f"sv_kv_{q}_q8").argtypes = getattr(L, f"sv_kv_{q}_q4").argtypes
+    L.sv_verify_attn_q8_workspace.argtypes = L.sv_verify_attn_q4_workspace.argtypes
+    L.sv_verify_attn_q8_workspace.restype = _SZ
+    L.sv_verify_attn_q8.argtypes = L.sv_verify_attn_q4.argtypes
     L.sv_logits_process.argtypes = [_P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P,
                                     _F32, _P, _P, _SZ, _P]
     L.sv_diag_exp.argtypes = [_P, _P, _I64, _P]
@@ -97,7 +102,8 @@ def _load():
                "sv_accept_sample_noalloc", "sv_kv_commit", "sv_kv_commit_paged", "sv_verify_attn_paged",
                "sv_diag_exp", "sv_diag_div", "sv_diag_philox", "sv_diag_canon", "sv_get_device_error", "sv_lm_head_argmax",
                "sv_accept_greedy_commit", "sv_accept_greedy_commit_paged", "sv_copy", "sv_kv_append_paged",
-               "sv_kv_append_q4", "sv_kv_commit_q4", "sv_kv_gather_q4", "sv_verify_attn_q4", "sv_logits_process"):
+               "sv_kv_append_q4", "sv_kv_commit_q4", "sv_kv_gather_q4", "sv_verify_attn_q4", "sv_kv_append_q8",
+               "sv_kv_commit_q8", "sv_kv_gather_q8", "sv_verify_attn_q8", "sv_logits_process"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -440,7 +446,7 @@ def copy(dst: torch.Tensor, src: torch.Tensor, stream=None) -> torch.Tensor:
 
 
 # ---------------------------------------------------------------------------
-# the paged cache filled, the 4-bit cache, sampling controls
+# the paged cache filled, the 4-bit and the 8-bit cache, sampling controls
 #
 # These calls know every argument's shape, so they check them all (the C ABI
 # cannot): TypeError or ValueError before anything is enqueued.  They launch with
@@ -448,6 +454,8 @@ def copy(dst: torch.Tensor, src: torch.Tensor, stream=None) -> torch.Tensor:
 # and take outputs and workspaces that they are not given from its memory.
 
 KV_Q4_BYTES = 4608   # bytes of one (page, head) of a 4-bit cache (SV_KV_Q4_BYTES)
+KV_Q8_BYTES = 8320   # of an 8-bit cache (SV_KV_Q8_BYTES)
+KV_Q8_RUN = 16       # positions that share a scale there (SV_KV_Q8_RUN)
 
 
 def _on(stream, like, f, *args):
@@ -464,29 +472,29 @@ def kv_append_paged(k, v, row_off, k_pool, v_pool, page_table, length, rope=None
     pools [num_pages,Hkv,64,D] bf16, page_table [B,max_pages], row_off [B+1],
     length [B] int32 (not advanced).  rope None or [positions,rot] fp32, each
     position's rot/2 cosines, then its sines: K is rotated on the way."""
-    args = (False, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
+    args = (16, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
     calls.kv_append(*args) if stream is None else _on(stream, k, calls.kv_append, *args)
 
 
 def kv_append_q4(k, v, row_off, k_pool, v_pool, page_table, length, rope=None, interleaved=False, stream=None):
     """kv_append_paged into 4-bit pools [num_pages,Hkv,4608] uint8 (D = 128)."""
-    args = (True, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
+    args = (4, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
     calls.kv_append(*args) if stream is None else _on(stream, k, calls.kv_append, *args)
 
 
 def kv_commit_q4(k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length, stream=None):
     """pools [L,num_pages,Hkv,4608] uint8; page_table [B,max_pages]; blocks [L,B,Hkv,R,128] bf16;
     path [B,R], n_acc [B], length [B] int32 (length updated in place)."""
-    args = (k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length)
-    calls.kv_commit_q4(*args) if stream is None else _on(stream, k_blk, calls.kv_commit_q4, *args)
+    args = (4, k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length)
+    calls.kv_commit(*args) if stream is None else _on(stream, k_blk, calls.kv_commit, *args)
 
 
 def kv_gather_q4(k_pool, v_pool, page_table, start, length, n, k_out=None, v_out=None, stream=None):
     """Positions start[b] .. start[b]+n-1 of every sequence of 4-bit pools
     [L,num_pages,Hkv,4608] uint8 as bf16 rows, zeros at and past length[b].
     Returns (k_out, v_out) [L,B,Hkv,n,128] bf16."""
-    args = (k_pool, v_pool, page_table, start, length, n, k_out, v_out)
-    return calls.kv_gather_q4(*args) if stream is None else _on(stream, k_pool, calls.kv_gather_q4, *args)
+    args = (4, k_pool, v_pool, page_table, start, length, n, k_out, v_out)
+    return calls.kv_gather(*args) if stream is None else _on(stream, k_pool, calls.kv_gather, *args)
 
 
 def verify_attn_q4_workspace(B, R, Hq, Hkv, D, T_cap) -> int:
@@ -499,8 +507,41 @@ def verify_attn_q4(q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent=N
     """verify_attn_paged over a 4-bit cache: pools [num_pages,Hkv,4608] uint8;
     q [B,R,Hq,128] and blocks [B,Hkv,R,128] bf16; page_table [B,max_pages],
     length [B] int32.  Returns out [B,R,Hq,128] bf16."""
-    args = (q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent, scale, out, ws, cache_ready)
-    return calls.verify_attn_q4(*args) if stream is None else _on(stream, q, calls.verify_attn_q4, *args)
+    args = (4, q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent, scale, out, ws, cache_ready)
+    return calls.verify_attn(*args) if stream is None else _on(stream, q, calls.verify_attn, *args)
+
+
+def kv_append_q8(k, v, row_off, k_pool, v_pool, page_table, length, rope=None, interleaved=False, stream=None):
+    """kv_append_paged into 8-bit pools [num_pages,Hkv,8320] uint8 (D = 128): e4m3 codes,
+    a power-of-two scale for each 16 positions of a head; earlier positions that share
+    the first new row's scale are rounded anew where it has to grow."""
+    args = (8, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
+    calls.kv_append(*args) if stream is None else _on(stream, k, calls.kv_append, *args)
+
+
+def kv_commit_q8(k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length, stream=None):
+    """kv_commit_q4 into 8-bit pools [L,num_pages,Hkv,8320] uint8."""
+    args = (8, k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length)
+    calls.kv_commit(*args) if stream is None else _on(stream, k_blk, calls.kv_commit, *args)
+
+
+def kv_gather_q8(k_pool, v_pool, page_table, start, length, n, k_out=None, v_out=None, stream=None):
+    """kv_gather_q4 from 8-bit pools [L,num_pages,Hkv,8320] uint8."""
+    args = (8, k_pool, v_pool, page_table, start, length, n, k_out, v_out)
+    return calls.kv_gather(*args) if stream is None else _on(stream, k_pool, calls.kv_gather, *args)
+
+
+def verify_attn_q8_workspace(B, R, Hq, Hkv, D, T_cap) -> int:
+    s = _AttnShape(B, R, Hq, Hkv, D, T_cap)
+    return int(lib.sv_verify_attn_q8_workspace(ctypes.byref(s)))
+
+
+def verify_attn_q8(q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent=None, scale=None, out=None, ws=None,
+                   stream=None, cache_ready=False):
+    """verify_attn_paged over an 8-bit cache: pools [num_pages,Hkv,8320] uint8; otherwise
+    as verify_attn_q4.  Returns out [B,R,Hq,128] bf16."""
+    args = (8, q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent, scale, out, ws, cache_ready)
+    return calls.verify_attn(*args) if stream is None else _on(stream, q, calls.verify_attn, *args)
 
 
 def logits_process(logits, tok=None, parent=None, hist=None, hist_len=None, prompt_len=None, repetition=None,

@@ -148,22 +148,45 @@ const uint16_t* rows(const Args& a, PyObject* o, const char* name, at::IntArrayR
     return static_cast<const uint16_t*>(t.data_ptr());
 }
 
-// (q4, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved)
+// A quantised cache: bits an element, bytes of a (page, head), and its calls.
+struct Cache {
+    int64_t bits, block;
+    const char *append_name, *commit_name, *gather_name, *attn_name;
+    decltype(&sv_kv_append_q4) append;
+    decltype(&sv_kv_commit_q4) commit;
+    decltype(&sv_kv_gather_q4) gather;
+    decltype(&sv_verify_attn_q4_workspace) workspace;
+    decltype(&sv_verify_attn_q4) attn;
+};
+const Cache g_caches[] = {
+    {4, SV_KV_Q4_BYTES, "sv_kv_append_q4", "sv_kv_commit_q4", "sv_kv_gather_q4", "sv_verify_attn_q4", sv_kv_append_q4,
+     sv_kv_commit_q4, sv_kv_gather_q4, sv_verify_attn_q4_workspace, sv_verify_attn_q4},
+    {8, SV_KV_Q8_BYTES, "sv_kv_append_q8", "sv_kv_commit_q8", "sv_kv_gather_q8", "sv_verify_attn_q8", sv_kv_append_q8,
+     sv_kv_commit_q8, sv_kv_gather_q8, sv_verify_attn_q8_workspace, sv_verify_attn_q8}};
+
+const Cache& cache(PyObject* bits) {
+    const int64_t n = whole(bits);
+    for (const Cache& c : g_caches)
+        if (c.bits == n) return c;
+    TORCH_CHECK_VALUE(false, "no cache of ", n, " bits");
+}
+
+// (bits, k, v, row_off, k_pool, v_pool, page_table, length, rope, interleaved); bits 16: the bf16 cache
 PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     want(n, 10);
-    const bool q4 = truth(o[0]);
+    const Cache* q = whole(o[0]) == 16 ? nullptr : &cache(o[0]);
     const at::Tensor& k = first(o[1], "k", 3);
     const Args a{k.device()};
     const c10::cuda::CUDAGuard guard(a.device);
     const int64_t N = k.size(0), H = k.size(1), D = k.size(2);
-    TORCH_CHECK_VALUE(!q4 || D == 128, "a 4-bit cache holds rows of 128 dims, got ", D);
+    TORCH_CHECK_VALUE(!q || D == 128, "a ", q ? q->bits : 16, "-bit cache holds rows of 128 dims, got ", D);
     int64_t ks, vs;
     const uint16_t* kp = rows(a, o[1], "k", {N, H, D}, ks);
     const uint16_t* vp = rows(a, o[2], "v", {N, H, D}, vs);
     const at::Tensor& table = dims_of(o[6], "page_table", 2);
     const int64_t B = table.size(0), max_pages = table.size(1);
-    const int64_t P = dims_of(o[4], "k_pool", q4 ? 3 : 4).size(0);
+    const int64_t P = dims_of(o[4], "k_pool", q ? 3 : 4).size(0);
     const int32_t* off = a.ints(o[3], "row_off", {B + 1});
     int64_t positions = 0, rot = 0;
     if (o[8] != Py_None) {
@@ -176,11 +199,11 @@ PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const uint32_t flags = truth(o[9]) ? SV_ROPE_INTERLEAVED : 0u;
     const int32_t n32 = size32(N, "N"), b32 = size32(B, "B"), h32 = size32(H, "Hkv"), p32 = size32(P, "num_pages"),
                   m32 = size32(max_pages, "max_pages"), pos32 = size32(positions, "rope's positions"), r32 = size32(rot, "rot");
-    if (q4) {
-        void* kc = a.get(o[4], "k_pool", at::kByte, {P, H, SV_KV_Q4_BYTES});
-        void* vc = a.get(o[5], "v_pool", at::kByte, {P, H, SV_KV_Q4_BYTES});
-        enqueue("sv_kv_append_q4", [&] {
-            return sv_kv_append_q4(kp, vp, ks, vs, n32, off, b32, h32, rp, pos32, r32, kc, vc, p32, tab, m32, len, flags,
+    if (q) {
+        void* kc = a.get(o[4], "k_pool", at::kByte, {P, H, q->block});
+        void* vc = a.get(o[5], "v_pool", at::kByte, {P, H, q->block});
+        enqueue(q->append_name, [&] {
+            return q->append(kp, vp, ks, vs, n32, off, b32, h32, rp, pos32, r32, kc, vc, p32, tab, m32, len, flags,
                                    a.stream());
         });
     } else {
@@ -196,25 +219,26 @@ PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length)
-PyObject* kv_commit_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
+// (bits, k_pool, v_pool, page_table, k_blk, v_blk, path, n_acc, length)
+PyObject* kv_commit(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    want(n, 8);
+    want(n, 9);
+    const Cache& q = cache(*o++);
     const at::Tensor& blk = first(o[3], "k_blk", 5);
     const Args a{blk.device()};
     const c10::cuda::CUDAGuard guard(a.device);
     const int64_t L = blk.size(0), B = blk.size(1), H = blk.size(2), R = blk.size(3);
     const int64_t P = dims_of(o[0], "k_pool", 4).size(1), max_pages = dims_of(o[2], "page_table", 2).size(1);
-    void* kp = a.get(o[0], "k_pool", at::kByte, {L, P, H, SV_KV_Q4_BYTES});
-    void* vp = a.get(o[1], "v_pool", at::kByte, {L, P, H, SV_KV_Q4_BYTES});
+    void* kp = a.get(o[0], "k_pool", at::kByte, {L, P, H, q.block});
+    void* vp = a.get(o[1], "v_pool", at::kByte, {L, P, H, q.block});
     const int32_t* tab = a.ints(o[2], "page_table", {B, max_pages});
     const uint16_t* kb = a.bf16(o[3], "k_blk", {L, B, H, R, 128});
     const uint16_t* vb = a.bf16(o[4], "v_blk", {L, B, H, R, 128});
     const int32_t* path = a.ints(o[5], "path", {B, R});
     const int32_t* acc = a.ints(o[6], "n_acc", {B});
     int32_t* len = a.as<int32_t>(o[7], "length", at::kInt, {B});
-    enqueue("sv_kv_commit_q4", [&] {
-        return sv_kv_commit_q4(kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), kb, vb, size32(L, "L"),
+    enqueue(q.commit_name, [&] {
+        return q.commit(kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), kb, vb, size32(L, "L"),
                                size32(B, "B"), size32(H, "Hkv"), size32(R, "R"), path, acc, len, a.stream());
     });
     Py_RETURN_NONE;
@@ -250,10 +274,11 @@ Output half_of(const at::Tensor& both, at::IntArrayRef shape, int64_t offset) {
     return {p, std::move(r)};
 }
 
-// (k_pool, v_pool, page_table, start, length, n, k_out, v_out) -> (k_out, v_out)
-PyObject* kv_gather_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
+// (bits, k_pool, v_pool, page_table, start, length, n, k_out, v_out) -> (k_out, v_out)
+PyObject* kv_gather(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    want(n, 8);
+    want(n, 9);
+    const Cache& q = cache(*o++);
     const at::Tensor& pool = first(o[0], "k_pool", 4);
     const Args a{pool.device()};
     const c10::cuda::CUDAGuard guard(a.device);
@@ -261,8 +286,8 @@ PyObject* kv_gather_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const at::Tensor& table = dims_of(o[2], "page_table", 2);
     const int64_t B = table.size(0), max_pages = table.size(1);
     const int32_t n32 = size32(count, "n");
-    const void* kp = a.get(o[0], "k_pool", at::kByte, {L, P, H, SV_KV_Q4_BYTES});
-    const void* vp = a.get(o[1], "v_pool", at::kByte, {L, P, H, SV_KV_Q4_BYTES});
+    const void* kp = a.get(o[0], "k_pool", at::kByte, {L, P, H, q.block});
+    const void* vp = a.get(o[1], "v_pool", at::kByte, {L, P, H, q.block});
     const int32_t* tab = a.ints(o[2], "page_table", {B, max_pages});
     const int32_t* start = a.ints(o[3], "start", {B});
     const int32_t* len = a.ints(o[4], "length", {B});
@@ -276,8 +301,8 @@ PyObject* kv_gather_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
         k = output(a, o[6], "k_out", at::kBFloat16, shape);
         v = output(a, o[7], "v_out", at::kBFloat16, shape);
     }
-    enqueue("sv_kv_gather_q4", [&] {
-        return sv_kv_gather_q4(kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), size32(L, "L"),
+    enqueue(q.gather_name, [&] {
+        return q.gather(kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), size32(L, "L"),
                                size32(B, "B"), size32(H, "Hkv"), start, len, n32, static_cast<uint16_t*>(k.ptr),
                                static_cast<uint16_t*>(v.ptr), a.stream());
     });
@@ -285,10 +310,11 @@ PyObject* kv_gather_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent, scale, out, ws, cache_ready) -> out
-PyObject* verify_attn_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
+// (bits, q, k_pool, v_pool, page_table, length, k_blk, v_blk, parent, scale, out, ws, cache_ready) -> out
+PyObject* verify_attn(PyObject*, PyObject* const* o, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    want(n, 12);
+    want(n, 13);
+    const Cache& cc = cache(*o++);
     const at::Tensor& q = first(o[0], "q", 4);
     const Args a{q.device()};
     const c10::cuda::CUDAGuard guard(a.device);
@@ -296,8 +322,8 @@ PyObject* verify_attn_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const at::Tensor& pool = dims_of(o[1], "k_pool", 3);
     const int64_t P = pool.size(0), H = pool.size(1), max_pages = dims_of(o[3], "page_table", 2).size(1);
     const uint16_t* qp = a.bf16(o[0], "q", {B, R, Hq, D});
-    const void* kp = a.get(o[1], "k_pool", at::kByte, {P, H, SV_KV_Q4_BYTES});
-    const void* vp = a.get(o[2], "v_pool", at::kByte, {P, H, SV_KV_Q4_BYTES});
+    const void* kp = a.get(o[1], "k_pool", at::kByte, {P, H, cc.block});
+    const void* vp = a.get(o[2], "v_pool", at::kByte, {P, H, cc.block});
     const int32_t* tab = a.ints(o[3], "page_table", {B, max_pages});
     const int32_t* len = a.ints(o[4], "length", {B});
     const uint16_t* kb = a.bf16(o[5], "k_blk", {B, H, R, D});
@@ -308,7 +334,7 @@ PyObject* verify_attn_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const uint32_t flags = truth(o[11]) ? SV_ATTN_CACHE_READY : 0u;
     const sv_attn_shape shape{size32(B, "B"), size32(R, "R"), size32(Hq, "Hq"), size32(H, "Hkv"), size32(D, "D"),
                               size32(max_pages * SV_KV_PAGE, "the page table's positions")};
-    const size_t bytes = sv_verify_attn_q4_workspace(&shape);
+    const size_t bytes = cc.workspace(&shape);
     at::Tensor ws;
     if (bytes > 0 && o[10] != Py_None) {
         ws = tensor(o[10], "ws");
@@ -320,8 +346,8 @@ PyObject* verify_attn_q4(PyObject*, PyObject* const* o, Py_ssize_t n) {
         ws = a.empty({static_cast<int64_t>(bytes)}, at::kByte);
     }
     Output out = output(a, o[9], "out", at::kBFloat16, {B, R, Hq, D});
-    enqueue("sv_verify_attn_q4", [&] {
-        return sv_verify_attn_q4(&shape, qp, kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), len, kb, vb,
+    enqueue(cc.attn_name, [&] {
+        return cc.attn(&shape, qp, kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), len, kb, vb,
                                  par, scale, static_cast<uint16_t*>(out.ptr), ws.defined() ? ws.data_ptr() : nullptr, bytes,
                                  flags, a.stream());
     });
@@ -383,8 +409,8 @@ PyObject* set_check(PyObject*, PyObject* f) {
 }
 
 #define SV_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {SV_FAST(kv_append),      SV_FAST(kv_commit_q4),   SV_FAST(kv_gather_q4),
-                           SV_FAST(verify_attn_q4), SV_FAST(logits_process), {"set_check", set_check, METH_O, nullptr},
+PyMethodDef g_methods[] = {SV_FAST(kv_append),   SV_FAST(kv_commit),      SV_FAST(kv_gather),
+                           SV_FAST(verify_attn), SV_FAST(logits_process), {"set_check", set_check, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "sv_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -430,38 +430,46 @@ sv_status sv_kv_append_paged(const uint16_t* k, const uint16_t* v, int64_t k_str
     return launch_status(sv::launch_kv_append(a, k_pool, v_pool, as_stream(stream)));
 }
 
-sv_status sv_kv_append_q4(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
-                          const int32_t* row_off, int32_t B, int32_t Hkv, const float* rope, int32_t rope_positions,
-                          int32_t rot, void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table,
-                          int32_t max_pages, const int32_t* len, uint32_t flags, void* stream) {
+// The calls on the 4-bit and the 8-bit cache differ in their kernels alone.
+static sv_status append_quantised(int64_t (*items)(int, int, int),
+                                  cudaError_t (*launch)(const sv::AppendArgs&, uint8_t*, uint8_t*, cudaStream_t),
+                                  const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
+                                  const int32_t* row_off, int32_t B, int32_t Hkv, const float* rope,
+                                  int32_t rope_positions, int32_t rot, void* k_pool, void* v_pool, int32_t num_pages,
+                                  const int32_t* page_table, int32_t max_pages, const int32_t* len, uint32_t flags,
+                                  void* stream) {
     if (N < 0) return SV_ERR_SHAPE;
     if (N == 0) return SV_OK;
     sv::AppendArgs a;
     const sv_status s = append_args(a, k, v, k_stride, v_stride, N, row_off, B, Hkv, 128, rope, rope_positions, rot,
                                     k_pool, v_pool, num_pages, page_table, max_pages, len, flags);
     if (s != SV_OK) return s;
-    if (sv::append_q4_items(N, B, Hkv) >= 2147483647) return SV_ERR_SHAPE;
-    return launch_status(sv::launch_append_q4(a, static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool),
-                                              as_stream(stream)));
+    if (items(N, B, Hkv) >= 2147483647) return SV_ERR_SHAPE;
+    return launch_status(launch(a, static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), as_stream(stream)));
 }
 
-sv_status sv_kv_commit_q4(void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table, int32_t max_pages,
-                          const uint16_t* k_blk, const uint16_t* v_blk, int32_t L, int32_t B, int32_t Hkv, int32_t R,
-                          const int32_t* path, const int32_t* n_acc, int32_t* len, void* stream) {
+using CommitLaunch = cudaError_t(uint8_t*, uint8_t*, const uint16_t*, const uint16_t*, int, int, int, int, const int32_t*,
+                                 const int32_t*, int32_t*, const int32_t*, int, int, cudaStream_t);
+static sv_status commit_quantised(CommitLaunch* launch, void* k_pool, void* v_pool, int32_t num_pages,
+                                  const int32_t* page_table, int32_t max_pages, const uint16_t* k_blk,
+                                  const uint16_t* v_blk, int32_t L, int32_t B, int32_t Hkv, int32_t R,
+                                  const int32_t* path, const int32_t* n_acc, int32_t* len, void* stream) {
     if (!k_pool || !v_pool || !page_table || !k_blk || !v_blk || !path || !n_acc || !len) return SV_ERR_ARG;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_blk) || !aligned16(v_blk)) return SV_ERR_ARG;
     if (L < 1 || B < 1 || Hkv < 1 || R < 1 || R > 128 || num_pages < 1 || max_pages < 1) return SV_ERR_SHAPE;
     if (static_cast<int64_t>(max_pages) * SV_KV_PAGE > 2147483647 || static_cast<int64_t>(B) * 8 > 2147483647 ||
         static_cast<int64_t>(L) * Hkv > (1 << 24))
         return SV_ERR_SHAPE;
-    return launch_status(sv::launch_commit_q4(static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), k_blk, v_blk,
-                                              L, B, Hkv, R, path, n_acc, len, page_table, max_pages, num_pages,
-                                              as_stream(stream)));
+    return launch_status(launch(static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), k_blk, v_blk, L, B, Hkv, R,
+                                path, n_acc, len, page_table, max_pages, num_pages, as_stream(stream)));
 }
 
-sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t num_pages, const int32_t* page_table,
-                          int32_t max_pages, int32_t L, int32_t B, int32_t Hkv, const int32_t* start,
-                          const int32_t* len, int32_t n, uint16_t* k_out, uint16_t* v_out, void* stream) {
+using GatherLaunch = cudaError_t(const uint8_t*, const uint8_t*, int, int, int, const int32_t*, const int32_t*, int,
+                                 const int32_t*, int, int, uint16_t*, uint16_t*, cudaStream_t);
+static sv_status gather_quantised(int64_t (*items)(int, int, int, int), GatherLaunch* launch, const void* k_pool,
+                                  const void* v_pool, int32_t num_pages, const int32_t* page_table, int32_t max_pages,
+                                  int32_t L, int32_t B, int32_t Hkv, const int32_t* start, const int32_t* len, int32_t n,
+                                  uint16_t* k_out, uint16_t* v_out, void* stream) {
     if (n < 0) return SV_ERR_SHAPE;
     if (n == 0) return SV_OK;
     if (!k_pool || !v_pool || !page_table || !start || !len || !k_out || !v_out) return SV_ERR_ARG;
@@ -469,22 +477,18 @@ sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t num_pa
     if (L < 1 || B < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1 || n > (1 << 30)) return SV_ERR_SHAPE;
     if (static_cast<int64_t>(max_pages) * SV_KV_PAGE > 2147483647) return SV_ERR_SHAPE;
     if (static_cast<int64_t>(L) * B > (1 << 30) || static_cast<int64_t>(L) * B * Hkv > (int64_t(1) << 31) ||
-        sv::gather_q4_items(L, B, Hkv, n) >= 2147483647)
+        items(L, B, Hkv, n) >= 2147483647)
         return SV_ERR_SHAPE;
-    return launch_status(sv::launch_gather_q4(static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), L,
-                                              B, Hkv, start, len, n, page_table, max_pages, num_pages, k_out, v_out,
-                                              as_stream(stream)));
+    return launch_status(launch(static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), L, B, Hkv, start,
+                                len, n, page_table, max_pages, num_pages, k_out, v_out, as_stream(stream)));
 }
 
-size_t sv_verify_attn_q4_workspace(const sv_attn_shape* shape) {
-    if (check_attn_shape(shape) != SV_OK) return 0;
-    return sv::attn_q4_workspace(*shape);
-}
-
-sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool, const void* v_pool,
-                            int32_t num_pages, const int32_t* page_table, int32_t max_pages, const int32_t* len,
-                            const uint16_t* k_blk, const uint16_t* v_blk, const int32_t* parent, float scale,
-                            uint16_t* out, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
+static sv_status attn_quantised(size_t (*workspace)(const sv_attn_shape&),
+                                cudaError_t (*launch)(const sv::CacheAttnArgs&, void*, cudaStream_t),
+                                const sv_attn_shape* shape, const uint16_t* q, const void* k_pool, const void* v_pool,
+                                int32_t num_pages, const int32_t* page_table, int32_t max_pages, const int32_t* len,
+                                const uint16_t* k_blk, const uint16_t* v_blk, const int32_t* parent, float scale,
+                                uint16_t* out, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
     if (flags & ~SV_ATTN_CACHE_READY) return SV_ERR_ARG;
     const sv_status st = check_attn_shape(shape);
     if (st != SV_OK) return st;
@@ -494,11 +498,11 @@ sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const
         return SV_ERR_ARG;
     if (num_pages < 1 || max_pages < 1) return SV_ERR_SHAPE;
     if (static_cast<int64_t>(max_pages) * SV_KV_PAGE != shape->T_cap) return SV_ERR_SHAPE;
-    const size_t need = sv::attn_q4_workspace(*shape);
+    const size_t need = workspace(*shape);
     if (!ws && need > 0) return SV_ERR_ARG;
     if (!(scale > 0.0f)) return SV_ERR_ARG;
     if (ws_bytes < need) return SV_ERR_WORKSPACE;
-    sv::AttnQ4Args a;
+    sv::CacheAttnArgs a;
     a.q = q;
     a.k_pool = static_cast<const uint8_t*>(k_pool);
     a.v_pool = static_cast<const uint8_t*>(v_pool);
@@ -518,7 +522,77 @@ sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const
     a.num_pages = num_pages;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.cache_ready = (flags & SV_ATTN_CACHE_READY) != 0;
-    return launch_status(sv::launch_verify_attn_q4(a, ws, as_stream(stream)));
+    return launch_status(launch(a, ws, as_stream(stream)));
+}
+
+sv_status sv_kv_append_q4(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
+                          const int32_t* row_off, int32_t B, int32_t Hkv, const float* rope, int32_t rope_positions,
+                          int32_t rot, void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table,
+                          int32_t max_pages, const int32_t* len, uint32_t flags, void* stream) {
+    return append_quantised(sv::append_q4_items, sv::launch_append_q4, k, v, k_stride, v_stride, N, row_off, B, Hkv, rope,
+                            rope_positions, rot, k_pool, v_pool, num_pages, page_table, max_pages, len, flags, stream);
+}
+
+sv_status sv_kv_commit_q4(void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table, int32_t max_pages,
+                          const uint16_t* k_blk, const uint16_t* v_blk, int32_t L, int32_t B, int32_t Hkv, int32_t R,
+                          const int32_t* path, const int32_t* n_acc, int32_t* len, void* stream) {
+    return commit_quantised(sv::launch_commit_q4, k_pool, v_pool, num_pages, page_table, max_pages, k_blk, v_blk, L, B, Hkv,
+                            R, path, n_acc, len, stream);
+}
+
+sv_status sv_kv_gather_q4(const void* k_pool, const void* v_pool, int32_t num_pages, const int32_t* page_table,
+                          int32_t max_pages, int32_t L, int32_t B, int32_t Hkv, const int32_t* start,
+                          const int32_t* len, int32_t n, uint16_t* k_out, uint16_t* v_out, void* stream) {
+    return gather_quantised(sv::gather_q4_items, sv::launch_gather_q4, k_pool, v_pool, num_pages, page_table, max_pages, L,
+                            B, Hkv, start, len, n, k_out, v_out, stream);
+}
+
+size_t sv_verify_attn_q4_workspace(const sv_attn_shape* shape) {
+    if (check_attn_shape(shape) != SV_OK) return 0;
+    return sv::attn_q4_workspace(*shape);
+}
+
+sv_status sv_verify_attn_q4(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool, const void* v_pool,
+                            int32_t num_pages, const int32_t* page_table, int32_t max_pages, const int32_t* len,
+                            const uint16_t* k_blk, const uint16_t* v_blk, const int32_t* parent, float scale,
+                            uint16_t* out, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
+    return attn_quantised(sv::attn_q4_workspace, sv::launch_verify_attn_q4, shape, q, k_pool, v_pool, num_pages, page_table,
+                          max_pages, len, k_blk, v_blk, parent, scale, out, ws, ws_bytes, flags, stream);
+}
+
+sv_status sv_kv_append_q8(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int32_t N,
+                          const int32_t* row_off, int32_t B, int32_t Hkv, const float* rope, int32_t rope_positions,
+                          int32_t rot, void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table,
+                          int32_t max_pages, const int32_t* len, uint32_t flags, void* stream) {
+    return append_quantised(sv::append_q8_items, sv::launch_append_q8, k, v, k_stride, v_stride, N, row_off, B, Hkv, rope,
+                            rope_positions, rot, k_pool, v_pool, num_pages, page_table, max_pages, len, flags, stream);
+}
+
+sv_status sv_kv_commit_q8(void* k_pool, void* v_pool, int32_t num_pages, const int32_t* page_table, int32_t max_pages,
+                          const uint16_t* k_blk, const uint16_t* v_blk, int32_t L, int32_t B, int32_t Hkv, int32_t R,
+                          const int32_t* path, const int32_t* n_acc, int32_t* len, void* stream) {
+    return commit_quantised(sv::launch_commit_q8, k_pool, v_pool, num_pages, page_table, max_pages, k_blk, v_blk, L, B, Hkv,
+                            R, path, n_acc, len, stream);
+}
+
+sv_status sv_kv_gather_q8(const void* k_pool, const void* v_pool, int32_t num_pages, const int32_t* page_table,
+                          int32_t max_pages, int32_t L, int32_t B, int32_t Hkv, const int32_t* start,
+                          const int32_t* len, int32_t n, uint16_t* k_out, uint16_t* v_out, void* stream) {
+    return gather_quantised(sv::gather_q8_items, sv::launch_gather_q8, k_pool, v_pool, num_pages, page_table, max_pages, L,
+                            B, Hkv, start, len, n, k_out, v_out, stream);
+}
+
+size_t sv_verify_attn_q8_workspace(const sv_attn_shape* shape) {
+    if (check_attn_shape(shape) != SV_OK) return 0;
+    return sv::attn_q8_workspace(*shape);
+}
+
+sv_status sv_verify_attn_q8(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool, const void* v_pool,
+                            int32_t num_pages, const int32_t* page_table, int32_t max_pages, const int32_t* len,
+                            const uint16_t* k_blk, const uint16_t* v_blk, const int32_t* parent, float scale,
+                            uint16_t* out, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
+    return attn_quantised(sv::attn_q8_workspace, sv::launch_verify_attn_q8, shape, q, k_pool, v_pool, num_pages, page_table,
+                          max_pages, len, k_blk, v_blk, parent, scale, out, ws, ws_bytes, flags, stream);
 }
 
 sv_status sv_logits_process(const float* logits, int32_t B, int32_t R, int32_t V, const int32_t* hist,

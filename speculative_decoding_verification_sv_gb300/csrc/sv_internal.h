@@ -148,7 +148,7 @@ cudaError_t launch_verify_attn(const sv_attn_shape& s, const uint16_t* q, const 
                                void* ws, bool cache_ready, const int32_t* pages, int max_pages, int num_pages,
                                cudaStream_t st);
 
-// kv_append.cu, kv_q4.cu
+// kv_append.cu, kv_q4.cu, kv_q8.cu
 struct AppendArgs;   // kv_append.cuh
 cudaError_t launch_kv_append(const AppendArgs& a, uint16_t* k_pool, uint16_t* v_pool, cudaStream_t st);
 int64_t append_q4_items(int N, int B, int Hkv);   // warps of the launch
@@ -161,8 +161,18 @@ cudaError_t launch_gather_q4(const uint8_t* k_pool, const uint8_t* v_pool, int L
                              const int32_t* len, int n, const int32_t* pages, int max_pages, int num_pages,
                              uint16_t* k_out, uint16_t* v_out, cudaStream_t st);
 
-// verify_attn_q4.cu
-struct AttnQ4Args {
+int64_t append_q8_items(int N, int B, int Hkv);   // warps of the launch
+cudaError_t launch_append_q8(const AppendArgs& a, uint8_t* k_pool, uint8_t* v_pool, cudaStream_t st);
+cudaError_t launch_commit_q8(uint8_t* k_pool, uint8_t* v_pool, const uint16_t* k_blk, const uint16_t* v_blk, int L,
+                             int B, int Hkv, int R, const int32_t* path, const int32_t* n_acc, int32_t* len,
+                             const int32_t* pages, int max_pages, int num_pages, cudaStream_t st);
+int64_t gather_q8_items(int L, int B, int Hkv, int n);   // warps of the launch
+cudaError_t launch_gather_q8(const uint8_t* k_pool, const uint8_t* v_pool, int L, int B, int Hkv, const int32_t* start,
+                             const int32_t* len, int n, const int32_t* pages, int max_pages, int num_pages,
+                             uint16_t* k_out, uint16_t* v_out, cudaStream_t st);
+
+// verify_attn_q4.cu, verify_attn_q8.cu
+struct CacheAttnArgs {
     const uint16_t* q;
     const uint8_t *k_pool, *v_pool;
     const int32_t* pages;    // [B][max_pages]
@@ -176,7 +186,9 @@ struct AttnQ4Args {
     bool cache_ready;
 };
 size_t attn_q4_workspace(const sv_attn_shape& s);
-cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st);
+cudaError_t launch_verify_attn_q4(const CacheAttnArgs& a, void* ws, cudaStream_t st);
+size_t attn_q8_workspace(const sv_attn_shape& s);
+cudaError_t launch_verify_attn_q8(const CacheAttnArgs& a, void* ws, cudaStream_t st);
 
 // logits_process.cu
 struct LogitsArgs {

@@ -60,6 +60,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "attn_cache.cuh"
 #include "kv_q4.cuh"
 #include "sv_internal.h"
 
@@ -68,13 +69,11 @@ namespace cg = cooperative_groups;
 namespace sv {
 namespace {
 
-constexpr int kRows = 64;                 // query rows of a tile
 constexpr int kStepKeys = 128;            // two pages
 constexpr int kStages = 6;
 constexpr int kStageBytes = 4 * kQ4Bytes; // K of two pages, V of two pages
 constexpr int kMaxR = 128;
 constexpr int kSoftWarps = 8, kKWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17, kQWarp = 18, kThreads = 32 * 19;
-constexpr int kGrain = 4;                 // pages a CTA takes at least (where there are as many)
 constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand,
 constexpr float kLeastSum = 0.5f;         // and at least (a reference that the row sees gives 1)
 constexpr int kRecFloats = kRows * (kQ4D + 2);   // a partial: O [64][128], then (m, l) [64]
@@ -105,141 +104,6 @@ constexpr int kSmemBytes = kOffScale + 4 * 512;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 static_assert(kStages * 4 <= 32, "bad-page words");
 
-struct Work {
-    int U;         // units of a sequence: Hkv * row tiles
-    int row_tiles;
-    int tile_rows; // rows of a tile but the last
-    int cluster;   // CTAs of a unit where each unit has a cluster, 0 where the pages are split evenly
-    int inv_g;     // ceil(2^16 / G): r * inv_g >> 16 is r / G for every row r < 2048 of G <= 16
-};
-
-// Pages of sequence b (its length clamped into the table), the block not counted.
-__device__ __forceinline__ int ctx_len(const AttnQ4Args& a, int b) {
-    const int t = a.len[b];
-    return t < 0 ? 0 : min(t, a.max_pages * kQ4Page);
-}
-__device__ __forceinline__ int ctx_pages(int t) { return (t + kQ4Page - 1) / kQ4Page; }
-
-// Work of all sequences (sum of pages + 1), and of those before sequence
-// `before`; one warp, every lane gets both.
-__device__ __forceinline__ int2 work_sums(const AttnQ4Args& a, int before) {
-    int all = 0, head = 0;
-    for (int b = threadIdx.x & 31; b < a.B; b += 32) {
-        const int w = ctx_pages(ctx_len(a, b)) + 1;
-        all += w;
-        if (b < before) head += w;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, off);
-        head += __shfl_xor_sync(0xffffffffu, head, off);
-    }
-    return make_int2(all, head);
-}
-
-// CTAs that share W pages, and the first page of CTA i among them.
-__device__ __forceinline__ int active_ctas(int W, int grid) { return max(1, min(grid, W / kGrain)); }
-__device__ __forceinline__ int cta_first(int W, int i, int n) {
-    return static_cast<int>(static_cast<int64_t>(W) * i / n);
-}
-// The CTA whose run holds page x: the largest i with floor(W i / n) <= x, that is
-// W i < (x + 1) n.
-__device__ __forceinline__ int cta_of(int W, int x, int n) {
-    const int64_t most = (static_cast<int64_t>(x) + 1) * n - 1;
-    return most < (int64_t(1) << 32) ? static_cast<int>(static_cast<uint32_t>(most) / static_cast<uint32_t>(W))
-                                     : static_cast<int>(most / W);
-}
-
-// The runs of this CTA, unit by unit; every warp walks them by itself.
-struct Walk {
-    int pos, end;          // what is left of the CTA's run
-    int b, unit, off;      // where pos lies: sequence, unit of it, page of the unit
-    int t, np;             // length and pages of sequence b
-    // the current run
-    int p0, p1;            // its pages
-    bool block, whole;     // the block is in it; it is all of the unit
-
-    __device__ __forceinline__ void start(const AttnQ4Args& a, const Work& w, int cta, int grid) {
-        const int lane = threadIdx.x & 31;
-        // (the first 32 lengths stay in registers: a round trip less for most batches)
-        const int t0 = lane < a.B ? ctx_len(a, lane) : 0;
-        const int w0 = lane < a.B ? (ctx_pages(t0) + 1) * w.U : 0;
-        int W = w0;
-        for (int i = 32 + lane; i < a.B; i += 32) W += (ctx_pages(ctx_len(a, i)) + 1) * w.U;
-        W = __reduce_add_sync(0xffffffffu, W);
-        const int n = active_ctas(W, grid);
-        pos = end = 0;
-        b = -1;
-        if (cta >= n) return;
-        pos = cta_first(W, cta, n);
-        end = cta_first(W, cta + 1, n);
-        // the sequence that pos lies in
-        int base = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int tb = b0 == 0 ? t0 : b0 + lane < a.B ? ctx_len(a, b0 + lane) : 0;
-            const int wt = b0 == 0 ? w0 : b0 + lane < a.B ? (ctx_pages(tb) + 1) * w.U : 0;
-            int sum = wt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += x;
-            }
-            const uint32_t m = __ballot_sync(0xffffffffu, base + sum > pos);
-            if (m != 0u) {
-                const int k = __ffs(m) - 1;
-                b = b0 + k;
-                base += __shfl_sync(0xffffffffu, sum - wt, k);
-                t = __shfl_sync(0xffffffffu, tb, k);
-                break;
-            }
-            base += __shfl_sync(0xffffffffu, sum, 31);
-        }
-        np = ctx_pages(t);
-        unit = (pos - base) / (np + 1);
-        off = (pos - base) % (np + 1);
-    }
-    // Unit u's pages for CTA `rank` of the cluster that has the unit.
-    __device__ __forceinline__ void start_unit(const AttnQ4Args& a, const Work& w, int u, int rank) {
-        b = u / w.U;
-        unit = u - b * w.U;
-        t = ctx_len(a, b);
-        np = ctx_pages(t);
-        pos = off = static_cast<int>(static_cast<int64_t>(np + 1) * rank / w.cluster);
-        end = static_cast<int>(static_cast<int64_t>(np + 1) * (rank + 1) / w.cluster);
-    }
-    __device__ __forceinline__ bool next(const AttnQ4Args& a, const Work& w) {
-        if (pos >= end) return false;
-        const int n = min(end - pos, np + 1 - off);
-        p0 = off;
-        p1 = min(off + n, np);
-        block = off + n == np + 1;
-        whole = n == np + 1;
-        pos += n;
-        cur_b = b;
-        cur_unit = unit;
-        cur_t = t;
-        off = 0;
-        if (block && ++unit == w.U) {
-            unit = 0;
-            if (++b < a.B) {
-                t = ctx_len(a, b);
-                np = ctx_pages(t);
-            }
-        }
-        return true;
-    }
-    int cur_b, cur_unit, cur_t;
-    __device__ __forceinline__ void save(volatile int* to) const {
-        to[0] = pos, to[1] = end, to[2] = b, to[3] = unit, to[4] = off;
-    }
-    __device__ __forceinline__ void load(const AttnQ4Args& a, const volatile int* from) {
-        pos = from[0], end = from[1], b = from[2], unit = from[3], off = from[4];
-        t = ctx_len(a, b);
-        np = ctx_pages(t);
-    }
-    __device__ __forceinline__ int ctx_steps() const { return (p1 - p0 + 1) / 2; }
-};
-
 // --- packed arithmetic ---------------------------------------------------------
 
 __device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -267,89 +131,10 @@ struct CodeMask {
 };
 constexpr uint32_t kM136 = 0xC308C308u;   // bf16 pair of -136
 
-// One lane of the (converged) warp, always the same one.  A branch on it is
-// known to be taken by one thread, and the MMAs' operands then stay in uniform
-// registers: 25 cycles an MMA issued in place of 45 under lane == 0 (M = 128, N
-// = 64, whose own time is 35).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r));
-    return r != 0u;
-}
-
-
-__device__ __forceinline__ float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// Sums of kN values over the lanes: half of the values are handed to the lane
-// whose number differs in the bit kN / 2, and so on; v[0] of lane e ends as value
-// e's sum over the lanes that agree with e below kN.
-template <int kN, int kLen>
-__device__ __forceinline__ void fold_sums_step(float (&v)[kLen]) {
-    const bool upper = (threadIdx.x & (kN / 2)) != 0;
-#pragma unroll
-    for (int i = 0; i < kN / 2; ++i) {
-        const float give = upper ? v[i] : v[i + kN / 2];
-        const float keep = upper ? v[i + kN / 2] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, kN / 2);
-    }
-    if constexpr (kN > 2) fold_sums_step<kN / 2>(v);
-}
-template <int kN>
-__device__ __forceinline__ void fold_sums(float (&v)[kN]) {
-    fold_sums_step<kN>(v);
-}
-
-// Joins n partials of a row, eight in flight; get(i, ml, o) loads the i-th's
-// (m, l) and the lane's four dims of its O.
-template <typename Get>
-__device__ __forceinline__ void join_row(int n, Get&& get, uint16_t* dst) {
-    const int lane = threadIdx.x & 31;
-    float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = 0; c0 < n; c0 += 8) {
-        float2 ml[8];
-        float4 o[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            ml[u] = make_float2(-INFINITY, 0.f);
-            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c0 + u < n) get(c0 + u, ml[u], o[u]);
-        }
-        float mn = M;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
-        const float c = M == -INFINITY ? 0.f : exp2f(M - mn);
-        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c, L *= c;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
-            const float w = exp2f(ml[u].x - mn);
-            L += w * ml[u].y;
-            acc.x += w * o[u].x;
-            acc.y += w * o[u].y;
-            acc.z += w * o[u].z;
-            acc.w += w * o[u].w;
-        }
-        M = mn;
-    }
-    const float inv = L != 0.f ? 1.0f / L : 0.f;
-    *reinterpret_cast<uint2*>(dst + 4 * lane) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-}
-
 // kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (their
 // columns of P stay zero)
 template <int kRT, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work wk, float* __restrict__ ws) {
+__global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(CacheAttnArgs a, Work wk, float* __restrict__ ws) {
     constexpr int kLive = 2 * kRT;
     // (aligned by its declaration: addresses are then constants, not registers)
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -1005,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(AttnQ4Args a, Work
 
 // Joins the partial rows of the units that lie in several CTAs' runs, a warp a row.
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_q4_kernel(AttnQ4Args a, Work wk, const float* __restrict__ ws, int grid) {
+    combine_q4_kernel(CacheAttnArgs a, Work wk, const float* __restrict__ ws, int grid) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -1028,16 +813,6 @@ __global__ void __launch_bounds__(kCombineThreads)
     };
     join_row(i1 - i0 + 1, get,
              a.out + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D);
-}
-
-Work work_of(int R, int G, int Hkv) {
-    Work w{};
-    const int rows = R * G;
-    w.row_tiles = (rows + kRows - 1) / kRows;
-    w.tile_rows = (rows + w.row_tiles - 1) / w.row_tiles;
-    w.U = Hkv * w.row_tiles;
-    w.inv_g = (65536 + G - 1) / G;
-    return w;
 }
 
 template <int kRT, bool kCluster>
@@ -1102,7 +877,7 @@ void plan(Work& w, int B, int max_pages, int& grid) {
 }
 
 template <int kRT>
-cudaError_t launch_rt(const AttnQ4Args& a, const Work& w, int grid, float* ws, cudaStream_t st) {
+cudaError_t launch_rt(const CacheAttnArgs& a, const Work& w, int grid, float* ws, cudaStream_t st) {
     if (w.cluster == 0) {
         const cudaError_t e = prepare<kRT, false>();
         if (e != cudaSuccess) return e;
@@ -1135,7 +910,7 @@ size_t attn_q4_workspace(const sv_attn_shape& s) {
     return grid > 1 && w.cluster == 0 ? static_cast<size_t>(grid) * 2 * kRecFloats * sizeof(float) : 0;
 }
 
-cudaError_t launch_verify_attn_q4(const AttnQ4Args& a, void* ws, cudaStream_t st) {
+cudaError_t launch_verify_attn_q4(const CacheAttnArgs& a, void* ws, cudaStream_t st) {
     Work w = work_of(a.R, a.G, a.Hkv);
     int grid;
     plan(w, a.B, a.max_pages, grid);
