@@ -53,8 +53,10 @@ __device__ __forceinline__ int2 work_sums(const CacheAttnArgs& a, int before) {
 
 // CTAs that share W pages, and the first page of CTA i among them.
 __device__ __forceinline__ int active_ctas(int W, int grid) { return max(1, min(grid, W / kGrain)); }
+// (n <= 2^15: products of remainders stay in 32 bits)
 __device__ __forceinline__ int cta_first(int W, int i, int n) {
-    return static_cast<int>(static_cast<int64_t>(W) * i / n);
+    const uint32_t q = static_cast<uint32_t>(W) / static_cast<uint32_t>(n), r = static_cast<uint32_t>(W) - q * n;
+    return static_cast<int>(q * i + r * i / static_cast<uint32_t>(n));
 }
 // The CTA whose run holds page x: the largest i with floor(W i / n) <= x, that is
 // W i < (x + 1) n.
@@ -118,8 +120,8 @@ struct Walk {
         unit = u - b * w.U;
         t = ctx_len(a, b);
         np = ctx_pages(t);
-        pos = off = static_cast<int>(static_cast<int64_t>(np + 1) * rank / w.cluster);
-        end = static_cast<int>(static_cast<int64_t>(np + 1) * (rank + 1) / w.cluster);
+        pos = off = cta_first(np + 1, rank, w.cluster);
+        end = cta_first(np + 1, rank + 1, w.cluster);
     }
     __device__ __forceinline__ bool next(const CacheAttnArgs& a, const Work& w) {
         if (pos >= end) return false;
@@ -195,12 +197,13 @@ __device__ __forceinline__ void fold_sums(float (&v)[kN]) {
 }
 
 // Joins n partials of a row, eight in flight; get(i, ml, o) loads the i-th's
-// (m, l) and the lane's four dims of its O.
-template <typename Get>
-__device__ __forceinline__ void join_row(int n, Get&& get, uint16_t* dst) {
+// (m, l) and the lane's four dims of its O: sums of P V, or, with kMeans, those over l.
+template <bool kMeans, typename Get>
+__device__ __forceinline__ void join_partials(int n, Get&& get, uint16_t* dst) {
     const int lane = threadIdx.x & 31;
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int c0 = 0; c0 < n; c0 += 8) {
         float2 ml[8];
         float4 o[8];
@@ -214,13 +217,15 @@ __device__ __forceinline__ void join_row(int n, Get&& get, uint16_t* dst) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
-        const float c = M == -INFINITY ? 0.f : exp2f(M - mn);
+        auto power = [](float x) { return kMeans ? fast_exp2(x) : exp2f(x); };
+        const float c = M == -INFINITY ? 0.f : power(M - mn);
         acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c, L *= c;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
-            const float w = exp2f(ml[u].x - mn);
+            float w = power(ml[u].x - mn);
             L += w * ml[u].y;
+            if constexpr (kMeans) w *= ml[u].y;
             acc.x += w * o[u].x;
             acc.y += w * o[u].y;
             acc.z += w * o[u].z;

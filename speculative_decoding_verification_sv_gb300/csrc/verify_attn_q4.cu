@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_kernel(CacheAttnArgs a, W
                 ml = *reinterpret_cast<const float2*>(rec + kRows * kQ4D + 2 * r);
                 o = *(reinterpret_cast<const float4*>(rec + r * kQ4D) + lane);
             };
-            join_row(wk.cluster, get, a.out + (static_cast<size_t>(b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ4D);
+            join_partials<false>(wk.cluster, get, a.out + (static_cast<size_t>(b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ4D);
         }
         __syncwarp();
         cluster_sync_warp();   // this CTA's partial has been read
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         ml = __ldcg(reinterpret_cast<const float2*>(rec + kRows * kQ4D + 2 * r));
         o = __ldcg(reinterpret_cast<const float4*>(rec + r * kQ4D) + lane);
     };
-    join_row(i1 - i0 + 1, get,
+    join_partials<false>(i1 - i0 + 1, get,
              a.out + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ4D);
 }
 

@@ -17,29 +17,36 @@
 //        power of two that takes its largest element to (224, 448], and what is lost
 //        lies below 2^-10 of such a unit: 2^-17.8 of the row's largest element.
 //        Scales of Q's rows and of K's runs, powers of two, multiply the scores.
-//   P:   exp2(s - m), bf16, written by the key's thread as one line of
+//   P:   exp2(s - m), f16, written by the key's thread as one line of
 //        [keys][64 rows] in shared memory, the MN-major B of the second product.
-//   O^T: lane = dim, column = row.  P far above or below 1 has to be held to 8 bits,
-//        which only bf16 does: V's codes are made bf16 by the warps that hold a dim each
-//        (a permute, a shift, a mask and a product for two codes) and are the A operand
-//        in tensor memory.
+//   O^T: lane = dim, column = row.  V's codes are made f16 by the warps that hold a dim
+//        each (one conversion and one product by the run's scale for two codes) and are
+//        the A operand in tensor memory; f16, because it holds P to 11 bits, an eighth of
+//        bf16's rounding, and every e4m3.  What it lacks is range.  V is therefore in units of the largest
+//        scale among the run's pages and its block (a value is exact where its own scale
+//        is no less than 2^-15 of that, and off by 2^-33 of the largest V otherwise), and P
+//        is 2^kUp at a reference, below.
 // The block's K rows are held as Q's are, two e4m3 in units of the row's own (four
-// products); its V rows are bf16 as they are.
-// A row's maximum runs across lanes here, so it is not formed: P is taken against
-// a reference, the row's score with the run's first key.  bf16 and fp32 have the
-// same range, so nothing is lost by a P far above 1 as long as no sum reaches
-// kMostSum; a run where one does (some score 60 powers of two above the first
-// key's) is done again with the reference moved to the maximum every step.  So is
-// one where a row's sum stays below kLeastSum: its reference is a key that it does
-// not see, or 0 for a score that is not finite, and its P may all be 0.
+// products); its V rows are rounded to f16 in those units: exact down to 2^-26 of the largest.
+// A row's maximum runs across lanes here, so it is formed once, over the first 32 keys
+// of the run (of the block, where the run has it: the row's own key and those next to
+// it), and is the row's reference m for the whole run.  P is 2^-4 at the reference: a
+// score 20 powers of two above it makes P infinite, and a P below 2^-25, a weight 2^-21
+// of the reference's, is lost.  A run whose O is not finite, or where a row's sum is so
+// small that what was lost could matter (kLost), is done again with references that the
+// sums give, P then summing to 2^15; one whose sums say nothing (the reference was a key that
+// the row does not see, or none was finite) with the reference moved to the maximum
+// every step.
 //
 // Work: units and runs as in attn_cache.cuh.  A unit that lies in several CTAs' runs
 // leaves partials in the workspace -- at most two a CTA -- and a second small kernel
-// joins them; a cluster's partials stay in shared memory and are joined over it.
+// joins them; a cluster's partials stay in shared memory and are joined over it.  A run
+// takes its block first: those rows are there before the first page.
 //
-// Warps: 8 softmax (TMEM quadrant w % 4, half of the tile's rows each), 4 that split
-// rows of bf16 into e4m3 pairs (Q of the next run, K of the block), 4 that unpack V, one
-// that issues the copies (two pages of K and V, 32 KB, a ring stage), one the MMAs.
+// Warps: 8 softmax (TMEM quadrant w % 4, half of the tile's rows each), 8 that convert
+// (Q and the block's K to e4m3 pairs, then V, a quadrant of the dims and half of a step's
+// keys each), one that issues the copies (two pages of K and V, 32 KB, a ring stage), and
+// one for the MMAs of either product.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -60,15 +67,22 @@ constexpr int kStages = 4;
 constexpr int kTileBytes = kStepKeys * kQ8D;     // codes of a step's K, or V
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kMaxR = 128;
-constexpr int kSoftWarps = 8, kSplitWarp = 8, kVWarp = 12, kTmaWarp = 16, kMmaWarp = 17, kThreads = 32 * 18;
-constexpr float kMostSum = 0x1p64f;       // of a row's P, for the result to stand,
-constexpr float kLeastSum = 0.5f;         // and at least (a reference that the row sees gives 1)
+constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 8, kTmaWarp = 16, kQkWarp = 17, kPvWarp = 18,
+              kThreads = 32 * 19;
+constexpr int kVUp = 4;                   // V is in units of 2^kVUp of its first scales
+constexpr float kUp = -4.0f;              // P is 2^kUp at the reference;
+constexpr float kUpSum = 15.0f;           // where the sums gave the reference, they are 2^kUpSum
+constexpr float kLost = 0x1p-15f;         // times the keys: the sum of a row's P, at least, for what is below
+                                          // 2^-25 to be less than 2^-10 of it
+constexpr float kLeastSum = 0x1p-100f;    // sums from here on give a reference
+constexpr int kKept = 4;                  // runs of a CTA whose references are kept for that
 constexpr int kRecFloats = kRows * (kQ8D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 256;
 constexpr int kMaxCluster = 8;
 
-// TMEM columns: two V operands (64 columns: 128 bf16 each), two S^T, one O^T
-constexpr uint32_t kColV = 0, kColS = 128, kColO = 256, kTmemCols = 512;
+// TMEM columns: two V operands (64 columns: 128 f16 each), kSBufs S^T, one O^T
+constexpr int kSBufs = 3;
+constexpr uint32_t kColV = 0, kColS = 128, kColO = kColS + kSBufs * 64, kTmemCols = 512;
 
 constexpr int kOffQ = 0;                                  // 2 x [2 parts][64 rows][128 B], swizzled
 constexpr int kQBytes = 2 * kRows * kQ8D;
@@ -78,29 +92,31 @@ constexpr int kPBytes = kStepKeys * kRows * 2;
 constexpr int kOffRing = kOffP + kPBufs * kPBytes;        // kStages x [K 128 keys][V 2 pages]
 // Scales of a step: of a context step K's two pages [2][4], V's [2][4]; of a block
 // [128 rows].  More slots than ring stages: a stage is free when its codes have been
-// read, which the scores' readers are up to two steps behind.
+// read, which the scores' readers are up to kSBufs steps behind.
 constexpr int kOffScl = kOffRing + kStages * kStageBytes;
 constexpr int kSclSlots = 8, kSclBytes = 512;
 constexpr int kOffBar = kOffScl + kSclSlots * kSclBytes;
 constexpr int kOffNm = kOffBar + 320;                     // [64] -m, m the rows' references
 constexpr int kOffMove = kOffNm + kRows * 4;              // [64] what O and l of the row are multiplied by
 constexpr int kOffRed = kOffMove + kRows * 4;             // [4 quadrants][64]
-constexpr int kOffFail = kOffRed + 4 * kRows * 4;         // a sum left its range; then where the runs start
+constexpr int kOffFail = kOffRed + 4 * kRows * 4;         // a run failed; where the runs start [5]; a run's sums are unsure; a wait gave up
 constexpr int kOffPar = kOffFail + 32;                    // [128] parents
 constexpr int kOffAnc = kOffPar + kMaxR * 4;              // [128][2] 64-bit path masks
 constexpr int kOffRow = kOffAnc + kMaxR * 16;             // [64] (sequence, block row, head) of a tile row, -1 past the last
 constexpr int kOffUnit = kOffRow + kRows * 4;             // [2][64] units of the query rows
-// [3 runs][128 dims][2] block rows whose V is not finite there.  Three, as V is unpacked up to
+// [3 runs][128 dims][2] block rows whose V is not finite there.  Three, as V is converted up to
 // two steps ahead of O^T, which can be two runs, and the epilogue behind that reads this.
 constexpr int kOffInf = kOffUnit + 2 * kRows * 4;
-constexpr int kSmemBytes = kOffInf + 3 * kQ8D * 16;
+constexpr int kOffVExp = kOffInf + 3 * kQ8D * 16;         // [3 runs] exponent of V's unit
+constexpr int kOffKept = kOffVExp + 16;           // [kKept][64] -m that the sums gave
+constexpr int kSmemBytes = kOffKept + kKept * kRows * 4;
 static_assert(kOffInf % 16 == 0, "16-byte masks");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 static_assert(kOffRing % 1024 == 0, "swizzled tiles");
 static_assert(kRecFloats * 4 <= kStages * kStageBytes, "a cluster's partial in the ring");
-// a slot is written again kSclSlots steps on, by when the scores of the step kStages + 2
-// before that one have been read
-static_assert(kSclSlots >= kStages + 2, "scale slots");
+// a slot is written again kSclSlots steps on, by when the scores of the step kStages +
+// kSBufs before that one have been read
+static_assert(kSclSlots >= kStages + kSBufs, "scale slots");
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: e4m3 A and B (K-major), fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
@@ -120,19 +136,69 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uin
 
 __device__ __forceinline__ uint16_t f32_bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// One row of bf16, 8 dims in each lane of a half-warp (dims 8 (lane & 15) ..), into row r
-// of two swizzled tiles of e4m3 (`second` bytes apart) and its unit.
-__device__ __forceinline__ void split_row(uint4 x, int r, uint8_t* tile, int second, float* unit) {
-    const int ch = threadIdx.x & 15;
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t m2 = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, w[i] & 0x7fff7fffu);
+// Instruction descriptor of tcgen05.mma kind::f16: f16 A and B (MN-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N) {
+    return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// two codes (16 bits) as an f16 pair: exact
+__device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t c) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(c)));
+    return r;
+}
+
+// A bounded wait on an mbarrier phase (each try gives up after a microsecond or so); one
+// that gives up is noted for the kernel's end.  There are many, and code that is run once a
+// step, or once, has to be short to be there in time.
+__device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, volatile int* late) {
+#pragma unroll 1
+    for (int i = 0; i < (1 << 21); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return;
+    }
+    *late = 1;
+}
+
+// Which of n buffers the next step uses, and the parity of that use.
+struct Turn {
+    int x = 0;
+    uint32_t parity = 0u;
+    __device__ __forceinline__ void next(int n) {
+        if (++x == n) x = 0, parity ^= 1u;
+    }
+};
+
+// A row of bf16, 8 dims in each lane of a half-warp (dims 8 (lane & 15) ..).
+// Its largest magnitude's bits:
+__device__ __forceinline__ uint32_t row_most(uint4 x) {
+    uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
-    const uint32_t m = max(m2 >> 16, m2 & 0xffffu);
-    const bool bad = m >= 0x7f80u;   // NaN or infinity: the row's scores are NaN
-    const int e = bad ? 0 : q8_exponent(__uint_as_float(m << 16));
+    return max(m2 >> 16, m2 & 0xffffu);
+}
+// The row in units of 2^e as row r of two swizzled tiles of e4m3, `second` bytes apart.
+// One that holds NaN or infinity is NaN.
+__device__ __forceinline__ void split_row(uint4 x, bool bad, int e, int r, uint8_t* tile, int second) {
+    const int ch = threadIdx.x & 15;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     const float rs = q8_pow2(-e);
     uint32_t c1[2], c2[2];
 #pragma unroll
@@ -148,11 +214,10 @@ __device__ __forceinline__ void split_row(uint4 x, int r, uint8_t* tile, int sec
     uint8_t* at = tile + r * 128 + (((ch >> 1) ^ (r & 7)) << 4) + (ch & 1) * 8;
     *reinterpret_cast<uint2*>(at) = make_uint2(c1[0], c1[1]);
     *reinterpret_cast<uint2*>(at + second) = make_uint2(c2[0], c2[1]);
-    if (ch == 0) *unit = q8_pow2(e);
 }
 
-// kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (their
-// columns of P stay zero)
+// kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (what their
+// columns of P and O hold is not looked at)
 template <int kRT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, Work wk, float* __restrict__ ws) {
     constexpr int kLive = 2 * kRT;
@@ -160,21 +225,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint64_t* ring_full = bars;                   // [kStages]
-    uint64_t* ring_empty = ring_full + kStages;   // [kStages] V unpacked (4 warps) and S^T formed
+    uint64_t* ring_empty = ring_full + kStages;   // [kStages] V converted and S^T formed
     uint64_t* ring_go = ring_empty + kStages;     // [kStages] free for a block's K
-    uint64_t* v_full = ring_go + kStages;         // [2] V operand unpacked
-    uint64_t* s_full = v_full + 2;                // [2] S^T formed
-    uint64_t* s_empty = s_full + 2;               // [2] scores read
-    uint64_t* p_full = s_empty + 2;               // [kPBufs] P written (and O rescaled): one each, as a warp may
-                                                  // be two steps ahead of another
-    uint64_t* pv_done = p_full + kPBufs;          // [2] O^T has the step (P and the V operand read)
-    uint64_t* q_ready = pv_done + 2;              // [2] query rows there
-    uint64_t* q_free = q_ready + 2;               // [2] the run's S^T are formed, and its units no longer wanted
+    uint64_t* v_full = ring_go + kStages;         // [2] V operand there
+    uint64_t* s_full = v_full + 2;                // [kSBufs] S^T formed
+    uint64_t* s_empty = s_full + kSBufs;          // [kSBufs] scores read
+    uint64_t* p_full = s_empty + kSBufs;          // [kPBufs] P written (and O rescaled)
+    uint64_t* pv_done = p_full + kPBufs;          // [kPBufs] O^T has the step (P and the V operand read)
+    uint64_t* q_ready = pv_done + kPBufs;         // [2] query rows there
+    uint64_t* q_free = q_ready + 2;               // [2] the run's S^T are formed, and what was found of it no longer wanted
     uint64_t* o_free = q_free + 2;                // O^T read by the epilogue
-    uint64_t* o_done = o_free + 1;                // O^T has the run's last step (pv_done is no help there: two
-                                                  // of its phases may be missing, and a wait passes at once)
+    uint64_t* o_done = o_free + 1;                // O^T has the run's last step
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(o_done + 1);
-    static_assert((3 * kStages + 14 + kPBufs) * 8 + 4 <= 320, "barrier area");
+    static_assert((3 * kStages + 8 + 2 * kSBufs + 2 * kPBufs) * 8 + 4 <= 320, "barrier area");
     float* nm_s = reinterpret_cast<float*>(smem + kOffNm);
     float* move_s = reinterpret_cast<float*>(smem + kOffMove);
     float* red_s = reinterpret_cast<float*>(smem + kOffRed);
@@ -182,36 +245,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     uint64_t* anc_s = reinterpret_cast<uint64_t*>(smem + kOffAnc);
     int* row_s = reinterpret_cast<int*>(smem + kOffRow);
     uint64_t* inf_s = reinterpret_cast<uint64_t*>(smem + kOffInf);
+    int* vexp_s = reinterpret_cast<int*>(smem + kOffVExp);
     auto scales = [](int it) { return reinterpret_cast<float*>(smem + kOffScl + it % kSclSlots * kSclBytes); };
     auto stage = [](int it) { return smem + kOffRing + it % kStages * kStageBytes; };
+    auto stage_use = [](int it) { return static_cast<uint32_t>(it / kStages) & 1u; };
+
+    volatile int* fail_s = reinterpret_cast<volatile int*>(smem + kOffFail);
+    volatile int* late = fail_s + 7;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        *reinterpret_cast<volatile int*>(smem + kOffFail) = 0;
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&ring_full[i], 1);
-            mbar_init(&ring_empty[i], 5);
-            mbar_init(&ring_go[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&v_full[i], 4);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], kSoftWarps);
-            mbar_init(&pv_done[i], 1);
-            mbar_init(&q_ready[i], 4);
-            mbar_init(&q_free[i], 1 + kSoftWarps);
-        }
-        for (int i = 0; i < kPBufs; ++i) mbar_init(&p_full[i], kSoftWarps);
-        mbar_init(o_free, kSoftWarps);
-        mbar_init(o_done, 1);
+        volatile int* f = reinterpret_cast<volatile int*>(smem + kOffFail);
+        f[0] = f[6] = f[7] = 0;
+        auto init = [](uint64_t* b, int n, int count) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) mbar_init(b + i, count);
+        };
+        init(ring_full, kStages, 1);
+        init(ring_empty, kStages, kConvWarps + 1);
+        init(ring_go, kStages, 1);
+        init(v_full, 2, kConvWarps);
+        init(s_full, kSBufs, 1);
+        init(s_empty, kSBufs, kSoftWarps);
+        init(p_full, kPBufs, kSoftWarps);
+        init(pv_done, kPBufs, 1);
+        init(q_ready, 2, kConvWarps);
+        init(q_free, 2, 1 + kSoftWarps);
+        init(o_free, 1, kSoftWarps);
+        init(o_done, 1, 1);
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tmem_alloc(tmem_s, kTmemCols);
-    if (kLive < kRows) {   // the columns of P past the live rows stay zero
-        for (int x = threadIdx.x; x < kPBufs * kPBytes / 16; x += kThreads)
-            reinterpret_cast<uint4*>(smem + kOffP)[x] = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-    }
+    if (warp == kPvWarp) tmem_alloc(tmem_s, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -231,21 +295,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     const int rank = kCluster ? blockIdx.x % wk.cluster : 0;
     if constexpr (kCluster) walk.start_unit(a, wk, blockIdx.x / wk.cluster, rank);
     else walk.start(a, wk, blockIdx.x, gridDim.x);
-    volatile int* fail_s = reinterpret_cast<volatile int*>(smem + kOffFail);
     if (threadIdx.x == 0) walk.save(fail_s + 1);
-    // Each role runs the CTA's runs once, and once more with `safe` where a sum
-    // left its range (the softmax warps' verdict, after all have finished).
-    bool safe = false;
+    // Each role does the CTA's runs once, and a second time where one of them failed (the
+    // softmax warps' verdict, after all have finished).
+    bool second = false;
     // a warp's wait; its lanes go on together (what follows is warp-collective)
-    auto wait = [&](uint64_t* bar, int parity) {
-        mbar_wait(bar, static_cast<uint32_t>(parity), a.err);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        bar_wait(bar, parity, late);
         __syncwarp();
     };
     auto again = [&]() {
-        if (safe) return false;
+        if (second) return false;
         __syncwarp();
         named_barrier(2, kThreads);
-        safe = true;
+        second = true;
         if (*fail_s == 0) return false;
         walk.load(a, fail_s + 1);
         return true;
@@ -261,300 +324,331 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 const int g = walk.cur_unit / wk.row_tiles;
                 const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
                 const int np = walk.p1 - walk.p0;
-                for (int i0 = 0; i0 < np; i0 += 32) {
-                    // 32 table entries at once: lane l holds page p0 + i0 + l
-                    int pg = i0 + lane < np ? __ldg(tab + walk.p0 + i0 + lane) : 0;
-                    const bool bad = pg < 0 || pg >= a.num_pages;
-                    if (bad) {
-                        raise_error(a.err, SV_DEVERR_PAGE);
+                // lane l holds page p0 + 32 k + l, 32 table entries at once, and its scales (of all else
+                // 16 bytes would be a copy of their own, as long to issue as one of 8 KB)
+                int pg = 0, i = walk.block ? -2 : 0;
+                uint4 fk = make_uint4(0u, 0u, 0u, 0u), fv = fk;
+#pragma unroll 1
+                for (; i < np; i += 2, ++it) {
+                    if ((i & 31) == 0) {
                         pg = -1;
-                    }
-                    for (int i = 0; i < 32 && i0 + i < np; i += 2, ++it) {
-                        const int pa = __shfl_sync(0xffffffffu, pg, i), pb = __shfl_sync(0xffffffffu, pg, i + 1);
-                        const bool two = i0 + i + 1 < np, la = pa >= 0, lb = two && pb >= 0;
-                        const int s = it % kStages;
-                        uint8_t* st = stage(it);
-                        float* sc = scales(it);
-                        wait(&ring_empty[s], ((it / kStages) & 1) ^ 1);
-                        if (!la || (two && !lb)) {   // a page outside the pool reads as zeros
-                            for (int p = 0; p < 2; ++p) {
-                                if (p == 0 ? la : lb || !two) continue;
-                                for (int x = lane; x < kQ8Codes / 16; x += 32) {
-                                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                                    reinterpret_cast<uint4*>(st + p * kQ8Codes)[x] = z;
-                                    reinterpret_cast<uint4*>(st + kTileBytes + p * kQ8Codes)[x] = z;
-                                }
-                                if (lane < 4) sc[4 * p + lane] = sc[8 + 4 * p + lane] = q8_pow2(kQ8MinExp);
+                        if (i + lane < np) {
+                            pg = __ldg(tab + walk.p0 + i + lane);
+                            if (pg < 0 || pg >= a.num_pages) {
+                                raise_error(a.err, SV_DEVERR_PAGE);
+                                pg = -1;
                             }
-                            fence_proxy_async_smem();
-                            __syncwarp();
                         }
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(&ring_full[s], ((la ? 2u : 0u) + (lb ? 2u : 0u)) * (kQ8Codes + 16u));
-                            auto copy = [&](int p, int page) {
-                                const size_t at = (static_cast<size_t>(page) * a.Hkv + g) * kQ8Bytes;
-                                bulk_g2s(st + p * kQ8Codes, a.k_pool + at, kQ8Codes, &ring_full[s]);
-                                bulk_g2s(sc + 4 * p, a.k_pool + at + kQ8Codes, 16, &ring_full[s]);
-                                bulk_g2s(st + kTileBytes + p * kQ8Codes, a.v_pool + at, kQ8Codes, &ring_full[s]);
-                                bulk_g2s(sc + 8 + 4 * p, a.v_pool + at + kQ8Codes, 16, &ring_full[s]);
-                            };
-                            if (la) copy(0, pa);
-                            if (lb) copy(1, pb);
+                        fk = fv = make_uint4(0u, 0u, 0u, 0u);
+                        if (pg >= 0) {
+                            const size_t at = (static_cast<size_t>(pg) * a.Hkv + g) * kQ8Bytes + kQ8Codes;
+                            fk = __ldg(reinterpret_cast<const uint4*>(a.k_pool + at));
+                            fv = __ldg(reinterpret_cast<const uint4*>(a.v_pool + at));
                         }
                         __syncwarp();
                     }
-                }
-                if (walk.block) {   // the stage of the block's K, whose writers do not follow the others' use of it
-                    wait(&ring_empty[it % kStages], ((it / kStages) & 1) ^ 1);
-                    if (lane == 0) mbar_arrive(&ring_go[it % kStages]);
+                    const int s = it % kStages;
+                    wait(&ring_empty[s], stage_use(it) ^ 1u);
+                    if (i < 0) {   // the stage of the block's K, whose writers do not follow the others' use of it
+                        if (lane == 0) mbar_arrive(&ring_go[s]);
+                        __syncwarp();
+                        continue;
+                    }
+                    uint8_t* st = stage(it);
+                    float* sc = scales(it);
+#pragma unroll 1
+                    for (int p = 0; p < 2; ++p) {
+                        const int page = __shfl_sync(0xffffffffu, pg, (i + p) & 31);
+                        if (page >= 0) {
+                            if (lane == 0) {
+                                const size_t at = (static_cast<size_t>(page) * a.Hkv + g) * kQ8Bytes;
+                                mbar_expect_tx(&ring_full[s], 2 * kQ8Codes);
+                                bulk_g2s(st + p * kQ8Codes, a.k_pool + at, kQ8Codes, &ring_full[s]);
+                                bulk_g2s(st + kTileBytes + p * kQ8Codes, a.v_pool + at, kQ8Codes, &ring_full[s]);
+                            }
+                        } else if (i + p < np) {   // a page outside the pool reads as zeros
+#pragma unroll 1
+                            for (int x = lane; x < kQ8Codes / 16; x += 32) {
+                                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                                reinterpret_cast<uint4*>(st + p * kQ8Codes)[x] = z;
+                                reinterpret_cast<uint4*>(st + kTileBytes + p * kQ8Codes)[x] = z;
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                    }
+                    if ((lane ^ (i & 31)) < 2) {   // lanes i and i + 1 (i is even)
+                        reinterpret_cast<uint4*>(sc)[lane & 1] = fk;
+                        reinterpret_cast<uint4*>(sc)[2 + (lane & 1)] = fv;
+                    }
                     __syncwarp();
-                    ++it;
+                    if (lane == 0) mbar_arrive(&ring_full[s]);
+                    __syncwarp();
                 }
             }
         } while (again());
-    } else if (warp == kMmaWarp) {
-        // ---------------- MMA issuer ----------------
+    } else if (warp == kQkWarp) {
+        // ---------------- S^T = K Q^T ----------------
         constexpr uint32_t id_s = idesc_e4m3_f32(128, kLive);
-        constexpr uint32_t id_o = idesc_bf16_f32(128, kRows, false, true);
         int it = 0, seg = 0;
+        Turn sb;
+        static_assert(kSBufs == kPBufs, "one turn for both");
         do {
             while (walk.next(a, wk)) {
                 const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
                 if (elect_one()) {
                     const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ + (seg & 1) * kQBytes), 16, 1024);
-                    // S of step i + 2 goes ahead of P V of step i: it only waits for the
-                    // scores of step i to be read, not for their P
-                    auto scores = [&](int i) {
-                        const int x = i & 1, s = i % kStages;
-                        mbar_wait(&ring_full[s], (i / kStages) & 1, a.err);
-                        mbar_wait(&s_empty[x], ((i >> 1) & 1) ^ 1, a.err);
+                    bar_wait(&q_ready[seg & 1], (seg >> 1) & 1, late);
+#pragma unroll 1
+                    for (int st = 0; st < n; ++st) {
+                        const int i = it + st, s = i % kStages;
+                        bar_wait(&ring_full[s], stage_use(i), late);
+                        bar_wait(&s_empty[sb.x], sb.parity ^ 1u, late);
+                        // (and for the buffer that these scores' P will take: P V of kPBufs steps before)
+                        bar_wait(&pv_done[sb.x], sb.parity ^ 1u, late);
                         tc_fence_after();
                         const uint64_t kd = smem_desc_sw128(smem_u32(stage(i)), 16, 1024);
-                        const bool last = i == it + n - 1;
-#pragma unroll
-                        for (int kc = 0; kc < kQ8D / 32; ++kc)
-                            tc_mma_e4m3(tS(x), kd + kc * 2, qd + kc * 2, id_s, kc > 0 ? 1u : 0u);
-#pragma unroll
-                        for (int kc = 0; kc < kQ8D / 32; ++kc)
-                            tc_mma_e4m3(tS(x), kd + kc * 2, qd + (kQBytes / 2 >> 4) + kc * 2, id_s, 1u);
-                        if (last && walk.block) {   // the remainders of the block's K
-#pragma unroll
-                            for (int kc = 0; kc < kQ8D / 32; ++kc)
-                                tc_mma_e4m3(tS(x), kd + (kTileBytes >> 4) + kc * 2, qd + kc * 2, id_s, 1u);
-#pragma unroll
-                            for (int kc = 0; kc < kQ8D / 32; ++kc)
-                                tc_mma_e4m3(tS(x), kd + (kTileBytes >> 4) + kc * 2, qd + (kQBytes / 2 >> 4) + kc * 2, id_s, 1u);
-                        }
-                        tc_commit(&s_full[x]);
-                        tc_commit(&ring_empty[s]);
-                        if (last) tc_commit(&q_free[seg & 1]);
-                    };
-                    mbar_wait(&q_ready[seg & 1], (seg >> 1) & 1, a.err);
+                        // K by either part of Q, and the remainders of a block's K
+                        const int parts = walk.block && st == 0 ? 4 : 2;
 #pragma unroll 1
-                    for (int st = -2; st < n; ++st) {
-                        if (st + 2 < n) scores(it + st + 2);
-                        if (st < 0) continue;
-                        const int i = it + st, x = i & 1;
-                        if (st == 0) mbar_wait(o_free, (seg & 1) ^ 1, a.err);
-                        mbar_wait(&v_full[x], (i >> 1) & 1, a.err);
-                        mbar_wait(&p_full[i % kPBufs], (i / kPBufs) & 1, a.err);
-                        tc_fence_after();
-                        const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + i % kPBufs * kPBytes), 16, 1024);
+                        for (int p = 0; p < parts; ++p) {
+                            const uint64_t kp = kd + (p >> 1) * (kTileBytes >> 4), qp = qd + (p & 1) * (kQBytes / 2 >> 4);
 #pragma unroll
-                        for (int kc = 0; kc < kStepKeys / 16; ++kc)
-                            tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), id_o, (kc > 0 || st > 0) ? 1u : 0u);
-                        tc_commit(&pv_done[x]);
-                        if (st == n - 1) tc_commit(o_done);
+                            for (int kc = 0; kc < kQ8D / 32; ++kc)
+                                tc_mma_e4m3(tS(sb.x), kp + kc * 2, qp + kc * 2, id_s, (p > 0 || kc > 0) ? 1u : 0u);
+                        }
+                        tc_commit(&s_full[sb.x]);
+                        tc_commit(&ring_empty[s]);
+                        sb.next(kSBufs);
                     }
+                    tc_commit(&q_free[seg & 1]);
                 }
                 __syncwarp();
+                sb.x = __shfl_sync(0xffffffffu, sb.x, 0), sb.parity = __shfl_sync(0xffffffffu, sb.parity, 0);
                 it += n;
                 ++seg;
             }
         } while (again());
-    } else if (warp >= kVWarp) {
-        // ---------------- V: a dim's codes to bf16 ----------------
-        const int l = q4 * 32 + lane;   // TMEM lane: the dim
-        int it = 0, seg = -1;
-        bool waited = !early;
+    } else if (warp == kPvWarp) {
+        // ---------------- O^T += V^T P^T ----------------
+        constexpr uint32_t id_o = idesc_f16_f32_bmn(128, kRows), id_blk = idesc_bf16_f32(128, kRows, false, true);
+        int it = 0, seg = 0;
+        Turn pb;
         do {
             while (walk.next(a, wk)) {
-                ++seg;
-                const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + walk.cur_unit / wk.row_tiles) * a.R * kQ8D;
-                // the block's rows, read at the end of the run by loads that wait for one
-                // another, are brought near meanwhile (256 bytes a row; a thread a line or two)
-                if (walk.block && waited)
-                    for (int x = l; x < 2 * a.R; x += 128)
-                        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.v_blk + blk0 + 64 * x));
-                for (int st = 0; st < walk.ctx_steps(); ++st, ++it) {
-                    const uint8_t* v = stage(it) + kTileBytes;
-                    wait(&ring_full[it % kStages], (it / kStages) & 1);
-                    // keys of the step that exist: what the others' codes hold is not looked
-                    // at (0 * a V that is not finite would be NaN)
-                    const int have = min(walk.cur_t - (walk.p0 + 2 * st) * kQ8Page, (walk.p1 - walk.p0 - 2 * st) * kQ8Page);
-                    const uint4 f0 = reinterpret_cast<const uint4*>(scales(it))[2], f1 = reinterpret_cast<const uint4*>(scales(it))[3];
-                    const uint32_t f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                    // NaN rows: all dims' codes are then NaN, so a lane looks at four positions of one
-                    // dim; and scales above 2^7, whose product with 2^120 bf16 cannot hold
-                    uint32_t odd = q8_nan_bytes(*reinterpret_cast<const uint32_t*>(v + q8_v_off(lane >> 1, q4 * 32) + 4 * (lane & 1)));
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) odd |= f[r] > 0x43000000u ? 1u : 0u;
-                    const bool general = __any_sync(0xffffffffu, odd != 0u) || have < kStepKeys;
-                    wait(&pv_done[it & 1], ((it >> 1) & 1) ^ 1);
-                    tc_fence_after();
-                    auto unpack = [&](auto general_c) {
-                        constexpr bool kGeneral = decltype(general_c)::value;
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {   // 32 keys: two runs
-                            uint32_t r[16];
-#pragma unroll
-                            for (int o = 0; o < 4; ++o) {
-                                uint2 w = *reinterpret_cast<const uint2*>(v + q8_v_off(4 * h + o, l));
-                                const uint32_t fs = f[2 * h + (o >> 1)];
-                                // 2^120 times the scale, as a bf16 pair
-                                uint32_t m = ((fs >> 23) + 120u) * 0x00800080u;
-                                if constexpr (kGeneral) {
-                                    const int left = have - 32 * h - 8 * o;   // keys of the octet that exist
-                                    if (left < 8) {
-                                        const uint64_t keep = left <= 0 ? 0ull : (1ull << 8 * left) - 1ull;
-                                        w.x &= static_cast<uint32_t>(keep);
-                                        w.y &= static_cast<uint32_t>(keep >> 32);
-                                        if (left <= 0) m = 0u;
-                                    }
-                                    if (fs > 0x43000000u) m = q8_pow2_pair(127);
-                                }
-                                uint32_t p[4] = {q8_pair<0, 1>(w.x, 0u), q8_pair<2, 3>(w.x, 0u), q8_pair<0, 1>(w.y, 0u),
-                                                 q8_pair<2, 3>(w.y, 0u)};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    uint32_t y = q8_mul2(p[k], m);
-                                    if constexpr (kGeneral) {
-                                        if (fs > 0x43000000u && have > 32 * h + 8 * o)
-                                            y = q8_mul2(y, ((fs >> 23) - 7u) * 0x00800080u);
-                                        y = q8_nan_pair(p[k], y);
-                                    }
-                                    r[4 * o + k] = y;
-                                }
-                            }
-                            tmem_st16(tV(it & 1) + lane_off + 16 * h, r);
-                        }
-                    };
-                    if (general) unpack(std::true_type{});
-                    else unpack(std::false_type{});
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&v_full[it & 1]);
-                        mbar_arrive(&ring_empty[it % kStages]);
-                    }
-                }
-                if (walk.block) {
-                    if (!waited) pdl_wait();
-                    waited = true;
-                    wait(&pv_done[it & 1], ((it >> 1) & 1) ^ 1);
-                    tc_fence_after();
-                    const uint16_t* src = a.v_blk + blk0 + l;
-                    uint32_t most = 0u;   // the largest magnitude's bits (in either half)
-                    uint64_t inf[2] = {0ull, 0ull};
-                    auto unpack = [&](auto fix_c) {
+                const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
+                if (elect_one()) {
+                    bar_wait(o_free, (seg & 1) ^ 1, late);
 #pragma unroll 1
-                        for (int h = 0; h < 4; ++h) {
-                            uint32_t r[16];
+                    for (int st = 0; st < n; ++st) {
+                        const int i = it + st, x = i & 1;
+                        const bool blk = walk.block && st == 0;
+                        bar_wait(&v_full[x], (i >> 1) & 1, late);
+                        bar_wait(&p_full[pb.x], pb.parity, late);
+                        tc_fence_after();
+                        uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + pb.x * kPBytes), 16, 1024);
+                        uint32_t more = st > 0 ? 1u : 0u;
+#pragma unroll 1
+                        for (int p = blk ? 0 : 1; p < 2; ++p) {   // a block's P is in two parts
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const int key = 32 * h + 2 * k;
-                                uint32_t lo = key < a.R ? __ldg(src + key * kQ8D) : 0u;
-                                uint32_t hi = key + 1 < a.R ? __ldg(src + (key + 1) * kQ8D) : 0u;
-                                if constexpr (decltype(fix_c)::value) {
-                                    if ((lo & 0x7f80u) == 0x7f80u) inf[h >> 1] |= 1ull << (key & 63), lo = 0u;
-                                    if ((hi & 0x7f80u) == 0x7f80u) inf[h >> 1] |= 2ull << (key & 63), hi = 0u;
-                                } else {
-                                    most = max(most, max(lo & 0x7fffu, hi & 0x7fffu));
-                                }
-                                r[k] = lo | hi << 16;
+                            for (int kc = 0; kc < kStepKeys / 16; ++kc) {
+                                tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), blk ? id_blk : id_o, more);
+                                more = 1u;
                             }
-                            tmem_st16(tV(it & 1) + lane_off + 16 * h, r);
+                            pd = smem_desc_sw128(smem_u32(stage(i)), 16, 1024);
                         }
-                    };
-                    unpack(std::false_type{});
-                    // V that is not finite would reach the rows that do not see it (0 times it is NaN):
-                    // it stays out of the product, and the epilogue adds it where it is seen
-                    if (__any_sync(0xffffffffu, most >= 0x7f80u)) unpack(std::true_type{});
-                    inf_s[(seg % 3 * kQ8D + l) * 2] = inf[0];
-                    inf_s[(seg % 3 * kQ8D + l) * 2 + 1] = inf[1];
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&v_full[it & 1]);
-                    // (an arrival before the block's K is there would count for the stage's use before)
-                    wait(&ring_full[it % kStages], (it / kStages) & 1);
-                    if (lane == 0) mbar_arrive(&ring_empty[it % kStages]);
-                    ++it;
+                        if (blk) tc_commit(&ring_empty[i % kStages]);
+                        tc_commit(&pv_done[pb.x]);
+                        pb.next(kPBufs);
+                    }
+                    tc_commit(o_done);
                 }
+                __syncwarp();
+                pb.x = __shfl_sync(0xffffffffu, pb.x, 0), pb.parity = __shfl_sync(0xffffffffu, pb.parity, 0);
+                it += n;
+                ++seg;
             }
         } while (again());
-        if (!waited) pdl_wait();
-    } else if (warp >= kSplitWarp) {
-        // ---------------- rows of bf16 to e4m3 pairs: Q, and the block's K ----------------
+    } else if (warp >= kConvWarp) {
+        // ---------------- to e4m3 pairs and to f16 ----------------
         if (early) pdl_wait();
-        constexpr int kAhead = 8;   // rows a half-warp has in flight
-        const int sub = 2 * (warp - kSplitWarp) + (lane >> 4), ch = lane & 15;   // half-warps take rows sub, sub + 8, ..
+        constexpr int kQRows = kLive / 16;   // query rows of a half-warp: hw, hw + 16, ..
+        const int cw = warp - kConvWarp, hw = 2 * cw + (lane >> 4), ch = lane & 15;
+        const int kh = cw >> 2;              // V: which half of a step's keys (a page),
+        const int l = q4 * 32 + lane;        // and the TMEM lane: the dim
         int it = 0, seg = 0;
-        uint32_t gone = 0;          // (bit s) parity of the next block in stage s
+        Turn pb;                             // of step it - 2
+        uint32_t gone = 0;                   // (bit s) parity of the next block in stage s
+        auto conv_sync = []() {
+            __syncwarp();
+            named_barrier(3, 32 * kConvWarps);
+        };
+        // the V operand of this step is free: P V of two steps before is done
+        auto v_free = [&]() {
+            if (it >= 2) {
+                wait(&pv_done[pb.x], pb.parity);
+                pb.next(kPBufs);
+            }
+            tc_fence_after();
+        };
+        auto v_done = [&](bool free) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&v_full[it & 1]);
+                if (free) mbar_arrive(&ring_empty[it % kStages]);
+            }
+            ++it;
+        };
         do {
             while (walk.next(a, wk)) {
                 const int g = walk.cur_unit / wk.row_tiles, row0 = walk.cur_unit % wk.row_tiles * wk.tile_rows;
                 const int nrows = min(wk.tile_rows, a.R * a.G - row0);
-                uint4 x[kAhead];
+                const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R * kQ8D;
+                // half-warps take the query rows, then the block's rows of K
+                const int jobs = kQRows + (walk.block ? (a.R + 15) >> 4 : 0);
+                auto k_row = [&](int job) {
+                    const int r = hw + 16 * (job - kQRows);
+                    return job < jobs && r < a.R ? __ldg(reinterpret_cast<const uint4*>(a.k_blk + blk0 + r * kQ8D) + ch)
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+                };
+                uint4 x[kQRows];
 #pragma unroll
-                for (int i = 0; i < kLive / 8; ++i) {
-                    const int r = sub + 8 * i, gr = row0 + r, j = gr * wk.inv_g >> 16;
+                for (int i = 0; i < kQRows; ++i) {
+                    const int r = hw + 16 * i, gr = row0 + r, j = gr * wk.inv_g >> 16;
                     x[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (r < nrows)
                         x[i] = __ldg(reinterpret_cast<const uint4*>(
                                          a.q + (static_cast<size_t>(walk.cur_b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ8D) + ch);
                 }
-                wait(&q_free[seg & 1], ((seg >> 1) & 1) ^ 1);
+                uint4 ahead = k_row(kQRows);
+                uint32_t most[kQRows];
 #pragma unroll
-                for (int i = 0; i < kLive / 8; ++i)
-                    split_row(x[i], sub + 8 * i, smem + kOffQ + (seg & 1) * kQBytes, kQBytes / 2,
-                              reinterpret_cast<float*>(smem + kOffUnit) + (seg & 1) * kRows + sub + 8 * i);
+                for (int i = 0; i < kQRows; ++i) most[i] = row_most(x[i]);
+                wait(&q_free[seg & 1], ((seg >> 1) & 1) ^ 1);
+                float* unit = reinterpret_cast<float*>(smem + kOffUnit) + (seg & 1) * kRows;
+                const int s = it % kStages;
+#pragma unroll 1
+                for (int job = 0; job < jobs; ++job) {
+                    const bool is_q = job < kQRows;
+                    uint4 y = ahead;
+                    uint32_t m = 0u;
+#pragma unroll
+                    for (int i = 0; i < kQRows; ++i)
+                        if (job == i) y = x[i], m = most[i];
+                    if (job == kQRows) {   // the query rows are there; now the stage for the block's K
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
+                        wait(&ring_go[s], gone >> s & 1u);
+                        gone ^= 1u << s;
+                    }
+                    if (!is_q) {
+                        ahead = k_row(job + 1);
+                        m = row_most(y);
+                    }
+                    const bool bad = m >= 0x7f80u;
+                    const int e = q8_exponent(__uint_as_float(bad ? 0u : m << 16));
+                    const int r = hw + 16 * (is_q ? job : job - kQRows);
+                    split_row(y, bad, e, r, is_q ? smem + kOffQ + (seg & 1) * kQBytes : stage(it), is_q ? kQBytes / 2 : kTileBytes);
+                    if (ch == 0) (is_q ? unit : scales(it))[r] = q8_pow2(e);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
-                ++seg;
-                it += walk.ctx_steps();
-                if (walk.block) {
-                    const int s = it % kStages;
-                    const uint4* src = reinterpret_cast<const uint4*>(a.k_blk + (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R * kQ8D) + ch;
-                    bool go = false;
+                if (!walk.block) {
+                    if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
+                } else {
+                    conv_sync();
+                    if (warp == kConvWarp && lane == 0) mbar_arrive(&ring_full[s]);
+                }
+                // V is in units of 2^ev: of the largest scale of the first pages (their live runs) with
+                // kVUp powers of two to spare; done again, of all.  Every warp finds it by itself.
+                int ev = 0;
+                if (walk.ctx_steps() > 0) {
+                    const int first = it + (walk.block ? 1 : 0);
+                    uint32_t top = 0u;
+                    if (!second) {
+                        wait(&ring_full[first % kStages], stage_use(first));
+                        const int left = walk.cur_t - walk.p0 * kQ8Page - kQ8Run * lane;
+                        if (lane < 8 && left > 0 && (lane < 4 || walk.p0 + 1 < walk.p1)) top = reinterpret_cast<const uint32_t*>(scales(first))[8 + lane];
+                    } else {
+                        const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
 #pragma unroll 1
-                    for (int r0 = 0; r0 < a.R; r0 += 8 * kAhead) {
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i) {
-                            const int r = r0 + sub + 8 * i;
-                            x[i] = make_uint4(0u, 0u, 0u, 0u);
-                            if (r < a.R) x[i] = __ldg(src + r * (kQ8D / 8));
-                        }
-                        if (!go) {
-                            wait(&ring_go[s], gone >> s & 1u);
-                            gone ^= 1u << s;
-                            go = true;
-                        }
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i) {
-                            if (r0 + 8 * i < a.R)
-                                split_row(x[i], r0 + sub + 8 * i, stage(it), kTileBytes, scales(it) + r0 + sub + 8 * i);
+                        for (int p = 4 * walk.p0 + lane; p < 4 * walk.p1; p += 32) {
+                            const int pg = __ldg(tab + (p >> 2));
+                            if (pg < 0 || pg >= a.num_pages || p * kQ8Run >= walk.cur_t) continue;
+                            top = max(top, __ldg(reinterpret_cast<const uint32_t*>(
+                                               a.v_pool + (static_cast<size_t>(pg) * a.Hkv + g) * kQ8Bytes + kQ8Codes) + (p & 3)));
                         }
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    named_barrier(3, 128);
-                    if (warp == kSplitWarp && lane == 0) mbar_arrive(&ring_full[s]);
-                    __syncwarp();
-                    ++it;
+                    ev = q8_stored_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, top))) + kVUp;
                 }
+                if (cw == 0 && lane == 0) vexp_s[seg % 3] = ev;
+                const float to = q8_pow2(-ev);
+                if (walk.block) {
+                    // V stays bf16: drafts that no row sees may be of any size.  Rows past the last are
+                    // zeros.  What is not finite would reach the rows that do not see it (0 times it is
+                    // NaN): it stays out of the product, and the epilogue adds it where it is seen
+                    v_free();
+                    const uint16_t* vsrc = a.v_blk + blk0 + l;
+                    uint64_t inf = 0ull;
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        const int k0 = 64 * kh + 16 * h;
+                        uint32_t w[16], r[8];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) w[k] = k0 + k < a.R ? __ldg(vsrc + (k0 + k) * kQ8D) : 0u;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if ((w[k] & 0x7f80u) == 0x7f80u) inf |= 1ull << (16 * h + k), w[k] = 0u;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            r[k] = pack_bf16x2(__uint_as_float(w[2 * k] << 16) * to, __uint_as_float(w[2 * k + 1] << 16) * to);
+                        tmem_st8(tV(it & 1) + lane_off + 32 * kh + 8 * h, r);
+                    }
+                    inf_s[(seg % 3 * kQ8D + l) * 2 + kh] = inf;
+                    // (the stage's place is kept for P's second part: one arrival comes from its product)
+                    v_done(cw != 0);
+                }
+#pragma unroll 1
+                for (int st = 0; st < walk.ctx_steps(); ++st) {
+                    uint8_t* v = stage(it) + kTileBytes + kh * kQ8Codes;
+                    wait(&ring_full[it % kStages], stage_use(it));
+                    const float4 f4 = reinterpret_cast<const float4*>(scales(it))[2 + kh];
+                    float f[4] = {f4.x * to, f4.y * to, f4.z * to, f4.w * to};
+                    // keys of this page that exist: what the others' codes hold is not looked
+                    // at (0 * a V that is not finite would be NaN)
+                    const int have = min(walk.cur_t - (walk.p0 + 2 * st + kh) * kQ8Page, (walk.p1 - walk.p0 - 2 * st - kh) * kQ8Page);
+                    if (have < kQ8Page) {
+#pragma unroll 1
+                        for (int o = max(have, 0) >> 3; o < 8; ++o) {   // (this thread's dim alone)
+                            uint64_t* w = reinterpret_cast<uint64_t*>(v + q8_v_off(o, l));
+                            const int left = have - 8 * o;
+                            *w = left <= 0 ? 0ull : *w & ((1ull << 8 * left) - 1ull);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (have <= kQ8Run * r) f[r] = 0.f;
+                    }
+                    v_free();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {   // 32 keys: two runs
+                        uint32_t r[16];
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            const uint2 w = *reinterpret_cast<const uint2*>(v + q8_v_off(4 * h + o, l));
+                            const uint32_t m = pack_f16x2(f[2 * h + (o >> 1)], f[2 * h + (o >> 1)]);
+                            r[4 * o] = mul_f16x2(f16x2_of_codes(w.x), m);
+                            r[4 * o + 1] = mul_f16x2(f16x2_of_codes(w.x >> 16), m);
+                            r[4 * o + 2] = mul_f16x2(f16x2_of_codes(w.y), m);
+                            r[4 * o + 3] = mul_f16x2(f16x2_of_codes(w.y >> 16), m);
+                        }
+                        tmem_st16(tV(it & 1) + lane_off + 32 * kh + 16 * h, r);
+                    }
+                    v_done(true);
+                }
+                ++seg;
             }
         } while (again());
     } else {
@@ -574,9 +668,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         const float sc = a.scale_log2;
         const int rows = a.R * a.G;
         int it = 0, seg = 0;
+        Turn sb;
+        uint32_t unsure = 0u;                  // (bit r) run r's sums give no references
+        float* kept_s = reinterpret_cast<float*>(smem + kOffKept);
         do {
-            int part = 0;
-            while (walk.next(a, wk)) {
+            int part = 0, run = 0;
+            for (; walk.next(a, wk); ++run) {
+                // done again: with the references that the sums gave, or moving ones
+                const bool kept = second && run < kKept && (unsure >> run & 1u) == 0u, safe = second && !kept;
                 const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
                 const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
                 if (tid == 0) {
@@ -586,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 if (tid < kRows) {
                     const int gr = row0 + tid, j = gr * wk.inv_g >> 16;
                     row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
-                    nm_s[tid] = 0.f;
+                    nm_s[tid] = kept ? kept_s[run * kRows + tid] : 0.f;
                 }
                 const bool tree = walk.block && a.parent != nullptr;
                 if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
@@ -596,6 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                         uint64_t m0 = 0, m1 = 0;
                         int i = tid;
                         bool bad = false;
+#pragma unroll 1
                         for (int n = 0; n <= a.R && i >= 0; ++n) {
                             if (i < 64) m0 |= 1ull << i;
                             else m1 |= 1ull << (i - 64);
@@ -616,30 +716,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     }
                     soft_sync();
                 }
-                // (the rows' units; everything else that the split warps write comes by way of S^T)
+                // (the rows' units; all else that the convert warps write comes by way of S^T)
                 const float* unit_s = reinterpret_cast<const float*>(smem + kOffUnit) + (seg & 1) * kRows;
                 wait(&q_ready[seg & 1], (seg >> 1) & 1);
-                float sums[kRT];
+                float2 sums[kRT / 2];
 #pragma unroll
-                for (int i = 0; i < kRT; ++i) sums[i] = 0.f;
+                for (int i = 0; i < kRT / 2; ++i) sums[i] = make_float2(0.f, 0.f);
                 bool found = false;   // (safe) row tid has a reference
-                const int nctx = walk.ctx_steps(), n = nctx + (walk.block ? 1 : 0);
+                const int lead = walk.block ? 1 : 0, n = walk.ctx_steps() + lead;
                 auto step = [&](int st, auto general_c) {
                     constexpr bool kGeneral = decltype(general_c)::value;
-                    const int x = it & 1;
-                    wait(&s_full[x], (it >> 1) & 1);
+                    const bool blk = kGeneral && st < lead;
+                    const uint32_t ts = tS(sb.x) + lane_off + hh * kRT;
+                    wait(&s_full[sb.x], sb.parity);
                     tc_fence_after();
                     // the key's scale: of its run, or of the block's row
                     const float* scl = scales(it);
-                    const float ks = sc * (kGeneral && st >= nctx ? scl[l] : scl[l >> 4]);
+                    const float ks = sc * scl[blk ? l : l >> 4];
                     // the rows that see this thread's key (bit e: row hh * kRT + e), in the
                     // steps where some do not: of the context, keys before the length (the
                     // second page of a step may be missing); block row l is seen from query
                     // rows l G on, or by the tree rows on whose path it lies
                     uint32_t seen = ~0u;
                     if constexpr (kGeneral) {
-                        if (st < nctx) {
-                            if ((walk.p0 + 2 * st) * kQ8Page + l >= min(walk.cur_t, walk.p1 * kQ8Page)) seen = 0u;
+                        if (!blk) {
+                            if ((walk.p0 + 2 * (st - lead)) * kQ8Page + l >= min(walk.cur_t, walk.p1 * kQ8Page)) seen = 0u;
                         } else if (!tree) {
                             const int lo = l < a.R ? l * a.G - row0 - hh * kRT : kRT;
                             seen = lo >= kRT ? 0u : lo > 0 ? ~0u << lo : ~0u;
@@ -648,158 +749,168 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                             seen = 0u;
                             const int r0 = row0 + hh * kRT, r1 = min(r0 + kRT, rows);
                             int j = r0 * wk.inv_g >> 16;
+#pragma unroll 1
                             for (int r = j * a.G - r0; l < a.R && r + r0 < r1; ++j, r += a.G) {
                                 if ((anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) == 0ull) continue;
                                 const uint32_t run = (1u << a.G) - 1u;   // (G <= 16)
                                 seen |= r >= 0 ? run << r : run >> -r;
                             }
                         }
+                        // the references (until now none, -m + kUp = 0): the maxima over the first 32
+                        // keys where those are finite, or, with `safe`, over all so far
+                        if (safe || (st == 0 && !second)) {
+                            if (safe || q4 == 0) {
+                                float most = 0.f;   // lane e's: row e's
+#pragma unroll 1
+                                for (int c0 = 0; c0 < kRT; c0 += 8) {
+                                    uint32_t s[8];
+                                    tmem_ld8_sync(ts + c0, s);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const float z = __fmul_rn(__uint_as_float(s[i]), __fmul_rn(unit_s[hh * kRT + c0 + i], ks));
+                                        const float m = warp_max(seen >> (c0 + i) & 1u ? z : -INFINITY);
+                                        if (lane == c0 + i) most = m;
+                                    }
+                                }
+                                if (lane < kRT) {
+                                    if (safe) red_s[q4 * kRows + hh * kRT + lane] = most;
+                                    else if (fabsf(most) < INFINITY) nm_s[hh * kRT + lane] = kUp - most;
+                                }
+                            }
+                            soft_sync();
+                            if (safe) {
+                                if (tid < kLive) {
+                                    // up, or where no score was finite so far (P, the sum and O are
+                                    // 0 then) to wherever the maximum is
+                                    const float m = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
+                                                          fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
+                                    const float was = kUp - nm_s[tid];
+                                    float move = 1.0f;
+                                    if (m > -INFINITY && (!found || m > was)) {
+                                        if (found) move = fast_exp2(was - m);
+                                        nm_s[tid] = kUp - m;
+                                        found = true;
+                                    }
+                                    move_s[tid] = move;
+                                }
+                                soft_sync();
+                                if (st > 0) {
+#pragma unroll
+                                    for (int i = 0; i < kRT / 2; ++i)
+                                        sums[i] = __fmul2_rn(sums[i], reinterpret_cast<const float2*>(move_s + hh * kRT)[i]);
+                                    // O^T (lane = dim) once the step before is in it
+                                    wait(&pv_done[(it - 1) % kPBufs], ((it - 1) / kPBufs) & 1);
+                                    tc_fence_after();
+#pragma unroll 1
+                                    for (int c0 = 0; c0 < kRT; c0 += 8) {
+                                        uint32_t o[8];
+                                        tmem_ld8_sync(tO + lane_off + hh * kRT + c0, o);
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e)
+                                            o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
+                                        tmem_st8(tO + lane_off + hh * kRT + c0, o);
+                                    }
+                                    tmem_st_wait();
+                                }
+                            }
+                        }
                     }
-                    // exponents of rows c0 .. of the thread's against their references
-                    auto exponents = [&](int c0, float(&e)[16]) {
-                        uint32_t s[16];
-                        tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 nm = reinterpret_cast<const float4*>(nm_s + hh * kRT + c0)[i];
-                            const float4 un = reinterpret_cast<const float4*>(unit_s + hh * kRT + c0)[i];
-                            // (the scales first: codes times one of them can pass fp32's largest; and in the
-                            // steps that may be `safe` the score is rounded before its reference is taken
-                            // off, so that the largest gives 0 however large it is)
-                            auto at = [&](uint32_t x, float u, float m) {
-                                if constexpr (kGeneral) return __fadd_rn(__fmul_rn(__uint_as_float(x), u * ks), m);
-                                else return fmaf(__uint_as_float(x), u * ks, m);
-                            };
-                            e[4 * i] = at(s[4 * i], un.x, nm.x);
-                            e[4 * i + 1] = at(s[4 * i + 1], un.y, nm.y);
-                            e[4 * i + 2] = at(s[4 * i + 2], un.z, nm.z);
-                            e[4 * i + 3] = at(s[4 * i + 3], un.w, nm.w);
-                        }
-                        if constexpr (kGeneral) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (!(seen >> (c0 + i) & 1u)) e[i] = -INFINITY;
-                        }
-                    };
-                    // the references (until now 0): the first key's scores where they are finite,
-                    // or, with `safe`, the running maxima.  (A row that does not see that key, or
-                    // whose score with it is not finite, may find its sum below kLeastSum.)
+                    // a key's line of P takes eight rows in 16 bytes
+                    uint8_t* prow = smem + kOffP + sb.x * kPBytes + l * 128;
                     if constexpr (kGeneral) {
-                        if (st == 0 && !safe) {
-                            if (q4 == 0) {
+                        // eight rows at a time; the sums go round, so that the loop's code serves them all
 #pragma unroll 1
-                                for (int c0 = 0; c0 < kRT; c0 += 16) {
-                                    uint32_t s[16];
-                                    tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
+                        for (int c0 = 0; c0 < kRT; c0 += 8) {
+                            uint32_t s[8], w[4], rest[4];
+                            tmem_ld8_sync(ts + c0, s);
+                            float2 now[4];
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) {
-                                        const float e = __uint_as_float(s[i]) * (unit_s[hh * kRT + c0 + i] * -ks);
-                                        s[i] = fabsf(e) < INFINITY ? __float_as_uint(e) : 0u;
-                                    }
-                                    if (lane == 0) {
-#pragma unroll
-                                        for (int i = 0; i < 16; i += 4)
-                                            *reinterpret_cast<uint4*>(nm_s + hh * kRT + c0 + i) =
-                                                make_uint4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-                                    }
-                                    __syncwarp();
+                            for (int i = 0; i < 8; i += 2) {
+                                // (the scales first: codes times one of them can pass fp32's largest; and the
+                                // score is rounded before its reference is taken off, so that with `safe` the
+                                // largest gives kUp however large it is: one by one, as the packed product and
+                                // sum would be fused)
+                                const float* un = unit_s + hh * kRT + c0 + i;
+                                const float* nm = nm_s + hh * kRT + c0 + i;
+                                float ex = __fadd_rn(__fmul_rn(__uint_as_float(s[i]), __fmul_rn(un[0], ks)), nm[0]);
+                                float ey = __fadd_rn(__fmul_rn(__uint_as_float(s[i + 1]), __fmul_rn(un[1], ks)), nm[1]);
+                                if (!(seen >> (c0 + i) & 1u)) ex = -INFINITY;
+                                if (!(seen >> (c0 + i + 1) & 1u)) ey = -INFINITY;
+                                const float2 p = make_float2(fast_exp2(ex), fast_exp2(ey));
+                                now[i / 2] = __fadd2_rn(sums[i / 2], p);
+                                if (blk) {   // bf16 (range) in two parts (16 bits)
+                                    w[i / 2] = pack_bf16x2(p.x, p.y);
+                                    rest[i / 2] = pack_bf16x2(p.x - __uint_as_float(w[i / 2] << 16),
+                                                              p.y - __uint_as_float(w[i / 2] & 0xffff0000u));
+                                } else {
+                                    w[i / 2] = pack_f16x2(p.x, p.y);
                                 }
                             }
-                            soft_sync();
+#pragma unroll
+                            for (int i = 0; i < kRT / 2 - 4; ++i) sums[i] = sums[i + 4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) sums[kRT / 2 - 4 + i] = now[i];
+                            const int to = ((hh * (kRT / 8) + c0 / 8) ^ (l & 7)) << 4;
+                            *reinterpret_cast<uint4*>(prow + to) = make_uint4(w[0], w[1], w[2], w[3]);
+                            // (the second part in the place of the block's K, which has been read)
+                            if (blk) *reinterpret_cast<uint4*>(stage(it) + l * 128 + to) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
                         }
-                        if (safe) {
-#pragma unroll 1
-                            for (int c0 = 0; c0 < kRT; c0 += 16) {
-                                uint32_t s[16];
-                                tmem_ld16_sync(tS(x) + lane_off + hh * kRT + c0, s);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_empty[sb.x]);
+                    } else {
+                        const float2 k2 = make_float2(ks, ks);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float z = __fmul_rn(__uint_as_float(s[i]), unit_s[hh * kRT + c0 + i] * ks);
-                                    const float m = warp_max(seen >> (c0 + i) & 1u ? z : -INFINITY);
-                                    if (lane == 0) red_s[q4 * kRows + hh * kRT + c0 + i] = m;
+                        for (int c0 = 0; c0 < kRT; c0 += 16) {
+                            uint32_t s[16];
+                            tmem_ld16_sync(ts + c0, s);
+                            if (c0 + 16 == kRT) {   // the scores are read
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&s_empty[sb.x]);
+                            }
+                            const float2* nm = reinterpret_cast<const float2*>(nm_s + hh * kRT + c0);
+                            const float2* un = reinterpret_cast<const float2*>(unit_s + hh * kRT + c0);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 4 * q; i < 4 * q + 4; ++i) {
+                                    // exponents of two rows against their references
+                                    const float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                                                __fmul2_rn(un[i], k2), nm[i]);
+                                    const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                                    sums[c0 / 2 + i] = __fadd2_rn(sums[c0 / 2 + i], p);
+                                    w[i & 3] = pack_f16x2(p.x, p.y);
                                 }
+                                *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + c0 / 8 + q) ^ (l & 7)) << 4)) =
+                                    make_uint4(w[0], w[1], w[2], w[3]);
                             }
-                            soft_sync();
-                            if (tid < kLive) {
-                                // up, or where no score was finite so far (P, the sum and O are
-                                // 0 then) to wherever the maximum is
-                                const float m = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
-                                                      fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
-                                const float was = -nm_s[tid];
-                                float move = 1.0f;
-                                if (m > -INFINITY && (!found || m > was)) {
-                                    if (found) move = fast_exp2(was - m);
-                                    nm_s[tid] = -m;
-                                    found = true;
-                                }
-                                move_s[tid] = move;
-                            }
-                            soft_sync();
-                            if (st > 0) {
-#pragma unroll
-                                for (int i = 0; i < kRT; ++i) sums[i] *= move_s[hh * kRT + i];
-                                // O^T (lane = dim) once the step before is in it
-                                wait(&pv_done[x ^ 1], ((it - 1) >> 1) & 1);
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c0 = 0; c0 < kRT; c0 += 16) {
-                                    const uint32_t ta = tO + lane_off + hh * kRT + c0;
-                                    uint32_t o[16];
-                                    tmem_ld16_sync(ta, o);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
-                                    tmem_st16(ta, o);
-                                }
-                                tmem_st_wait();
-                            }
-                        }
-                    }
-                    // a key's line of P takes eight rows in 16 bytes.  (The buffer is free: S of
-                    // this step was issued behind P V of three steps before.)
-                    uint8_t* prow = smem + kOffP + it % kPBufs * kPBytes + l * 128;
-#pragma unroll
-                    for (int c0 = 0; c0 < kRT; c0 += 16) {
-                        float e[16];
-                        exponents(c0, e);
-                        if (c0 + 16 == kRT) {   // the scores are read
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&s_empty[x]);
-                        }
-#pragma unroll
-                        for (int ch = 0; ch < 2; ++ch) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float p = fast_exp2(e[8 * ch + 2 * i]), q = fast_exp2(e[8 * ch + 2 * i + 1]);
-                                sums[c0 + 8 * ch + 2 * i] += p;
-                                sums[c0 + 8 * ch + 2 * i + 1] += q;
-                                w[i] = pack_bf16x2(p, q);
-                            }
-                            *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + c0 / 8 + ch) ^ (l & 7)) << 4)) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[it % kPBufs]);
+                    if (lane == 0) mbar_arrive(&p_full[sb.x]);
+                    sb.next(kSBufs);
                     ++it;
                 };
                 // the plain steps -- whole context steps but the run's first -- apart, so
                 // that they carry neither masks nor references
-                const bool ragged = nctx > 0 && ((walk.p1 - walk.p0) & 1 || walk.p1 * kQ8Page > walk.cur_t);
-                const int nwhole = safe ? 0 : nctx - (ragged ? 1 : 0);
+                const bool ragged = (walk.p1 - walk.p0) & 1 || walk.p1 * kQ8Page > walk.cur_t;
+                const int nwhole = safe ? 0 : n - (ragged ? 1 : 0), first = kept ? lead : 1;
 #pragma unroll 1
                 for (int st = 0; st < n; ++st) {
-                    if (st > 0 && st < nwhole) step(st, std::false_type{});
+                    if (st >= first && st < nwhole) step(st, std::false_type{});
                     else step(st, std::true_type{});
                 }
                 // the rows' sums over the keys: lane e of a warp ends with its row e's
                 // (halving the rows and the lanes that differ, step by step)
-                fold_sums(sums);
-                if (kRT == 16) sums[0] += __shfl_xor_sync(0xffffffffu, sums[0], 16);
-                if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sums[0];
+                float sum[kRT];
+#pragma unroll
+                for (int i = 0; i < kRT / 2; ++i) sum[2 * i] = sums[i].x, sum[2 * i + 1] = sums[i].y;
+                fold_sums(sum);
+                if (kRT == 16) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 16);
+                if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sum[0];
                 // (a cluster's partials stay on chip: the copies into the ring have all been read)
                 float* rec = kCluster ? reinterpret_cast<float*>(smem + kOffRing)
                              : walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
@@ -808,56 +919,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 float lsum = 0.f;
                 if (tid < kLive) {
                     lsum = (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
-                    bad = !(lsum < kMostSum) || (lsum < kLeastSum && tid < nrows);
-                    move_s[tid] = lsum != 0.f ? 1.0f / lsum : 0.f;
+                    const float least = kLost * static_cast<float>(kStepKeys * n);
+                    bad = !(lsum < INFINITY) || (lsum < least && tid < nrows);
+                    const bool sure = (lsum >= kLeastSum && lsum < INFINITY) || tid >= nrows;
+                    if (!sure) fail_s[6] = 1;
+                    if (!second && run < kKept)
+                        kept_s[run * kRows + tid] = sure ? nm_s[tid] + kUpSum - __log2f(fmaxf(lsum, kLeastSum)) : 0.f;
+                    move_s[tid] = lsum != 0.f ? __fdividef(1.0f, lsum) : 0.f;
                 }
                 wait(o_done, seg & 1);
+                const float v_unit = q8_pow2(vexp_s[seg % 3]);
                 // (a cluster's partial overwrites the ring: only now have all pages been read)
                 if (rec && tid < kLive)
-                    *reinterpret_cast<float2*>(rec + kRows * kQ8D + 2 * tid) = make_float2(-nm_s[tid], lsum);
+                    *reinterpret_cast<float2*>(rec + kRows * kQ8D + 2 * tid) = make_float2(-nm_s[tid], lsum);   // (kUp below the reference)
                 tc_fence_after();
                 soft_sync();
-                const uint64_t inf0 = inf_s[(seg % 3 * kQ8D + l) * 2], inf1 = inf_s[(seg % 3 * kQ8D + l) * 2 + 1];
-#pragma unroll
-                for (int c0 = 0; c0 < kRT; c0 += 16) {
-                    uint32_t o[16];
-                    tmem_ld16_sync(tO + lane_off + hh * kRT + c0, o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) bad |= !(fabsf(__uint_as_float(o[e])) < INFINITY);
-                    if (walk.block && (inf0 | inf1) != 0ull) {   // (rare) V that is not finite and that the row sees
+                if (fail_s[6] != 0) unsure |= run < kKept ? 1u << run : 0u;
+                uint64_t inf0 = 0ull, inf1 = 0ull;
+                if (walk.block) inf0 = inf_s[(seg % 3 * kQ8D + l) * 2], inf1 = inf_s[(seg % 3 * kQ8D + l) * 2 + 1];
 #pragma unroll 1
-                        for (int e = 0; e < 16; ++e) {
+                for (int c0 = 0; c0 < kRT; c0 += 8) {
+                    uint32_t o[8];
+                    tmem_ld8_sync(tO + lane_off + hh * kRT + c0, o);
+                    float mean[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // the row's mean over the run, which cannot pass V's largest
+                        const float x = __uint_as_float(o[e]);
+                        bad |= !(fabsf(x) < INFINITY);
+                        mean[e] = x * move_s[hh * kRT + c0 + e] * v_unit;
+                    }
+                    if ((inf0 | inf1) != 0ull) {   // (rare) V that is not finite and that the row sees
+#pragma unroll 1
+                        for (int e = 0; e < 8; ++e) {
                             const int j = (row0 + hh * kRT + c0 + e) * wk.inv_g >> 16;   // (any row past the tile's last)
                             if (j >= a.R) continue;
                             uint64_t m0 = inf0, m1 = inf1;
                             if (tree) m0 &= anc_s[2 * j], m1 &= anc_s[2 * j + 1];
                             else m0 &= ~0ull >> (63 - min(j, 63)), m1 &= j < 64 ? 0ull : ~0ull >> (127 - j);
                             float add = 0.f;
+#pragma unroll 1
                             for (; m0 | m1; (m0 ? m0 : m1) &= (m0 ? m0 : m1) - 1ull) {
                                 const int key = m0 ? __ffsll(m0) - 1 : 63 + __ffsll(m1);
                                 add += __uint_as_float(static_cast<uint32_t>(__ldg(
                                     a.v_blk + ((static_cast<size_t>(b) * a.Hkv + g) * a.R + key) * kQ8D + l)) << 16);
                             }
-                            if (add != 0.f) {   // (NaN too)
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (i == e) o[i] = __float_as_uint(__uint_as_float(o[i]) + add);
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                if (i == e) mean[i] += add;
                         }
                     }
-                    if (rec) {   // (rows past the tile's last are written too, and never read)
-                        float* dst = rec + (hh * kRT + c0) * kQ8D + l;
+                    // (rows past the tile's last are written to a partial too, and never read)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            if constexpr (kCluster) dst[e * kQ8D] = __uint_as_float(o[e]);
-                            else __stcg(dst + e * kQ8D, __uint_as_float(o[e]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int row = row_s[hh * kRT + c0 + e];
-                            const uint16_t v = f32_bf16_bits(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
-                            if (row >= 0) a.out[static_cast<size_t>(row) * kQ8D + l] = v;
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = hh * kRT + c0 + e;
+                        if constexpr (kCluster) {
+                            rec[r * kQ8D + l] = mean[e];
+                        } else if (rec) {
+                            __stcg(rec + r * kQ8D + l, mean[e]);
+                        } else {
+                            const int row = row_s[r];
+                            if (row >= 0) a.out[static_cast<size_t>(row) * kQ8D + l] = f32_bf16_bits(mean[e]);
                         }
                     }
                 }
@@ -866,6 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 part = 1;   // a partial run that is not the CTA's first is its last
                 tc_fence_before();
                 soft_sync();   // red_s and nm_s read by everyone before the next run writes them
+                if (tid == 0) fail_s[6] = 0;
                 if (lane == 0) {
                     mbar_arrive(o_free);
                     mbar_arrive(&q_free[seg & 1]);
@@ -884,6 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         cg::cluster_group cluster = cg::this_cluster();
         const int u = blockIdx.x / wk.cluster, b = u / wk.U, ub = u - b * wk.U, g = ub / wk.row_tiles;
         const int row0 = (ub - g * wk.row_tiles) * wk.tile_rows, nrows = min(wk.tile_rows, a.R * a.G - row0);
+#pragma unroll 1
         for (int r = rank + wk.cluster * warp; r < nrows; r += wk.cluster * (kThreads / 32)) {
             const int gr = row0 + r, j = gr * wk.inv_g >> 16;
             auto get = [&](int i, float2& ml, float4& o) {
@@ -891,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 ml = *reinterpret_cast<const float2*>(rec + kRows * kQ8D + 2 * r);
                 o = *(reinterpret_cast<const float4*>(rec + r * kQ8D) + lane);
             };
-            join_row(wk.cluster, get, a.out + (static_cast<size_t>(b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ8D);
+            join_partials<true>(wk.cluster, get, a.out + (static_cast<size_t>(b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ8D);
         }
         __syncwarp();
         cluster_sync_warp();   // this CTA's partial has been read
@@ -899,9 +1023,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     if constexpr (!kCluster) pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kPvWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+        if (*late != 0) raise_error(a.err, SV_DEVERR_TIMEOUT);
     }
 }
 
@@ -928,7 +1053,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         ml = __ldcg(reinterpret_cast<const float2*>(rec + kRows * kQ8D + 2 * r));
         o = __ldcg(reinterpret_cast<const float4*>(rec + r * kQ8D) + lane);
     };
-    join_row(i1 - i0 + 1, get,
+    join_partials<true>(i1 - i0 + 1, get,
              a.out + ((static_cast<size_t>(b) * a.R + gr / a.G) * a.Hq + g * a.G + gr % a.G) * kQ8D);
 }
 

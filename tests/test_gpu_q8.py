@@ -240,16 +240,29 @@ def test_gather_bad_inputs_and_nan(sv):
 # attention
 # ---------------------------------------------------------------------------
 
-def tol(want, wgt, big, units, keys):
-    """As for the 4-bit cache -- P and the output are each rounded to bf16, a half step of
-    2^-8 of what they are; sums of 128 products (in two or four parts) move a score by at
-    most 260 * 2^-22 of their magnitudes (p by that factor, twice: numerator and
-    denominator), the exponentials by 2^-20; sums over the keys and their rescalings by
-    2^-22 a term -- and the elements of Q and of the block's K are off by 2^-17 of their
-    row's largest (2^-10 of units of which the largest is at least 224), which moves a
-    score by 2^-17 `units`."""
-    p = 2.0 ** -8 + 2 * (260 * 2.0 ** -22 * big + 2.0 ** -17 * units + 2.0 ** -20) + 2 * keys * 2.0 ** -22
-    return 2.0 ** -8 * np.abs(want) + 1.01 * p * wgt + 1e-30
+def tol(want, wgt, big, units, keys, lost):
+    """The output is rounded to bf16, a half step of 2^-8 of what it is, and P to f16, 2^-11;
+    sums of 128 products (in two or four parts) move a score by at most 260 * 2^-22 of
+    their magnitudes (p by that factor, twice: numerator and denominator), the
+    exponentials by 2^-20; sums over the keys and their rescalings by 2^-22 a term; the
+    elements of Q and of the block's K are off by 2^-17 of their row's largest (2^-10 of
+    units of which the largest is at least 224), which moves a score by 2^-17 `units`.
+    `lost` (below): what f16 holds of the smallest P and V."""
+    p = 2.0 ** -11 + 2 * (260 * 2.0 ** -22 * big + 2.0 ** -17 * units + 2.0 ** -20) + 2 * keys * 2.0 ** -22
+    return 2.0 ** -8 * np.abs(want) + 1.01 * (p * wgt + lost) + 1e-30
+
+
+def lost_of(scale, v_ctx, vb, G):
+    """[Hq, 128]: f16's steps end at 2^-24.  A P is 2^3 at a key that the row sees, so that the
+    sum of P is 2^3 or more: rounding it there moves a weight by at most 2^-25 / 2^3, and
+    the result by the sum of those and |v|.  V there is in units of the largest scale of
+    the pages and the block: a value moves by at most 2^-25 of that."""
+    h = []
+    for k in range(vb.shape[0]):
+        v = np.concatenate([v_ctx[k], np.where(np.isfinite(vb[k]), vb[k], 0.0)])
+        unit = max(scale, 2.0 ** ref8.exponent(np.abs(v).max()))
+        h += [2.0 ** -21 * np.abs(v).sum(0) + 2.0 ** -25 * unit] * G
+    return np.stack(h)
 
 
 def units_of(q, k_ctx, kb, scale):
@@ -288,10 +301,10 @@ def run(sv, B, R, Hq, H, lens, parent=None, scale=None, seed=0, mp=None, lo=-8, 
     for b in range(B):
         n = (lens[b] + 63) // 64
         rows = lambda pool, is_v: ref8.get_rows(pool[table[b, :n]], is_v).transpose(1, 0, 2, 3).reshape(H, n * 64, 128)[:, :lens[b]]  # noqa: E731
-        k = rows(kp, False)
-        want, wgt, big = ref.attention(q[b], k, rows(vp, True), kb[b], vb[b], None if parent is None else parent[b:b + 1], s)
+        k, v = rows(kp, False), rows(vp, True)
+        want, wgt, big = ref.attention(q[b], k, v, kb[b], vb[b], None if parent is None else parent[b:b + 1], s)
         err = np.abs(got[b] - want)
-        bound = tol(want, wgt, big, units_of(q[b], k, kb[b], s), lens[b] + R)
+        bound = tol(want, wgt, big, units_of(q[b], k, kb[b], s), lens[b] + R, lost_of(2.0 ** (hi - 1), v, vb[b], Hq // H))
         assert np.all(err <= bound), (b, float((err / bound).max()), np.argwhere(~(err <= bound))[:4].tolist())
     assert sv.get_device_error() == 0
     return out
@@ -363,10 +376,10 @@ def one_sequence(sv, q, kp, vp, table, t, kb, vb, scale, parent=None, lost=0):
                             None if parent is None else i32(parent), scale=scale)
     n = (t + 63) // 64
     rows = lambda pool, is_v: ref8.get_rows(pool[table[0, :n]], is_v).transpose(1, 0, 2, 3).reshape(H, n * 64, 128)[:, lost:t]  # noqa: E731
-    k = rows(kp, False)
+    k, v = rows(kp, False), rows(vp, True)
     seen = parent if parent is None else np.where(np.asarray(parent) >= R, -1, parent)
-    want, wgt, big = ref.attention(q[0], k, rows(vp, True), kb[0], vb[0], seen, scale)
-    bound = tol(want, wgt, big, units_of(q[0], k, kb[0], scale), t + R)
+    want, wgt, big = ref.attention(q[0], k, v, kb[0], vb[0], seen, scale)
+    bound = tol(want, wgt, big, units_of(q[0], k, kb[0], scale), t + R, lost_of(2.0 ** -5, v, vb[0], q.shape[2] // H))
     err = np.abs(out[0].double().cpu().numpy() - want)
     assert np.all(err <= bound), (float((err / bound).max()), np.argwhere(~(err <= bound))[:4].tolist())
 
@@ -503,7 +516,8 @@ def test_attn_query_rows_of_all_sizes(sv):
                 one = q[0].copy()
                 one[:] = one[j, h]
                 want, wgt, big = ref.attention(one, k, v, kb[0], vb[0], None, 128 ** -0.5)
-                bound = tol(want, wgt, big, units_of(one, k, kb[0], 128 ** -0.5), t + R)[j, h]
+                bound = tol(want, wgt, big, units_of(one, k, kb[0], 128 ** -0.5), t + R,
+                            lost_of(2.0 ** -5, v, vb[0], Hq))[j, h]
                 assert np.all(np.abs(out[j, h] - want[j, h]) <= bound), (j, h)
     assert sv.get_device_error() == 0
 
@@ -521,7 +535,8 @@ def test_attn_bad_inputs_are_reported(sv):
 
     def check(got, k, v):
         want, wgt, big = ref.attention(q[0], k, v, kb[0], vb[0], None, 128 ** -0.5)
-        assert np.all(np.abs(got[0] - want) <= tol(want, wgt, big, units_of(q[0], k, kb[0], 128 ** -0.5), k.shape[1] + 2))
+        lost = lost_of(2.0 ** -5, v, vb[0], 2)
+        assert np.all(np.abs(got[0] - want) <= tol(want, wgt, big, units_of(q[0], k, kb[0], 128 ** -0.5), k.shape[1] + 2, lost))
     rows = lambda pool, pg, is_v: ref8.get_rows(pool[pg, 0], is_v).reshape(1, -1, 128)  # noqa: E731
     # a page outside the pool reads as zeros, on either side of a step
     for table, n, cut in (([[0, 7]], 100, None), ([[-1, 2]], 128, None)):
@@ -562,8 +577,8 @@ def _device_inputs(B, R, Hq, H, t, seed):
     (16, 3, 28, 4, 2286), (2, 1, 28, 4, 9927)])
 def test_attn_many_steps(sv, B, R, Hq, H, t):
     """Runs long enough that every ring stage is used again: each group of 32 dims
-    within twice what rounding P and the output leave at random (halves of 2^-8 of
-    their magnitudes, uniform: / sqrt(3)), its root mean square over the rows."""
+    within twice what rounding P to bf16 and the output would leave at random (halves of
+    2^-8 of their magnitudes, uniform: / sqrt(3)), its root mean square over the rows."""
     q, (kp, vp), table, kb, vb = _device_inputs(B, R, Hq, H, t, seed=t)
     lens = i32([t - 29 * b for b in range(B)])
     k, v = sv.kv_gather_q8(kp[None], vp[None], table, i32([0] * B), lens, t)
@@ -629,6 +644,8 @@ def test_attn_full_size_against_torch64(sv, B, R, Hq, H, t, tree):
             err = np.abs(out[b, :, h * G:(h + 1) * G].double().cpu().numpy() - want)
             # sums over a long context go through many partial sums: their error
             # grows with the square root of the terms, not with their number
-            bound = tol(want, wgt, big, units, int(16 * (lens[b] + R) ** 0.5))
+            # (as does that of P's last steps)
+            lost = 2.0 ** -21 * 16 * vv.pow(2).sum(0).sqrt().cpu().numpy() + 2.0 ** -25 * 2.0 ** -5
+            bound = tol(want, wgt, big, units, int(16 * (lens[b] + R) ** 0.5), lost)
             assert np.all(err <= bound), (b, h, float((err / bound).max()))
     assert sv.get_device_error() == 0
