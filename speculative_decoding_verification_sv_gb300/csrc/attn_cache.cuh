@@ -113,18 +113,28 @@ struct Walk {
         np = ctx_pages(t);
         unit = (pos - base) / (np + 1);
         off = (pos - base) % (np + 1);
+        raw = a.len[b];
+        bad_len = raw != t;
     }
     // Unit u's pages for CTA `rank` of the cluster that has the unit.
     __device__ __forceinline__ void start_unit(const CacheAttnArgs& a, const Work& w, int u, int rank) {
         b = u / w.U;
         unit = u - b * w.U;
         t = ctx_len(a, b);
+        raw = a.len[b];
+        bad_len = raw != t;
         np = ctx_pages(t);
         pos = off = cta_first(np + 1, rank, w.cluster);
         end = cta_first(np + 1, rank + 1, w.cluster);
     }
     __device__ __forceinline__ bool next(const CacheAttnArgs& a, const Work& w) {
         if (pos >= end) return false;
+        if (fresh) {   // (the length was sent for when the run before began)
+            t = max(0, min(raw, a.max_pages * kPage));
+            bad_len = raw != t;
+            np = ctx_pages(t);
+            fresh = false;
+        }
         const int n = min(end - pos, np + 1 - off);
         p0 = off;
         p1 = min(off + n, np);
@@ -138,20 +148,23 @@ struct Walk {
         if (block && ++unit == w.U) {
             unit = 0;
             if (++b < a.B) {
-                t = ctx_len(a, b);
-                np = ctx_pages(t);
+                raw = a.len[b];
+                fresh = true;
             }
         }
         return true;
     }
+    int raw;                           // length of sequence b as given
+    bool fresh = false;                // which t and np do not follow yet
+    bool bad_len = false;              // of the current run: the length was clamped
     int cur_b, cur_unit, cur_t;
     __device__ __forceinline__ void save(volatile int* to) const {
         to[0] = pos, to[1] = end, to[2] = b, to[3] = unit, to[4] = off;
     }
     __device__ __forceinline__ void load(const CacheAttnArgs& a, const volatile int* from) {
         pos = from[0], end = from[1], b = from[2], unit = from[3], off = from[4];
-        t = ctx_len(a, b);
-        np = ctx_pages(t);
+        fresh = true;
+        raw = a.len[b];
     }
     __device__ __forceinline__ int ctx_steps() const { return (p1 - p0 + 1) / 2; }
 };

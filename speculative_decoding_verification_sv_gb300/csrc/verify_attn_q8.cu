@@ -43,10 +43,10 @@
 // joins them; a cluster's partials stay in shared memory and are joined over it.  A run
 // takes its block first: those rows are there before the first page.
 //
-// Warps: 8 softmax (TMEM quadrant w % 4, half of the tile's rows each), 8 that convert
-// (Q and the block's K to e4m3 pairs, then V, a quadrant of the dims and half of a step's
-// keys each), one that issues the copies (two pages of K and V, 32 KB, a ring stage), and
-// one for the MMAs of either product.
+// Warps: 8 softmax (TMEM quadrant w % 4, half of the tile's rows each), 4 that convert
+// (Q and the block's K to e4m3 pairs, then V, a quadrant of the dims each), one that issues
+// the copies (two pages of K and V, 32 KB, a ring stage), and one for the MMAs of either
+// product.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -67,8 +67,8 @@ constexpr int kStages = 4;
 constexpr int kTileBytes = kStepKeys * kQ8D;     // codes of a step's K, or V
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kMaxR = 128;
-constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 8, kTmaWarp = 16, kQkWarp = 17, kPvWarp = 18,
-              kThreads = 32 * 19;
+constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kTmaWarp = 12, kQkWarp = 13, kPvWarp = 14,
+              kThreads = 32 * 15;
 constexpr int kVUp = 4;                   // V is in units of 2^kVUp of its first scales
 constexpr float kUp = -4.0f;              // P is 2^kUp at the reference;
 constexpr float kUpSum = 15.0f;           // where the sums gave the reference, they are 2^kUpSum
@@ -113,7 +113,7 @@ constexpr int kSmemBytes = kOffKept + kKept * kRows * 4;
 static_assert(kOffInf % 16 == 0, "16-byte masks");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 static_assert(kOffRing % 1024 == 0, "swizzled tiles");
-static_assert(kRecFloats * 4 <= kStages * kStageBytes, "a cluster's partial in the ring");
+static_assert(kRecFloats * 4 <= kPBufs * kPBytes, "a partial in P's place");
 // a slot is written again kSclSlots steps on, by when the scores of the step kStages +
 // kSBufs before that one have been read
 static_assert(kSclSlots >= kStages + kSBufs, "scale slots");
@@ -158,22 +158,13 @@ __device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t c) {
     return r;
 }
 
-// A bounded wait on an mbarrier phase (each try gives up after a microsecond or so); one
-// that gives up is noted for the kernel's end.  There are many, and code that is run once a
-// step, or once, has to be short to be there in time.
+// A bounded wait on an mbarrier phase; one that gives up is noted for the kernel's end.
+// There are many, and code that is run once a step, or once, has to be short to be there in
+// time.  (A limit on the time of a try would make the compiler sleep between tries.)
 __device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, volatile int* late) {
 #pragma unroll 1
-    for (int i = 0; i < (1 << 21); ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return;
-    }
+    for (int i = 0; i < (1 << 24); ++i)
+        if (mbar_try_wait(bar, parity)) return;
     *late = 1;
 }
 
@@ -215,6 +206,16 @@ __device__ __forceinline__ void split_row(uint4 x, bool bad, int e, int r, uint8
     *reinterpret_cast<uint2*>(at) = make_uint2(c1[0], c1[1]);
     *reinterpret_cast<uint2*>(at + second) = make_uint2(c2[0], c2[1]);
 }
+
+// A bulk copy shared -> global by one thread, the wait for all of that thread's to have read
+// their source, and for all of them.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (what their
 // columns of P and O hold is not looked at)
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 const int g = walk.cur_unit / wk.row_tiles;
                 const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
                 const int np = walk.p1 - walk.p0;
+                if (lane == 0 && walk.bad_len) raise_error(a.err, SV_DEVERR_LENGTH);
                 // lane l holds page p0 + 32 k + l, 32 table entries at once, and its scales (of all else
                 // 16 bytes would be a copy of their own, as long to issue as one of 8 KB)
                 int pg = 0, i = walk.block ? -2 : 0;
@@ -472,10 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     } else if (warp >= kConvWarp) {
         // ---------------- to e4m3 pairs and to f16 ----------------
         if (early) pdl_wait();
-        constexpr int kQRows = kLive / 16;   // query rows of a half-warp: hw, hw + 16, ..
+        constexpr int kQRows = kLive / 8;    // query rows of a half-warp: hw, hw + 8, ..
         const int cw = warp - kConvWarp, hw = 2 * cw + (lane >> 4), ch = lane & 15;
-        const int kh = cw >> 2;              // V: which half of a step's keys (a page),
-        const int l = q4 * 32 + lane;        // and the TMEM lane: the dim
+        const int l = q4 * 32 + lane;        // V: the TMEM lane, a dim
         int it = 0, seg = 0;
         Turn pb;                             // of step it - 2
         uint32_t gone = 0;                   // (bit s) parity of the next block in stage s
@@ -507,16 +508,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 const int nrows = min(wk.tile_rows, a.R * a.G - row0);
                 const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R * kQ8D;
                 // half-warps take the query rows, then the block's rows of K
-                const int jobs = kQRows + (walk.block ? (a.R + 15) >> 4 : 0);
+                const int jobs = kQRows + (walk.block ? (a.R + 7) >> 3 : 0);
                 auto k_row = [&](int job) {
-                    const int r = hw + 16 * (job - kQRows);
+                    const int r = hw + 8 * (job - kQRows);
                     return job < jobs && r < a.R ? __ldg(reinterpret_cast<const uint4*>(a.k_blk + blk0 + r * kQ8D) + ch)
                                                  : make_uint4(0u, 0u, 0u, 0u);
                 };
                 uint4 x[kQRows];
 #pragma unroll
                 for (int i = 0; i < kQRows; ++i) {
-                    const int r = hw + 16 * i, gr = row0 + r, j = gr * wk.inv_g >> 16;
+                    const int r = hw + 8 * i, gr = row0 + r, j = gr * wk.inv_g >> 16;
                     x[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (r < nrows)
                         x[i] = __ldg(reinterpret_cast<const uint4*>(
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     }
                     const bool bad = m >= 0x7f80u;
                     const int e = q8_exponent(__uint_as_float(bad ? 0u : m << 16));
-                    const int r = hw + 16 * (is_q ? job : job - kQRows);
+                    const int r = hw + 8 * (is_q ? job : job - kQRows);
                     split_row(y, bad, e, r, is_q ? smem + kOffQ + (seg & 1) * kQBytes : stage(it), is_q ? kQBytes / 2 : kTileBytes);
                     if (ch == 0) (is_q ? unit : scales(it))[r] = q8_pow2(e);
                 }
@@ -592,48 +593,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     // NaN): it stays out of the product, and the epilogue adds it where it is seen
                     v_free();
                     const uint16_t* vsrc = a.v_blk + blk0 + l;
-                    uint64_t inf = 0ull;
+                    uint64_t inf0 = 0ull, inf1 = 0ull;
 #pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {
-                        const int k0 = 64 * kh + 16 * h;
-                        uint32_t w[16], r[8];
+                    for (int k0 = 0; k0 < kStepKeys; k0 += 16) {
+                        uint32_t r[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                        if (k0 < a.R) {
+                            uint32_t w[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) w[k] = k0 + k < a.R ? __ldg(vsrc + (k0 + k) * kQ8D) : 0u;
+                            for (int k = 0; k < 16; ++k) w[k] = k0 + k < a.R ? __ldg(vsrc + (k0 + k) * kQ8D) : 0u;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if ((w[k] & 0x7f80u) == 0x7f80u) inf |= 1ull << (16 * h + k), w[k] = 0u;
+                            for (int k = 0; k < 16; ++k)
+                                if ((w[k] & 0x7f80u) == 0x7f80u) (k0 < 64 ? inf0 : inf1) |= 1ull << ((k0 & 63) + k), w[k] = 0u;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            r[k] = pack_bf16x2(__uint_as_float(w[2 * k] << 16) * to, __uint_as_float(w[2 * k + 1] << 16) * to);
-                        tmem_st8(tV(it & 1) + lane_off + 32 * kh + 8 * h, r);
+                            for (int k = 0; k < 8; ++k)
+                                r[k] = pack_bf16x2(__uint_as_float(w[2 * k] << 16) * to, __uint_as_float(w[2 * k + 1] << 16) * to);
+                        }
+                        tmem_st8(tV(it & 1) + lane_off + (k0 >> 1), r);
                     }
-                    inf_s[(seg % 3 * kQ8D + l) * 2 + kh] = inf;
+                    inf_s[(seg % 3 * kQ8D + l) * 2] = inf0;
+                    inf_s[(seg % 3 * kQ8D + l) * 2 + 1] = inf1;
                     // (the stage's place is kept for P's second part: one arrival comes from its product)
                     v_done(cw != 0);
                 }
 #pragma unroll 1
                 for (int st = 0; st < walk.ctx_steps(); ++st) {
-                    uint8_t* v = stage(it) + kTileBytes + kh * kQ8Codes;
+                    uint8_t* v = stage(it) + kTileBytes;
                     wait(&ring_full[it % kStages], stage_use(it));
-                    const float4 f4 = reinterpret_cast<const float4*>(scales(it))[2 + kh];
-                    float f[4] = {f4.x * to, f4.y * to, f4.z * to, f4.w * to};
-                    // keys of this page that exist: what the others' codes hold is not looked
-                    // at (0 * a V that is not finite would be NaN)
-                    const int have = min(walk.cur_t - (walk.p0 + 2 * st + kh) * kQ8Page, (walk.p1 - walk.p0 - 2 * st - kh) * kQ8Page);
-                    if (have < kQ8Page) {
+                    const float4 fa = reinterpret_cast<const float4*>(scales(it))[2], fb = reinterpret_cast<const float4*>(scales(it))[3];
+                    float f[8] = {fa.x * to, fa.y * to, fa.z * to, fa.w * to, fb.x * to, fb.y * to, fb.z * to, fb.w * to};
+                    // keys of the step that exist: what the others' codes hold is not looked at (0 * a
+                    // V that is not finite would be NaN)
+                    const int have = min(walk.cur_t - (walk.p0 + 2 * st) * kQ8Page, (walk.p1 - walk.p0 - 2 * st) * kQ8Page);
+                    if (have < kStepKeys) {
 #pragma unroll 1
-                        for (int o = max(have, 0) >> 3; o < 8; ++o) {   // (this thread's dim alone)
+                        for (int o = have >> 3; o < kStepKeys / 8; ++o) {   // (this thread's dim alone)
                             uint64_t* w = reinterpret_cast<uint64_t*>(v + q8_v_off(o, l));
                             const int left = have - 8 * o;
                             *w = left <= 0 ? 0ull : *w & ((1ull << 8 * left) - 1ull);
                         }
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
+                        for (int r = 0; r < 8; ++r)
                             if (have <= kQ8Run * r) f[r] = 0.f;
                     }
                     v_free();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {   // 32 keys: two runs
+                    for (int h = 0; h < 4; ++h) {   // 32 keys: two runs
                         uint32_t r[16];
 #pragma unroll
                         for (int o = 0; o < 4; ++o) {
@@ -644,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                             r[4 * o + 2] = mul_f16x2(f16x2_of_codes(w.y), m);
                             r[4 * o + 3] = mul_f16x2(f16x2_of_codes(w.y >> 16), m);
                         }
-                        tmem_st16(tV(it & 1) + lane_off + 32 * kh + 16 * h, r);
+                        tmem_st16(tV(it & 1) + lane_off + 16 * h, r);
                     }
                     v_done(true);
                 }
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         // A cluster's successor may start now.  (Not before the wait: the successor may
         // read a cache that only this kernel's predecessor must not be writing.)
         if constexpr (kCluster) pdl_launch_dependents();
-        const int hh = warp >> 2;              // rows hh * kRT .. of the tile
+        const int hh = warp >> 2;              // rows hh * kRT .. of the tile (of its halves)
         const int l = q4 * 32 + lane;          // key of the step; dim in the epilogue
         const int tid = threadIdx.x;
         const float sc = a.scale_log2;
@@ -678,10 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 const bool kept = second && run < kKept && (unsure >> run & 1u) == 0u, safe = second && !kept;
                 const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
                 const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
-                if (tid == 0) {
-                    const int t = a.len[b];
-                    if (t < 0 || t > a.max_pages * kQ8Page) raise_error(a.err, SV_DEVERR_LENGTH);
-                }
+                // (a partial of the run before may still be on its way out of P's place)
+                if (tid == 0) bulk_wait_read();
                 if (tid < kRows) {
                     const int gr = row0 + tid, j = gr * wk.inv_g >> 16;
                     row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
@@ -724,184 +726,187 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 for (int i = 0; i < kRT / 2; ++i) sums[i] = make_float2(0.f, 0.f);
                 bool found = false;   // (safe) row tid has a reference
                 const int lead = walk.block ? 1 : 0, n = walk.ctx_steps() + lead;
-                auto step = [&](int st, auto general_c) {
-                    constexpr bool kGeneral = decltype(general_c)::value;
-                    const bool blk = kGeneral && st < lead;
-                    const uint32_t ts = tS(sb.x) + lane_off + hh * kRT;
+                // the rows that see this thread's key (bit e: row hh * kRT + e): of the context, keys
+                // before the length (the second page of a step may be missing); block row l is seen
+                // from query rows l G on, or by the tree rows on whose path it lies
+                auto seen_by = [&](int st) {
+                    if (st >= lead)
+                        return (walk.p0 + 2 * (st - lead)) * kQ8Page + l < min(walk.cur_t, walk.p1 * kQ8Page) ? ~0u : 0u;
+                    if (!tree) {
+                        const int lo = l < a.R ? l * a.G - row0 - hh * kRT : kRT;
+                        return lo >= kRT ? 0u : lo > 0 ? ~0u << lo : ~0u;
+                    }
+                    // block row by block row: its G query rows see the same keys
+                    uint32_t seen = 0u;
+                    const int r0 = row0 + hh * kRT, r1 = min(r0 + kRT, rows);
+                    int j = r0 * wk.inv_g >> 16;
+#pragma unroll 1
+                    for (int r = j * a.G - r0; l < a.R && r + r0 < r1; ++j, r += a.G) {
+                        if ((anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) == 0ull) continue;
+                        const uint32_t run = (1u << a.G) - 1u;   // (G <= 16)
+                        seen |= r >= 0 ? run << r : run >> -r;
+                    }
+                    return seen;
+                };
+                // the key's scale: of its run, or of the block's row
+                auto key_scale = [&](int st) { return sc * scales(it)[st < lead ? l : l >> 4]; };
+                auto s_wait = [&]() {
                     wait(&s_full[sb.x], sb.parity);
                     tc_fence_after();
-                    // the key's scale: of its run, or of the block's row
-                    const float* scl = scales(it);
-                    const float ks = sc * scl[blk ? l : l >> 4];
-                    // the rows that see this thread's key (bit e: row hh * kRT + e), in the
-                    // steps where some do not: of the context, keys before the length (the
-                    // second page of a step may be missing); block row l is seen from query
-                    // rows l G on, or by the tree rows on whose path it lies
-                    uint32_t seen = ~0u;
-                    if constexpr (kGeneral) {
-                        if (!blk) {
-                            if ((walk.p0 + 2 * (st - lead)) * kQ8Page + l >= min(walk.cur_t, walk.p1 * kQ8Page)) seen = 0u;
-                        } else if (!tree) {
-                            const int lo = l < a.R ? l * a.G - row0 - hh * kRT : kRT;
-                            seen = lo >= kRT ? 0u : lo > 0 ? ~0u << lo : ~0u;
-                        } else {
-                            // block row by block row: its G query rows see the same keys
-                            seen = 0u;
-                            const int r0 = row0 + hh * kRT, r1 = min(r0 + kRT, rows);
-                            int j = r0 * wk.inv_g >> 16;
-#pragma unroll 1
-                            for (int r = j * a.G - r0; l < a.R && r + r0 < r1; ++j, r += a.G) {
-                                if ((anc_s[2 * j + (l >> 6)] >> (l & 63) & 1ull) == 0ull) continue;
-                                const uint32_t run = (1u << a.G) - 1u;   // (G <= 16)
-                                seen |= r >= 0 ? run << r : run >> -r;
-                            }
+                };
+                // The references (until now none, -m + kUp = 0): the maxima over the run's first 32 keys
+                // where those are finite, or, with `safe`, over all so far.  A score is rounded before
+                // anything is done with it, here and in the steps with masks, so that with `safe` the
+                // largest gives kUp however large it is (the scales first: codes times one of them can
+                // pass fp32's largest).
+                auto references = [&](int st, uint32_t seen) {
+                    const float ks = key_scale(st);
+                    if (safe || q4 == 0) {
+                        float most = 0.f;   // lane e's: row e's
+                        uint32_t s[kRT];
+                        if constexpr (kRT == 32) tmem_ld32_sync(tS(sb.x) + lane_off + hh * kRT, s);
+                        else tmem_ld16_sync(tS(sb.x) + lane_off + hh * kRT, s);
+#pragma unroll
+                        for (int i = 0; i < kRT; ++i) {
+                            const float z = __fmul_rn(__uint_as_float(s[i]), __fmul_rn(unit_s[hh * kRT + i], ks));
+                            const float m = warp_max(seen >> i & 1u ? z : -INFINITY);
+                            if (lane == i) most = m;
                         }
-                        // the references (until now none, -m + kUp = 0): the maxima over the first 32
-                        // keys where those are finite, or, with `safe`, over all so far
-                        if (safe || (st == 0 && !second)) {
-                            if (safe || q4 == 0) {
-                                float most = 0.f;   // lane e's: row e's
-#pragma unroll 1
-                                for (int c0 = 0; c0 < kRT; c0 += 8) {
-                                    uint32_t s[8];
-                                    tmem_ld8_sync(ts + c0, s);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const float z = __fmul_rn(__uint_as_float(s[i]), __fmul_rn(unit_s[hh * kRT + c0 + i], ks));
-                                        const float m = warp_max(seen >> (c0 + i) & 1u ? z : -INFINITY);
-                                        if (lane == c0 + i) most = m;
-                                    }
-                                }
-                                if (lane < kRT) {
-                                    if (safe) red_s[q4 * kRows + hh * kRT + lane] = most;
-                                    else if (fabsf(most) < INFINITY) nm_s[hh * kRT + lane] = kUp - most;
-                                }
-                            }
-                            soft_sync();
-                            if (safe) {
-                                if (tid < kLive) {
-                                    // up, or where no score was finite so far (P, the sum and O are
-                                    // 0 then) to wherever the maximum is
-                                    const float m = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]),
-                                                          fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
-                                    const float was = kUp - nm_s[tid];
-                                    float move = 1.0f;
-                                    if (m > -INFINITY && (!found || m > was)) {
-                                        if (found) move = fast_exp2(was - m);
-                                        nm_s[tid] = kUp - m;
-                                        found = true;
-                                    }
-                                    move_s[tid] = move;
-                                }
-                                soft_sync();
-                                if (st > 0) {
-#pragma unroll
-                                    for (int i = 0; i < kRT / 2; ++i)
-                                        sums[i] = __fmul2_rn(sums[i], reinterpret_cast<const float2*>(move_s + hh * kRT)[i]);
-                                    // O^T (lane = dim) once the step before is in it
-                                    wait(&pv_done[(it - 1) % kPBufs], ((it - 1) / kPBufs) & 1);
-                                    tc_fence_after();
-#pragma unroll 1
-                                    for (int c0 = 0; c0 < kRT; c0 += 8) {
-                                        uint32_t o[8];
-                                        tmem_ld8_sync(tO + lane_off + hh * kRT + c0, o);
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e)
-                                            o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
-                                        tmem_st8(tO + lane_off + hh * kRT + c0, o);
-                                    }
-                                    tmem_st_wait();
-                                }
-                            }
+                        if (lane < kRT) {
+                            if (safe) red_s[q4 * kRows + hh * kRT + lane] = most;
+                            else if (fabsf(most) < INFINITY) nm_s[hh * kRT + lane] = kUp - most;
                         }
                     }
-                    // a key's line of P takes eight rows in 16 bytes
-                    uint8_t* prow = smem + kOffP + sb.x * kPBytes + l * 128;
-                    if constexpr (kGeneral) {
-                        // eight rows at a time; the sums go round, so that the loop's code serves them all
-#pragma unroll 1
-                        for (int c0 = 0; c0 < kRT; c0 += 8) {
-                            uint32_t s[8], w[4], rest[4];
-                            tmem_ld8_sync(ts + c0, s);
-                            float2 now[4];
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                // (the scales first: codes times one of them can pass fp32's largest; and the
-                                // score is rounded before its reference is taken off, so that with `safe` the
-                                // largest gives kUp however large it is: one by one, as the packed product and
-                                // sum would be fused)
-                                const float* un = unit_s + hh * kRT + c0 + i;
-                                const float* nm = nm_s + hh * kRT + c0 + i;
-                                float ex = __fadd_rn(__fmul_rn(__uint_as_float(s[i]), __fmul_rn(un[0], ks)), nm[0]);
-                                float ey = __fadd_rn(__fmul_rn(__uint_as_float(s[i + 1]), __fmul_rn(un[1], ks)), nm[1]);
-                                if (!(seen >> (c0 + i) & 1u)) ex = -INFINITY;
-                                if (!(seen >> (c0 + i + 1) & 1u)) ey = -INFINITY;
-                                const float2 p = make_float2(fast_exp2(ex), fast_exp2(ey));
-                                now[i / 2] = __fadd2_rn(sums[i / 2], p);
-                                if (blk) {   // bf16 (range) in two parts (16 bits)
-                                    w[i / 2] = pack_bf16x2(p.x, p.y);
-                                    rest[i / 2] = pack_bf16x2(p.x - __uint_as_float(w[i / 2] << 16),
-                                                              p.y - __uint_as_float(w[i / 2] & 0xffff0000u));
-                                } else {
-                                    w[i / 2] = pack_f16x2(p.x, p.y);
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < kRT / 2 - 4; ++i) sums[i] = sums[i + 4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sums[kRT / 2 - 4 + i] = now[i];
-                            const int to = ((hh * (kRT / 8) + c0 / 8) ^ (l & 7)) << 4;
-                            *reinterpret_cast<uint4*>(prow + to) = make_uint4(w[0], w[1], w[2], w[3]);
-                            // (the second part in the place of the block's K, which has been read)
-                            if (blk) *reinterpret_cast<uint4*>(stage(it) + l * 128 + to) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                    soft_sync();
+                    if (!safe) return;
+                    if (tid < kLive) {
+                        // up, or where no score was finite so far (P, the sum and O are 0 then) to
+                        // wherever the maximum is
+                        const float m = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]), fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
+                        const float was = kUp - nm_s[tid];
+                        float move = 1.0f;
+                        if (m > -INFINITY && (!found || m > was)) {
+                            if (found) move = fast_exp2(was - m);
+                            nm_s[tid] = kUp - m;
+                            found = true;
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s_empty[sb.x]);
-                    } else {
-                        const float2 k2 = make_float2(ks, ks);
-#pragma unroll
-                        for (int c0 = 0; c0 < kRT; c0 += 16) {
-                            uint32_t s[16];
-                            tmem_ld16_sync(ts + c0, s);
-                            if (c0 + 16 == kRT) {   // the scores are read
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&s_empty[sb.x]);
-                            }
-                            const float2* nm = reinterpret_cast<const float2*>(nm_s + hh * kRT + c0);
-                            const float2* un = reinterpret_cast<const float2*>(unit_s + hh * kRT + c0);
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 4 * q; i < 4 * q + 4; ++i) {
-                                    // exponents of two rows against their references
-                                    const float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
-                                                                __fmul2_rn(un[i], k2), nm[i]);
-                                    const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-                                    sums[c0 / 2 + i] = __fadd2_rn(sums[c0 / 2 + i], p);
-                                    w[i & 3] = pack_f16x2(p.x, p.y);
-                                }
-                                *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + c0 / 8 + q) ^ (l & 7)) << 4)) =
-                                    make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
+                        move_s[tid] = move;
                     }
+                    soft_sync();
+                    if (st == 0) return;
+#pragma unroll
+                    for (int i = 0; i < kRT / 2; ++i)
+                        sums[i] = __fmul2_rn(sums[i], reinterpret_cast<const float2*>(move_s + hh * kRT)[i]);
+                    // O^T (lane = dim) once the step before is in it
+                    wait(&pv_done[(it - 1) % kPBufs], ((it - 1) / kPBufs) & 1);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kRT; c0 += 8) {
+                        uint32_t o[8];
+                        tmem_ld8_sync(tO + lane_off + hh * kRT + c0, o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * move_s[hh * kRT + c0 + e]);
+                        tmem_st8(tO + lane_off + hh * kRT + c0, o);
+                    }
+                    tmem_st_wait();
+                };
+                auto step_done = [&]() {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[sb.x]);
                     sb.next(kSBufs);
                     ++it;
                 };
-                // the plain steps -- whole context steps but the run's first -- apart, so
-                // that they carry neither masks nor references
+                // a step that every row sees whole.  (A key's line of P takes eight rows in 16 bytes.)
+                auto plain_step = [&](int st) {
+                    s_wait();
+                    const float ks = key_scale(st);
+                    uint32_t s[kRT];
+                    if constexpr (kRT == 32) tmem_ld32_sync(tS(sb.x) + lane_off + hh * kRT, s);
+                    else tmem_ld16_sync(tS(sb.x) + lane_off + hh * kRT, s);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[sb.x]);   // the scores are read
+                    const float2 k2 = make_float2(ks, ks);
+                    const float2* nm = reinterpret_cast<const float2*>(nm_s + hh * kRT);
+                    const float2* un = reinterpret_cast<const float2*>(unit_s + hh * kRT);
+                    uint8_t* prow = smem + kOffP + sb.x * kPBytes + l * 128;
+#pragma unroll
+                    for (int q = 0; q < kRT / 8; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 4 * q; i < 4 * q + 4; ++i) {
+                            // exponents of two rows against their references
+                            const float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                                        __fmul2_rn(un[i], k2), nm[i]);
+                            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                            sums[i] = __fadd2_rn(sums[i], p);
+                            w[i & 3] = pack_f16x2(p.x, p.y);
+                        }
+                        *reinterpret_cast<uint4*>(prow + (((hh * (kRT / 8) + q) ^ (l & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    step_done();
+                };
+                // any step, the block's among them: eight rows at a time; the sums go round, so that the
+                // loop's code serves them all
+                auto any_step = [&](int st) {
+                    s_wait();
+                    const bool blk = st < lead;
+                    const uint32_t seen = seen_by(st);
+                    if (safe || (st == 0 && !second)) references(st, seen);
+                    const float ks = key_scale(st);
+                    uint8_t* prow = smem + kOffP + sb.x * kPBytes + l * 128;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kRT; c0 += 8) {
+                        uint32_t s[8], w[4], rest[4];
+                        tmem_ld8_sync(tS(sb.x) + lane_off + hh * kRT + c0, s);
+                        float2 now[4];
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            // (one by one: the packed product and sum would be fused)
+                            const float* un = unit_s + hh * kRT + c0 + i;
+                            const float* nm = nm_s + hh * kRT + c0 + i;
+                            float ex = __fadd_rn(__fmul_rn(__uint_as_float(s[i]), __fmul_rn(un[0], ks)), nm[0]);
+                            float ey = __fadd_rn(__fmul_rn(__uint_as_float(s[i + 1]), __fmul_rn(un[1], ks)), nm[1]);
+                            if (!(seen >> (c0 + i) & 1u)) ex = -INFINITY;
+                            if (!(seen >> (c0 + i + 1) & 1u)) ey = -INFINITY;
+                            const float2 p = make_float2(fast_exp2(ex), fast_exp2(ey));
+                            now[i / 2] = __fadd2_rn(sums[i / 2], p);
+                            if (blk) {   // bf16 (range) in two parts (16 bits)
+                                w[i / 2] = pack_bf16x2(p.x, p.y);
+                                rest[i / 2] = pack_bf16x2(p.x - __uint_as_float(w[i / 2] << 16), p.y - __uint_as_float(w[i / 2] & 0xffff0000u));
+                            } else {
+                                w[i / 2] = pack_f16x2(p.x, p.y);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kRT / 2 - 4; ++i) sums[i] = sums[i + 4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sums[kRT / 2 - 4 + i] = now[i];
+                        const int to = ((hh * (kRT / 8) + c0 / 8) ^ (l & 7)) << 4;
+                        *reinterpret_cast<uint4*>(prow + to) = make_uint4(w[0], w[1], w[2], w[3]);
+                        // (the second part in the place of the block's K, which has been read)
+                        if (blk) *reinterpret_cast<uint4*>(stage(it) + l * 128 + to) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[sb.x]);
+                    step_done();
+                };
+                // whole context steps apart, so that they carry no masks
                 const bool ragged = (walk.p1 - walk.p0) & 1 || walk.p1 * kQ8Page > walk.cur_t;
-                const int nwhole = safe ? 0 : n - (ragged ? 1 : 0), first = kept ? lead : 1;
+                const int nwhole = safe ? 0 : n - (ragged ? 1 : 0);
 #pragma unroll 1
                 for (int st = 0; st < n; ++st) {
-                    if (st >= first && st < nwhole) step(st, std::false_type{});
-                    else step(st, std::true_type{});
+                    if (st >= lead && st < nwhole) {
+                        if (st == 0 && !second) {
+                            s_wait();
+                            references(0, ~0u);
+                        }
+                        plain_step(st);
+                    } else {
+                        any_step(st);
+                    }
                 }
                 // the rows' sums over the keys: lane e of a warp ends with its row e's
                 // (halving the rows and the lanes that differ, step by step)
@@ -909,11 +914,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
 #pragma unroll
                 for (int i = 0; i < kRT / 2; ++i) sum[2 * i] = sums[i].x, sum[2 * i + 1] = sums[i].y;
                 fold_sums(sum);
-                if (kRT == 16) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 16);
+#pragma unroll
+                for (int o = kRT; o < 32; o <<= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
                 if (lane < kRT) red_s[q4 * kRows + hh * kRT + lane] = sum[0];
-                // (a cluster's partials stay on chip: the copies into the ring have all been read)
-                float* rec = kCluster ? reinterpret_cast<float*>(smem + kOffRing)
-                             : walk.whole ? nullptr : ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats;
+                // Partials go by way of P's place, where a cluster's stay; so do the rows of a unit that
+                // is whole, as bf16.
+                float* rec = reinterpret_cast<float*>(smem + kOffP);
+                const bool direct = !kCluster && walk.whole;
                 soft_sync();
                 bool bad = false;
                 float lsum = 0.f;
@@ -929,8 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 }
                 wait(o_done, seg & 1);
                 const float v_unit = q8_pow2(vexp_s[seg % 3]);
-                // (a cluster's partial overwrites the ring: only now have all pages been read)
-                if (rec && tid < kLive)
+                // (only now has all of P been read)
+                if (!direct && tid < kLive)
                     *reinterpret_cast<float2*>(rec + kRows * kQ8D + 2 * tid) = make_float2(-nm_s[tid], lsum);   // (kUp below the reference)
                 tc_fence_after();
                 soft_sync();
@@ -969,36 +976,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                                 if (i == e) mean[i] += add;
                         }
                     }
-                    // (rows past the tile's last are written to a partial too, and never read)
+                    // (rows past the tile's last are written too, and never read)
+                    if (direct) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = hh * kRT + c0 + e;
-                        if constexpr (kCluster) {
-                            rec[r * kQ8D + l] = mean[e];
-                        } else if (rec) {
-                            __stcg(rec + r * kQ8D + l, mean[e]);
-                        } else {
-                            const int row = row_s[r];
-                            if (row >= 0) a.out[static_cast<size_t>(row) * kQ8D + l] = f32_bf16_bits(mean[e]);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<uint16_t*>(rec)[(hh * kRT + c0 + e) * kQ8D + l] = f32_bf16_bits(mean[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) rec[(hh * kRT + c0 + e) * kQ8D + l] = mean[e];
                     }
                 }
-                if constexpr (kCluster) fence_proxy_async_smem();   // (copies may be made there again)
                 if (bad) *fail_s = 1;
-                part = 1;   // a partial run that is not the CTA's first is its last
                 tc_fence_before();
-                soft_sync();   // red_s and nm_s read by everyone before the next run writes them
-                if (tid == 0) fail_s[6] = 0;
+                if (!direct) fence_proxy_async_smem();
+                soft_sync();   // red_s and nm_s read by everyone before the next run writes them; the rows are there
                 if (lane == 0) {
                     mbar_arrive(o_free);
                     mbar_arrive(&q_free[seg & 1]);
                 }
+                if (tid == 0) fail_s[6] = 0;
+                if (direct) {
+#pragma unroll 1
+                    for (int r = warp; r < nrows; r += kSoftWarps)
+                        reinterpret_cast<uint2*>(a.out + static_cast<size_t>(row_s[r]) * kQ8D)[lane] =
+                            reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(rec) + r * kQ8D)[lane];
+                    soft_sync();   // (P's place and row_s are free)
+                } else if (!kCluster) {
+                    if (tid == 0) bulk_s2g(ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats, rec, kRecFloats * 4);
+                }
+                part = 1;   // a partial run that is not the CTA's first is its last
                 ++seg;
             }
         } while (again());
+        if (tid == 0) bulk_wait();
         if constexpr (kCluster) {   // no page of the unit fell to this CTA
             if (seg == 0 && tid < kRows)
-                *reinterpret_cast<float2*>(smem + kOffRing + (kRows * kQ8D + 2 * tid) * 4) = make_float2(-INFINITY, 0.f);
+                *reinterpret_cast<float2*>(smem + kOffP + (kRows * kQ8D + 2 * tid) * 4) = make_float2(-INFINITY, 0.f);
         }
     }
     __syncwarp();
@@ -1011,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         for (int r = rank + wk.cluster * warp; r < nrows; r += wk.cluster * (kThreads / 32)) {
             const int gr = row0 + r, j = gr * wk.inv_g >> 16;
             auto get = [&](int i, float2& ml, float4& o) {
-                const float* rec = reinterpret_cast<const float*>(cluster.map_shared_rank(smem + kOffRing, i));
+                const float* rec = reinterpret_cast<const float*>(cluster.map_shared_rank(smem + kOffP, i));
                 ml = *reinterpret_cast<const float2*>(rec + kRows * kQ8D + 2 * r);
                 o = *(reinterpret_cast<const float4*>(rec + r * kQ8D) + lane);
             };
