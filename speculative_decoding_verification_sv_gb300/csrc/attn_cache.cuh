@@ -209,13 +209,18 @@ __device__ __forceinline__ void fold_sums(float (&v)[kN]) {
     fold_sums_step<kN>(v);
 }
 
-// Joins n partials of a row, eight in flight; get(i, ml, o) loads the i-th's
-// (m, l) and the lane's four dims of its O: sums of P V, or, with kMeans, those over l.
+// What some partials of a row sum up to, a lane four dims of it: O, l, relative to m.
+struct RowSum {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+};
+
+// Adds n partials of a row, eight in flight; get(i, ml, o) loads the i-th's (m, l) and the
+// lane's four dims of its O: sums of P V, or, with kMeans, those over l.
 template <bool kMeans, typename Get>
-__device__ __forceinline__ void join_partials(int n, Get&& get, uint16_t* dst) {
-    const int lane = threadIdx.x & 31;
-    float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+__device__ __forceinline__ RowSum add_partials(int n, Get&& get) {
+    auto power = [](float x) { return kMeans ? fast_exp2(x) : exp2f(x); };
+    RowSum r;
 #pragma unroll 1
     for (int c0 = 0; c0 < n; c0 += 8) {
         float2 ml[8];
@@ -226,29 +231,37 @@ __device__ __forceinline__ void join_partials(int n, Get&& get, uint16_t* dst) {
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (c0 + u < n) get(c0 + u, ml[u], o[u]);
         }
-        float mn = M;
+        float mn = r.m;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
-        auto power = [](float x) { return kMeans ? fast_exp2(x) : exp2f(x); };
-        const float c = M == -INFINITY ? 0.f : power(M - mn);
-        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c, L *= c;
+        const float c = r.m == -INFINITY ? 0.f : power(r.m - mn);
+        r.o.x *= c, r.o.y *= c, r.o.z *= c, r.o.w *= c, r.l *= c;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
             float w = power(ml[u].x - mn);
-            L += w * ml[u].y;
+            r.l += w * ml[u].y;
             if constexpr (kMeans) w *= ml[u].y;
-            acc.x += w * o[u].x;
-            acc.y += w * o[u].y;
-            acc.z += w * o[u].z;
-            acc.w += w * o[u].w;
+            r.o.x += w * o[u].x;
+            r.o.y += w * o[u].y;
+            r.o.z += w * o[u].z;
+            r.o.w += w * o[u].w;
         }
-        M = mn;
+        r.m = mn;
     }
-    const float inv = L != 0.f ? 1.0f / L : 0.f;
-    *reinterpret_cast<uint2*>(dst + 4 * lane) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    return r;
+}
+
+__device__ __forceinline__ void store_row(const RowSum& r, uint16_t* dst) {
+    const float inv = r.l != 0.f ? 1.0f / r.l : 0.f;
+    *reinterpret_cast<uint2*>(dst + 4 * (threadIdx.x & 31)) =
+        make_uint2(pack_bf16x2(r.o.x * inv, r.o.y * inv), pack_bf16x2(r.o.z * inv, r.o.w * inv));
+}
+
+template <bool kMeans, typename Get>
+__device__ __forceinline__ void join_partials(int n, Get&& get, uint16_t* dst) {
+    store_row(add_partials<kMeans>(n, get), dst);
 }
 
 inline Work work_of(int R, int G, int Hkv) {
