@@ -1161,25 +1161,33 @@ int resident_clusters(int c) {
     return n;
 }
 
-// How the work is split, in pages that the busiest CTA takes: evenly over the SMs
-// and joined by a second kernel, or a cluster of 2, 4 or 8 CTAs for each unit, joined
-// on chip, whose barriers and remote reads cost about two pages.  The second kernel and
-// the partials' way through L2 cost about ten, and three for each ten partials of a unit.
-// Measured, cluster against even split: 5 x 12 heads over 2 of 4096 positions 10.4 and
-// 11.8 us, of 16384 (the rule splits there) 18.1 and 19.2; 9 x 28 over 4, 4096: 11.5 and
-// 14.6, 12288: 17.4 and 17.4, 16384: 20.3 and 17.4; 65 x 28 over 4, 4096: 17.0 and 19.7,
-// 8192: 22.9 and 24.6.  The table's capacity decides, as the lengths are on the device: 5
-// x 12 heads over 4096 positions take 12.3 us with a table for 131072.
+// How the work is split: a cluster of up to 8 CTAs for each unit, joined on chip, or all
+// pages evenly over the SMs and partials joined by a second kernel, whichever is expected to
+// take less time.  A page takes 0.30 us of a CTA, or 2.8 ns for each CTA that reads at the
+// same time where that is more (HBM); a CTA's start and end and a cluster's join 6.5 us, 11
+// with tiles of more than 32 rows; of the even split, which has CTAs with two units and the
+// second kernel, 11.5 and 17.  Measured in us, clusters as the rule takes them against the
+// even split: 5 x 12 heads over 2 of 4096 positions 10.1 and 10.6, of 16384 (the rule splits)
+// 17.2 and 12.6; 9 x 28 over 4, 4096: 13.3 and 19.0, 16384 (splits): 21.3 and 16.9; four such
+// of 8192: 20.3 and 27.2; 16 of 8192: 35.6 and 41.4; 65 x 28 over 4, 8192: 24.7 and 31.0; 32
+// single tokens of 2048: 20.1 and 24.9; 64 of 4096 (splits): 60.2 and 55.7.  The table's
+// capacity decides, as the lengths are on the device.
 void plan(Work& w, int B, int max_pages, int& grid) {
     const int64_t units = static_cast<int64_t>(B) * w.U, pages = units * (static_cast<int64_t>(max_pages) + 1);
-    const int sms = device_sm_count();
+    const int64_t sms = device_sm_count();
+    const bool tall = w.tile_rows > 32;
+    auto page_ns = [](int64_t ctas) { return ctas * 28 > 3000 ? ctas * 28 / 10 : int64_t(300); };
     const int64_t most = pages / kGrain;
     grid = static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
     w.cluster = 0;
-    int64_t best = (pages + grid - 1) / grid + (grid > 1 ? 10 + 3 * (grid / units) / 10 : 0);
-    for (int c = kMaxCluster; c >= 2; c /= 2) {
-        const int64_t cost = (max_pages + c) / c + 2;
-        if (cost >= best || units > resident_clusters(c)) continue;
+    int64_t best = (pages + grid - 1) / grid * page_ns(grid) + (grid == 1 ? 6500 : tall ? 17000 : 11500);
+    for (int c = 1; c <= kMaxCluster; ++c) {
+        const int64_t at_once = c == 1 ? sms : resident_clusters(c);   // clusters
+        if (at_once < 1 || (c > 1 && units > at_once)) continue;
+        int64_t cost = 0;
+        for (int64_t left = units; left > 0 && cost < best; left -= at_once)
+            cost += (max_pages + c) / c * page_ns((left < at_once ? left : at_once) * c) + (tall ? 11000 : 6500);
+        if (cost >= best) continue;
         best = cost;
         w.cluster = c;
     }
@@ -1228,7 +1236,7 @@ cudaError_t launch_verify_attn_q8(const CacheAttnArgs& a, void* ws, cudaStream_t
     const cudaError_t e = w.tile_rows <= 32 ? launch_rt<16>(a, w, grid, part, st) : launch_rt<32>(a, w, grid, part, st);
     if (e != cudaSuccess || grid == 1 || w.cluster != 0) return e;
     constexpr int kWarps = kCombineThreads / 32;
-    if (grid > kWarps * a.B * w.U)
+    if (grid > 2 * kWarps * a.B * w.U)
         return launch_pdl(combine_q8_kernel<kWarps>, dim3(a.R * a.G, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w, part, grid);
     return launch_pdl(combine_q8_kernel<1>, dim3((a.R * a.G + kWarps - 1) / kWarps, a.B * a.Hkv), dim3(kCombineThreads), 0, st, a, w,
                       part, grid);

@@ -351,14 +351,13 @@ def test_attn_scales_far_apart(sv, lo, hi):
     run(sv, 2, 5, 12, 2, [300, 77], seed=hi + 200, lo=lo, hi=hi, scale=2.0 ** -12 if hi > 1 else None)
 
 
-@pytest.mark.parametrize("B,R,Hq,H,lens,is_tree", [
-    (1, 5, 12, 2, [1000], False), (3, 9, 28, 4, [63, 0, 700], False), (2, 65, 28, 4, [130, 5], True), (1, 1, 1, 1, [1], False),
-    (2, 20, 16, 2, [640, 129], True)])
-def test_attn_split_over_all_sms(sv, B, R, Hq, H, lens, is_tree):
+@pytest.mark.parametrize("B,R,Hq,H,lens,is_tree,mp", [
+    (1, 5, 12, 2, [1000], False, 250), (3, 5, 12, 2, [63, 0, 700], False, 500), (2, 9, 28, 4, [700, 0], False, 800),
+    (3, 65, 28, 4, [130, 5, 0], True, 250), (1, 1, 1, 1, [1], False, 250), (2, 20, 16, 2, [640, 129], True, 2000)])
+def test_attn_split_over_all_sms(sv, B, R, Hq, H, lens, is_tree, mp):
     """A long table (its capacity sets how the work is split): the pages are laid
     end to end over the SMs, and units in several of them joined by the second
     kernel.  Shorter tables give each unit a cluster of CTAs."""
-    mp = 250
     assert sv.verify_attn_q8_workspace(B, R, Hq, H, 128, mp * 64) > 0
     assert sv.verify_attn_q8_workspace(1, 5, 12, 2, 128, 2048) == 0
     r = np.random.default_rng(R)
@@ -367,6 +366,30 @@ def test_attn_split_over_all_sms(sv, B, R, Hq, H, lens, is_tree):
         par[:, j] = r.integers(max(0, j - 6), j, B)
     run(sv, B, R, Hq, H, lens, parent=par if is_tree else None, seed=R, mp=mp)
     run(sv, B, R, Hq, H, lens, parent=par if is_tree else None, seed=R, mp=mp, scale=9.0)
+
+
+@pytest.mark.parametrize("t", [4096, 40, 0])
+def test_attn_every_cluster_size(sv, t):
+    """Page tables whose capacity gives units clusters of 1 to 8 CTAs (and none), which
+    the lengths fill, hardly reach or leave empty."""
+    for B, R, Hq, H in ((1, 5, 12, 2), (4, 2, 28, 4), (3, 9, 28, 4), (6, 9, 28, 4), (9, 9, 28, 4), (14, 9, 28, 4), (20, 3, 12, 4), (40, 1, 28, 4)):
+        q, (kp, vp), table, kb, vb = _device_inputs(B, R, Hq, H, 4096, seed=B)
+        lens = i32([max(0, t - 17 * b) for b in range(B)])
+        out = sv.verify_attn_q8(q, kp, vp, table, lens, kb, vb)
+        k, v = sv.kv_gather_q8(kp[None], vp[None], table, i32([0] * B), lens, max(t, 1))
+        k, v = torch.cat([k[0].float(), kb.float()], 2), torch.cat([v[0].float(), vb.float()], 2)
+        n = max(t, 1)
+        see = torch.zeros(B, R, n + R, dtype=torch.bool, device="cuda")
+        see[:, :, :n] = (torch.arange(n, device="cuda")[None, :] < lens[:, None])[:, None]
+        see[:, :, n:] = torch.ones(R, R, device="cuda").tril() > 0
+        G = Hq // H
+        z = torch.einsum("brhgd,bhkd->bhrgk", q.float().view(B, R, H, G, 128), k) * 128 ** -0.5
+        p = torch.softmax(z.masked_fill(~see[:, None, :, None], float("-inf")), -1)
+        want = torch.einsum("bhrgk,bhkd->brhgd", p, v).reshape(B, R, Hq, 128)
+        wgt = torch.einsum("bhrgk,bhkd->brhgd", p, v.abs()).reshape(B, R, Hq, 128)
+        # the output's rounding (2^-8) and P's (2^-11), and as much again as P's for both sides' sums and scores in fp32
+        assert bool(((out.float() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * wgt + 1e-6).all()), (B, R)
+    assert sv.get_device_error() == 0
 
 
 def one_sequence(sv, q, kp, vp, table, t, kb, vb, scale, parent=None, lost=0):
