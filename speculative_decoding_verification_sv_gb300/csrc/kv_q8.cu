@@ -11,6 +11,21 @@
 // earlier codes anew.  V's words hold eight positions of a dim: what a partly filled
 // octet held before is read back and merged.  No two warps of a launch share a run, and
 // none waits for another.
+//
+// Measured, graph replays over inputs larger than L2: append of 8 prompts of 2048 rows (4
+// heads; 34 MB read, 17 MB written, 7.9 us at copy rate) 16.1 us; of 4 chunks of 1000 rows 6.5,
+// of one token in each of 64 sequences 4.8.  A run of K is 16 rows of angles beside 16
+// rows of data, and both come from L2 or beyond before a code can leave: latency and, at
+// 0.5 instructions a cycle, issue bound it, so warps hold eight rows' angles on their way
+// (23.5 us with the read-back for the prompts; four 24.9, two 27.1, sixteen 26.3: fewer warps
+// fit or registers spill) in CTAs of four warps, which leave room for 20 on an SM (three of
+// eight 26.7, with spills).  With lanes of four dims side by side, whose rotation takes two
+// shuffles and eight selects a row and loads every angle twice, the same took 32.2.
+// Commit of 28 layers x 4 heads, 16 sequences of up to 9 rows: 13.7 us, of which the launch, len
+// and the cluster's barriers are 2.9: three rounds of scattered rows and runs for each of 2048
+// warps.  Fetching the later rounds' lines to L2 first gained nothing (25.6 and 25.1 us with
+// the read-back), 1024 threads a CTA lost (28.6), 256 too (25.5).
+// Gather of 8 x 8192 positions: 32.3 us, 196 MB at 6.1 TB/s.
 #include <cooperative_groups.h>
 
 #include "kv_append.cuh"
@@ -22,14 +37,13 @@ namespace cg = cooperative_groups;
 namespace sv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kCommitThreads = 512;
 constexpr int kMaxR = 128;
 constexpr int kCluster = 8;
 
-// Largest magnitude among the lane's four dims of each row (bf16 bits, two rows'
-// maxima side by side would not help: one number is wanted), and the rows that hold
-// NaN or infinity, over the warp; such rows become NaN and do not count.
+// Largest magnitude in the rows, over the warp, and which rows hold NaN or infinity:
+// such rows become NaN and do not count.
 __device__ __forceinline__ float run_amax(uint2 (&x)[kQ8Run], uint32_t& bad) {
     uint32_t m2 = 0u;   // a maximum in each half
 #pragma unroll
@@ -62,13 +76,61 @@ __device__ __forceinline__ float run_amax(uint2 (&x)[kQ8Run], uint32_t& bad) {
     return __uint_as_float(m << 16);
 }
 
+// The four dims that a lane has of a row of K, in two pairs: dims a, a + 1 and b, b + 1.
+// In a row whose halves are turned against each other (dims d and d + rot / 2) both
+// members of two rotation pairs, so that no value and no angle passes between lanes;
+// else four dims side by side.
+struct KDims {
+    int a, b;
+};
+__device__ __forceinline__ KDims k_dims(const AppendArgs& g) {
+    const int l = threadIdx.x & 31, half = g.rot / 2;
+    if (!g.rope || g.interleaved) return {4 * l, 4 * l + 2};
+    if (2 * l < half) return {2 * l, 2 * l + half};
+    return {2 * l + half, 2 * l + 64};   // of the dims from rot on, which are not turned
+}
+
+// Turns the lane's dims of the sixteen rows of K and rounds them to bf16: the rows that
+// the bf16 cache would hold.  cs is the rope table's row of the run's first position;
+// rows outside first .. last are copies of the first or last one, and so are their angles.
+__device__ __forceinline__ void turn_run(uint2 (&x)[kQ8Run], int first, int last, const float* cs, int rot, bool interleaved) {
+    const int f = 2 * (threadIdx.x & 31), half = rot / 2;   // two angles: f, f + 1
+    if (f >= half) return;
+    constexpr int kAhead = 8;   // rows whose angles are on their way at a time
+#pragma unroll
+    for (int i0 = 0; i0 < kQ8Run; i0 += kAhead) {
+        float2 co[kAhead], si[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float* c = cs + min(max(i0 + i, first), last) * rot + f;
+            co[i] = __ldg(reinterpret_cast<const float2*>(c));
+            si[i] = __ldg(reinterpret_cast<const float2*>(c + half));
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            uint2& w = x[i0 + i];
+            float v[4];
+            unpack4(w, v);
+            if (interleaved) {
+                rope_turn(v[0], v[1], co[i].x, si[i].x);
+                rope_turn(v[2], v[3], co[i].y, si[i].y);
+            } else {
+                rope_turn(v[0], v[2], co[i].x, si[i].x);
+                rope_turn(v[1], v[3], co[i].y, si[i].y);
+            }
+            w = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+    }
+}
+
 // One warp writes positions first .. last (of the sixteen) of a run of a (page, head)
-// block; x holds the lane's four dims (packed bf16) of the sixteen rows, zeros outside
-// first .. last.  Positions before `first` keep their values, held anew where the
+// block; x holds the lane's four dims (packed bf16; of V four side by side, of K those
+// of kd) of the sixteen rows, zeros or copies of the first or last one outside first .. last.
+// Positions before `first` keep their values, held anew where the
 // scale grows; where the run's first position is written, what the run held is gone.
 // Returns whether a row was not finite.
-template <bool kV>
-__device__ __forceinline__ bool write_run(uint8_t* blk, int run, int first, int last, uint2 (&x)[kQ8Run]) {
+template <bool kV, bool kApart = false>
+__device__ __forceinline__ bool write_run(uint8_t* blk, int run, int first, int last, uint2 (&x)[kQ8Run], KDims kd = {0, 0}) {
     const int lane = threadIdx.x & 31;
     float* scale = reinterpret_cast<float*>(blk + q8_scale_off(run));
     const float s_old = first > 0 ? *scale : 0.f;
@@ -94,11 +156,11 @@ __device__ __forceinline__ bool write_run(uint8_t* blk, int run, int first, int 
     const float rs = q8_pow2(-e), f = q8_pow2(max(e_old - e, -126));
     if (lane == 0) *scale = q8_pow2(e);
     if constexpr (!kV) {
-        const int col = (lane & 3) * 4, chunk = lane >> 2;
+        uint8_t* rows = blk + q8_k_off(kQ8Run * run, 0);   // dim d of row i: at 128 i + (d ^ i % 8 * 16)
         if (again) {
 #pragma unroll 4
             for (int i = 0; i < first; ++i) {
-                uint32_t* p = reinterpret_cast<uint32_t*>(blk + q8_k_off(kQ8Run * run + i, chunk) + col);
+                uint32_t* p = reinterpret_cast<uint32_t*>(rows + 128 * i + (4 * lane ^ (i & 7) << 4));
                 *p = q8_rescale4(*p, f);
             }
         }
@@ -107,8 +169,13 @@ __device__ __forceinline__ bool write_run(uint8_t* blk, int run, int first, int 
             if (i < first || i > last) continue;
             float v[4];
             unpack4(x[i], v);
-            *reinterpret_cast<uint32_t*>(blk + q8_k_off(kQ8Run * run + i, chunk) + col) =
-                q8_codes4(v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs);
+            const uint32_t lo = q8_codes2(v[0] * rs, v[1] * rs), hi = q8_codes2(v[2] * rs, v[3] * rs);
+            if constexpr (kApart) {
+                *reinterpret_cast<uint16_t*>(rows + 128 * i + (kd.a ^ (i & 7) << 4)) = static_cast<uint16_t>(lo);
+                *reinterpret_cast<uint16_t*>(rows + 128 * i + (kd.b ^ (i & 7) << 4)) = static_cast<uint16_t>(hi);
+            } else {
+                *reinterpret_cast<uint32_t*>(rows + 128 * i + (4 * lane ^ (i & 7) << 4)) = lo | hi << 16;
+            }
         }
     } else {
 #pragma unroll
@@ -156,7 +223,7 @@ __device__ __forceinline__ bool write_run(uint8_t* blk, int run, int first, int 
 // Append: warp items (slot, head, K or V).  A sequence of n rows touches at most
 // n / 16 + 2 runs, so slots row_off[b] / 16 + 2 b .. hold its runs, and no count has
 // to be summed over the sequences before a warp finds its own.
-__global__ void __launch_bounds__(kThreads, 3) append_q8_kernel(AppendArgs a, uint8_t* __restrict__ k_pool,
+__global__ void __launch_bounds__(kThreads, 5) append_q8_kernel(AppendArgs a, uint8_t* __restrict__ k_pool,
                                                              uint8_t* __restrict__ v_pool, uint32_t items) {
     pdl_wait();
     pdl_launch_dependents();
@@ -191,24 +258,22 @@ __global__ void __launch_bounds__(kThreads, 3) append_q8_kernel(AppendArgs a, ui
     }
     const size_t blk = (static_cast<size_t>(pg) * a.Hkv + h) * kQ8Bytes;
     const int base = p0 & ~(kQ8Run - 1), first = p0 - base, last = p1 - 1 - base, r = (p0 & (kQ8Page - 1)) / kQ8Run;
-    const int64_t stride = sub & 1 ? a.v_stride : a.k_stride;
-    const uint16_t* src = (sub & 1 ? a.v : a.k) + h * kQ8D + 4 * lane + (r0 + (base - t)) * stride;
+    const bool is_v = sub & 1;
+    const KDims kd = is_v ? KDims{4 * lane, 4 * lane + 2} : k_dims(a);
+    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+    const uint16_t* src = (is_v ? a.v : a.k) + h * kQ8D + (r0 + (base - t)) * stride;
     uint2 x[kQ8Run];
 #pragma unroll
     for (int i = 0; i < kQ8Run; ++i) {
-        x[i] = make_uint2(0u, 0u);
-        if (i >= first && i <= last) x[i] = __ldg(reinterpret_cast<const uint2*>(src + i * stride));
+        const uint16_t* row = src + min(max(i, first), last) * stride;
+        x[i] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row + kd.a)), __ldg(reinterpret_cast<const uint32_t*>(row + kd.b)));
     }
     bool bad;
-    if (sub & 1) {
+    if (is_v) {
         bad = write_run<true>(v_pool + blk, r, first, last, x);
     } else {
-        if (a.rope) {
-            const float* cs = a.rope + static_cast<int64_t>(base) * a.rot;
-            if (a.interleaved) turn_rows<true>(x, first, last, cs, a.rot);
-            else turn_rows<false>(x, first, last, cs, a.rot);
-        }
-        bad = write_run<false>(k_pool + blk, r, first, last, x);
+        if (a.rope) turn_run(x, first, last, a.rope + static_cast<int64_t>(base) * a.rot, a.rot, a.interleaved);
+        bad = write_run<false, true>(k_pool + blk, r, first, last, x, kd);
     }
     if (bad) raise_error(a.err, SV_DEVERR_NONFINITE);
 }
