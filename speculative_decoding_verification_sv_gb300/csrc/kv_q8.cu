@@ -13,7 +13,7 @@
 // none waits for another.
 //
 // Measured, graph replays over inputs larger than L2: append of 8 prompts of 2048 rows (4
-// heads; 34 MB read, 17 MB written, 7.9 us at copy rate) 16.1 us; of 4 chunks of 1000 rows 6.5,
+// heads; 34 MB read, 17 MB written, 7.4 us at copy rate) 16.1 us; of 4 chunks of 1000 rows 6.5,
 // of one token in each of 64 sequences 4.8.  A run of K is 16 rows of angles beside 16
 // rows of data, and both come from L2 or beyond before a code can leave: latency and, at
 // 0.5 instructions a cycle, issue bound it, so warps hold eight rows' angles on their way
