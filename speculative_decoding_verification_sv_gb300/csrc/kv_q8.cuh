@@ -107,9 +107,6 @@ __device__ __forceinline__ uint32_t q8_mul2(uint32_t a, uint32_t b) {
 // 2^e as a bf16 pair, -126 <= e <= 127
 __device__ __forceinline__ uint32_t q8_pow2_pair(int e) { return static_cast<uint32_t>(e + 127) * 0x00800080u; }
 
-// bytes of w that are NaN codes (0x7f, 0xff): bit 7 of each
-__device__ __forceinline__ uint32_t q8_nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
 // y, NaN where the code of pair p was NaN (0x7f: the pair holds 480 * 2^-120 there)
 __device__ __forceinline__ uint32_t q8_nan_pair(uint32_t p, uint32_t y) {
     if ((p & 0x00007fffu) == 0x000007f0u) y |= 0x00007fc0u;

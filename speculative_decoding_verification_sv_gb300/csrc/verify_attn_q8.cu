@@ -2,11 +2,9 @@
 // cache (format: kv_q8.cuh) and the block's own bf16 K/V.
 //
 // out = softmax(scale q K^T) V over the cached positions and the block rows that the
-// row may see.  The cache is half of the bf16 cache's bytes, and what bounds the kernel
-// is to be reading them.
-//
-// Both products run transposed, S^T = K Q^T and O^T = V^T P^T (M = 128 keys or dims,
-// N = 64 query rows), so that a block of few rows still fills the tensor core.
+// row may see.  Both products run transposed, S^T = K Q^T and O^T = V^T P^T (M = 128 keys or
+// dims, N = the tile's query rows, 32 or 64), so that a block of few rows still fills the
+// tensor core.
 //   S^T: lane = key, column = query row.  K's codes are e4m3 and lie in memory as the
 //        swizzled tile that the MMA reads: they go from memory to shared memory to the
 //        product (kind::f8f6f4) without passing a register.  Q has to be e4m3 then, and
@@ -22,12 +20,14 @@
 //   O^T: lane = dim, column = row.  V's codes are made f16 by the warps that hold a dim
 //        each (one conversion and one product by the run's scale for two codes) and are
 //        the A operand in tensor memory; f16, because it holds P to 11 bits, an eighth of
-//        bf16's rounding, and every e4m3.  What it lacks is range.  V is therefore in units of the largest
-//        scale among the run's pages and its block (a value is exact where its own scale
-//        is no less than 2^-15 of that, and off by 2^-33 of the largest V otherwise), and P
-//        is 2^kUp at a reference, below.
+//        bf16's rounding (0.0017 of the result against 0.0023), and every e4m3.  What it
+//        lacks is range.  V is therefore in units of the largest scale of the run's first two
+//        pages, 2^kVUp of it (a value is exact where its own scale is no less than 2^-11
+//        of that; one too large for f16 makes O infinite), and P is 2^kUp at a reference, below.
 // The block's K rows are held as Q's are, two e4m3 in units of the row's own (four
-// products); its V rows are rounded to f16 in those units: exact down to 2^-26 of the largest.
+// products).  Its V rows may be of any size, whether seen or not, and stay bf16 in V's units; its P is
+// in two bf16 parts then (16 bits).  What of them is not finite is kept out of the product and
+// added to the rows that see it at the end.
 // A row's maximum runs across lanes here, so it is formed once, over the first 32 keys
 // of the run (of the block, where the run has it: the row's own key and those next to
 // it), and is the row's reference m for the whole run.  P is 2^-4 at the reference: a
@@ -37,6 +37,19 @@
 // sums give, P then summing to 2^15; one whose sums say nothing (the reference was a key that
 // the row does not see, or none was finite) with the reference moved to the maximum
 // every step.
+//
+// What bounds it, in us of graph replays over inputs larger than L2 (heads and positions as
+// named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 35.5, for 137 MB, which take
+// 20.1 at copy rate; 64 single tokens of up to 4097: 46.5 (175 MB, 25.7).  CTAs that stream
+// reach 5.5 to 5.9 TB/s; the rest is the start (the chain length, page table, page, scores, P:
+// 5 to 9) and the end (last sums, O, join: 4).  A step of two pages takes 0.61 of a CTA by itself
+// with tiles of up to 32 rows, 0.75 with more: 128 KB that pass its shared memory at 128 bytes a
+// cycle, K twice as there are two parts of Q.  5 rows x 12 heads over 2, 4096: 10.1, and 100001
+// positions 20.3 (floor 7.5), both latency: few pages a CTA.  A tree of 65 rows: 24.8; eight
+// tiles of rows stream the same pages, 17 steps of 0.75 each behind a start of 9.
+// Tried: P in bf16; an MMA warp for both products, and one copier (a step waits for the
+// other's); 16 softmax warps of 16 rows (tensor memory reads and references double); two
+// groups of softmax warps in turn (16 sequences 42 -> 51.8: spills).
 //
 // Work: units and runs as in attn_cache.cuh.  A unit that lies in several CTAs' runs
 // leaves partials in the workspace -- at most two a CTA -- and a second small kernel
