@@ -39,6 +39,59 @@ constexpr int kCommitThreads = 512;
 constexpr int kMaxR = 128;
 constexpr int kCluster = 8;
 
+// Turns the lane's four dims (4 lane .., packed bf16) of the rows of positions
+// base + first .. base + last of a K octet and rounds them to bf16: the rows that
+// the bf16 cache would hold.  cs is the table's row of position base.  Two rows'
+// cosines and sines are on their way at a time (four took 104 bytes of spills).
+template <bool kInterleaved>
+__device__ __forceinline__ void turn_rows(uint2 (&x)[8], int first, int last, const float* cs, int rot) {
+    const int lane = threadIdx.x & 31, d = 4 * lane, half = rot / 2;
+    const bool in = d < rot, lower = d < half;   // lower: the first member of its pair (halves)
+    const int mate = !in ? lane : lower ? lane + half / 4 : lane - half / 4;
+    const int f = !in ? 0 : kInterleaved ? d / 2 : lower ? d : d - half;
+#pragma unroll
+    for (int i0 = 0; i0 < 8; i0 += 2) {
+        float4 co[2], si[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i0 + i < first || i0 + i > last) continue;
+            const float* c = cs + static_cast<int64_t>(i0 + i) * rot + f;
+            if constexpr (kInterleaved) {
+                const float2 a = __ldg(reinterpret_cast<const float2*>(c));
+                const float2 b = __ldg(reinterpret_cast<const float2*>(c + half));
+                co[i] = make_float4(a.x, a.y, 0.0f, 0.0f);
+                si[i] = make_float4(b.x, b.y, 0.0f, 0.0f);
+            } else {
+                co[i] = __ldg(reinterpret_cast<const float4*>(c));
+                si[i] = __ldg(reinterpret_cast<const float4*>(c + half));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i0 + i < first || i0 + i > last) continue;
+            uint2& w = x[i0 + i];
+            float v[4];
+            unpack4(w, v);
+            if constexpr (kInterleaved) {
+                rope_turn(v[0], v[1], co[i].x, si[i].x);
+                rope_turn(v[2], v[3], co[i].y, si[i].y);
+            } else {
+                float y[4];
+                unpack4(make_uint2(__shfl_sync(0xffffffffu, w.x, mate), __shfl_sync(0xffffffffu, w.y, mate)), y);
+                const float cc[4] = {co[i].x, co[i].y, co[i].z, co[i].w}, ss[4] = {si[i].x, si[i].y, si[i].z, si[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float a = lower ? v[e] : y[e], b = lower ? y[e] : v[e];
+                    rope_turn(a, b, cc[e], ss[e]);
+                    v[e] = lower ? a : b;
+                }
+            }
+            const uint2 r = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            w = in ? r : w;
+        }
+    }
+}
+
 // One warp writes positions first .. last (of the eight) of an octet of a
 // (page, head) block; rows holds the lane's four dims (packed bf16) of the eight
 // rows, zeros outside first .. last.  Returns whether a group held NaN or

@@ -1194,12 +1194,9 @@ void plan(Work& w, int B, int max_pages, int& grid) {
     grid = static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
     w.cluster = 0;
     int64_t best = (pages + grid - 1) / grid * page_ns(grid) + (grid == 1 ? 6500 : tall ? 17000 : 11500);
-    for (int c = 1; c <= kMaxCluster; ++c) {
-        const int64_t at_once = c == 1 ? sms : resident_clusters(c);   // clusters
-        if (at_once < 1 || (c > 1 && units > at_once)) continue;
-        int64_t cost = 0;
-        for (int64_t left = units; left > 0 && cost < best; left -= at_once)
-            cost += (max_pages + c) / c * page_ns((left < at_once ? left : at_once) * c) + (tall ? 11000 : 6500);
+    for (int c = 1; c <= kMaxCluster; ++c) {   // (one a unit, not a second wave: that never came out ahead)
+        if (units > (c == 1 ? sms : resident_clusters(c))) continue;
+        const int64_t cost = (max_pages + c) / c * page_ns(units * c) + (tall ? 11000 : 6500);
         if (cost >= best) continue;
         best = cost;
         w.cluster = c;

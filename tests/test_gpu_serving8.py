@@ -211,6 +211,22 @@ def test_captured_appends_replay(sv):
     assert sv.get_device_error() == 0
 
 
+def test_nothing_to_do(sv):
+    """No rows to append, none to read back, sequences without new rows: nothing changes."""
+    s = Server(9)
+    keep = [s.kp.clone(), s.vp.clone()]
+    z = torch.zeros(0, H, 128, dtype=torch.bfloat16, device="cuda")
+    sv.kv_append_q8(z, z, i32([0] * (B + 1)), s.kp[0], s.vp[0], s.table, s.length)
+    x = bf(s.r.standard_normal((5, H, 128))).cuda()
+    sv.kv_append_q8(x, x, i32([2] * (B + 1)), s.kp[0], s.vp[0], s.table, s.length)      # rows 2 .. 2 of each
+    k, v = sv.kv_gather_q8(s.kp, s.vp, s.table, s.length, s.length, 0)
+    assert k.shape == v.shape == (1, B, H, 0, 128)
+    k, v = sv.kv_gather_q8(s.kp, s.vp, s.table, s.length, s.length, 20)                 # empty sequences
+    assert not k.any() and not v.any()
+    assert torch.equal(s.kp, keep[0]) and torch.equal(s.vp, keep[1])
+    assert sv.get_device_error() == 0
+
+
 # ---------------------------------------------------------------------------
 # streams, threads, graphs
 # ---------------------------------------------------------------------------
