@@ -11,7 +11,7 @@
 //        is, without loss: a bf16 has 8 significant bits, and the nearest e4m3 to a
 //        value and the e4m3 of what that leaves hold 4 + 4 (the remainder of a
 //        rounding to 4 bits is at most half a step, 8 halves of which are 4 bits).  So
-//        K Q^T is K Q1^T + K Q2^T into one accumulator.  A row of Q is in units of a
+//        K Q^T is K Q1^T + K Q2^T.  A row of Q is in units of a
 //        power of two that takes its largest element to (224, 448], and what is lost
 //        lies below 2^-10 of such a unit: 2^-17.8 of the row's largest element.
 //        Scales of Q's rows and of K's runs, powers of two, multiply the scores.
@@ -40,12 +40,12 @@
 //
 // What bounds it, in us of graph replays over inputs larger than L2 (heads and positions as
 // named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 35.5, for 137 MB, which take
-// 20.1 at copy rate; 64 single tokens of up to 4097: 46.5 (175 MB, 25.7).  CTAs that stream
+// 20.1 at copy rate; 64 single tokens of up to 4097: 43.1 (175 MB, 25.7).  CTAs that stream
 // reach 5.5 to 5.9 TB/s; the rest is the start (the chain length, page table, page, scores, P:
 // 5 to 9) and the end (last sums, O, join: 4).  A step of two pages takes 0.61 of a CTA by itself
-// with tiles of up to 32 rows, 0.75 with more: 128 KB that pass its shared memory at 128 bytes a
-// cycle, K twice as there are two parts of Q.  5 rows x 12 heads over 2, 4096: 10.1, and 100001
-// positions 20.3 (floor 7.5), both latency: few pages a CTA.  A tree of 65 rows: 24.8; eight
+// with tiles of up to 32 rows, 0.75 with more: 112 and 128 KB that pass its shared memory at 128
+// bytes a cycle.  5 rows x 12 heads over 2, 4096: 9.8, and 100001 positions 18.6 (floor 7.5), both
+// latency: few pages a CTA.  A tree of 65 rows: 24.8; eight
 // tiles of rows stream the same pages, 17 steps of 0.75 each behind a start of 9.
 // Tried: P in bf16; an MMA warp for both products, and one copier (a step waits for the
 // other's); 16 softmax warps of 16 rows (tensor memory reads and references double); two
@@ -247,6 +247,12 @@ __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_g
 template <int kRT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, Work wk, float* __restrict__ ws) {
     constexpr int kLive = 2 * kRT;
+    // Q's two parts side by side in N, sixteen rows of one beside those of the other, and the scores
+    // in two columns that are added when they are read: K then passes shared memory once a step
+    // (four products of 63 cycles for eight of 40; 64 single tokens 45.7 -> 43.1 us, 100001 positions 19.3
+    // -> 18.6).  The larger tile has no room for three such S^T in tensor memory, and with two its
+    // steps take as long as with the parts one after the other (16 sequences 35.9 and 35.7 us).
+    constexpr bool kStacked = kRT == 16;
     // (aligned by its declaration: addresses are then constants, not registers)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         } while (again());
     } else if (warp == kQkWarp) {
         // ---------------- S^T = K Q^T ----------------
-        constexpr uint32_t id_s = idesc_e4m3_f32(128, kLive);
+        constexpr uint32_t id_s = idesc_e4m3_f32(128, kStacked ? 2 * kLive : kLive);
         int it = 0, seg = 0;
         Turn sb;
         static_assert(kSBufs == kPBufs, "one turn for both");
@@ -449,10 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                         tc_fence_after();
                         const uint64_t kd = smem_desc_sw128(smem_u32(stage(i)), 16, 1024);
                         // K by either part of Q, and the remainders of a block's K
-                        const int parts = walk.block && st == 0 ? 4 : 2;
+                        const int parts = (walk.block && st == 0 ? 2 : 1) * (kStacked ? 1 : 2);
 #pragma unroll 1
                         for (int p = 0; p < parts; ++p) {
-                            const uint64_t kp = kd + (p >> 1) * (kTileBytes >> 4), qp = qd + (p & 1) * (kQBytes / 2 >> 4);
+                            const uint64_t kp = kd + (kStacked ? p : p >> 1) * (kTileBytes >> 4);
+                            const uint64_t qp = qd + (kStacked ? 0 : p & 1) * (kQBytes / 2 >> 4);
 #pragma unroll
                             for (int kc = 0; kc < kQ8D / 32; ++kc)
                                 tc_mma_e4m3(tS(sb.x), kp + kc * 2, qp + kc * 2, id_s, (p > 0 || kc > 0) ? 1u : 0u);
@@ -575,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                         if (kQRows > 4 && i0 > 0) y = x[kQRows - 4 + i], m = most[kQRows - 4 + i];
                         const bool bad = m >= 0x7f80u;
                         const int e = q8_exponent(__uint_as_float(bad ? 0u : m << 16)), r = hw + 8 * (i0 + i);
-                        split_row(y, bad, e, r, smem + kOffQ + (seg & 1) * kQBytes, kQBytes / 2);
+                        split_row(y, bad, e, kStacked ? 2 * r - (r & 15) : r, smem + kOffQ + (seg & 1) * kQBytes,
+                                  kStacked ? 16 * 128 : kQBytes / 2);
                         if (ch == 0) unit[r] = q8_pow2(e);
                     }
                 }
@@ -832,8 +840,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 // the key's scale: of its run, or of the block's row
                 auto key_scale = [&](int st) { return sc * scales(it)[st < lead ? l : l >> 4]; };
                 auto scores = [&](uint32_t(&s)[kRT]) {
-                    if constexpr (kRT == 32) tmem_ld32_sync(tS(sb.x) + lane_off + hh * kRT, s);
-                    else tmem_ld16_sync(tS(sb.x) + lane_off + hh * kRT, s);
+                    if constexpr (!kStacked) {
+                        tmem_ld32_sync(tS(sb.x) + lane_off + hh * kRT, s);
+                    } else {
+                        uint32_t z[32];
+                        tmem_ld32_sync(tS(sb.x) + lane_off + hh * 32, z);
+#pragma unroll
+                        for (int i = 0; i < kRT / 2; ++i) {
+                            const float2 y = __fadd2_rn(make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1])),
+                                                        make_float2(__uint_as_float(z[16 + 2 * i]), __uint_as_float(z[17 + 2 * i])));
+                            s[2 * i] = __float_as_uint(y.x), s[2 * i + 1] = __float_as_uint(y.y);
+                        }
+                    }
+                };
+                auto scores8 = [&](int c0, uint32_t(&s)[8]) {
+                    tmem_ld8_sync(tS(sb.x) + lane_off + hh * 32 + c0, s);
+                    if constexpr (kStacked) {
+                        uint32_t z[8];
+                        tmem_ld8_sync(tS(sb.x) + lane_off + hh * 32 + 16 + c0, z);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s[i] = __float_as_uint(__fadd_rn(__uint_as_float(s[i]), __uint_as_float(z[i])));
+                    }
                 };
                 auto s_wait = [&]() {
                     wait(&s_full[sb.x], sb.parity);
@@ -851,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
 #pragma unroll (kRT == 16 ? 2 : 1)
                         for (int c0 = 0; c0 < kRT; c0 += 8) {
                             uint32_t s[8];
-                            tmem_ld8_sync(tS(sb.x) + lane_off + hh * kRT + c0, s);
+                            scores8(c0, s);
                             const float4* un = reinterpret_cast<const float4*>(unit_s + hh * kRT + c0);
                             const float4 ua = un[0], ub = un[1];
                             const float u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
@@ -956,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                         for (int i = 0; i < 4; ++i) now[i] = sums[i];
                         if (!none) {
                             uint32_t s[8];
-                            tmem_ld8_sync(tS(sb.x) + lane_off + hh * kRT + c0, s);
+                            scores8(c0, s);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 // (one by one: the packed product and sum would be fused)
@@ -1099,17 +1126,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
 
 // Joins the partial rows of the units that lie in several CTAs' runs: kWide warps a row.
 // (One sequence of 100001 positions, whose two units lie in 77 runs each: 8 us less with
-// 8 warps a row than with one.)
+// 8 warps a row than with one.)  Which CTAs had a unit follows from the lengths, which the
+// attention does not write and was past its own wait for: they are read before the wait here
+// (the same 20.3 -> 19.5 us, 64 single tokens 46.4 -> 45.6).
 template <int kWide>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_q8_kernel(CacheAttnArgs a, Work wk, const float* __restrict__ ws, int grid) {
     __shared__ float2 ml_s[kWide];
     __shared__ float4 o_s[kWide][32];
-    pdl_wait();
-    pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gr = blockIdx.x * (kCombineThreads / 32 / kWide) + warp / kWide, part = warp % kWide;
-    if (gr >= a.R * a.G) return;   // (a whole CTA where a row has one)
     const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
     const int rt = gr / wk.tile_rows, r = gr % wk.tile_rows;
     const int2 sums = work_sums(a, b);
@@ -1118,6 +1144,9 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int w0 = sums.y * wk.U + (g * wk.row_tiles + rt) * (np + 1), w1 = w0 + np + 1;
     const int i0 = cta_of(W, w0, n), i1 = cta_of(W, w1 - 1, n);
     const bool later = static_cast<int64_t>(w0) * n > static_cast<int64_t>(W) * i0;   // w0 is past CTA i0's first page
+    pdl_wait();
+    pdl_launch_dependents();
+    if (gr >= a.R * a.G) return;   // (a whole CTA where a row has one)
     if (i0 == i1) return;   // one CTA had the whole unit and wrote its rows
     auto get = [&](int k, float2& ml, float4& o) {
         // a unit that starts inside CTA i0's run is its second partial
