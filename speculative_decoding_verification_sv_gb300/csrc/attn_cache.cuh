@@ -24,6 +24,7 @@ struct Work {
     int row_tiles;
     int tile_rows; // rows of a tile but the last
     int cluster;   // CTAs of a unit where each unit has a cluster, 0 where the pages are split evenly
+    int even;      // where more CTAs than this share the pages, a multiple of it do
     int inv_g;     // ceil(2^16 / G): r * inv_g >> 16 is r / G for every row r < 2048 of G <= 16
 };
 
@@ -52,7 +53,10 @@ __device__ __forceinline__ int2 work_sums(const CacheAttnArgs& a, int before) {
 }
 
 // CTAs that share W pages, and the first page of CTA i among them.
-__device__ __forceinline__ int active_ctas(int W, int grid) { return max(1, min(grid, W / kGrain)); }
+__device__ __forceinline__ int active_ctas(const Work& w, int W, int grid) {
+    const int n = max(1, min(grid, W / kGrain));
+    return n > w.even ? n - n % w.even : n;
+}
 // (n <= 2^15: products of remainders stay in 32 bits)
 __device__ __forceinline__ int cta_first(int W, int i, int n) {
     const uint32_t q = static_cast<uint32_t>(W) / static_cast<uint32_t>(n), r = static_cast<uint32_t>(W) - q * n;
@@ -83,7 +87,7 @@ struct Walk {
         int W = w0;
         for (int i = 32 + lane; i < a.B; i += 32) W += (ctx_pages(ctx_len(a, i)) + 1) * w.U;
         W = __reduce_add_sync(0xffffffffu, W);
-        const int n = active_ctas(W, grid);
+        const int n = active_ctas(w, W, grid);
         pos = end = 0;
         b = -1;
         if (cta >= n) return;
@@ -270,6 +274,7 @@ inline Work work_of(int R, int G, int Hkv) {
     w.row_tiles = (rows + kRows - 1) / kRows;
     w.tile_rows = (rows + w.row_tiles - 1) / w.row_tiles;
     w.U = Hkv * w.row_tiles;
+    w.even = 1;
     w.inv_g = (65536 + G - 1) / G;
     return w;
 }

@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
     const int rt = gr / wk.tile_rows, r = gr % wk.tile_rows;
     const int2 sums = work_sums(a, b);
-    const int W = sums.x * wk.U, n = active_ctas(W, grid);
+    const int W = sums.x * wk.U, n = active_ctas(wk, W, grid);
     const int np = ctx_pages(ctx_len(a, b));
     const int w0 = sums.y * wk.U + (g * wk.row_tiles + rt) * (np + 1), w1 = w0 + np + 1;
     const int i0 = cta_of(W, w0, n), i1 = cta_of(W, w1 - 1, n);

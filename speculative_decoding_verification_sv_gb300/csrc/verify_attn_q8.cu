@@ -1139,7 +1139,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
     const int rt = gr / wk.tile_rows, r = gr % wk.tile_rows;
     const int2 sums = work_sums(a, b);
-    const int W = sums.x * wk.U, n = active_ctas(W, grid);
+    const int W = sums.x * wk.U, n = active_ctas(wk, W, grid);
     const int np = ctx_pages(ctx_len(a, b));
     const int w0 = sums.y * wk.U + (g * wk.row_tiles + rt) * (np + 1), w1 = w0 + np + 1;
     const int i0 = cta_of(W, w0, n), i1 = cta_of(W, w1 - 1, n);
@@ -1208,12 +1208,15 @@ int resident_clusters(int c) {
 // take less time.  A page takes 0.30 us of a CTA, or 2.8 ns for each CTA that reads at the
 // same time where that is more (HBM); a CTA's start and end and a cluster's join 6.5 us, 11
 // with tiles of more than 32 rows; of the even split, which has CTAs with two units and the
-// second kernel, 11.5 and 17.  Measured in us, clusters as the rule takes them against the
-// even split: 5 x 12 heads over 2 of 4096 positions 10.1 and 10.6, of 16384 (the rule splits)
-// 17.2 and 12.6; 9 x 28 over 4, 4096: 13.3 and 19.0, 16384 (splits): 21.3 and 16.9; four such
-// of 8192: 20.3 and 27.2; 16 of 8192: 35.6 and 41.4; 65 x 28 over 4, 8192: 24.7 and 31.0; 32
-// single tokens of 2048: 20.1 and 24.9; 64 of 4096 (splits): 60.2 and 55.7.  The table's
-// capacity decides, as the lengths are on the device.
+// second kernel, 11.5 and 17.  A single sequence's units are alike, and a multiple of their
+// number of CTAs splits them without a CTA that has two: 9 and 13.5 (9 x 28 over 4, 4096
+// positions: 18.2 -> 14.4).  Measured in us, clusters against the even split, the side that
+// the rule takes first: 5 x 12 heads over 2 of 4096 positions, clusters 9.9, split 10.0; of 8192,
+// split 10.4, clusters 11.8; of 16384, split 11.9, clusters 15.7; 9 x 28 over 4, 4096: clusters
+// 13.2, split 14.4; 8192: split 15.3, clusters 15.8; four such of 8192: clusters 20.0, split
+// 27.2; 16 of 8192: clusters 35.4, split 41.4; 65 x 28 over 4, 8192: clusters 24.5, split 26.6;
+// 32 single tokens of 2048: clusters 19.2, split 23.1; 1 of 8192: split 11.9, clusters 11.4.  The
+// table's capacity decides, as the lengths are on the device.
 void plan(Work& w, int B, int max_pages, int& grid) {
     const int64_t units = static_cast<int64_t>(B) * w.U, pages = units * (static_cast<int64_t>(max_pages) + 1);
     const int64_t sms = device_sm_count();
@@ -1222,7 +1225,10 @@ void plan(Work& w, int B, int max_pages, int& grid) {
     const int64_t most = pages / kGrain;
     grid = static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
     w.cluster = 0;
-    int64_t best = (pages + grid - 1) / grid * page_ns(grid) + (grid == 1 ? 6500 : tall ? 17000 : 11500);
+    w.even = B == 1 ? w.U : 1;
+    if (grid > w.even) grid -= grid % w.even;
+    const int ends = B == 1 ? (tall ? 13500 : 9000) : (tall ? 17000 : 11500);
+    int64_t best = (pages + grid - 1) / grid * page_ns(grid) + (grid == 1 ? 6500 : ends);
     for (int c = 1; c <= kMaxCluster; ++c) {   // (one a unit, not a second wave: that never came out ahead)
         if (units > (c == 1 ? sms : resident_clusters(c))) continue;
         const int64_t cost = (max_pages + c) / c * page_ns(units * c) + (tall ? 11000 : 6500);
