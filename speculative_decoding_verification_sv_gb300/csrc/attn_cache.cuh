@@ -219,30 +219,32 @@ struct RowSum {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 };
 
-// Adds n partials of a row, eight in flight; get(i, ml, o) loads the i-th's (m, l) and the
-// lane's four dims of its O: sums of P V, or, with kMeans, those over l.
-template <bool kMeans, typename Get>
-__device__ __forceinline__ RowSum add_partials(int n, Get&& get) {
-    auto power = [](float x) { return kMeans ? fast_exp2(x) : exp2f(x); };
-    RowSum r;
-#pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += 8) {
-        float2 ml[8];
-        float4 o[8];
+// Up to kN partials of a row: get(i, ml, o) loads the i-th's (m, l) and the lane's four
+// dims of its O: sums of P V, or, with kMeans, those over l.
+template <int kN>
+struct PartialRows {
+    float2 ml[kN];
+    float4 o[kN];
+    template <typename Get>
+    __device__ __forceinline__ void load(int n, Get&& get) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kN; ++u) {
             ml[u] = make_float2(-INFINITY, 0.f);
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c0 + u < n) get(c0 + u, ml[u], o[u]);
+            if (u < n) get(u, ml[u], o[u]);
         }
+    }
+    template <bool kMeans>
+    __device__ __forceinline__ void add_to(RowSum& r) const {
+        auto power = [](float x) { return kMeans ? fast_exp2(x) : exp2f(x); };
         float mn = r.m;
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < kN; ++u)
             if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
         const float c = r.m == -INFINITY ? 0.f : power(r.m - mn);
         r.o.x *= c, r.o.y *= c, r.o.z *= c, r.o.w *= c, r.l *= c;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kN; ++u) {
             if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
             float w = power(ml[u].x - mn);
             r.l += w * ml[u].y;
@@ -253,6 +255,18 @@ __device__ __forceinline__ RowSum add_partials(int n, Get&& get) {
             r.o.w += w * o[u].w;
         }
         r.m = mn;
+    }
+};
+
+// Adds n partials of a row, eight in flight.
+template <bool kMeans, typename Get>
+__device__ __forceinline__ RowSum add_partials(int n, Get&& get) {
+    RowSum r;
+#pragma unroll 1
+    for (int c0 = 0; c0 < n; c0 += 8) {
+        PartialRows<8> p;
+        p.load(n - c0, [&](int u, float2& ml, float4& o) { get(c0 + u, ml, o); });
+        p.template add_to<kMeans>(r);
     }
     return r;
 }
