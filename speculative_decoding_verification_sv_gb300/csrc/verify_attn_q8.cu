@@ -1219,35 +1219,42 @@ int resident_clusters(int c) {
 
 // How the work is split: a cluster of up to 8 CTAs for each unit, joined on chip, or all
 // pages evenly over the SMs and partials joined by a second kernel, whichever is expected to
-// take less time.  A page takes 0.30 us of a CTA, or 2.8 ns for each CTA that reads at the
-// same time where that is more (HBM); a CTA's start and end and a cluster's join 6.5 us, 11
-// with tiles of more than 32 rows; of the even split, which has CTAs with two units and the
-// second kernel, 11.5 and 17.  A single sequence's units are alike, and a multiple of their
-// number of CTAs splits them without a CTA that has two: 9 and 13.5 (9 x 28 over 4, 4096
-// positions: 18.2 -> 14.4).  Measured in us, clusters against the even split, the side that
-// the rule takes first: 5 x 12 heads over 2 of 4096 positions, clusters 9.9, split 10.0; of 8192,
-// split 10.4, clusters 11.8; of 16384, split 11.9, clusters 15.7; 9 x 28 over 4, 4096: clusters
-// 13.2, split 14.4; 8192: split 15.3, clusters 15.8; four such of 8192: clusters 20.0, split
-// 27.2; 16 of 8192: clusters 35.4, split 41.4; 65 x 28 over 4, 8192: clusters 24.5, split 26.6;
-// 32 single tokens of 2048: clusters 19.2, split 23.1; 1 of 8192: split 11.9, clusters 11.4.  The
+// take less time.  The terms, in ns, were fitted to some sixty shapes:
+//   - a page takes a CTA 300, or, where CTAs that read at the same time fill HBM, 2.8 for each
+//     of them; 2.3 and 2.55 where they are out of step (units in several waves, the even split);
+//   - a CTA's start and end and a cluster's join take 6500, 11000 with tiles of more than 32 rows;
+//   - the even split's, with the second kernel, 11500 and 17000, and a CTA that goes on to
+//     another unit 5500 and 10000 more, beside steps of 250 and 375 a page.  A single sequence's
+//     units are alike, and a multiple of their number of CTAs splits them without such CTAs:
+//     9000 and 13500 (9 x 28 heads over 4, 4096 positions: 18.2 -> 14.4 us).
+// Measured in us, the side that the rule takes first: 5 x 12 heads over 2 of 4096 positions,
+// clusters 9.9, split 10.0; of 8192, split 10.4, clusters 11.8; of 16384, split 11.9, clusters
+// 15.7; 9 x 28 over 4, 8192: split 15.3, clusters 15.8; four such: clusters 20.2, split 21.9;
+// 16: clusters of two 34.6, split 41.3; 64 of 4096: one CTA a unit 63.6, split 71.9; 40: split 50.5,
+// one a unit 60.4; 65 x 28 over 4, 8192: clusters 24.4, split 26.4; 32 single tokens of 2048: one
+// a unit 17.8, split 22.8; 64 of 256: 16.9 and 22.6; 64 of 4096: split 52.8, one a unit 54.2.  The
 // table's capacity decides, as the lengths are on the device.
 void plan(Work& w, int B, int max_pages, int& grid) {
     const int64_t units = static_cast<int64_t>(B) * w.U, pages = units * (static_cast<int64_t>(max_pages) + 1);
     const int64_t sms = device_sm_count();
     const bool tall = w.tile_rows > 32;
-    auto page_ns = [](int64_t ctas) { return ctas * 28 > 3000 ? ctas * 28 / 10 : int64_t(300); };
+    auto page_ns = [](int64_t ctas, int64_t ps) { return ctas * ps > 300000 ? ctas * ps / 1000 : int64_t(300); };
     const int64_t most = pages / kGrain;
     grid = static_cast<int>(most < 1 ? 1 : most < sms ? most : sms);
     w.cluster = 0;
     w.even = B == 1 ? w.U : 1;
     if (grid > w.even) grid -= grid % w.even;
-    const int ends = B == 1 ? (tall ? 13500 : 9000) : (tall ? 17000 : 11500);
-    int64_t best = (pages + grid - 1) / grid * page_ns(grid) + (grid == 1 ? 6500 : ends);
-    for (int c = 1; c <= kMaxCluster; ++c) {   // (one a unit, not a second wave: that never came out ahead)
-        if (units > (c == 1 ? sms : resident_clusters(c))) continue;
-        const int64_t cost = (max_pages + c) / c * page_ns(units * c) + (tall ? 11000 : 6500);
-        if (cost >= best) continue;
-        best = cost;
+    const int64_t each = (pages + grid - 1) / grid, stream = each * page_ns(grid, 2550);
+    const int64_t steps = each * (tall ? 375 : 250) + (B == 1 ? 0 : units * (tall ? 10000 : 5500) / grid);
+    int64_t best = (stream > steps ? stream : steps) + (B == 1 ? (tall ? 13500 : 9000) : (tall ? 17000 : 11500));
+    auto cost = [&](int64_t n, int c, int64_t ps) { return (max_pages + c) / c * page_ns(n * c, ps) + (tall ? 11000 : 6500); };
+    for (int c = 1; c <= kMaxCluster; ++c) {
+        int64_t t;
+        if (units <= (c == 1 ? sms : resident_clusters(c))) t = cost(units, c, 2800);
+        else if (c == 1) t = units / sms * cost(sms, 1, 2300) + (units % sms ? cost(units % sms, 1, 2300) : 0);
+        else continue;
+        if (t >= best) continue;
+        best = t;
         w.cluster = c;
     }
     if (w.cluster) grid = static_cast<int>(units) * w.cluster;

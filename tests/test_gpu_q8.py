@@ -372,7 +372,8 @@ def test_attn_split_over_all_sms(sv, B, R, Hq, H, lens, is_tree, mp):
 def test_attn_every_cluster_size(sv, t):
     """Page tables whose capacity gives units clusters of 1 to 8 CTAs (and none), which
     the lengths fill, hardly reach or leave empty."""
-    for B, R, Hq, H in ((1, 5, 12, 2), (4, 2, 28, 4), (3, 9, 28, 4), (6, 9, 28, 4), (9, 9, 28, 4), (14, 9, 28, 4), (20, 3, 12, 4), (40, 1, 28, 4)):
+    for B, R, Hq, H in ((1, 5, 12, 2), (4, 2, 28, 4), (3, 9, 28, 4), (6, 9, 28, 4), (9, 9, 28, 4), (14, 9, 28, 4), (20, 3, 12, 4), (40, 1, 28, 4),
+                        (40, 9, 28, 4), (90, 2, 12, 4)):
         q, (kp, vp), table, kb, vb = _device_inputs(B, R, Hq, H, 4096, seed=B)
         lens = i32([max(0, t - 17 * b) for b in range(B)])
         out = sv.verify_attn_q8(q, kp, vp, table, lens, kb, vb)

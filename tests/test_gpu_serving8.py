@@ -463,12 +463,12 @@ def test_every_tensor_is_checked(sv, name):
 
 
 def test_other_refusals_of_the_binding(sv):
-    b = 100      # more units than clusters: the partials need scratch
-    need = sv.verify_attn_q8_workspace(b, R, HQ, H, 128, 64)
+    mp = 300     # long enough that the pages are split over all SMs: the partials need scratch
+    need = sv.verify_attn_q8_workspace(1, R, HQ, H, 128, mp * 64)
     assert need > 0
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     pool = torch.zeros(9, H, sv.KV_Q8_BYTES, dtype=torch.uint8, device="cuda")
-    a = (z(b, R, HQ, 128), pool, pool.clone(), i32([[0]] * b), i32([0] * b), z(b, H, R, 128), z(b, H, R, 128))
+    a = (z(1, R, HQ, 128), pool, pool.clone(), i32([[0] * mp]), i32([0]), z(1, H, R, 128), z(1, H, R, 128))
     with pytest.raises(ValueError):
         sv.verify_attn_q8(*a, ws=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
