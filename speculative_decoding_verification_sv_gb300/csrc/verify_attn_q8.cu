@@ -242,6 +242,11 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+template <int kN>
+struct Rows {
+    uint4 v[kN];
+};
+
 // kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (what their
 // columns of P and O hold is not looked at)
 template <int kRT, bool kCluster>
@@ -362,6 +367,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         if (*fail_s == 0) return false;
         walk.load(a, fail_s + 1);
         return true;
+    };
+
+    // The rows of Q of a run, by half-warps: rows hw, hw + 64 / kN .. of the tile (of its kLive).
+    auto load_q = [&](auto& x, const Walk& of, int hw) {
+        constexpr int kN = sizeof(x.v) / 16;
+        const int g = of.cur_unit / wk.row_tiles, row0 = of.cur_unit % wk.row_tiles * wk.tile_rows;
+        const int nrows = min(wk.tile_rows, a.R * a.G - row0);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int r = hw + kLive / kN * i, gr = row0 + r, j = gr * wk.inv_g >> 16;
+            x.v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < nrows)
+                x.v[i] = __ldg(reinterpret_cast<const uint4*>(
+                                   a.q + (static_cast<size_t>(of.cur_b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ8D) +
+                               (lane & 15));
+        }
+    };
+    auto split_q = [&](const auto& x, int seg, int hw) {
+        constexpr int kN = sizeof(x.v) / 16, kAtOnce = kN < 4 ? kN : 4;   // (side by side: a row is a chain of some 300 cycles)
+        float* unit = reinterpret_cast<float*>(smem + kOffUnit) + (seg & 1) * kRows;
+        uint32_t most[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) most[i] = row_most(x.v[i]);
+#pragma unroll 1
+        for (int i0 = 0; i0 < kN; i0 += kAtOnce) {
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                uint4 y = x.v[i];
+                uint32_t m = most[i];
+                if (kN > kAtOnce && i0 > 0) y = x.v[kN - kAtOnce + i], m = most[kN - kAtOnce + i];
+                const bool bad = m >= 0x7f80u;
+                const int e = q8_exponent(__uint_as_float(bad ? 0u : m << 16)), r = hw + kLive / kN * (i0 + i);
+                split_row(y, bad, e, kStacked ? 2 * r - (r & 15) : r, smem + kOffQ + (seg & 1) * kQBytes,
+                          kStacked ? 16 * 128 : kQBytes / 2);
+                if ((lane & 15) == 0) unit[r] = q8_pow2(e);
+            }
+        }
     };
 
     // Every step, of the context or a block, has a ring stage: step `it` stage it %
@@ -519,7 +561,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     } else if (warp >= kConvWarp) {
         // ---------------- to e4m3 pairs and to f16 ----------------
         if (early) pdl_wait();
-        constexpr int kQRows = kLive / 8;    // query rows of a half-warp: hw, hw + 8, ..
         const int cw = warp - kConvWarp, hw = 2 * cw + (lane >> 4), ch = lane & 15;
         const int l = q4 * 32 + lane;        // V: the TMEM lane, a dim
         int it = 0, seg = 0;
@@ -549,47 +590,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         };
         do {
             while (walk.next(a, wk)) {
-                const int g = walk.cur_unit / wk.row_tiles, row0 = walk.cur_unit % wk.row_tiles * wk.tile_rows;
-                const int nrows = min(wk.tile_rows, a.R * a.G - row0);
+                const int g = walk.cur_unit / wk.row_tiles;
                 const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R * kQ8D;
-                // half-warps take the query rows, then the block's rows of K
+                // half-warps take the query rows, and the block's rows of K
                 auto k_row = [&](int r) {
                     return walk.block && r < a.R ? __ldg(reinterpret_cast<const uint4*>(a.k_blk + blk0 + r * kQ8D) + ch)
                                                  : make_uint4(0u, 0u, 0u, 0u);
                 };
-                uint4 x[kQRows];
-#pragma unroll
-                for (int i = 0; i < kQRows; ++i) {
-                    const int r = hw + 8 * i, gr = row0 + r, j = gr * wk.inv_g >> 16;
-                    x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < nrows)
-                        x[i] = __ldg(reinterpret_cast<const uint4*>(
-                                         a.q + (static_cast<size_t>(walk.cur_b * a.R + j) * a.Hq + g * a.G + gr - j * a.G) * kQ8D) + ch);
-                }
                 uint4 ahead[2] = {k_row(hw), k_row(hw + 8)};
-                uint32_t most[kQRows];
-#pragma unroll
-                for (int i = 0; i < kQRows; ++i) most[i] = row_most(x[i]);
-                wait(&q_free[seg & 1], ((seg >> 1) & 1) ^ 1);
-                float* unit = reinterpret_cast<float*>(smem + kOffUnit) + (seg & 1) * kRows;
                 const int s = it % kStages;
-#pragma unroll 1
-                for (int i0 = 0; i0 < kQRows; i0 += 4) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // (side by side: a row is a chain of some 300 cycles)
-                        uint4 y = x[i];
-                        uint32_t m = most[i];
-                        if (kQRows > 4 && i0 > 0) y = x[kQRows - 4 + i], m = most[kQRows - 4 + i];
-                        const bool bad = m >= 0x7f80u;
-                        const int e = q8_exponent(__uint_as_float(bad ? 0u : m << 16)), r = hw + 8 * (i0 + i);
-                        split_row(y, bad, e, kStacked ? 2 * r - (r & 15) : r, smem + kOffQ + (seg & 1) * kQBytes,
-                                  kStacked ? 16 * 128 : kQBytes / 2);
-                        if (ch == 0) unit[r] = q8_pow2(e);
-                    }
+                // (a cluster's first run, mostly its only one, leaves them to the softmax warps, who have nothing
+                // else to do yet: 16 sequences 34.6 -> 34.0 us, a tree 24.8 -> 24.0, batch 1 10.0 -> 9.7.  Where
+                // more runs follow, this code is better run, and fetched, before memory is busy: 64 single
+                // tokens 43.4 us, 57 with the softmax warps' help)
+                if (!kCluster || seg > 0) {
+                    Rows<kLive / 8> rows;
+                    load_q(rows, walk, hw);
+                    wait(&q_free[seg & 1], ((seg >> 1) & 1) ^ 1);
+                    split_q(rows, seg, hw);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_ready[seg & 1]);
                 if (walk.block) {   // the block's K, into the stage that is kept for it
                     wait(&ring_go[s], gone >> s & 1u);
                     gone ^= 1u << s;
@@ -771,6 +793,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 const bool kept = second && run < kKept && (unsure >> run & 1u) == 0u, safe = second && !kept;
                 const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
                 const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
+                const bool first = kCluster && seg == 0;
+                Rows<kLive / 16> qrows;
+                if (first) load_q(qrows, walk, 2 * warp + (lane >> 4));
                 // (a partial of the run before may still be on its way out of P's place)
                 if (tid == 0) bulk_wait_read();
                 if (tid < kRows) {
@@ -780,7 +805,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 }
                 const bool tree = walk.block && a.parent != nullptr;
                 if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
+                if (first) {
+                    split_q(qrows, 0, 2 * warp + (lane >> 4));
+                    fence_proxy_async_smem();
+                }
                 soft_sync();   // row_s, nm_s, par_s
+                if (first && warp < kConvWarps && lane == 0) mbar_arrive(&q_ready[0]);
                 if (tree) {
                     if (tid < a.R) {
                         uint64_t m0 = 0, m1 = 0;
