@@ -30,8 +30,8 @@
 // added to the rows that see it at the end.
 // A row's maximum runs across lanes here, so it is formed once, over the first 32 keys
 // of the run (of the block, where the run has it: the row's own key and those next to
-// it), and is the row's reference m for the whole run.  P is 2^-4 at the reference: a
-// score 20 powers of two above it makes P infinite, and a P below 2^-25, a weight 2^-21
+// it), and is the row's reference m for the whole run.  P is 2^-5 at the reference: a
+// score 21 powers of two above it makes P infinite, and a P below 2^-25, a weight 2^-20
 // of the reference's, is lost.  A run whose O is not finite, or where a row's sum is so
 // small that what was lost could matter (kLost), is done again with references that the
 // sums give, P then summing to 2^15; one whose sums say nothing (the reference was a key that
@@ -83,10 +83,15 @@ constexpr int kMaxR = 128;
 constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kTmaWarp = 12, kQkWarp = 14, kPvWarp = 15,
               kThreads = 32 * 16;
 constexpr int kVUp = 4;                   // V is in units of 2^kVUp of its first scales
-constexpr float kUp = -4.0f;              // P is 2^kUp at the reference;
+constexpr float kUp = -5.0f;              // P is 2^kUp at the reference;
 constexpr float kUpSum = 15.0f;           // where the sums gave the reference, they are 2^kUpSum
-constexpr float kLost = 0x1p-15f;         // times the keys: the sum of a row's P, at least, for what is below
-                                          // 2^-25 to be less than 2^-10 of it
+// A row's P sum to kLost times the keys or the run is done again: roundings below f16's smallest
+// steps, 2^-25 at most for each key, then move the row by at most 2^-8 of the mean |V| if all of
+// them went one way, and by that over the root of the keys as they do.  (A row that sees one of
+// 4096 keys alone, by the reference, sums to 2^-5, which is kLost times those.  Single tokens
+// have one key of the block for a reference: 64 of them x 28 heads, whose K had a few dims six
+// times the others, had one done again, 62 us for 44, in every eighth call with kUp = -4.)
+constexpr float kLost = 0x1p-17f;
 constexpr float kLeastSum = 0x1p-100f;    // sums from here on give a reference
 constexpr int kKept = 4;                  // runs of a CTA whose references are kept for that
 constexpr int kRecFloats = kRows * (kQ8D + 2);   // a partial: O [64][128], then (m, l) [64]

@@ -253,15 +253,15 @@ def tol(want, wgt, big, units, keys, lost):
 
 
 def lost_of(scale, v_ctx, vb, G):
-    """[Hq, 128]: f16's steps end at 2^-24.  A P is 2^3 at a key that the row sees, so that the
-    sum of P is 2^3 or more: rounding it there moves a weight by at most 2^-25 / 2^3, and
-    the result by the sum of those and |v|.  V there is in units of the largest scale of
-    the pages and the block: a value moves by at most 2^-25 of that."""
+    """[Hq, 128]: f16's steps end at 2^-24.  A P is 2^-5 at a key that the row sees, so that the
+    sum of P is 2^-5 or more: rounding it there moves a weight by at most 2^-25 / 2^-5, and
+    the result by the sum of those and |v|.  V there is in units of 2^4 times the largest scale
+    of the first pages: a value moves by at most 2^-25 of that, 2^-21 of the largest scale."""
     h = []
     for k in range(vb.shape[0]):
         v = np.concatenate([v_ctx[k], np.where(np.isfinite(vb[k]), vb[k], 0.0)])
         unit = max(scale, 2.0 ** ref8.exponent(np.abs(v).max()))
-        h += [2.0 ** -21 * np.abs(v).sum(0) + 2.0 ** -25 * unit] * G
+        h += [2.0 ** -20 * np.abs(v).sum(0) + 2.0 ** -21 * unit] * G
     return np.stack(h)
 
 
