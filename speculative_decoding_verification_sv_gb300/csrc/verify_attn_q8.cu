@@ -39,17 +39,22 @@
 // every step.
 //
 // What bounds it, in us of graph replays over inputs larger than L2 (heads and positions as
-// named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 35.5, for 137 MB, which take
-// 20.1 at copy rate; 64 single tokens of up to 4097: 43.1 (175 MB, 25.7).  CTAs that stream
-// reach 5.5 to 5.9 TB/s; the rest is the start (the chain length, page table, page, scores, P:
-// 5 to 9) and the end (last sums, O, join: 4).  A step of two pages takes 0.61 of a CTA by itself
-// with tiles of up to 32 rows, 0.75 with more: 112 and 128 KB that pass its shared memory at 128
-// bytes a cycle.  5 rows x 12 heads over 2, 4096: 9.8, and 100001 positions 18.6 (floor 7.5), both
-// latency: few pages a CTA.  A tree of 65 rows: 24.8; eight
-// tiles of rows stream the same pages, 17 steps of 0.75 each behind a start of 9.
+// named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 34.0, for 137 MB, which take
+// 20.1 at copy rate; 64 single tokens of up to 4097: 43.4 (175 MB, 25.7).  CTAs that stream reach
+// 5.5 to 5.9 TB/s; the rest is the start and the end of a run, chains of steps that each run
+// once, most of whose instructions come from L2 then: from the launch to the end of the
+// block's step 13,000 cycles with tiles of more than 32 rows (Q's rows made e4m3 2000, the
+// block's K 2300, its scores 1500, references 2500, P 2400: the last three take half of that
+// once their code is there), 7000 with others; the sums, O and their join 4000.  A CTA that goes on
+// to another unit pays 6000 of these again.  A step of two pages takes 1100 and 1300 cycles:
+// 112 and 128 KB pass shared memory at 128 bytes a cycle.  5 rows x 12 heads over 2, 4096: 9.7, and
+// 100001 positions 19.0 (floor 7.5), both latency: few pages a CTA.  A tree of 65 rows: 24.1; eight
+// tiles of rows a head stream the same pages, 17 steps each.
 // Tried: P in bf16; an MMA warp for both products, and one copier (a step waits for the
 // other's); 16 softmax warps of 16 rows (tensor memory reads and references double); two
-// groups of softmax warps in turn (16 sequences 42 -> 51.8: spills).
+// groups of softmax warps in turn (16 sequences 42 -> 51.8: spills); the block as a run's second
+// step, so that references are of 32 keys of the cache (64 single tokens 43.4 -> 49.3: the first
+// pages come late); the next 32 pages' table and scales fetched ahead (43.4 -> 45.4).
 //
 // Work: units and runs as in attn_cache.cuh.  A unit that lies in several CTAs' runs
 // leaves partials in the workspace -- at most two a CTA -- and a second small kernel
