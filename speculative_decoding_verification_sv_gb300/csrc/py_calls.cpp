@@ -204,7 +204,7 @@ PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
         void* vc = a.get(o[5], "v_pool", at::kByte, {P, H, q->block});
         enqueue(q->append_name, [&] {
             return q->append(kp, vp, ks, vs, n32, off, b32, h32, rp, pos32, r32, kc, vc, p32, tab, m32, len, flags,
-                                   a.stream());
+                             a.stream());
         });
     } else {
         uint16_t* kc = a.bf16(o[4], "k_pool", {P, H, SV_KV_PAGE, D});
@@ -239,7 +239,7 @@ PyObject* kv_commit(PyObject*, PyObject* const* o, Py_ssize_t n) {
     int32_t* len = a.as<int32_t>(o[7], "length", at::kInt, {B});
     enqueue(q.commit_name, [&] {
         return q.commit(kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), kb, vb, size32(L, "L"),
-                               size32(B, "B"), size32(H, "Hkv"), size32(R, "R"), path, acc, len, a.stream());
+                        size32(B, "B"), size32(H, "Hkv"), size32(R, "R"), path, acc, len, a.stream());
     });
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
@@ -303,8 +303,8 @@ PyObject* kv_gather(PyObject*, PyObject* const* o, Py_ssize_t n) {
     }
     enqueue(q.gather_name, [&] {
         return q.gather(kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), size32(L, "L"),
-                               size32(B, "B"), size32(H, "Hkv"), start, len, n32, static_cast<uint16_t*>(k.ptr),
-                               static_cast<uint16_t*>(v.ptr), a.stream());
+                        size32(B, "B"), size32(H, "Hkv"), start, len, n32, static_cast<uint16_t*>(k.ptr),
+                        static_cast<uint16_t*>(v.ptr), a.stream());
     });
     return PyTuple_Pack(2, k.ref.get(), v.ref.get());
     END_HANDLE_TH_ERRORS
@@ -348,8 +348,8 @@ PyObject* verify_attn(PyObject*, PyObject* const* o, Py_ssize_t n) {
     Output out = output(a, o[9], "out", at::kBFloat16, {B, R, Hq, D});
     enqueue(cc.attn_name, [&] {
         return cc.attn(&shape, qp, kp, vp, size32(P, "num_pages"), tab, size32(max_pages, "max_pages"), len, kb, vb,
-                                 par, scale, static_cast<uint16_t*>(out.ptr), ws.defined() ? ws.data_ptr() : nullptr, bytes,
-                                 flags, a.stream());
+                       par, scale, static_cast<uint16_t*>(out.ptr), ws.defined() ? ws.data_ptr() : nullptr, bytes,
+                       flags, a.stream());
     });
     return out.ref.release();
     END_HANDLE_TH_ERRORS
