@@ -708,6 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                             const int left = have - 8 * o;
                             *w = left <= 0 ? 0ull : *w & ((1ull << 8 * left) - 1ull);
                         }
+                        // (the next copy into the stage comes by the other proxy: these stores before it)
+                        fence_proxy_async_smem();
                     }
                     const float2* f2 = reinterpret_cast<const float2*>(scales(it) + 8);
                     v_free();

@@ -1,0 +1,59 @@
+"""The attention over the 8-bit cache at the ends of what its numbers hold: values and
+scores far apart, runs that are done again, and what memory order such runs rely on."""
+import numpy as np
+import pytest
+import torch
+
+import _serving_ref8 as ref8
+from test_gpu_q8 import dev, i32, sv  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def pools_of(k, v, P, table, lens):
+    """8-bit pools that hold rows k, v [B][H, len, 128] (float64), NaN behind them."""
+    H = k[0].shape[0]
+    out = []
+    for rows, is_v in ((k, False), (v, True)):
+        pool = np.full((P, H, ref8.Q8), 0x7F, np.uint8)
+        for b in range(len(lens)):
+            for p in range(0, lens[b], 16):
+                for h in range(H):
+                    ref8.put_rows(pool[table[b, p // 64], h], p % 64, rows[b][h, p:min(p + 16, lens[b])], is_v)
+        out.append(pool)
+    return out
+
+
+def test_attn_units_that_end_inside_a_step_repeat(sv):  # noqa: F811
+    """A CTA goes on from unit to unit, each of which ends inside a step whose other codes are
+    NaN: the stage that it cleared is copied into again.  The same bits each time."""
+    r = np.random.default_rng(1)
+    B, R, Hq, H, mp = 48, 1, 28, 4, 64
+    lens = r.integers(1, 1100, B)
+    used = (lens + 63) // 64
+    P = 64
+    table = np.full((B, mp), -1, np.int32)
+    for b in range(B):
+        table[b, :used[b]] = r.permutation(P)[:used[b]]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    # (sequences share pages: the last page of each is its own, NaN from its end on)
+    k, v = (r.integers(0, 127, (P + B, H, ref8.Q8)).astype(np.uint8) for _ in range(2))
+    for pool, is_v in ((k, False), (v, True)):
+        pool[..., 8192:8208] = np.full(4, 2.0 ** -8, "<f4").view(np.uint8)
+        for b in range(B):
+            table[b, used[b] - 1] = P + b
+            at = ref8._code_bytes(is_v)[np.arange(64) >= (lens[b] - 1) % 64 + 1]
+            pool[P + b][:, at.reshape(-1)] = 0x7F
+    assert sv.verify_attn_q8_workspace(B, R, Hq, H, 128, mp * 64) > 0   # the pages are split over the SMs
+    a = [mk(B, R, Hq, 128), dev(k), dev(v), i32(table), i32(lens), mk(B, H, R, 128), mk(B, H, R, 128)]
+    want = sv.verify_attn_q8(*a)
+    assert not bool(want.isnan().any())
+    flush = torch.empty(2 ** 28, dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(100):
+        if i % 2:
+            flush.fill_(i)
+        differ += (sv.verify_attn_q8(*a) != want).any()
+    assert int(differ) == 0
+    assert sv.get_device_error() == 0
