@@ -375,6 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         named_barrier(2, kThreads);
         second = true;
         if (*fail_s == 0) return false;
+        // (bulk copies are not ordered among themselves: the failed run's partial has to have arrived
+        // before the next one is sent to its place)
+        if (threadIdx.x == 0) bulk_wait();
+        __syncwarp();
         walk.load(a, fail_s + 1);
         return true;
     };

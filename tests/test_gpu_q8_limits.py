@@ -57,3 +57,39 @@ def test_attn_units_that_end_inside_a_step_repeat(sv):  # noqa: F811
         differ += (sv.verify_attn_q8(*a) != want).any()
     assert int(differ) == 0
     assert sv.get_device_error() == 0
+
+
+def test_attn_runs_done_again_repeat(sv):  # noqa: F811
+    """Units that lie in several CTAs' runs, one key of which outweighs its reference by 60
+    powers of two: what the run left in the workspace first is written again.  The
+    same bits each time, and the heavy key's V."""
+    r = np.random.default_rng(2)
+    B, R, H, mp, t = 1, 1, 2, 250, 4000
+    P = 70
+    table = np.full((1, mp), -1, np.int32)
+    table[0, :63] = r.permutation(P)[:63]
+    k = r.standard_normal((H, t, 128)) * 0.01
+    v = r.standard_normal((H, t, 128))
+    q = np.zeros((B, R, H, 128))
+    q[..., 0] = 1.0
+    heavy = [700, 3100]
+    for h in range(H):
+        k[h, :, 0] = 0.0
+        k[h, heavy[h], 0] = 60.0
+    kp, vp = pools_of([k], [v], P, table, [t])
+    assert sv.verify_attn_q8_workspace(B, R, H, H, 128, mp * 64) > 0
+    z = torch.zeros(B, H, R, 128, dtype=torch.bfloat16, device="cuda")
+    a = [torch.from_numpy(q).to(torch.bfloat16).cuda(), dev(kp), dev(vp), i32(table), i32([t]), z, z]
+    want = sv.verify_attn_q8(*a, scale=0.6931471805599453)
+    for h in range(H):
+        x = ref8.get_rows(vp[table[0, heavy[h] // 64], h], True)[heavy[h] % 64]
+        # (the others' weights are 2^-60 each; roundings of the output, 2^-8, and of P to f16, 2^-11)
+        assert np.all(np.abs(want[0, 0, h].double().cpu().numpy() - x) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(x) + 1e-12)
+    flush = torch.empty(2 ** 28, dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(100):
+        if i % 2:
+            flush.fill_(i)
+        differ += (sv.verify_attn_q8(*a, scale=0.6931471805599453) != want).any()
+    assert int(differ) == 0
+    assert sv.get_device_error() == 0
