@@ -181,14 +181,19 @@ __device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t c) {
     return r;
 }
 
-// A bounded wait on an mbarrier phase; one that gives up is noted for the kernel's end, and
-// the others then give up soon.  There are many, and code that is run once a step, or once,
-// has to be short to be there in time.
+// A bounded wait on an mbarrier phase, of 2 s of wall time as the library's others; one that gives
+// up is noted for the kernel's end, and the others then give up soon.  There are many, and code
+// that is run once a step, or once, has to be short to be there in time.
 __device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, volatile int* late) {
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < (1 << 20); ++i) {
+    for (uint32_t i = 1; i < (1u << 28); ++i) {
         if (mbar_try_wait(bar, parity)) return;
-        if ((i & 4095) == 4095 && *late != 0) return;
+        if ((i & 255u) != 0u) continue;
+        if (*late != 0) return;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > 2000000000ull) break;
     }
     *late = 1;
 }
@@ -457,6 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     }
                     const int s = it % kStages;
                     const int pa = __shfl_sync(0xffffffffu, pg, i & 31), pb = __shfl_sync(0xffffffffu, pg, (i + 1) & 31);
+                    // (once the ring is full this warp waits for those that wait for the preceding kernel, and a
+                    // wait's limit must not count that kernel's time)
+                    if (early && it == kStages) pdl_wait();
                     wait(&ring_empty[s], stage_use(it) ^ 1u);
                     if (i < 0) {   // the stage of the block's K, whose writers do not follow the others' use of it
                         if (lane == 0 && !is_v) mbar_arrive(&ring_go[s]);
@@ -491,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         } while (again());
     } else if (warp == kQkWarp) {
         // ---------------- S^T = K Q^T ----------------
+        if (early) pdl_wait();   // (as all that it waits for do)
         constexpr uint32_t id_s = idesc_e4m3_f32(128, kStacked ? 2 * kLive : kLive);
         int it = 0, seg = 0;
         Turn sb;
@@ -534,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         } while (again());
     } else if (warp == kPvWarp) {
         // ---------------- O^T += V^T P^T ----------------
+        if (early) pdl_wait();
         constexpr uint32_t id_o = idesc_f16_f32_bmn(128, kLive), id_blk = idesc_bf16_f32(128, kLive, false, true);
         int it = 0, seg = 0;
         Turn pb;
@@ -1180,7 +1190,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     if (warp == kPvWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
-        if (*late != 0) raise_error(a.err, SV_DEVERR_TIMEOUT);
+        if (*late != 0) {
+            raise_error(a.err, SV_DEVERR_TIMEOUT);
+            // copies may be on their way into this CTA's shared memory: some thousand times as long as one takes
+            const uint64_t t0 = global_timer_ns();
+            for (int i = 0; i < (1 << 20) && global_timer_ns() - t0 < 2000000ull; ++i) {}
+        }
     }
 }
 

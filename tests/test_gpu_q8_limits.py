@@ -93,3 +93,49 @@ def test_attn_runs_done_again_repeat(sv):  # noqa: F811
         differ += (sv.verify_attn_q8(*a, scale=0.6931471805599453) != want).any()
     assert int(differ) == 0
     assert sv.get_device_error() == 0
+
+
+# Lets its dependents start at once, takes `ms`, and only then writes its output.
+SLOW = r"""
+extern "C" __global__ void slow_fill(unsigned short* out, const unsigned short* in, int n, int ms) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (int i = 0; i < (1 << 24); ++i) {
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t - t0 > 1000000ull * ms) break;
+        __nanosleep(1000);
+    }
+    for (int i = threadIdx.x; i < n; i += blockDim.x) out[i] = in[i];
+}
+"""
+
+
+@pytest.mark.parametrize("B,mp", [(64, 33), (2, 250)])
+def test_attn_cache_ready_under_a_long_kernel(sv, B, mp):  # noqa: F811
+    """With cache_ready the copies start under the preceding kernel; one that takes longer than
+    the limit of a wait is waited for all the same, and what it writes last is read."""
+    if not hasattr(torch.cuda, "_compile_kernel"):
+        pytest.skip("no way to compile a kernel here")
+    slow = torch.cuda._compile_kernel(SLOW, "slow_fill")
+    r = np.random.default_rng(3)
+    R, Hq, H, t = 2, 12, 4, mp * 64 - 5
+    P = 300
+    pools = []
+    for _ in range(2):
+        pool = r.integers(0, 127, (P, H, ref8.Q8)).astype(np.uint8)
+        pool[..., 8192:8208] = np.full(4, 2.0 ** -8, "<f4").view(np.uint8)
+        pools.append(dev(pool))
+    table = i32(np.stack([r.permutation(P)[:mp] for _ in range(B)]))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    src, kb, vb = mk(B, R, Hq, 128), mk(B, H, R, 128), mk(B, H, R, 128)
+    lens = i32([t] * B)
+    want = sv.verify_attn_q8(src, *pools, table, lens, kb, vb)
+    q = torch.zeros_like(src)
+    torch.cuda.synchronize()
+    slow(grid=(1, 1, 1), block=(256, 1, 1), args=(q, src, q.numel(), 2500))
+    got = sv.verify_attn_q8(q, *pools, table, lens, kb, vb, cache_ready=True)
+    torch.cuda.synchronize()
+    assert sv.get_device_error() == 0
+    assert torch.equal(got, want)
