@@ -213,6 +213,12 @@ __device__ __forceinline__ void fold_sums(float (&v)[kN]) {
     fold_sums_step<kN>(v);
 }
 
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // What some partials of a row sum up to, a lane four dims of it: O, l, relative to m.
 struct RowSum {
     float m = -INFINITY, l = 0.f;
@@ -237,18 +243,24 @@ struct PartialRows {
     template <bool kMeans>
     __device__ __forceinline__ void add_to(RowSum& r) const {
         auto power = [](float x) { return kMeans ? fast_exp2(x) : exp2f(x); };
+        // A mean weighs 2^m l, here the single power 2^(m + log2 l), of which the largest is 2^-8:
+        // l can be large and a mean as large as V, so neither their product nor a sum of
+        // 256 means may be formed.  (The difference of two m first, as m + log2 l rounds.)
+        float lg[kN];
         float mn = r.m;
 #pragma unroll
-        for (int u = 0; u < kN; ++u)
-            if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
+        for (int u = 0; u < kN; ++u) {
+            lg[u] = kMeans ? fast_log2(ml[u].y) : 0.f;   // (-inf for 0)
+            if constexpr (kMeans) mn = fmaxf(mn, ml[u].x + lg[u] + 8.0f);
+            else if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
+        }
         const float c = r.m == -INFINITY ? 0.f : power(r.m - mn);
         r.o.x *= c, r.o.y *= c, r.o.z *= c, r.o.w *= c, r.l *= c;
 #pragma unroll
         for (int u = 0; u < kN; ++u) {
             if (ml[u].y == 0.f) continue;   // all of the row's scores there are -inf
-            float w = power(ml[u].x - mn);
-            r.l += w * ml[u].y;
-            if constexpr (kMeans) w *= ml[u].y;
+            const float w = power(kMeans ? (ml[u].x - mn) + lg[u] : ml[u].x - mn);
+            r.l += kMeans ? w : w * ml[u].y;
             r.o.x += w * o[u].x;
             r.o.y += w * o[u].y;
             r.o.z += w * o[u].z;

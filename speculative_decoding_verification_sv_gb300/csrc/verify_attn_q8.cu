@@ -98,6 +98,9 @@ constexpr float kUpSum = 15.0f;           // where the sums gave the reference, 
 // times the others, had one done again, 62 us for 44, in every eighth call with kUp = -4.)
 constexpr float kLost = 0x1p-17f;
 constexpr float kLeastSum = 0x1p-100f;    // sums from here on give a reference
+// and from here on a run is done again.  The block's P is bf16 and reaches 2^128, where the row's own
+// key is not among those that give its reference; 1 / sum is 0 from 2^126 on.
+constexpr float kMostSum = 0x1p64f;
 constexpr int kKept = 4;                  // runs of a CTA whose references are kept for that
 constexpr int kRecFloats = kRows * (kQ8D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 256;
@@ -1105,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 if (tid < kLive) {
                     lsum = (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
                     const float least = kLost * static_cast<float>(kStepKeys * n);
-                    bad = !(lsum < INFINITY) || (lsum < least && tid < nrows);
+                    bad = !(lsum < kMostSum) || (lsum < least && tid < nrows);
                     const bool sure = (lsum >= kLeastSum && lsum < INFINITY) || tid >= nrows;
                     if (!sure) fail_s[6] = 1;
                     if (!second && run < kKept)

@@ -139,3 +139,68 @@ def test_attn_cache_ready_under_a_long_kernel(sv, B, mp):  # noqa: F811
     torch.cuda.synchronize()
     assert sv.get_device_error() == 0
     assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# scores and values far apart
+# ---------------------------------------------------------------------------
+
+LN2 = 0.6931471805599453   # the scale that makes scores powers of two
+
+
+def softmax64(q, k, v, see):
+    """q [R, Hq, 128], k, v [H, n, 128], see [R, n]: float64, by powers of two of q . k."""
+    R, Hq, H = q.shape[0], q.shape[1], k.shape[0]
+    z = torch.einsum("rhgd,hkd->rhgk", q.double().view(R, H, Hq // H, 128), k.double())
+    z = z.masked_fill(~see[:, None, None, :], float("-inf"))
+    p = torch.exp2(z - z.amax(-1, keepdim=True))
+    p = p / p.sum(-1, keepdim=True)
+    return (torch.einsum("rhgk,hkd->rhgd", p, v.double()).reshape(R, Hq, 128),
+            torch.einsum("rhgk,hkd->rhgd", p, v.double().abs()).reshape(R, Hq, 128))
+
+
+def close(got, want, wgt):
+    """Where scores are one exact product each: the output's rounding (2^-8), P's to f16 (2^-11),
+    and as much again for the exponentials and the scale's own rounding (2^-23 of scores up to
+    2^8, in numerator and denominator), and sums in fp32."""
+    return bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * wgt + 2.0 ** -126).all())
+
+
+def held(pool, table, t, is_v):
+    """[H, t, 128] on the GPU: what an 8-bit pool holds for a sequence."""
+    n = (t + 63) // 64
+    x = ref8.get_rows(pool[np.asarray(table)[:n]], is_v).transpose(1, 0, 2, 3)
+    return torch.from_numpy(np.ascontiguousarray(x.reshape(pool.shape[1], n * 64, 128)[:, :t])).cuda()
+
+
+def causal(R, t):
+    return torch.cat([torch.ones(R, t, dtype=torch.bool), torch.ones(R, R).tril() > 0], 1).cuda()
+
+
+def bf16(x):
+    return torch.as_tensor(x).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("R", [40, 65])
+@pytest.mark.parametrize("t,mp", [(0, 1), (100, 2), (520, 9), (520, 250)])
+def test_attn_sums_near_the_end_of_their_range(sv, R, t, mp):  # noqa: F811
+    """The last row's own key, which is not among the 32 that give references, lies 100 to 140
+    powers of two above the others: its sum ends short of infinity, or past it."""
+    r = np.random.default_rng(R + mp)
+    P = mp + 1
+    table = r.permutation(P)[:mp].reshape(1, mp)
+    for size in (0.5, 500.0):
+        v = size * r.choice([1.0, 0.75, -0.5], (1, t, 128))
+        kp, vp = pools_of([np.zeros((1, t, 128))], [v], P, table, [t])
+        q = torch.zeros(1, R, 1, 128)
+        q[..., 0] = 1.0
+        vb = bf16(size * r.choice([1.0, 0.75, -0.5], (1, 1, R, 128)))
+        a = (dev(kp), dev(vp), i32(table), i32([t]))
+        kc, vc = held(kp, table[0], t, False), held(vp, table[0], t, True)
+        for gap in range(100, 141):
+            kb = torch.zeros(1, 1, R, 128)
+            kb[0, 0, R - 1, 0] = gap
+            got = sv.verify_attn_q8(bf16(q), *a, bf16(kb), vb, scale=LN2)[0]
+            want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
+            assert close(got, want, wgt), (size, gap, float((got.double() - want).abs().max()))
+    assert sv.get_device_error() == 0
