@@ -33,10 +33,12 @@
 // it), and is the row's reference m for the whole run.  P is 2^-5 at the reference: a
 // score 21 powers of two above it makes P infinite, and a P below 2^-25, a weight 2^-20
 // of the reference's, is lost.  A run whose O is not finite, or where a row's sum is so
-// small that what was lost could matter (kLost), is done again with references that the
-// sums give, P then summing to 2^15; one whose sums say nothing (the reference was a key that
-// the row does not see, or none was finite) with the reference moved to the maximum
-// every step.
+// small that what was lost could matter (kLost), is done again, and then nothing has f16's range:
+// V is bf16 in units of 1, as the read-back gives it, and P in two bf16 parts as the block's is.  Its
+// references are those that the sums give, P then summing to 1; where they say nothing (the
+// reference was a key that the row does not see, or none was finite) they rise with the maximum.
+// (64 single tokens x 28 heads, where each token scores the first position 30 nats above itself:
+// 91 us for 44; where one of the 64 does, 66.  16 sequences: 86 for 34.)
 //
 // What bounds it, in us of graph replays over inputs larger than L2 (heads and positions as
 // named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 34.0, for 137 MB, which take
@@ -88,8 +90,9 @@ constexpr int kMaxR = 128;
 constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kTmaWarp = 12, kQkWarp = 14, kPvWarp = 15,
               kThreads = 32 * 16;
 constexpr int kVUp = 4;                   // V is in units of 2^kVUp of its first scales
-constexpr float kUp = -5.0f;              // P is 2^kUp at the reference;
-constexpr float kUpSum = 15.0f;           // where the sums gave the reference, they are 2^kUpSum
+constexpr float kUp = -5.0f;              // P is 2^kUp at the reference
+constexpr float kUpSum = 0.0f;            // where the sums gave the reference, they are 2^kUpSum
+constexpr float kSlack = 4.0f;            // which, done again, stays where the maximum rises by no more
 // A row's P sum to kLost times the keys or the run is done again: roundings below f16's smallest
 // steps, 2^-25 at most for each key, then move the row by at most 2^-8 of the mean |V| if all of
 // them went one way, and by that over the root of the keys as they do.  (A row that sees one of
@@ -98,10 +101,10 @@ constexpr float kUpSum = 15.0f;           // where the sums gave the reference, 
 // times the others, had one done again, 62 us for 44, in every eighth call with kUp = -4.)
 constexpr float kLost = 0x1p-17f;
 constexpr float kLeastSum = 0x1p-100f;    // sums from here on give a reference
-// and from here on a run is done again.  The block's P is bf16 and reaches 2^128, where the row's own
+constexpr int kKept = 4;                  // runs of a CTA whose references are kept for that
+// A sum from here on too.  The block's P is bf16 and reaches 2^128, where the row's own
 // key is not among those that give its reference; 1 / sum is 0 from 2^126 on.
 constexpr float kMostSum = 0x1p64f;
-constexpr int kKept = 4;                  // runs of a CTA whose references are kept for that
 constexpr int kRecFloats = kRows * (kQ8D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 256;
 constexpr int kMaxCluster = 8;
@@ -125,7 +128,8 @@ constexpr int kOffBar = kOffScl + kSclSlots * kSclBytes;
 constexpr int kOffNm = kOffBar + 320;                     // [64] -m, m the rows' references
 constexpr int kOffMove = kOffNm + kRows * 4;              // [64] what O and l of the row are multiplied by
 constexpr int kOffRed = kOffMove + kRows * 4;             // [4 quadrants][64]
-constexpr int kOffFail = kOffRed + 4 * kRows * 4;         // a run failed; where the runs start [5]; a run's sums are unsure; a wait gave up
+// [8] the runs that failed; where the runs start [5]; (bit r) run r's sums give no references; a wait gave up
+constexpr int kOffFail = kOffRed + 4 * kRows * 4;
 constexpr int kOffPar = kOffFail + 32;                    // [128] parents
 constexpr int kOffAnc = kOffPar + kMaxR * 4;              // [128][2] 64-bit path masks
 constexpr int kOffRow = kOffAnc + kMaxR * 16;             // [64] (sequence, block row, head) of a tile row, -1 past the last
@@ -265,6 +269,29 @@ struct Rows {
     uint4 v[kN];
 };
 
+// What follows is rare, and what is long of it functions of their own: the SMs' caches do not hold all
+// that a CTA's warps run (64 single tokens 44.4 us; with this in line 46 to 55, by where it came to lie).
+
+// V of a context step as bf16 into tensor memory at `to`: dim l of 128 positions, `have` of which exist.
+__device__ __noinline__ void wide_v(const uint8_t* v, const float* scale, int have, int l, uint32_t to) {
+    const uint32_t up = q8_pow2_pair(120);
+#pragma unroll 1
+    for (int h = 0; h < 8; ++h) {   // 16 keys: a run
+        const uint32_t sb = have > 16 * h ? __float_as_uint(scale[h]) >> 16 : 0u, s2 = sb | sb << 16;
+        auto value = [&](uint32_t p) { return q8_nan_pair(p, q8_mul2(q8_mul2(p, up), s2)); };
+        uint32_t r[8];
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const uint2 w = *reinterpret_cast<const uint2*>(v + q8_v_off(2 * h + o, l));
+            r[4 * o] = value(q8_pair<0, 1>(w.x, 0u));
+            r[4 * o + 1] = value(q8_pair<2, 3>(w.x, 0u));
+            r[4 * o + 2] = value(q8_pair<0, 1>(w.y, 0u));
+            r[4 * o + 3] = value(q8_pair<2, 3>(w.y, 0u));
+        }
+        tmem_st8(to + 8 * h, r);
+    }
+}
+
 // kRT: rows a softmax thread takes; the tile's rows past 2 kRT do not exist (what their
 // columns of P and O hold is not looked at)
 template <int kRT, bool kCluster>
@@ -369,27 +396,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
             }
         }
     }
-    // Each role does the CTA's runs once, and a second time where one of them failed (the
-    // softmax warps' verdict, after all have finished).
-    bool second = false;
+    // Each role does the CTA's runs once, and those of them that failed (found while they are done,
+    // looked at after all have finished) a second time, `wide`.
+    int run = -1;              // the current one
+    uint32_t failed = 0u;      // (bit r) run r failed; bit 31: one of those from there on
+    auto next_run = [&](auto wide) {
+        do {
+            if (!walk.next(a, wk)) return false;
+            run = min(run + 1, 31);
+        } while (wide && (failed >> run & 1u) == 0u);
+        return true;
+    };
+    auto run_failed = [&]() { atomicOr(reinterpret_cast<int*>(smem + kOffFail), 1 << run); };
     // a warp's wait; its lanes go on together (what follows is warp-collective)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         bar_wait(bar, parity, late);
         __syncwarp();
     };
     auto again = [&]() {
-        if (second) return false;
         __syncwarp();
         named_barrier(2, kThreads);
-        second = true;
-        if (*fail_s == 0) return false;
+        failed = static_cast<uint32_t>(*fail_s);
+        if (failed == 0u) return false;
         // (bulk copies are not ordered among themselves: the failed run's partial has to have arrived
         // before the next one is sent to its place)
         if (threadIdx.x == 0) bulk_wait();
         __syncwarp();
         walk.load(a, fail_s + 1);
+        run = -1;
         return true;
     };
+    // With `own_code` the second pass has code of its own, so that the first one's is short: the roles
+    // that do other things then.  (Of the others it was measured: in clusters one code for both, 16
+    // sequences 34.3 us for 34.7, a tree 24.2 for 25.0; in the even split 64 single tokens 52.0 for 44.4.)
+    auto passes = [&](auto own_code, auto&& runs) {
+        if constexpr (own_code) {
+            runs(std::false_type{});
+            if (again()) runs(std::true_type{});
+        } else {
+            bool wide = false;
+            while (true) {
+                runs(wide);
+                if (wide || !again()) return;
+                wide = true;
+            }
+        }
+    };
+    constexpr std::bool_constant<!kCluster> kApart{};
 
     // The rows of Q of a run, by half-warps: rows hw, hw + 64 / kN .. of the tile (of its kLive).
     auto load_q = [&](auto& x, const Walk& of, int hw) {
@@ -437,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         uint64_t once;
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         int it = 0;
-        do {
-            while (walk.next(a, wk)) {
+        passes(kApart, [&](auto wide) {
+            while (next_run(wide)) {
                 const int g = walk.cur_unit / wk.row_tiles;
                 const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
                 const int np = walk.p1 - walk.p0;
@@ -499,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     __syncwarp();
                 }
             }
-        } while (again());
+        });
     } else if (warp == kQkWarp) {
         // ---------------- S^T = K Q^T ----------------
         if (early) pdl_wait();   // (as all that it waits for do)
@@ -507,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         int it = 0, seg = 0;
         Turn sb;
         static_assert(kSBufs == kPBufs, "one turn for both");
-        do {
-            while (walk.next(a, wk)) {
+        passes(kApart, [&](auto wide) {
+            while (next_run(wide)) {
                 const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
                 if (elect_one()) {
                     const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ + (seg & 1) * kQBytes), 16, 1024);
@@ -543,37 +596,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 it += n;
                 ++seg;
             }
-        } while (again());
+        });
     } else if (warp == kPvWarp) {
         // ---------------- O^T += V^T P^T ----------------
         if (early) pdl_wait();
-        constexpr uint32_t id_o = idesc_f16_f32_bmn(128, kLive), id_blk = idesc_bf16_f32(128, kLive, false, true);
+        constexpr uint32_t id_o = idesc_f16_f32_bmn(128, kLive), id_two = idesc_bf16_f32(128, kLive, false, true);
         int it = 0, seg = 0;
         Turn pb;
-        do {
-            while (walk.next(a, wk)) {
+        passes(kApart, [&](auto wide) {
+            while (next_run(wide)) {
                 const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
                 if (elect_one()) {
                     bar_wait(o_free, (seg & 1) ^ 1, late);
 #pragma unroll 1
                     for (int st = 0; st < n; ++st) {
                         const int i = it + st, x = i & 1;
-                        const bool blk = walk.block && st == 0;
+                        const bool two = (walk.block && st == 0) || wide;   // bf16, P in two parts
                         bar_wait(&v_full[x], (i >> 1) & 1, late);
                         bar_wait(&p_full[pb.x], pb.parity, late);
                         tc_fence_after();
                         uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP + pb.x * kPBytes), 16, 1024);
                         uint32_t more = st > 0 ? 1u : 0u;
 #pragma unroll 1
-                        for (int p = blk ? 0 : 1; p < 2; ++p) {   // a block's P is in two parts
+                        for (int p = two ? 0 : 1; p < 2; ++p) {
 #pragma unroll
                             for (int kc = 0; kc < kStepKeys / 16; ++kc) {
-                                tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), blk ? id_blk : id_o, more);
+                                tc_mma_ts(tO, tV(x) + kc * 8, pd + kc * (2048 >> 4), two ? id_two : id_o, more);
                                 more = 1u;
                             }
                             pd = smem_desc_sw128(smem_u32(stage(i)), 16, 1024);
                         }
-                        if (blk) tc_commit(&ring_empty[i % kStages]);
+                        if (two) tc_commit(&ring_empty[i % kStages]);
                         tc_commit(&pv_done[pb.x]);
                         pb.next(kPBufs);
                     }
@@ -584,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 it += n;
                 ++seg;
             }
-        } while (again());
+        });
     } else if (warp >= kConvWarp) {
         // ---------------- to e4m3 pairs and to f16 ----------------
         if (early) pdl_wait();
@@ -615,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
             }
             ++it;
         };
-        do {
-            while (walk.next(a, wk)) {
+        passes(std::true_type{}, [&](auto wide) {
+            while (next_run(wide)) {
                 const int g = walk.cur_unit / wk.row_tiles;
                 const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R * kQ8D;
                 // half-warps take the query rows, and the block's rows of K
@@ -660,25 +713,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     if (warp < kConvWarp + 2 && lane == 0) mbar_arrive(&ring_full[s]);
                 }
                 // V is in units of 2^ev: of the largest scale of the first pages (their live runs) with
-                // kVUp powers of two to spare; done again, of all.  Every warp finds it by itself.
+                // kVUp powers of two to spare; done again, of 1.  Every warp finds it by itself.
                 int ev = 0;
-                if (walk.ctx_steps() > 0) {
+                if (walk.ctx_steps() > 0 && !wide) {
                     const int first = it + (walk.block ? 1 : 0);
                     uint32_t top = 0u;
-                    if (!second) {
-                        wait(&ring_full[first % kStages], stage_use(first));
-                        const int left = walk.cur_t - walk.p0 * kQ8Page - kQ8Run * lane;
-                        if (lane < 8 && left > 0 && (lane < 4 || walk.p0 + 1 < walk.p1)) top = reinterpret_cast<const uint32_t*>(scales(first))[8 + lane];
-                    } else {
-                        const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
-#pragma unroll 1
-                        for (int p = 4 * walk.p0 + lane; p < 4 * walk.p1; p += 32) {
-                            const int pg = __ldg(tab + (p >> 2));
-                            if (pg < 0 || pg >= a.num_pages || p * kQ8Run >= walk.cur_t) continue;
-                            top = max(top, __ldg(reinterpret_cast<const uint32_t*>(
-                                               a.v_pool + (static_cast<size_t>(pg) * a.Hkv + g) * kQ8Bytes + kQ8Codes) + (p & 3)));
-                        }
-                    }
+                    wait(&ring_full[first % kStages], stage_use(first));
+                    const int left = walk.cur_t - walk.p0 * kQ8Page - kQ8Run * lane;
+                    if (lane < 8 && left > 0 && (lane < 4 || walk.p0 + 1 < walk.p1)) top = reinterpret_cast<const uint32_t*>(scales(first))[8 + lane];
                     ev = q8_stored_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, top))) + kVUp;
                 }
                 if (cw == 0 && lane == 0) vexp_s[seg % 3] = ev;
@@ -729,6 +771,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                         fence_proxy_async_smem();
                     }
                     const float2* f2 = reinterpret_cast<const float2*>(scales(it) + 8);
+                    if (wide) {
+                        v_free();
+                        wide_v(v, scales(it) + 8, have, l, tV(it & 1) + lane_off);
+                        v_done(cw != 0);   // (P's second part goes to the stage, as a block's)
+                        continue;
+                    }
                     v_free();
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {   // 32 keys: two runs
@@ -750,13 +798,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 }
                 ++seg;
             }
-        } while (again());
+        });
     } else {
         // ---------------- softmax, epilogue ----------------
         // (the barrier counts whole warps: they arrive converged)
         auto soft_sync = []() {
             __syncwarp();
             named_barrier(1, 32 * kSoftWarps);
+        };
+        auto soft_any = [](bool x) {   // the same, and whether x holds in any of the threads
+            uint32_t r;
+            __syncwarp();
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"(x ? 1u : 0u), "n"(32 * kSoftWarps)
+                : "memory");
+            return r != 0u;
         };
         if (early) pdl_wait();
         // A cluster's successor may start now.  (Not before the wait: the successor may
@@ -769,8 +827,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         const int rows = a.R * a.G;
         int it = 0, seg = 0;
         Turn sb;
-        uint32_t unsure = 0u;                  // (bit r) run r's sums give no references
-        float* kept_s = reinterpret_cast<float*>(smem + kOffKept);
         // The rows' means over the run, each thread's dim: store(row of the tile, mean), which cannot
         // pass V's largest.  True where something was not finite.
         auto means = [&](int b, int g, int row0, bool tree, auto&& store) {
@@ -814,12 +870,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
             }
             return bad;
         };
-        int part = 0, run = 0;
-        do {
-            part = run = 0;
-            for (; walk.next(a, wk); ++run) {
+        float* kept_s = reinterpret_cast<float*>(smem + kOffKept);
+        passes(std::true_type{}, [&](auto wide) {
+            while (next_run(wide)) {
                 // done again: with the references that the sums gave, or moving ones
-                const bool kept = second && run < kKept && (unsure >> run & 1u) == 0u, safe = second && !kept;
+                const bool kept = wide && run < kKept && (fail_s[6] >> run & 1) == 0, safe = wide && !kept;
                 const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
                 const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
                 const bool first = kCluster && seg == 0;
@@ -932,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 // pass fp32's largest).
                 auto references = [&](int st, uint32_t seen) {
                     const float ks = key_scale(st);
-                    if (safe || q4 == 0) {
+                    if (wide || q4 == 0) {
                         float most = 0.f;   // lane e's: row e's
 #pragma unroll (kRT == 16 ? 2 : 1)
                         for (int c0 = 0; c0 < kRT; c0 += 8) {
@@ -949,27 +1004,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                             }
                         }
                         if (lane < kRT) {
-                            if (safe) red_s[q4 * kRows + hh * kRT + lane] = most;
+                            if (wide) red_s[q4 * kRows + hh * kRT + lane] = most;
                             else if (fabsf(most) < INFINITY) nm_s[hh * kRT + lane] = kUp - most;
                         }
                     }
                     soft_sync();
-                    if (!safe) return;
+                    if (!wide) return;
+                    bool moved = false;
                     if (tid < kLive) {
-                        // up, or where no score was finite so far (P, the sum and O are 0 then) to
-                        // wherever the maximum is
+                        // up where the maximum has risen by more than kSlack, or where no score was finite so
+                        // far (P, the sum and O are 0 then) to wherever it is
                         const float m = fmaxf(fmaxf(red_s[tid], red_s[kRows + tid]), fmaxf(red_s[2 * kRows + tid], red_s[3 * kRows + tid]));
                         const float was = kUp - nm_s[tid];
                         float move = 1.0f;
-                        if (m > -INFINITY && (!found || m > was)) {
+                        if (m > -INFINITY && (!found || m > was + kSlack)) {
                             if (found) move = fast_exp2(was - m);
+                            moved = found;
                             nm_s[tid] = kUp - m;
                             found = true;
                         }
                         move_s[tid] = move;
                     }
-                    soft_sync();
-                    if (st == 0) return;
+                    if (!soft_any(moved)) return;
 #pragma unroll
                     for (int i = 0; i < kRT / 2; ++i)
                         sums[i] = __fmul2_rn(sums[i], reinterpret_cast<const float2*>(move_s + hh * kRT)[i]);
@@ -1023,13 +1079,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     step_done();
                 };
                 // any step, the block's among them, whose P is bf16 (range) in two parts (16 bits), the second
-                // in the place of the block's K, which has been read.  Eight rows at a time; the sums go
-                // round, so that the loop's code serves them all (unrolled, the larger tile's spills).
+                // in the place of the step's K, which has been read; so is all P of a run done again.  Eight
+                // rows at a time; the sums go round, so that the loop's code serves them all (unrolled, the
+                // larger tile's spills).
                 auto any_step = [&](int st) {
                     s_wait();
-                    const bool blk = st < lead;
+                    const bool two = st < lead || wide;
                     const uint32_t seen = seen_by(st);
-                    if (safe || (st == 0 && !second)) references(st, seen);
+                    if (safe || (st == 0 && !wide)) references(st, seen);
                     const float ks = key_scale(st);
                     uint8_t* prow = smem + kOffP + sb.x * kPBytes + l * 128;
                     uint8_t* rest = stage(it) + l * 128;
@@ -1053,7 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                                 const float2 p = make_float2(seen >> (c0 + 2 * i) & 1u ? fast_exp2(ex) : 0.f,
                                                              seen >> (c0 + 2 * i + 1) & 1u ? fast_exp2(ey) : 0.f);
                                 now[i] = __fadd2_rn(now[i], p);
-                                if (blk) {
+                                if (two) {
                                     w[i] = pack_bf16x2(p.x, p.y);
                                     v[i] = pack_bf16x2(p.x - __uint_as_float(w[i] << 16), p.y - __uint_as_float(w[i] & 0xffff0000u));
                                 } else {
@@ -1067,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                         for (int i = 0; i < 4; ++i) sums[kRT / 2 - 4 + i] = now[i];
                         const int to = ((hh * (kRT / 8) + c0 / 8) ^ (l & 7)) << 4;
                         *reinterpret_cast<uint4*>(prow + to) = make_uint4(w[0], w[1], w[2], w[3]);
-                        if (blk) *reinterpret_cast<uint4*>(rest + to) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (two) *reinterpret_cast<uint4*>(rest + to) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -1076,11 +1133,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 };
                 // whole context steps apart, so that they carry no masks
                 const bool ragged = (walk.p1 - walk.p0) & 1 || walk.p1 * kQ8Page > walk.cur_t;
-                const int nwhole = safe ? 0 : n - (ragged ? 1 : 0);
+                const int nwhole = wide ? 0 : n - (ragged ? 1 : 0);
 #pragma unroll 1
                 for (int st = 0; st < n; ++st) {
                     if (st >= lead && st < nwhole) {
-                        if (st == 0 && !second) {
+                        if (st == 0) {
                             s_wait();
                             references(0, ~0u);
                         }
@@ -1109,10 +1166,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     lsum = (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
                     const float least = kLost * static_cast<float>(kStepKeys * n);
                     bad = !(lsum < kMostSum) || (lsum < least && tid < nrows);
-                    const bool sure = (lsum >= kLeastSum && lsum < INFINITY) || tid >= nrows;
-                    if (!sure) fail_s[6] = 1;
-                    if (!second && run < kKept)
-                        kept_s[run * kRows + tid] = sure ? nm_s[tid] + kUpSum - __log2f(fmaxf(lsum, kLeastSum)) : 0.f;
+                    if (!wide && run < kKept) {
+                        if ((lsum >= kLeastSum && lsum < INFINITY) || tid >= nrows)
+                            kept_s[run * kRows + tid] = nm_s[tid] + kUpSum - __log2f(fmaxf(lsum, kLeastSum));
+                        else
+                            atomicOr(reinterpret_cast<int*>(smem + kOffFail) + 6, 1 << run);
+                    }
                     move_s[tid] = lsum != 0.f ? __fdividef(1.0f, lsum) : 0.f;
                 }
                 wait(o_done, seg & 1);
@@ -1121,12 +1180,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     *reinterpret_cast<float2*>(rec + kRows * kQ8D + 2 * tid) = make_float2(-nm_s[tid], lsum);   // (kUp below the reference)
                 tc_fence_after();
                 soft_sync();
-                if (fail_s[6] != 0) unsure |= run < kKept ? 1u << run : 0u;
                 bad |= means(b, g, row0, tree, [&](int r, float mean) {
                     if (direct) reinterpret_cast<uint16_t*>(rec)[r * kQ8D + l] = f32_bf16_bits(mean);
                     else rec[r * kQ8D + l] = mean;   // (rows past the tile's last too, never read)
                 });
-                if (bad) *fail_s = 1;
+                if (bad && !wide) run_failed();
                 tc_fence_before();
                 if (!kCluster && !direct) fence_proxy_async_smem();
                 soft_sync();   // red_s and nm_s read by everyone before the next run writes them; the rows are there
@@ -1134,7 +1192,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     mbar_arrive(o_free);
                     mbar_arrive(&q_free[seg & 1]);
                 }
-                if (tid == 0) fail_s[6] = 0;
                 if (direct) {
 #pragma unroll 1
                     for (int r = warp; r < nrows; r += kSoftWarps)
@@ -1142,12 +1199,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                             reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(rec) + r * kQ8D)[lane];
                     soft_sync();   // (P's place and row_s are free)
                 } else if (!kCluster) {
-                    if (tid == 0) bulk_s2g(ws + (static_cast<size_t>(blockIdx.x) * 2 + part) * kRecFloats, rec, kRecFloats * 4);
+                    // (a partial run that is not the CTA's first is its last)
+                    if (tid == 0) bulk_s2g(ws + (static_cast<size_t>(blockIdx.x) * 2 + (run > 0 ? 1 : 0)) * kRecFloats, rec, kRecFloats * 4);
                 }
-                part = 1;   // a partial run that is not the CTA's first is its last
                 ++seg;
             }
-        } while (again());
+        });
         if (tid == 0) bulk_wait();
         if constexpr (kCluster) {   // no page of the unit fell to this CTA
             if (seg == 0 && tid < kRows)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import _serving_ref8 as ref8
-from test_gpu_q8 import dev, i32, sv  # noqa: F401
+from test_gpu_q8 import _device_inputs, dev, i32, sv  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -203,4 +203,105 @@ def test_attn_sums_near_the_end_of_their_range(sv, R, t, mp):  # noqa: F811
             got = sv.verify_attn_q8(bf16(q), *a, bf16(kb), vb, scale=LN2)[0]
             want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
             assert close(got, want, wgt), (size, gap, float((got.double() - want).abs().max()))
+    assert sv.get_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# runs that are done again
+# ---------------------------------------------------------------------------
+
+def _one_heavy_key(t, at, low, P=128):
+    """A sequence of t positions (64 P at most) in pages 0 .. of one head: position `at` scores 30 and
+    has V 0, the others score 30 - low and have V 1."""
+    k, v = np.zeros((1, t, 128)), np.ones((1, t, 128))
+    k[0, :, 0], k[0, :, 1] = 30.0, -low      # (two dims: each is held exactly)
+    k[0, at, 1], v[0, at] = 0.0, 0.0
+    table = np.arange(P).reshape(1, P)
+    return pools_of([k], [v], P, table, [t])
+
+
+@pytest.mark.parametrize("B,mp", [(160, 128), (1000, 128), (1000, 400)])
+@pytest.mark.parametrize("nan_row", [False, True])
+def test_attn_weights_far_below_the_largest(sv, B, mp, nan_row):  # noqa: F811
+    """One key has all but a hundredth of the weight, which thousands of others share: also where a
+    CTA's run is its fifth or later, or a row beside it is not finite, and is done again."""
+    t, R = 8100, 2
+    kp, vp = _one_heavy_key(t, 5000, 20.0)
+    table = np.full((B, mp), -1, np.int32)
+    table[:, :128] = np.arange(128)
+    q = torch.zeros(B, R, 1, 128)
+    q[..., :2] = 1.0
+    if nan_row:
+        q[:, 0] = float("nan")
+    kb, vb = torch.zeros(B, 1, R, 128), torch.zeros(B, 1, R, 128)
+    kb[..., 1] = -81.0       # the block itself has no weight
+    got = sv.verify_attn_q8(bf16(q), dev(kp), dev(vp), i32(table), i32([t] * B), bf16(kb), bf16(vb), scale=LN2).double()
+    w = (t - 1) * 2.0 ** -20
+    want = w / (1 + w)
+    # the output's rounding and P's, as much again as P's for the rest
+    assert bool(((got[:, 1] - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want).all()), (want, float(got[:, 1].min()), float(got[:, 1].max()))
+    assert bool(got[:, 0].isnan().all()) if nan_row else bool(((got[:, 0] - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want).all())
+    assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("mp", [40, 400])
+def test_attn_some_of_many_runs_fail(sv, mp):  # noqa: F811
+    """Ragged sequences, several to a CTA, some of which hold a key far above their references: all
+    give their rows."""
+    r = np.random.default_rng(mp)
+    B, R, Hq, H = 300, 2, 6, 2
+    lens = r.integers(0, 700, B)
+    P = 64
+    k, v = r.standard_normal((2, H, P * 64, 128))
+    k[..., 0] = 0.0
+    heavy = r.integers(0, 64, P)
+    for p in range(P):
+        k[:, 64 * p + heavy[p], 0] = (p % 4 == 0) * r.integers(0, 90)
+    kp, vp = pools_of([k], [v], P, np.arange(P).reshape(1, P), [P * 64])
+    table = np.full((B, mp), -1, np.int32)
+    for b in range(B):
+        n = (lens[b] + 63) // 64
+        table[b, :n] = r.permutation(P)[:n]
+    q = r.standard_normal((B, R, Hq, 128)) * 0.05
+    q[..., 0] = 1.0
+    q, kb, vb = bf16(q), bf16(r.standard_normal((B, H, R, 128)) * 0.1), bf16(r.standard_normal((B, H, R, 128)))
+    got = sv.verify_attn_q8(q, dev(kp), dev(vp), i32(table), i32(lens), kb, vb, scale=LN2)
+    for b in range(B):
+        t = int(lens[b])
+        kc, vc = held(kp, table[b], t, False), held(vp, table[b], t, True)
+        want, wgt = softmax64(q[b], torch.cat([kc, kb[b].double()], 1), torch.cat([vc, vb[b].double()], 1), causal(R, t))
+        # scores of sums: 260 * 2^-22 of their magnitudes (below 2^8) and 2^-17 of |q|'s largest, 1, by the
+        # largest sum of a row's |k| (below 2^8), each moving p twice
+        s = 2 * (260 * 2.0 ** -22 * 2.0 ** 7 + 2.0 ** -17 * 2.0 ** 8)
+        assert bool(((got[b].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -10 + s) * wgt).all()), b
+    assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("B,R,Hq,H,t", [(1, 1, 28, 4, 7744), (9, 1, 8, 8, 2160), (6, 23, 12, 2, 4000), (16, 3, 28, 4, 2286), (2, 1, 28, 4, 9927)])
+def test_attn_long_runs_round_p_to_f16(sv, B, R, Hq, H, t):  # noqa: F811
+    """How often the output is not the bf16 next to the exact result: as often as P's rounding to 11
+    bits takes it across a border (an error of deviation e crosses one of the borders between
+    steps of u in 0.8 e / u of cases), not as often as 8 bits would, eight times that."""
+    q, (kp, vp), table, kb, vb = _device_inputs(B, R, Hq, H, t, seed=t + 1)
+    lens = i32([t - 29 * b for b in range(B)])
+    k, v = sv.kv_gather_q8(kp[None], vp[None], table, i32([0] * B), lens, t)
+    out = sv.verify_attn_q8(q, kp, vp, table, lens, kb, vb)
+    see = torch.cat([torch.arange(t, device="cuda")[None, :] < lens[:, None],
+                     torch.ones(B, R, dtype=torch.bool, device="cuda")], 1)[:, None, :].repeat(1, R, 1)
+    see[:, :, t:] = torch.tril(torch.ones(R, R, dtype=torch.bool, device="cuda"))
+    differ = expect = 0.0
+    for h in range(H):
+        kk, vv = (torch.cat([c[0, :, h].double(), n[:, h].double()], 1) for c, n in ((k, kb), (v, vb)))
+        z = torch.einsum("brgd,bkd->brgk", q.view(B, R, H, Hq // H, 128)[:, :, h].double(), kk) * 128 ** -0.5
+        p = torch.softmax(z.masked_fill(~see[:, :, None, :], float("-inf")), -1)
+        want = torch.einsum("brgk,bkd->brgd", p, vv)
+        # half a step of 11 bits, 2^-11 of a value at most, uniform; 2^-21 for what sums in fp32 add
+        e = (2.0 ** -11 / 3 ** 0.5) * torch.einsum("brgk,bkd->brgd", p ** 2, vv ** 2).sqrt() + 2.0 ** -21 * torch.einsum(
+            "brgk,bkd->brgd", p, vv.abs())
+        u = torch.exp2(torch.floor(torch.log2(want.abs().clamp_min(1e-30))) - 7)
+        expect += float((0.8 * e / u).clamp_max(1.0).sum())
+        differ += float((out.view(B, R, H, Hq // H, 128)[:, :, h] != want.to(torch.bfloat16)).sum())
+    n = out.numel()
+    # (three deviations of a count)
+    assert differ <= 2 * expect + 3 * expect ** 0.5, (differ / n, expect / n)
     assert sv.get_device_error() == 0
