@@ -23,7 +23,8 @@
 //        bf16's rounding (0.0017 of the result against 0.0023), and every e4m3.  What it
 //        lacks is range.  V is therefore in units of the largest scale of the run's first two
 //        pages, 2^kVUp of it (a value is exact where its own scale is no less than 2^-11
-//        of that; one too large for f16 makes O infinite), and P is 2^kUp at a reference, below.
+//        of that, which is looked at; one too large for f16 makes O infinite), and P is 2^kUp
+//        at a reference, below.
 // The block's K rows are held as Q's are, two e4m3 in units of the row's own (four
 // products).  Its V rows may be of any size, whether seen or not, and stay bf16 in V's units; its P is
 // in two bf16 parts then (16 bits).  What of them is not finite is kept out of the product and
@@ -37,6 +38,7 @@
 // V is bf16 in units of 1, as the read-back gives it, and P in two bf16 parts as the block's is.  Its
 // references are those that the sums give, P then summing to 1; where they say nothing (the
 // reference was a key that the row does not see, or none was finite) they rise with the maximum.
+// V whose scales lie further apart than f16 holds is done that way too.
 // (64 single tokens x 28 heads, where each token scores the first position 30 nats above itself:
 // 91 us for 44; where one of the 64 does, 66.  16 sequences: 86 for 34.)
 //
@@ -90,6 +92,10 @@ constexpr int kMaxR = 128;
 constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kTmaWarp = 12, kQkWarp = 14, kPvWarp = 15,
               kThreads = 32 * 16;
 constexpr int kVUp = 4;                   // V is in units of 2^kVUp of its first scales
+// f16 holds a run exactly whose scale is 2^-15 of the unit or more (its steps end at 2^-24, e4m3's
+// at 2^-9), 2^-kVDown of the largest scale there.  One below that, and not all zeros, is left to the
+// second pass.  (The warp that copies V looks at the scales, which it has in registers.)
+constexpr int kVDown = 15 - kVUp;
 constexpr float kUp = -5.0f;              // P is 2^kUp at the reference
 constexpr float kUpSum = 0.0f;            // where the sums gave the reference, they are 2^kUpSum
 constexpr float kSlack = 4.0f;            // which, done again, stays where the maximum rises by no more
@@ -271,6 +277,30 @@ struct Rows {
 
 // What follows is rare, and what is long of it functions of their own: the SMs' caches do not hold all
 // that a CTA's warps run (64 single tokens 44.4 us; with this in line 46 to 55, by where it came to lie).
+
+// The least scale of V that f16 holds beside `top` (a scale's bits).
+__device__ __forceinline__ float least_scale(uint32_t top) {
+    return q8_pow2(max(q8_stored_exponent(__uint_as_float(top)) - kVDown, -126));
+}
+// Whether one of a lane's runs, those of `low` of block `blk` (of V, `left` positions of which count),
+// holds anything but zeros; one warp, for all of its lanes' blocks.
+__device__ __noinline__ bool any_codes(const uint8_t* blk, uint32_t low, int left) {
+    uint32_t any = 0u;
+#pragma unroll 1
+    for (uint32_t lanes = __ballot_sync(0xffffffffu, low != 0u); lanes != 0u; lanes &= lanes - 1u) {
+        const int x = __ffs(lanes) - 1, end = __shfl_sync(0xffffffffu, left, x);
+        const uint32_t runs = __shfl_sync(0xffffffffu, low, x);
+        const uint2* src = reinterpret_cast<const uint2*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(blk), x));
+#pragma unroll 1
+        for (int i = threadIdx.x & 31; i < kQ8Codes / 8; i += 32) {   // eight positions of a dim
+            const int n = min(end - 8 * (i >> 7), 8);
+            if (n <= 0 || (runs >> (i >> 8) & 1u) == 0u) continue;
+            const uint2 w = __ldg(src + i);
+            any |= (w.x & 0x7f7f7f7fu >> 8 * max(4 - n, 0)) | (n > 4 ? w.y & 0x7f7f7f7fu >> 8 * (8 - n) : 0u);
+        }
+    }
+    return __any_sync(0xffffffffu, any != 0u);
+}
 
 // V of a context step as bf16 into tensor memory at `to`: dim l of 128 positions, `have` of which exist.
 __device__ __noinline__ void wide_v(const uint8_t* v, const float* scale, int have, int l, uint32_t to) {
@@ -500,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 // their 16 bytes would take as long to issue as one of 8 KB)
                 int pg = 0, i = walk.block ? -2 : 0;
                 uint4 f = make_uint4(0u, 0u, 0u, 0u);
+                float least = 0.f;   // (V, first pass) scales from here on are held by f16
 #pragma unroll 1
                 for (; i < np; i += 2, ++it) {
                     if ((i & 31) == 0) {
@@ -550,6 +581,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ring_full[s]);
                     __syncwarp();
+                    if (is_v && !wide && (i & 31) == 0) {
+                        const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+                        const int left = pg < 0 ? 0 : walk.cur_t - (walk.p0 + i + lane) * kQ8Page;
+                        if (i == 0) {   // the largest of the first two pages, as the unit is found
+                            uint32_t top = 0u;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (lane < 2 && left > kQ8Run * r) top = max(top, w[r]);
+                            least = least_scale(__reduce_max_sync(0xffffffffu, top));
+                        }
+                        uint32_t low = 0u;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (left > kQ8Run * r && __uint_as_float(w[r]) < least) low |= 1u << r;
+                        if (__any_sync(0xffffffffu, low != 0u) &&   // (rare)
+                            any_codes(pool + (static_cast<size_t>(max(pg, 0)) * a.Hkv + g) * kQ8Bytes, low, left))
+                            run_failed();
+                    }
                 }
             }
         });

@@ -305,3 +305,54 @@ def test_attn_long_runs_round_p_to_f16(sv, B, R, Hq, H, t):  # noqa: F811
     # (three deviations of a count)
     assert differ <= 2 * expect + 3 * expect ** 0.5, (differ / n, expect / n)
     assert sv.get_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# values far apart
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("t,mp", [(520, 9), (520, 250), (200, 4)])
+@pytest.mark.parametrize("big_at", [3, 70, 190])
+def test_attn_one_large_value_of_no_weight(sv, big_at, t, mp):  # noqa: F811
+    """One position's V is 2^8 to 2^60 times the others' and has no weight: it sets the unit of the
+    others, or passes it, and they count as ever."""
+    r = np.random.default_rng(big_at + mp)
+    P = mp + 1
+    table = r.permutation(P)[:mp].reshape(1, mp)
+    k = np.zeros((1, t, 128))
+    k[0, big_at, :2] = -200.0
+    k[0, 150, 1] = 30.0
+    q = torch.zeros(1, 2, 1, 128)     # row 0 sees the others alike, row 1 one of them
+    q[0, 0, 0, 0] = q[0, 1, 0, 1] = 1.0
+    kb = torch.zeros(1, 1, 2, 128)
+    vb = bf16(r.standard_normal((1, 1, 2, 128)))
+    v0 = r.standard_normal((1, t, 128)) + 0.5
+    for power in (8, 11, 12, 14, 17, 20, 21, 22, 24, 27, 31, 40, 60, 100):
+        v = v0.copy()
+        v[0, big_at] = 2.0 ** power * np.sign(v[0, big_at])
+        kp, vp = pools_of([k], [v], P, table, [t])
+        got = sv.verify_attn_q8(bf16(q), dev(kp), dev(vp), i32(table), i32([t]), bf16(kb), vb, scale=LN2)[0]
+        kc, vc = held(kp, table[0], t, False), held(vp, table[0], t, True)
+        want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(2, t))
+        assert close(got, want, wgt), (power, float((got.double() - want).abs().max()))
+    assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("t,mp", [(130, 3), (520, 250), (1, 1)])
+@pytest.mark.parametrize("least", [2.0 ** -115, 2.0 ** -100, 2.0 ** -40, 2.0 ** 60, 2.0 ** 118])
+def test_attn_values_of_any_size_alone(sv, least, t, mp):  # noqa: F811
+    """All of V next to nothing, or next to the largest that the cache holds."""
+    r = np.random.default_rng(mp)
+    P, R = mp + 1, 3
+    table = r.permutation(P)[:mp].reshape(1, mp)
+    v = least * r.integers(1, 9, (1, t, 128)) * r.choice([1.0, -1.0], (1, t, 128))
+    kp, vp = pools_of([r.integers(-3, 4, (1, t, 128)) * 1.0], [v], P, table, [t])
+    q = torch.zeros(1, R, 1, 128)
+    q[0, :, 0, 5] = 1.0
+    kb = torch.zeros(1, 1, R, 128)
+    vb = bf16(least * r.integers(1, 9, (1, 1, R, 128)))
+    got = sv.verify_attn_q8(bf16(q), dev(kp), dev(vp), i32(table), i32([t]), bf16(kb), vb, scale=LN2)[0]
+    kc, vc = held(kp, table[0], t, False), held(vp, table[0], t, True)
+    want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
+    assert close(got, want, wgt), float(((got.double() - want).abs() / wgt).max())
+    assert sv.get_device_error() == 0
