@@ -27,7 +27,8 @@
 //        at a reference, below.
 // The block's K rows are held as Q's are, two e4m3 in units of the row's own (four
 // products).  Its V rows may be of any size, whether seen or not, and stay bf16 in V's units; its P is
-// in two bf16 parts then (16 bits).  What of them is not finite is kept out of the product and
+// in two bf16 parts then (16 bits).  (One too large in those units is infinite there, and O not finite;
+// one too small is looked for; either way the run is done again.)  What of them is not finite is kept out of the product and
 // added to the rows that see it at the end.
 // A row's maximum runs across lanes here, so it is formed once, over the first 32 keys
 // of the run (of the block, where the run has it: the row's own key and those next to
@@ -300,6 +301,17 @@ __device__ __noinline__ bool any_codes(const uint8_t* blk, uint32_t low, int lef
         }
     }
     return __any_sync(0xffffffffu, any != 0u);
+}
+
+// Whether a value of the block's V (dim v, R rows) is too small for bf16 in units of 2^ev.
+__device__ __noinline__ bool any_small(const uint16_t* v, int R, int ev) {
+    bool small = false;
+#pragma unroll 8
+    for (int k = 0; k < R; ++k) {
+        const uint32_t w = __ldg(v + k * kQ8D) & 0x7fffu;
+        small |= w != 0u && static_cast<int>(w >> 7) <= ev;
+    }
+    return small;
 }
 
 // V of a context step as bf16 into tensor memory at `to`: dim l of 128 positions, `have` of which exist.
@@ -799,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     }
                     inf_s[(seg % 3 * kQ8D + l) * 2] = inf0;
                     inf_s[(seg % 3 * kQ8D + l) * 2 + 1] = inf1;
+                    if (ev > 0 && any_small(vsrc, a.R, ev)) run_failed();
                     // (the stage's place is kept for P's second part: one arrival comes from its product)
                     v_done(cw != 0);
                 }
@@ -890,9 +903,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 float mean[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float x = __uint_as_float(o[e]);
+                    const float x = __uint_as_float(o[e]) * move_s[hh * kRT + c0 + e];
                     bad |= !(fabsf(x) < INFINITY);
-                    mean[e] = x * move_s[hh * kRT + c0 + e] * v_unit;
+                    mean[e] = x * v_unit;
                 }
                 if ((inf0 | inf1) != 0ull) {   // (rare) V that is not finite and that the row sees
 #pragma unroll 1

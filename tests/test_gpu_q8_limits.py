@@ -356,3 +356,70 @@ def test_attn_values_of_any_size_alone(sv, least, t, mp):  # noqa: F811
     want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
     assert close(got, want, wgt), float(((got.double() - want).abs() / wgt).max())
     assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("t,mp", [(0, 1), (100, 2), (520, 9), (520, 250)])
+def test_attn_block_values_of_any_size(sv, t, mp):  # noqa: F811
+    """A draft's V of 3e38, seen by the later rows alone and with or without weight there, beside an
+    ordinary cache, and beside one whose values are next to nothing."""
+    r = np.random.default_rng(mp + 7)
+    P, R = mp + 1, 3
+    table = r.permutation(P)[:mp].reshape(1, mp)
+    q = torch.zeros(1, R, 1, 128)
+    q[..., 0] = 1.0
+    for size in (1.0, 2.0 ** -30, 2.0 ** -100):
+        kp, vp = pools_of([r.integers(-2, 3, (1, t, 128)) * 1.0], [size * r.standard_normal((1, t, 128))], P, table, [t])
+        kc, vc = held(kp, table[0], t, False), held(vp, table[0], t, True)
+        for at in (1, 2):
+            for score in (-300.0, -3.0, 0.0, 4.0):
+                kb, vb = torch.zeros(1, 1, R, 128), torch.from_numpy(size * r.standard_normal((1, 1, R, 128)))
+                kb[0, 0, at, 0] = score
+                vb[0, 0, at] = 3e38 * torch.where(vb[0, 0, at] > 0, 1.0, -1.0)
+                vb = bf16(vb)
+                got = sv.verify_attn_q8(bf16(q), dev(kp), dev(vp), i32(table), i32([t]), bf16(kb), vb, scale=LN2)[0]
+                want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
+                assert close(got, want, wgt), (size, at, score, got[:, 0, :3], want[:, 0, :3])
+    assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("R,t,mp", [(3, 100, 2), (40, 520, 9), (40, 520, 250), (65, 100, 250)])
+def test_attn_zeros_in_the_cache(sv, R, t, mp):  # noqa: F811
+    """A pool of zeros (as a server's warm-up has it) beside a block of any values, also where the
+    run is done again as the last row's own key outweighs what gives references."""
+    r = np.random.default_rng(R)
+    P = mp + 1
+    table = r.permutation(P)[:mp].reshape(1, mp)
+    kp, vp = pools_of([np.zeros((1, t, 128))], [np.zeros((1, t, 128))], P, table, [t])
+    kc, vc = held(kp, table[0], t, False), held(vp, table[0], t, True)
+    q = torch.zeros(1, R, 1, 128)
+    q[..., 0] = 1.0
+    for size in (1e-30, 1.0, 5000.0, 1e30):
+        for gap in (0.0, 60.0, 131.0, 200.0):
+            kb, vb = torch.zeros(1, 1, R, 128), bf16(size * r.standard_normal((1, 1, R, 128)))
+            kb[0, 0, R - 1, 0] = gap
+            got = sv.verify_attn_q8(bf16(q), dev(kp), dev(vp), i32(table), i32([t]), bf16(kb), vb, scale=LN2)[0]
+            want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
+            assert close(got, want, wgt), (size, gap, got[R - 1, 0, :3], want[R - 1, 0, :3])
+    assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("t,mp", [(100, 2), (520, 9), (520, 250)])
+@pytest.mark.parametrize("top", [2.0 ** 7, 2.0 ** 60, 2.0 ** 110])
+def test_attn_block_values_far_below_the_caches(sv, top, t, mp):  # noqa: F811
+    """The cache's values have no weight and are up to 2^200 times the block's, which are all that
+    the rows see."""
+    r = np.random.default_rng(mp + 3)
+    P, R = mp + 1, 3
+    table = r.permutation(P)[:mp].reshape(1, mp)
+    k = np.zeros((1, t, 128))
+    k[0, :, 0] = -320.0
+    kp, vp = pools_of([k], [top * r.standard_normal((1, t, 128))], P, table, [t])
+    kc, vc = held(kp, table[0], t, False), held(vp, table[0], t, True)
+    q = torch.zeros(1, R, 1, 128)
+    q[..., 0] = 1.0
+    for size in (1.0, 2.0 ** -40, 2.0 ** -90):
+        kb, vb = torch.zeros(1, 1, R, 128), bf16(size * r.standard_normal((1, 1, R, 128)))
+        got = sv.verify_attn_q8(bf16(q), dev(kp), dev(vp), i32(table), i32([t]), bf16(kb), vb, scale=LN2)[0]
+        want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
+        assert close(got, want, wgt), (size, float((got.double() - want).abs().max()))
+    assert sv.get_device_error() == 0
