@@ -647,11 +647,16 @@ SV_API sv_status sv_kv_gather_q8(const void* k_pool, const void* v_pool, int32_t
                                  uint16_t* v_out, void* stream);
 
 /* sv_verify_attn_paged over an 8-bit cache (k_pool, v_pool as above; the block's K and
- * V stay bf16).  The cache's values enter the products exactly; a query row, and a
- * block row of K, enter to within 2^-17 of their largest element, and one that holds
- * NaN or infinity as NaN; otherwise numerics, masks, flags and errors are those of
- * sv_verify_attn_paged, and the workspace (sv_verify_attn_q8_workspace bytes, any
- * contents, possibly 0) is as for sv_verify_attn_q4. */
+ * V stay bf16).  The cache's values and the block's V enter the products exactly (but
+ * beside larger V, V of at most 448 * 2^-120, or 2^-106 in the block, may count as 0); a
+ * query row, and a block row of K, enter to within 2^-17 of their largest element, and
+ * one that holds NaN or infinity as NaN; a weight is held to 11 bits, and those too
+ * small for f16 are left out where all of a row's together move it by at most 2^-8 of
+ * the mean |V|.  Where scale |q| |k| of the
+ * largest elements passes 2^127 scores may not be finite.  Otherwise numerics, masks,
+ * flags and errors are those of sv_verify_attn_paged, and the workspace
+ * (sv_verify_attn_q8_workspace bytes, any contents, possibly 0) is as for
+ * sv_verify_attn_q4. */
 SV_API size_t sv_verify_attn_q8_workspace(const sv_attn_shape* shape);
 SV_API sv_status sv_verify_attn_q8(const sv_attn_shape* shape, const uint16_t* q, const void* k_pool,
                                    const void* v_pool, int32_t num_pages, const int32_t* page_table,

@@ -27,8 +27,8 @@
 //        at a reference, below.
 // The block's K rows are held as Q's are, two e4m3 in units of the row's own (four
 // products).  Its V rows may be of any size, whether seen or not, and stay bf16 in V's units; its P is
-// in two bf16 parts then (16 bits).  (One too large in those units is infinite there, and O not finite;
-// one too small is looked for; either way the run is done again.)  What of them is not finite is kept out of the product and
+// in two bf16 parts then (16 bits).  (One too large in those units is infinite there, and O not finite:
+// the run is done again; so it is in units so large that others could be lost.)  What of them is not finite is kept out of the product and
 // added to the rows that see it at the end.
 // A row's maximum runs across lanes here, so it is formed once, over the first 32 keys
 // of the run (of the block, where the run has it: the row's own key and those next to
@@ -94,12 +94,14 @@ constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kTmaWarp = 12, kQkW
               kThreads = 32 * 16;
 constexpr int kVUp = 4;                   // V is in units of 2^kVUp of its first scales
 // f16 holds a run exactly whose scale is 2^-15 of the unit or more (its steps end at 2^-24, e4m3's
-// at 2^-9), 2^-kVDown of the largest scale there.  One below that, and not all zeros, is left to the
-// second pass.  (The warp that copies V looks at the scales, which it has in registers.)
+// at 2^-9), 2^-kVDown of the largest scale there.  One below that is left to the second pass, but
+// for those of the least scale there is: zeros, or as good (448 * 2^-120 at most).  (The warp that
+// copies V looks at the scales, which it has in registers.)
 constexpr int kVDown = 15 - kVUp;
-constexpr float kUp = -5.0f;              // P is 2^kUp at the reference
-constexpr float kUpSum = 0.0f;            // where the sums gave the reference, they are 2^kUpSum
-constexpr float kSlack = 4.0f;            // which, done again, stays where the maximum rises by no more
+constexpr int kMostUnit = 20;             // beside a block; its V of 2^-106 and more is exact then
+constexpr float kUp = -5.0f;              // P is 2^kUp at the reference;
+constexpr float kUpSum = 0.0f;            // where the sums gave the reference, they are 2^kUpSum;
+constexpr float kSlack = 4.0f;            // where it rises with the maximum, it stays up to that far below
 // A row's P sum to kLost times the keys or the run is done again: roundings below f16's smallest
 // steps, 2^-25 at most for each key, then move the row by at most 2^-8 of the mean |V| if all of
 // them went one way, and by that over the root of the keys as they do.  (A row that sees one of
@@ -107,11 +109,11 @@ constexpr float kSlack = 4.0f;            // which, done again, stays where the 
 // have one key of the block for a reference: 64 of them x 28 heads, whose K had a few dims six
 // times the others, had one done again, 62 us for 44, in every eighth call with kUp = -4.)
 constexpr float kLost = 0x1p-17f;
-constexpr float kLeastSum = 0x1p-100f;    // sums from here on give a reference
-constexpr int kKept = 4;                  // runs of a CTA whose references are kept for that
-// A sum from here on too.  The block's P is bf16 and reaches 2^128, where the row's own
-// key is not among those that give its reference; 1 / sum is 0 from 2^126 on.
+// So is one that sums to kMostSum: the block's P is bf16 and reaches 2^128, where the row's own
+// key is not among those that give its reference, and 1 / sum is 0 from 2^126 on.
 constexpr float kMostSum = 0x1p64f;
+constexpr float kLeastSum = 0x1p-100f;    // sums from here on give a reference for that,
+constexpr int kKept = 4;                  // and so many runs of a CTA keep theirs
 constexpr int kRecFloats = kRows * (kQ8D + 2);   // a partial: O [64][128], then (m, l) [64]
 constexpr int kCombineThreads = 256;
 constexpr int kMaxCluster = 8;
@@ -276,45 +278,9 @@ struct Rows {
     uint4 v[kN];
 };
 
-// What follows is rare, and what is long of it functions of their own: the SMs' caches do not hold all
-// that a CTA's warps run (64 single tokens 44.4 us; with this in line 46 to 55, by where it came to lie).
-
-// The least scale of V that f16 holds beside `top` (a scale's bits).
-__device__ __forceinline__ float least_scale(uint32_t top) {
-    return q8_pow2(max(q8_stored_exponent(__uint_as_float(top)) - kVDown, -126));
-}
-// Whether one of a lane's runs, those of `low` of block `blk` (of V, `left` positions of which count),
-// holds anything but zeros; one warp, for all of its lanes' blocks.
-__device__ __noinline__ bool any_codes(const uint8_t* blk, uint32_t low, int left) {
-    uint32_t any = 0u;
-#pragma unroll 1
-    for (uint32_t lanes = __ballot_sync(0xffffffffu, low != 0u); lanes != 0u; lanes &= lanes - 1u) {
-        const int x = __ffs(lanes) - 1, end = __shfl_sync(0xffffffffu, left, x);
-        const uint32_t runs = __shfl_sync(0xffffffffu, low, x);
-        const uint2* src = reinterpret_cast<const uint2*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(blk), x));
-#pragma unroll 1
-        for (int i = threadIdx.x & 31; i < kQ8Codes / 8; i += 32) {   // eight positions of a dim
-            const int n = min(end - 8 * (i >> 7), 8);
-            if (n <= 0 || (runs >> (i >> 8) & 1u) == 0u) continue;
-            const uint2 w = __ldg(src + i);
-            any |= (w.x & 0x7f7f7f7fu >> 8 * max(4 - n, 0)) | (n > 4 ? w.y & 0x7f7f7f7fu >> 8 * (8 - n) : 0u);
-        }
-    }
-    return __any_sync(0xffffffffu, any != 0u);
-}
-
-// Whether a value of the block's V (dim v, R rows) is too small for bf16 in units of 2^ev.
-__device__ __noinline__ bool any_small(const uint16_t* v, int R, int ev) {
-    bool small = false;
-#pragma unroll 8
-    for (int k = 0; k < R; ++k) {
-        const uint32_t w = __ldg(v + k * kQ8D) & 0x7fffu;
-        small |= w != 0u && static_cast<int>(w >> 7) <= ev;
-    }
-    return small;
-}
-
 // V of a context step as bf16 into tensor memory at `to`: dim l of 128 positions, `have` of which exist.
+// A function of its own, as it is rare: an SM's instruction cache does not hold all that a CTA's warps
+// run (64 single tokens 44 us; with this in line 46 to 55, by where it came to lie).
 __device__ __noinline__ void wide_v(const uint8_t* v, const float* scale, int have, int l, uint32_t to) {
     const uint32_t up = q8_pow2_pair(120);
 #pragma unroll 1
@@ -468,23 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         run = -1;
         return true;
     };
-    // With `own_code` the second pass has code of its own, so that the first one's is short: the roles
-    // that do other things then.  (Of the others it was measured: in clusters one code for both, 16
-    // sequences 34.3 us for 34.7, a tree 24.2 for 25.0; in the even split 64 single tokens 52.0 for 44.4.)
-    auto passes = [&](auto own_code, auto&& runs) {
-        if constexpr (own_code) {
-            runs(std::false_type{});
-            if (again()) runs(std::true_type{});
-        } else {
-            bool wide = false;
-            while (true) {
-                runs(wide);
-                if (wide || !again()) return;
-                wide = true;
-            }
-        }
+    // (The second pass has code of its own, so that the first one's is short.)
+    auto passes = [&](auto&& runs) {
+        runs(std::false_type{});
+        if (again()) runs(std::true_type{});
     };
-    constexpr std::bool_constant<!kCluster> kApart{};
 
     // The rows of Q of a run, by half-warps: rows hw, hw + 64 / kN .. of the tile (of its kLive).
     auto load_q = [&](auto& x, const Walk& of, int hw) {
@@ -532,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         uint64_t once;
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         int it = 0;
-        passes(kApart, [&](auto wide) {
+        passes([&](auto wide) {
             while (next_run(wide)) {
                 const int g = walk.cur_unit / wk.row_tiles;
                 const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
@@ -601,15 +555,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 if (lane < 2 && left > kQ8Run * r) top = max(top, w[r]);
-                            least = least_scale(__reduce_max_sync(0xffffffffu, top));
+                            least = q8_pow2(max(q8_stored_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, top))) - kVDown, kQ8MinExp));
                         }
-                        uint32_t low = 0u;
+                        bool low = false;
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (left > kQ8Run * r && __uint_as_float(w[r]) < least) low |= 1u << r;
-                        if (__any_sync(0xffffffffu, low != 0u) &&   // (rare)
-                            any_codes(pool + (static_cast<size_t>(max(pg, 0)) * a.Hkv + g) * kQ8Bytes, low, left))
-                            run_failed();
+                            low |= left > kQ8Run * r && __uint_as_float(w[r]) < least && __uint_as_float(w[r]) > q8_pow2(kQ8MinExp);
+                        if (low) run_failed();
                     }
                 }
             }
@@ -621,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         int it = 0, seg = 0;
         Turn sb;
         static_assert(kSBufs == kPBufs, "one turn for both");
-        passes(kApart, [&](auto wide) {
+        passes([&](auto wide) {
             while (next_run(wide)) {
                 const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
                 if (elect_one()) {
@@ -664,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         constexpr uint32_t id_o = idesc_f16_f32_bmn(128, kLive), id_two = idesc_bf16_f32(128, kLive, false, true);
         int it = 0, seg = 0;
         Turn pb;
-        passes(kApart, [&](auto wide) {
+        passes([&](auto wide) {
             while (next_run(wide)) {
                 const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
                 if (elect_one()) {
@@ -729,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
             }
             ++it;
         };
-        passes(std::true_type{}, [&](auto wide) {
+        passes([&](auto wide) {
             while (next_run(wide)) {
                 const int g = walk.cur_unit / wk.row_tiles;
                 const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R * kQ8D;
@@ -787,6 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 if (cw == 0 && lane == 0) vexp_s[seg % 3] = ev;
                 const float to = q8_pow2(-ev);
                 if (walk.block) {
+                    if (ev > kMostUnit) run_failed();
                     // V stays bf16: drafts that no row sees may be of any size.  Rows past the last are
                     // zeros.  What is not finite would reach the rows that do not see it (0 times it is
                     // NaN): it stays out of the product, and the epilogue adds it where it is seen
@@ -811,7 +764,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     }
                     inf_s[(seg % 3 * kQ8D + l) * 2] = inf0;
                     inf_s[(seg % 3 * kQ8D + l) * 2 + 1] = inf1;
-                    if (ev > 0 && any_small(vsrc, a.R, ev)) run_failed();
                     // (the stage's place is kept for P's second part: one arrival comes from its product)
                     v_done(cw != 0);
                 }
@@ -933,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
             return bad;
         };
         float* kept_s = reinterpret_cast<float*>(smem + kOffKept);
-        passes(std::true_type{}, [&](auto wide) {
+        passes([&](auto wide) {
             while (next_run(wide)) {
                 // done again: with the references that the sums gave, or moving ones
                 const bool kept = wide && run < kKept && (fail_s[6] >> run & 1) == 0, safe = wide && !kept;

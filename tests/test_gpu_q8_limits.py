@@ -423,3 +423,24 @@ def test_attn_block_values_far_below_the_caches(sv, top, t, mp):  # noqa: F811
         want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
         assert close(got, want, wgt), (size, float((got.double() - want).abs().max()))
     assert sv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("t,mp", [(520, 9), (520, 250), (200, 4)])
+@pytest.mark.parametrize("which", ["first", "later", "every second", "all but one"])
+def test_attn_runs_of_zeros_in_v(sv, which, t, mp):  # noqa: F811
+    """Sixteen and more positions whose V is 0, before, behind and between others."""
+    r = np.random.default_rng(mp + 5)
+    P, R = mp + 1, 2
+    table = r.permutation(P)[:mp].reshape(1, mp)
+    v = r.standard_normal((1, t, 128))
+    run = np.arange(t) // 16
+    v[:, {"first": run < 9, "later": run > 5, "every second": run % 2 == 0, "all but one": run != 10}[which]] = 0.0
+    kp, vp = pools_of([r.integers(-2, 3, (1, t, 128)) * 1.0], [v], P, table, [t])
+    kc, vc = held(kp, table[0], t, False), held(vp, table[0], t, True)
+    q = torch.zeros(1, R, 1, 128)
+    q[..., 0] = 1.0
+    kb, vb = torch.zeros(1, 1, R, 128), bf16(r.standard_normal((1, 1, R, 128)))
+    got = sv.verify_attn_q8(bf16(q), dev(kp), dev(vp), i32(table), i32([t]), bf16(kb), vb, scale=LN2)[0]
+    want, wgt = softmax64(q[0].cuda(), torch.cat([kc, kb[0].cuda()], 1), torch.cat([vc, vb[0]], 1), causal(R, t))
+    assert close(got, want, wgt), float(((got.double() - want).abs() / wgt).max())
+    assert sv.get_device_error() == 0
