@@ -41,11 +41,11 @@
 // reference was a key that the row does not see, or none was finite) they rise with the maximum.
 // V whose scales lie further apart than f16 holds is done that way too.
 // (64 single tokens x 28 heads, where each token scores the first position 30 nats above itself:
-// 91 us for 44; where one of the 64 does, 66.  16 sequences: 86 for 34.)
+// 92 us for 44; where one of the 64 does, 66.  16 sequences: 87 for 35.)
 //
 // What bounds it, in us of graph replays over inputs larger than L2 (heads and positions as
-// named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 34.0, for 137 MB, which take
-// 20.1 at copy rate; 64 single tokens of up to 4097: 43.4 (175 MB, 25.7).  CTAs that stream reach
+// named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 34.6, for 137 MB, which take
+// 20.1 at copy rate; 64 single tokens of up to 4097: 44.0 (175 MB, 25.7).  CTAs that stream reach
 // 5.5 to 5.9 TB/s; the rest is the start and the end of a run, chains of steps that each run
 // once, most of whose instructions come from L2 then: from the launch to the end of the
 // block's step 13,000 cycles with tiles of more than 32 rows (Q's rows made e4m3 2000, the
@@ -53,13 +53,15 @@
 // once their code is there), 7000 with others; the sums, O and their join 4000.  A CTA that goes on
 // to another unit pays 6000 of these again.  A step of two pages takes 1100 and 1300 cycles:
 // 112 and 128 KB pass shared memory at 128 bytes a cycle.  5 rows x 12 heads over 2, 4096: 9.7, and
-// 100001 positions 19.0 (floor 7.5), both latency: few pages a CTA.  A tree of 65 rows: 24.1; eight
+// 100001 positions 18.9 (floor 7.5), both latency: few pages a CTA.  A tree of 65 rows: 24.6; eight
 // tiles of rows a head stream the same pages, 17 steps each.
 // Tried: P in bf16; an MMA warp for both products, and one copier (a step waits for the
 // other's); 16 softmax warps of 16 rows (tensor memory reads and references double); two
 // groups of softmax warps in turn (16 sequences 42 -> 51.8: spills); the block as a run's second
 // step, so that references are of 32 keys of the cache (64 single tokens 43.4 -> 49.3: the first
-// pages come late); the next 32 pages' table and scales fetched ahead (43.4 -> 45.4).
+// pages come late); the next 32 pages' table and scales fetched ahead (43.4 -> 45.4); V's scales looked
+// at by the warps that convert (44.4 -> 50.1), zeros told from what f16 loses by reading their codes
+// again (587 where half of V is zeros); one code for both passes (44.0 -> 48 to 54).
 //
 // Work: units and runs as in attn_cache.cuh.  A unit that lies in several CTAs' runs
 // leaves partials in the workspace -- at most two a CTA -- and a second small kernel
@@ -107,7 +109,8 @@ constexpr float kSlack = 4.0f;            // where it rises with the maximum, it
 // them went one way, and by that over the root of the keys as they do.  (A row that sees one of
 // 4096 keys alone, by the reference, sums to 2^-5, which is kLost times those.  Single tokens
 // have one key of the block for a reference: 64 of them x 28 heads, whose K had a few dims six
-// times the others, had one done again, 62 us for 44, in every eighth call with kUp = -4.)
+// times the others, had one done again, 66 us for 44, in every eighth call with kUp = -4, in one of
+// thirty with -5.)
 constexpr float kLost = 0x1p-17f;
 // So is one that sums to kMostSum: the block's P is bf16 and reaches 2^128, where the row's own
 // key is not among those that give its reference, and 1 / sum is 0 from 2^126 on.
@@ -1361,13 +1364,13 @@ int resident_clusters(int c) {
 //   - the even split's, with the second kernel, 11500 and 17000, and a CTA that goes on to
 //     another unit 5500 and 10000 more, beside steps of 250 and 375 a page.  A single sequence's
 //     units are alike, and a multiple of their number of CTAs splits them without such CTAs:
-//     9000 and 13500 (9 x 28 heads over 4, 4096 positions: 18.2 -> 14.4 us).
+//     9000 and 13500 (9 x 28 heads over 4, 4096 positions: 18.2 -> 14.4 us when that came in).
 // Measured in us, the side that the rule takes first: 5 x 12 heads over 2 of 4096 positions,
-// clusters 9.9, split 10.0; of 8192, split 10.4, clusters 11.8; of 16384, split 11.9, clusters
-// 15.7; 9 x 28 over 4, 8192: split 15.3, clusters 15.8; four such: clusters 20.2, split 21.9;
-// 16: clusters of two 34.6, split 41.3; 64 of 4096: one CTA a unit 63.6, split 71.9; 40: split 50.5,
-// one a unit 60.4; 65 x 28 over 4, 8192: clusters 24.4, split 26.4; 32 single tokens of 2048: one
-// a unit 17.8, split 22.8; 64 of 256: 16.9 and 22.6; 64 of 4096: split 52.8, one a unit 54.2.  The
+// clusters 9.4, split 10.2; of 8192, split 10.1, clusters 11.6; of 16384, split 11.6, clusters
+// 16.0; 9 x 28 over 4, 8192: split 14.9, clusters 15.4; four such: clusters 19.7, split 21.1;
+// 16: clusters of two 34.5, split 40.5; 64 of 4096: one CTA a unit 64.5, split 75.8; 40: split 51.1,
+// one a unit 61.4; 65 x 28 over 4, 8192: clusters 24.4, split 25.9; 32 single tokens of 2048: one
+// a unit 17.6, split 23.5; 64 of 256: 16.8 and 22.8; 64 of 4096: split 53.2, one a unit 55.0.  The
 // table's capacity decides, as the lengths are on the device.
 void plan(Work& w, int B, int max_pages, int& grid) {
     const int64_t units = static_cast<int64_t>(B) * w.U, pages = units * (static_cast<int64_t>(max_pages) + 1);
