@@ -27,24 +27,25 @@
 //        at a reference, below.
 // The block's K rows are held as Q's are, two e4m3 in units of the row's own (four
 // products).  Its V rows may be of any size, whether seen or not, and stay bf16 in V's units; its P is
-// in two bf16 parts then (16 bits).  (One too large in those units is infinite there, and O not finite:
-// the run is done again; so it is in units so large that others could be lost.)  What of them is not finite is kept out of the product and
-// added to the rows that see it at the end.
+// in two bf16 parts then (16 bits).  (A V too large in those units is infinite there, and O not finite:
+// the run is done again, in the end without units; so is one whose units are so large that V could be
+// lost.)  What of them is not finite is kept out of the product and added to the rows that see it at
+// the end.
 // A row's maximum runs across lanes here, so it is formed once, over the first 32 keys
 // of the run (of the block, where the run has it: the row's own key and those next to
 // it), and is the row's reference m for the whole run.  P is 2^-5 at the reference: a
 // score 21 powers of two above it makes P infinite, and a P below 2^-25, a weight 2^-20
 // of the reference's, is lost.  A run whose O is not finite, or where a row's sum is so
-// small that what was lost could matter (kLost), is done again, and then nothing has f16's range:
-// V is bf16 in units of 1, as the read-back gives it, and P in two bf16 parts as the block's is.  Its
-// references are those that the sums give, P then summing to 1; where they say nothing (the
-// reference was a key that the row does not see, or none was finite) they rise with the maximum.
-// V whose scales lie further apart than f16 holds is done that way too.
+// small that what was lost could matter (kLost), is done again with references that the sums
+// give, P then summing to 2^15.  Where they give none (the reference was a key that the row does
+// not see, or none was finite), where V's scales lie further apart than f16 holds, and where that
+// fails too, the run is done without f16: V in bf16 in units of 1, as the read-back gives it, P in two
+// bf16 parts as the block's is, references from the sums (then 1) or rising with the maximum.
 // (64 single tokens x 28 heads, where each token scores the first position 30 nats above itself:
-// 92 us for 44; where one of the 64 does, 66.  16 sequences: 87 for 35.)
+// 67 us for 44, where one of the 64 does 51; 16 sequences 58 for 35.  Without f16: 92, 66 and 87.)
 //
 // What bounds it, in us of graph replays over inputs larger than L2 (heads and positions as
-// named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 34.6, for 137 MB, which take
+// named).  16 sequences x 9 rows, 28 heads over 4, 8192 positions: 34.5, for 137 MB, which take
 // 20.1 at copy rate; 64 single tokens of up to 4097: 44.0 (175 MB, 25.7).  CTAs that stream reach
 // 5.5 to 5.9 TB/s; the rest is the start and the end of a run, chains of steps that each run
 // once, most of whose instructions come from L2 then: from the launch to the end of the
@@ -52,7 +53,7 @@
 // block's K 2300, its scores 1500, references 2500, P 2400: the last three take half of that
 // once their code is there), 7000 with others; the sums, O and their join 4000.  A CTA that goes on
 // to another unit pays 6000 of these again.  A step of two pages takes 1100 and 1300 cycles:
-// 112 and 128 KB pass shared memory at 128 bytes a cycle.  5 rows x 12 heads over 2, 4096: 9.7, and
+// 112 and 128 KB pass shared memory at 128 bytes a cycle.  5 rows x 12 heads over 2, 4096: 9.8, and
 // 100001 positions 18.9 (floor 7.5), both latency: few pages a CTA.  A tree of 65 rows: 24.6; eight
 // tiles of rows a head stream the same pages, 17 steps each.
 // Tried: P in bf16; an MMA warp for both products, and one copier (a step waits for the
@@ -61,7 +62,7 @@
 // step, so that references are of 32 keys of the cache (64 single tokens 43.4 -> 49.3: the first
 // pages come late); the next 32 pages' table and scales fetched ahead (43.4 -> 45.4); V's scales looked
 // at by the warps that convert (44.4 -> 50.1), zeros told from what f16 loses by reading their codes
-// again (587 where half of V is zeros); one code for both passes (44.0 -> 48 to 54).
+// again (587 where half of V is zeros); one code for all passes (44.0 -> 48 to 54).
 //
 // Work: units and runs as in attn_cache.cuh.  A unit that lies in several CTAs' runs
 // leaves partials in the workspace -- at most two a CTA -- and a second small kernel
@@ -96,20 +97,21 @@ constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kTmaWarp = 12, kQkW
               kThreads = 32 * 16;
 constexpr int kVUp = 4;                   // V is in units of 2^kVUp of its first scales
 // f16 holds a run exactly whose scale is 2^-15 of the unit or more (its steps end at 2^-24, e4m3's
-// at 2^-9), 2^-kVDown of the largest scale there.  One below that is left to the second pass, but
+// at 2^-9), 2^-kVDown of the largest scale there.  One below that is left to the last pass, but
 // for those of the least scale there is: zeros, or as good (448 * 2^-120 at most).  (The warp that
 // copies V looks at the scales, which it has in registers.)
 constexpr int kVDown = 15 - kVUp;
 constexpr int kMostUnit = 20;             // beside a block; its V of 2^-106 and more is exact then
 constexpr float kUp = -5.0f;              // P is 2^kUp at the reference;
-constexpr float kUpSum = 0.0f;            // where the sums gave the reference, they are 2^kUpSum;
+constexpr float kUpSum = 15.0f;           // where the sums gave the reference, they are 2^kUpSum,
+constexpr float kUpWide = 0.0f;           // or, in the last pass, 2^kUpWide;
 constexpr float kSlack = 4.0f;            // where it rises with the maximum, it stays up to that far below
 // A row's P sum to kLost times the keys or the run is done again: roundings below f16's smallest
 // steps, 2^-25 at most for each key, then move the row by at most 2^-8 of the mean |V| if all of
 // them went one way, and by that over the root of the keys as they do.  (A row that sees one of
 // 4096 keys alone, by the reference, sums to 2^-5, which is kLost times those.  Single tokens
 // have one key of the block for a reference: 64 of them x 28 heads, whose K had a few dims six
-// times the others, had one done again, 66 us for 44, in every eighth call with kUp = -4, in one of
+// times the others, had one done again, 51 us for 44, in every eighth call with kUp = -4, in one of
 // thirty with -5.)
 constexpr float kLost = 0x1p-17f;
 // So is one that sums to kMostSum: the block's P is bf16 and reaches 2^128, where the row's own
@@ -140,9 +142,11 @@ constexpr int kOffBar = kOffScl + kSclSlots * kSclBytes;
 constexpr int kOffNm = kOffBar + 320;                     // [64] -m, m the rows' references
 constexpr int kOffMove = kOffNm + kRows * 4;              // [64] what O and l of the row are multiplied by
 constexpr int kOffRed = kOffMove + kRows * 4;             // [4 quadrants][64]
-// [8] the runs that failed; where the runs start [5]; (bit r) run r's sums give no references; a wait gave up
+// [12] (bit r) run r failed; where the runs start [5]; its sums give no references; a wait gave up; f16
+// does not hold its V; it failed in the second pass
+constexpr int kFailed = 0, kNoSums = 6, kNoF16 = 8, kFailedAgain = 9;
 constexpr int kOffFail = kOffRed + 4 * kRows * 4;
-constexpr int kOffPar = kOffFail + 32;                    // [128] parents
+constexpr int kOffPar = kOffFail + 48;                    // [128] parents
 constexpr int kOffAnc = kOffPar + kMaxR * 4;              // [128][2] 64-bit path masks
 constexpr int kOffRow = kOffAnc + kMaxR * 16;             // [64] (sequence, block row, head) of a tile row, -1 past the last
 constexpr int kOffUnit = kOffRow + kRows * 4;             // [2][64] units of the query rows
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         volatile int* f = reinterpret_cast<volatile int*>(smem + kOffFail);
-        f[0] = f[6] = f[7] = 0;
+        f[kFailed] = f[kNoSums] = f[7] = f[kNoF16] = f[kFailedAgain] = 0;
         auto init = [](uint64_t* b, int n, int count) {
 #pragma unroll 1
             for (int i = 0; i < n; ++i) mbar_init(b + i, count);
@@ -407,40 +411,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
             }
         }
     }
-    // Each role does the CTA's runs once, and those of them that failed (found while they are done,
-    // looked at after all have finished) a second time, `wide`.
-    int run = -1;              // the current one
-    uint32_t failed = 0u;      // (bit r) run r failed; bit 31: one of those from there on
-    auto next_run = [&](auto wide) {
+    // Each role does the CTA's runs once.  Those of them that failed (found while they are done, looked
+    // at after all have finished) are done a second time, with references that the first pass's sums
+    // give; those to which they give none, or V's scales no f16, or which fail again, `wide`.
+    int run = -1;               // the current one
+    uint32_t todo = ~0u;        // (bit r) run r is to be done; bit 31: those from there on
+    bool by_sums = false;       // the second pass
+    auto next_run = [&]() {
         do {
             if (!walk.next(a, wk)) return false;
             run = min(run + 1, 31);
-        } while (wide && (failed >> run & 1u) == 0u);
+        } while ((todo >> run & 1u) == 0u);
         return true;
     };
-    auto run_failed = [&]() { atomicOr(reinterpret_cast<int*>(smem + kOffFail), 1 << run); };
+    auto note_run = [&](int word) { atomicOr(reinterpret_cast<int*>(smem + kOffFail) + word, 1 << run); };
     // a warp's wait; its lanes go on together (what follows is warp-collective)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         bar_wait(bar, parity, late);
         __syncwarp();
     };
-    auto again = [&]() {
-        __syncwarp();
-        named_barrier(2, kThreads);
-        failed = static_cast<uint32_t>(*fail_s);
-        if (failed == 0u) return false;
+    auto restart = [&]() {
         // (bulk copies are not ordered among themselves: the failed run's partial has to have arrived
         // before the next one is sent to its place)
         if (threadIdx.x == 0) bulk_wait();
         __syncwarp();
         walk.load(a, fail_s + 1);
         run = -1;
-        return true;
     };
-    // (The second pass has code of its own, so that the first one's is short.)
+    // (The last pass has code of its own, so that the others' is short.)
     auto passes = [&](auto&& runs) {
-        runs(std::false_type{});
-        if (again()) runs(std::true_type{});
+        uint32_t last = 0u;
+        while (true) {
+            runs(std::false_type{});
+            __syncwarp();
+            named_barrier(2, kThreads);
+            if (by_sums) {
+                last |= static_cast<uint32_t>(fail_s[kFailedAgain]);
+                break;
+            }
+            const uint32_t failed = fail_s[kFailed], no_sums = fail_s[kNoSums], no_f16 = fail_s[kNoF16];
+            todo = failed & ~(no_sums | no_f16) & ((1u << kKept) - 1u);
+            last = (failed | no_f16) & ~todo;
+            if (todo == 0u) break;
+            by_sums = true;
+            restart();
+        }
+        if (last == 0u) return;
+        todo = last;
+        by_sums = false;
+        restart();
+        runs(std::true_type{});
     };
 
     // The rows of Q of a run, by half-warps: rows hw, hw + 64 / kN .. of the tile (of its kLive).
@@ -490,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         int it = 0;
         passes([&](auto wide) {
-            while (next_run(wide)) {
+            while (next_run()) {
                 const int g = walk.cur_unit / wk.row_tiles;
                 const int32_t* tab = a.pages + static_cast<size_t>(walk.cur_b) * a.max_pages;
                 const int np = walk.p1 - walk.p0;
@@ -550,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ring_full[s]);
                     __syncwarp();
-                    if (is_v && !wide && (i & 31) == 0) {
+                    if (is_v && !wide && !by_sums && (i & 31) == 0) {
                         const uint32_t w[4] = {f.x, f.y, f.z, f.w};
                         const int left = pg < 0 ? 0 : walk.cur_t - (walk.p0 + i + lane) * kQ8Page;
                         if (i == 0) {   // the largest of the first two pages, as the unit is found
@@ -564,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             low |= left > kQ8Run * r && __uint_as_float(w[r]) < least && __uint_as_float(w[r]) > q8_pow2(kQ8MinExp);
-                        if (low) run_failed();
+                        if (low) note_run(kNoF16);
                     }
                 }
             }
@@ -577,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         Turn sb;
         static_assert(kSBufs == kPBufs, "one turn for both");
         passes([&](auto wide) {
-            while (next_run(wide)) {
+            while (next_run()) {
                 const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
                 if (elect_one()) {
                     const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ + (seg & 1) * kQBytes), 16, 1024);
@@ -620,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         int it = 0, seg = 0;
         Turn pb;
         passes([&](auto wide) {
-            while (next_run(wide)) {
+            while (next_run()) {
                 const int n = walk.ctx_steps() + (walk.block ? 1 : 0);
                 if (elect_one()) {
                     bar_wait(o_free, (seg & 1) ^ 1, late);
@@ -685,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
             ++it;
         };
         passes([&](auto wide) {
-            while (next_run(wide)) {
+            while (next_run()) {
                 const int g = walk.cur_unit / wk.row_tiles;
                 const size_t blk0 = (static_cast<size_t>(walk.cur_b) * a.Hkv + g) * a.R * kQ8D;
                 // half-warps take the query rows, and the block's rows of K
@@ -729,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     if (warp < kConvWarp + 2 && lane == 0) mbar_arrive(&ring_full[s]);
                 }
                 // V is in units of 2^ev: of the largest scale of the first pages (their live runs) with
-                // kVUp powers of two to spare; done again, of 1.  Every warp finds it by itself.
+                // kVUp powers of two to spare; in the last pass of 1.  Every warp finds it by itself.
                 int ev = 0;
                 if (walk.ctx_steps() > 0 && !wide) {
                     const int first = it + (walk.block ? 1 : 0);
@@ -742,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 if (cw == 0 && lane == 0) vexp_s[seg % 3] = ev;
                 const float to = q8_pow2(-ev);
                 if (walk.block) {
-                    if (ev > kMostUnit) run_failed();
+                    if (ev > kMostUnit) note_run(kNoF16);
                     // V stays bf16: drafts that no row sees may be of any size.  Rows past the last are
                     // zeros.  What is not finite would reach the rows that do not see it (0 times it is
                     // NaN): it stays out of the product, and the epilogue adds it where it is seen
@@ -889,9 +909,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
         };
         float* kept_s = reinterpret_cast<float*>(smem + kOffKept);
         passes([&](auto wide) {
-            while (next_run(wide)) {
-                // done again: with the references that the sums gave, or moving ones
-                const bool kept = wide && run < kKept && (fail_s[6] >> run & 1) == 0, safe = wide && !kept;
+            while (next_run()) {
+                // done again: with the references that the sums gave, or, in the last pass, moving ones
+                const bool kept = run < kKept && (wide ? (fail_s[kNoSums] >> run & 1) == 0 : by_sums), safe = wide && !kept;
                 const int b = walk.cur_b, g = walk.cur_unit / wk.row_tiles, rt = walk.cur_unit % wk.row_tiles;
                 const int row0 = rt * wk.tile_rows, nrows = min(wk.tile_rows, rows - row0);
                 const bool first = kCluster && seg == 0;
@@ -902,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                 if (tid < kRows) {
                     const int gr = row0 + tid, j = gr * wk.inv_g >> 16;
                     row_s[tid] = tid < nrows ? (b * a.R + j) * a.Hq + g * a.G + gr - j * a.G : -1;
-                    nm_s[tid] = kept ? kept_s[run * kRows + tid] : 0.f;
+                    nm_s[tid] = kept ? kept_s[run * kRows + tid] + (wide ? kUpWide : kUpSum) : 0.f;
                 }
                 const bool tree = walk.block && a.parent != nullptr;
                 if (tree && tid < a.R) par_s[tid] = __ldg(a.parent + static_cast<size_t>(b) * a.R + tid);
@@ -1096,14 +1116,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     step_done();
                 };
                 // any step, the block's among them, whose P is bf16 (range) in two parts (16 bits), the second
-                // in the place of the step's K, which has been read; so is all P of a run done again.  Eight
+                // in the place of the step's K, which has been read; so is all P of the last pass.  Eight
                 // rows at a time; the sums go round, so that the loop's code serves them all (unrolled, the
                 // larger tile's spills).
                 auto any_step = [&](int st) {
                     s_wait();
                     const bool two = st < lead || wide;
                     const uint32_t seen = seen_by(st);
-                    if (safe || (st == 0 && !wide)) references(st, seen);
+                    if (safe || (st == 0 && !kept)) references(st, seen);
                     const float ks = key_scale(st);
                     uint8_t* prow = smem + kOffP + sb.x * kPBytes + l * 128;
                     uint8_t* rest = stage(it) + l * 128;
@@ -1154,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
 #pragma unroll 1
                 for (int st = 0; st < n; ++st) {
                     if (st >= lead && st < nwhole) {
-                        if (st == 0) {
+                        if (st == 0 && !kept) {
                             s_wait();
                             references(0, ~0u);
                         }
@@ -1183,11 +1203,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     lsum = (red_s[tid] + red_s[kRows + tid]) + (red_s[2 * kRows + tid] + red_s[3 * kRows + tid]);
                     const float least = kLost * static_cast<float>(kStepKeys * n);
                     bad = !(lsum < kMostSum) || (lsum < least && tid < nrows);
-                    if (!wide && run < kKept) {
+                    if (!wide && !by_sums && run < kKept) {
                         if ((lsum >= kLeastSum && lsum < INFINITY) || tid >= nrows)
-                            kept_s[run * kRows + tid] = nm_s[tid] + kUpSum - __log2f(fmaxf(lsum, kLeastSum));
+                            kept_s[run * kRows + tid] = nm_s[tid] - __log2f(fmaxf(lsum, kLeastSum));
                         else
-                            atomicOr(reinterpret_cast<int*>(smem + kOffFail) + 6, 1 << run);
+                            note_run(kNoSums);
                     }
                     move_s[tid] = lsum != 0.f ? __fdividef(1.0f, lsum) : 0.f;
                 }
@@ -1201,7 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(CacheAttnArgs a, W
                     if (direct) reinterpret_cast<uint16_t*>(rec)[r * kQ8D + l] = f32_bf16_bits(mean);
                     else rec[r * kQ8D + l] = mean;   // (rows past the tile's last too, never read)
                 });
-                if (bad && !wide) run_failed();
+                if (bad && !wide) note_run(by_sums ? kFailedAgain : kFailed);
                 tc_fence_before();
                 if (!kCluster && !direct) fence_proxy_async_smem();
                 soft_sync();   // red_s and nm_s read by everyone before the next run writes them; the rows are there
